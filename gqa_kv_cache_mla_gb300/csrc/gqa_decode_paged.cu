@@ -1,39 +1,45 @@
 // Attention of new tokens over a paged GQA key-value cache.
 //
-// Mathematics, for one token and one group of up to 16 query heads that read
-// the same key-value head: one pass over the context with the running maximum
-// m and sum l of a softmax.  For each 16 positions, S = Q K^T (16 heads x 16
-// positions), the scores' cap, distance bias and mask, m' = max(m, rowmax S),
-// P = 2^(S - m'), l' = l 2^(m - m') + sum P, O' = O 2^(m - m') + P V; pieces
-// with their own (m, l, O) join by the same rule.
+// Mathematics, for a row block of up to 16 rows (the query heads of a group
+// times the tokens of a chunk) that read the same key-value head: one pass
+// over the context with the running maximum m and sum l of a softmax.  For
+// each 16 positions, S = Q K^T (16 rows x 16 positions), the scores' cap,
+// distance bias and mask, m' = max(m, rowmax S), P = 2^(S - m'),
+// l' = l 2^(m - m') + sum P, O' = O 2^(m - m') + P V; parts with their own
+// (m, l, O) join by the same rule.
 //
-// Bound: HBM.  Each cache row is read once for 4 * heads flops per byte, far
-// below the ridge, so what counts is bytes in flight.  The units of all
-// tokens are cut into equal pieces (kva_split.cuh), one per resident CTA.
-// Inside a CTA every warp is a stream of its own: it takes every fourth slice
-// of 16 positions, keeps a private ring of slices in shared memory filled by
-// 16-byte asynchronous copies (any page size and stride; rows that are not
-// there are zero-filled), and its own (m, l, O) in registers; no barrier
-// stands between warps until a segment ends, where the four join through
-// their own ring memory.  With 96 KB of ring per CTA and two CTAs per SM about
-// 130 KB are in flight per SM, three times what HBM latency asks for.
+// Bound: HBM.  Each cache row is read once for 4 * 16 flops per value at
+// most, far below the ridge, so what counts is bytes in flight.  The units of
+// all chunks are cut into equal pieces (kva_split.cuh), one per resident CTA,
+// two CTAs per SM.  In a CTA one warp feeds a ring of half tiles (64
+// positions of K or of V) with tensor-map copies, running ahead across the
+// ends of segments, and four warps consume it, 16 positions of each tile
+// each, with (m, l, O) in registers of their own; nothing stands between the
+// four until a segment ends, where they join in shared memory.  96 KB of ring
+// per CTA keep up to 190 KB in flight per SM.
 //
-// The products use mma.sync m16n8k16: at 16 rows of which a group fills 4 to
-// 16, the kernel needs about 1% of the matrix units' rate, and these
-// instructions take their operands from registers, where the E4M3 codes are
-// converted (exactly) to fp16 on the way.
+// The products use mma.sync m16n8k16: at 16 rows the kernel needs a few
+// percent of the matrix units' rate, and these instructions take their
+// operands from registers, where the E4M3 codes are converted (exactly) to
+// fp16 on the way.
 #include <cstdint>
 #include <type_traits>
 
 #include "kva_split.cuh"
+#include "kva_tma.cuh"
 
 namespace kvw {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kSlice = kTile / kWarps;  // positions a warp takes at a time
-constexpr int kRows = 16;               // query heads of a row block
+constexpr int kWarps = 4;                   // consumers
+// Two warpgroups: the consumers, and one whose first warp feeds.  The launch
+// gives every thread 128 registers (two CTAs fill an SM's file); the feeding
+// group hands 72 of them on to the consumers.
+constexpr int kThreads = 32 * 2 * kWarps;
+constexpr int kConsumerRegs = 200, kFeederRegs = 56;
+static_assert(kConsumerRegs + kFeederRegs <= 2 * 128, "registers of the launch");
+constexpr int kSlice = kTile / kWarps;      // positions of a tile that a warp takes
+constexpr int kRows = 16;                   // rows of a row block
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 static_assert(kSlice == 16, "one m16n8k16 operand");
 
@@ -43,17 +49,16 @@ struct GqaArgs {
     float* lse;
     const uint16_t* q;
     int64_t q_stride;
-    const unsigned char* k_base;  // K plane of the layer
-    int64_t kv_bytes;             // from the K plane to the V plane
-    int64_t s_page, s_token, s_head;
     const uint32_t* page_table;
     const float* slopes;
     uint32_t* err_flags;
     unsigned char* workspace;
-    float sm_scale, softcap, k_scale, v_scale;
-    uint32_t Hq, Hk, G, HB, D;  // query heads, kv heads, group, row blocks per group, head size
-    uint32_t num_pages, max_pages, pieces;
+    float sm_scale, softcap, cap_factor, k_scale, v_scale;
+    uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
+    uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
+    uint32_t num_pages, max_pages, pieces, copy_rows;
     FastDiv ps;
+    uint64_t wait_ns;
 };
 
 template <int DP>
@@ -65,17 +70,6 @@ template <int DP>
 __device__ __forceinline__ float* slot_of(unsigned char* ws, uint32_t c, uint32_t s) {
     return reinterpret_cast<float*>(ws + kMaxPieces * sizeof(OpenPiece)) +
            (uint64_t)(2 * c + s) * slot_floats<DP>();
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(there ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -114,11 +108,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// Two E4M3 codes (low byte first) -> f16x2, exact.
-__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t two) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four E4M3 codes -> two f16x2 (low bytes first), exact.
+__device__ __forceinline__ void codes_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 
 template <bool F16>
@@ -149,148 +144,302 @@ __device__ __forceinline__ void row_power(uint32_t top, float& up, float& down) 
 template <int DP, bool FP8>
 struct Shape {
     static constexpr int kEsz = FP8 ? 1 : 2;
-    static constexpr int kRowBytes = DP * kEsz;
-    static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
-    static constexpr int kPlane = kSlice * kRowBytes;
-    static constexpr int kStage = 2 * kPlane;  // K and V of one slice
-    static constexpr int kBudget = (DP > 128 && !FP8 ? 192 : 96) * 1024;
-    static constexpr int kFit = kBudget / (kWarps * kStage);
-    static constexpr int kStages = kFit > 8 ? 8 : kFit;
-    static constexpr int kCtasPerSm = DP > 128 && !FP8 ? 1 : 2;
+    // Bytes of a swizzled line.  Always 128: a copy may be a single row, and
+    // its place in shared memory has to be 128-byte aligned (64-wide E4M3
+    // rows leave half of a line empty).
+    static constexpr int kLine = 128;
+    static constexpr int kBlocks = (DP * kEsz + kLine - 1) / kLine;  // lines of a row
+    static constexpr int kBlock = kTile * kLine;     // one line of every row of a tile
+    static constexpr int kHalf = kBlocks * kBlock;   // K or V of one tile
+    static constexpr int kHalves = 96 * 1024 / kHalf > 12 ? 12 : 96 * 1024 / kHalf;
+    static constexpr bool kPair = kHalves >= 12;  // two slices at a time: half the softmax's cost
+    static constexpr int kRing = kHalves * kHalf;
+    // queries stay in registers while the accumulators leave room
     static constexpr bool kQInRegs = DP <= 128;
-    static constexpr int kQBytes = kQInRegs ? 0 : DP / 16 * 512;
-    static constexpr int kScratchPitch = DP + 4;
-    static constexpr int kSmem = kWarps * kStages * kStage + kQBytes;
-    static_assert(kStages >= 3 && kStages * kStage >= kRows * kScratchPitch * 4, "ring size");
+    static constexpr int kQBufs = kQInRegs ? 2 : 1;
+    static constexpr int kQRaw = kRows * DP * 2;
+    // rows that join at a time; their memory holds Q's operands in between
+    // where these are not in registers
+    static constexpr int kJoinRows = 1024 / (kWarps * DP / 2);
+    static constexpr int kJoin = 8192;
+    static_assert(kHalves >= 3 && kWarps * kJoinRows * DP * 4 == kJoin, "shared memory");
+    static_assert(kQInRegs || DP / 16 * 512 <= kJoin, "Q operands");
 };
 
-// Byte offset of chunk c of row r in a plane: the chunk is exchanged within
-// its 128-byte line so that eight rows of one chunk fall on distinct banks.
-template <int CHUNKS>
+template <int DP, bool FP8>
+struct Smem {
+    using Sh = Shape<DP, FP8>;
+    unsigned char ring[Sh::kRing];
+    unsigned char q_raw[Sh::kQBufs][Sh::kQRaw];
+    unsigned char join[Sh::kJoin];
+    uint64_t full[Sh::kHalves], empty[Sh::kHalves], q_full[2], q_empty[2], meet;
+    uint64_t there[Sh::kHalves];  // of a K half: positions of the tile that are there
+    float m[kWarps][kRows], l[kWarps][kRows];
+    SplitShared<kThreads> split;
+    uint32_t stop;  // a wait ran out
+};
+
+// Byte offset in a half tile of 16-byte chunk c of row r.
+template <int DP, bool FP8>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
-    if constexpr (CHUNKS >= 8)
-        return (r * CHUNKS + (c ^ (r & 7u))) * 16u;
-    else
-        return (r * CHUNKS + (c ^ ((r >> 1) & 3u))) * 16u;
+    return (c >> 3) * Shape<DP, FP8>::kBlock + r * 128u + (((c ^ r) & 7u) << 4);
 }
 
-template <int DP, bool FP8>
-__global__ void __launch_bounds__(kThreads, (Shape<DP, FP8>::kCtasPerSm))
-    gqa_decode_kernel(const GqaArgs a) {
+// Bounded wait of a whole warp that ends early when another role gave up;
+// the answer is the same for all lanes.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t* stop,
+                                           uint64_t limit_ns) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (*reinterpret_cast<volatile uint32_t*>(stop)) break;
+            if (global_ns() - t0 > limit_ns) {
+                *reinterpret_cast<volatile uint32_t*>(stop) = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// A ring position: slot and the parity of its present round.
+template <int N>
+struct RingPos {
+    uint32_t slot = 0, parity = 0;
+    __device__ __forceinline__ void step() {
+        if (++slot == (uint32_t)N) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// The feeding warp: walks the piece's tiles ahead of the arithmetic.
+template <int DP, bool FP8, bool WITHHOLD>
+__device__ __forceinline__ void feed(const GqaArgs& a, const CUtensorMap* map,
+                                     Smem<DP, FP8>& sm) {
     using Sh = Shape<DP, FP8>;
-    constexpr int KS = DP / 16, NT = DP / 8, CH = Sh::kChunks;
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ SplitShared<kThreads> s_split;
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    __shared__ uint32_t s_there[kWarps][Sh::kStages];
+    const uint32_t lane = threadIdx.x & 31u;
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    RingPos<Sh::kHalves> at;
+    RingPos<Sh::kQBufs> q_at;
+    uint32_t bad_page = 0, issued = 0;
+    bool ok = true, first_half = true;
+    const uint32_t R = a.copy_rows, copies = kTile / R;
+    while (ok && !w.done()) {
+        const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
+        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        // ---- the queries: one copy per token
+        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_ns);
+        if (!ok) break;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&sm.q_full[q_at.slot], w.span.tokens * in_block * a.D * 2);
+        __syncwarp();
+        if (lane < w.span.tokens)
+            bulk_load(sm.q_raw[q_at.slot] + lane * in_block * a.D * 2,
+                      a.q + (int64_t)(w.t + lane) * a.q_stride +
+                          (int64_t)(kvh * a.G + hb * kRows) * a.D,
+                      in_block * a.D * 2, &sm.q_full[q_at.slot]);
+        q_at.step();
+        // ---- the tiles
+        for (uint32_t i = w.first; ok && i < w.last; ++i) {
+            const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
+            // lane l looks up copies l and l + 32
+            uint32_t page[2], row[2];
+            uint64_t there = 0;
+            uint32_t n = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t c = lane + 32u * h;
+                const int64_t p = p_tile + (int64_t)c * R;
+                page[h] = KVW_PAGE_UNMAPPED;
+                row[h] = 0;
+                uint64_t mine = 0;
+                if (c < copies && p < w.span.hi && p + R > w.span.start) {
+                    const uint32_t idx = fast_div((uint32_t)p, a.ps);
+                    row[h] = (uint32_t)p - idx * a.ps.d;
+                    const uint32_t id =
+                        idx < a.max_pages
+                            ? __ldg(a.page_table + (uint64_t)w.b * a.max_pages + idx)
+                            : KVW_PAGE_UNMAPPED;
+                    if (id < a.num_pages) {
+                        page[h] = id;
+                        const int64_t lo = p > w.span.start ? p : w.span.start;
+                        const int64_t hi = p + R < w.span.hi ? p + R : w.span.hi;
+                        const uint32_t len = (uint32_t)(hi - lo);
+                        mine = (len == 64 ? ~0ull : (1ull << len) - 1) << (uint32_t)(lo - p_tile);
+                    } else {
+                        bad_page = 1;
+                    }
+                }
+                n += __popc(__ballot_sync(0xffffffffu, mine != 0));
+                there |= mine;
+                if (copies <= 32) {
+                    page[1] = KVW_PAGE_UNMAPPED;
+                    break;
+                }
+            }
+            const uint32_t t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
+            const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+#pragma unroll 1
+            for (uint32_t plane = 0; plane < 2; ++plane) {
+                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (plane == 0) sm.there[at.slot] = ((uint64_t)t_hi << 32) | t_lo;
+                    mbar_arrive_expect_tx(&sm.full[at.slot], n * R * Sh::kLine * Sh::kBlocks);
+                }
+                __syncwarp();
+                if (!(WITHHOLD && first_half)) {
+                    const uint32_t bar = smem_addr(&sm.full[at.slot]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (page[h] == KVW_PAGE_UNMAPPED) continue;
+                        const uint32_t dst = smem_addr(sm.ring + at.slot * Sh::kHalf) +
+                                             (lane + 32u * h) * R * Sh::kLine;
+#pragma unroll
+                        for (int blk = 0; blk < Sh::kBlocks; ++blk)
+                            tma_rows(dst + blk * Sh::kBlock, map, blk * (Sh::kLine / Sh::kEsz),
+                                     kvh, row[h], page[h], plane, bar);
+                    }
+                }
+                first_half = false;
+                at.step();
+                ++issued;
+            }
+        }
+        if (ok) w.next(a.split);
+    }
+    if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
+    if (!ok) {
+        // copies still under way land in this CTA's memory: wait for them (a
+        // bounded time) before the CTA may end
+        if (lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+        const uint32_t n = issued < (uint32_t)Sh::kHalves ? issued : (uint32_t)Sh::kHalves;
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint32_t x = issued - 1 - i;
+            mbar_wait(&sm.full[x % Sh::kHalves], (x / Sh::kHalves) & 1u, a.wait_ns);
+        }
+        for (uint32_t i = 0; i < (uint32_t)Sh::kQBufs; ++i)
+            mbar_wait(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_ns);
+    }
+}
+
+template <int DP, bool FP8, bool MODS, bool WITHHOLD>
+__global__ void __launch_bounds__(kThreads, 2)
+    gqa_decode_kernel(const GqaArgs a, const __grid_constant__ CUtensorMap map) {
+    using Sh = Shape<DP, FP8>;
+    constexpr int KS = DP / 16, NT = DP / 8, CH = DP * Sh::kEsz / 16, NP = Sh::kPair ? 2 : 1;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    Smem<DP, FP8>& sm = *reinterpret_cast<Smem<DP, FP8>*>(dyn);
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    const uint32_t quad = lane >> 2, in_quad = lane & 3u;
-    unsigned char* ring = smem + warp * (Sh::kStages * Sh::kStage);
-    const uint32_t ring_addr = smem_addr(ring);
-    [[maybe_unused]] uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + kWarps * Sh::kStages * Sh::kStage);
-
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    PieceStart piece;
-    const bool ok = find_piece(a.split, a.pieces, blockIdx.x, s_split, piece);
+    if (tid == 0) {
+        for (int i = 0; i < Sh::kHalves; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], kWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], kWarps);
+        }
+        mbar_init(&sm.meet, kWarps);
+        sm.stop = 0;
+        mbar_init_fence();
+        prefetch_map(&map);
+    }
+    const bool ok = find_piece(a.split, a.pieces, blockIdx.x, sm.split);
     OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
     if (tid == 0) open->units = 0;
     if (!ok) {
         if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
         return;
     }
+    if (warp >= kWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeederRegs));
+        if (warp == kWarps) feed<DP, FP8, WITHHOLD>(a, &map, sm);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+
+    const uint32_t quad = lane >> 2, in_quad = lane & 3u;
+    const uint32_t ring_addr = smem_addr(sm.ring);
+    float* s_join = reinterpret_cast<float*>(sm.join);
+    [[maybe_unused]] uint32_t* s_q = reinterpret_cast<uint32_t*>(sm.join);
+    RingPos<Sh::kHalves> at;
+    RingPos<Sh::kQBufs> q_at;
+    uint32_t meet_parity = 0;
+    auto ready = [&](const RingPos<Sh::kHalves>& x) {
+        return wait_phase(&sm.full[x.slot], x.parity, &sm.stop, a.wait_ns);
+    };
+    // the consumers meet (bounded, so that one that gave up strands nobody)
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.meet);
+        const bool met = wait_phase(&sm.meet, meet_parity, &sm.stop, a.wait_ns);
+        meet_parity ^= 1u;
+        return met;
+    };
     Walk w;
-    w.begin(a.split, piece);
-    uint32_t bad_page = 0;
-
-    while (w.u < w.u1) {
-        uint32_t block, first, last;
-        uint64_t end;
-        w.segment(block, first, last, end);
-        const uint32_t kvh = block / a.HB, hb = block - kvh * a.HB;
-        const uint32_t rows = a.G - hb * kRows < kRows ? a.G - hb * kRows : kRows;
+    w.begin(a.split, sm.split.start);
+    bool alive = true;
+    while (!w.done()) {
+        const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
+        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        const uint32_t rows = w.span.tokens * in_block;
         const uint32_t head0 = kvh * a.G + hb * kRows;
-        const uint64_t pos = w.len0 + w.i;
-        const uint64_t start = w.span.start, hi = w.span.hi;
-        const int64_t head_off = (int64_t)kvh * a.s_head;
-        if (pos >= a.split.cap) bad_page = 1;
-
-        // ---- one slice of K and V on its way into stage `st`
-        const uint32_t slices = last - first;
-        const uint32_t p_first = (w.span.tile0 + first) * kTile + warp * kSlice;
-        auto issue = [&](uint32_t k) {
-            const uint32_t st = k % Sh::kStages;
-            const uint32_t p0 = p_first + k * kTile;
-            int64_t off = -1;
-            if (lane < kSlice) {
-                const uint64_t p = (uint64_t)p0 + lane;
-                if (p >= start && p < hi) {
-                    off = slot_row(a.page_table, a.max_pages, a.num_pages, a.ps, a.s_page,
-                                   a.s_token, head_off, w.b, p);
-                    if (off < 0)
-                        bad_page = 1;
-                    else
-                        off *= Sh::kEsz;
-                }
-            }
-            const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
-            if (lane == 0) s_there[warp][st] = there;
-            const uint32_t k_dst = ring_addr + st * Sh::kStage, v_dst = k_dst + Sh::kPlane;
-            constexpr int kRowsPer = 32 / CH > 0 ? 32 / CH : 1;
-            constexpr int kIters = kSlice * CH / 32;
-#pragma unroll
-            for (int it = 0; it < kIters; ++it) {
-                const uint32_t r = CH >= 32 ? it * 32 / CH : it * kRowsPer + lane / CH;
-                const uint32_t c = CH >= 32 ? lane + (it * 32) % CH : lane % CH;
-                const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                const bool in = o >= 0 && c * (16 / Sh::kEsz) < a.D;
-                const unsigned char* src = a.k_base + (in ? o + c * 16 : 0);
-                cp_async16(k_dst + chunk_at<CH>(r, c), src, in);
-                cp_async16(v_dst + chunk_at<CH>(r, c), src + a.kv_bytes, in);
-            }
-        };
-#pragma unroll
-        for (int k = 0; k < Sh::kStages - 1; ++k) {
-            if ((uint32_t)k < slices) issue(k);
-            cp_commit();
-        }
+        const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
+        if (pos0 + w.span.tokens > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
 
         // ---- queries: A operands, fp16 rows brought into range by 2^x
         const uint32_t r0 = quad, r1 = quad + 8;
-        const uint16_t* q0 = a.q + (int64_t)w.t * a.q_stride + (int64_t)(head0 + r0) * a.D;
-        const uint16_t* q1 = q0 + 8ll * a.D;
+        const uint32_t t0 = r0 / in_block, t1 = r1 / in_block;  // tokens of the chunk
+        alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_ns);
+        if (!alive) break;
+        const uint16_t* q0 = reinterpret_cast<const uint16_t*>(sm.q_raw[q_at.slot]) + r0 * a.D;
+        const uint16_t* q1 = q0 + 8 * a.D;
         // two neighbouring values of a row; column order of the k16 operand
         // (bf16: as the instruction has it; fp16: the order in which the
         // E4M3 codes of a lane's 4-byte word are unpacked)
         auto q_word = [&](const uint16_t* p, uint32_t r, int ks, int half) -> uint32_t {
             const uint32_t d = 16 * ks + (FP8 ? 4 * in_quad + 2 * half : 2 * in_quad + 8 * half);
-            return r < rows && d < a.D ? __ldg(reinterpret_cast<const uint32_t*>(p + d)) : 0u;
+            return r < rows && d < a.D ? *reinterpret_cast<const uint32_t*>(p + d) : 0u;
         };
         float qs0 = a.sm_scale, qs1 = a.sm_scale, up0 = 1.0f, up1 = 1.0f;
         if constexpr (FP8) {
-            uint32_t t0 = 0, t1 = 0;
+            uint32_t top0 = 0, top1 = 0;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    t0 = __vmaxu2(t0, q_word(q0, r0, ks, h) & 0x7fff7fffu);
-                    t1 = __vmaxu2(t1, q_word(q1, r1, ks, h) & 0x7fff7fffu);
+                    top0 = __vmaxu2(top0, q_word(q0, r0, ks, h) & 0x7fff7fffu);
+                    top1 = __vmaxu2(top1, q_word(q1, r1, ks, h) & 0x7fff7fffu);
                 }
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
-                t0 = __vmaxu2(t0, __shfl_xor_sync(0xffffffffu, t0, o));
-                t1 = __vmaxu2(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+                top0 = __vmaxu2(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+                top1 = __vmaxu2(top1, __shfl_xor_sync(0xffffffffu, top1, o));
             }
-            t0 = max(t0 & 0xffffu, t0 >> 16);
-            t1 = max(t1 & 0xffffu, t1 >> 16);
+            top0 = max(top0 & 0xffffu, top0 >> 16);
+            top1 = max(top1 & 0xffffu, top1 >> 16);
             float d0, d1;
-            row_power(t0, up0, d0);
-            row_power(t1, up1, d1);
+            row_power(top0, up0, d0);
+            row_power(top1, up1, d1);
             qs0 = a.sm_scale * a.k_scale * d0;
             qs1 = a.sm_scale * a.k_scale * d1;
         }
+        if constexpr (!MODS) {  // scores in units of log2 straight from the product
+            qs0 *= kLog2e;
+            qs1 *= kLog2e;
+        }
+        // never 0: a masked score is -inf times this
+        qs0 = fmaxf(qs0, 1.17549435e-38f);
+        qs1 = fmaxf(qs1, 1.17549435e-38f);
         auto q_conv = [&](uint32_t v, float up) -> uint32_t {
             if constexpr (FP8) return pack2<true>(bf16_lo(v) * up, bf16_hi(v) * up);
             return v;
@@ -313,87 +462,143 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, FP8>::kCtasPerSm))
                 v.w = q_conv(q_word(q1, r1, ks, 1), up1);
                 *reinterpret_cast<uint4*>(s_q + (ks * 32 + lane) * 4) = v;
             }
-            __syncthreads();
+            alive = meet();
+            if (!alive) break;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[q_at.slot]);
+        q_at.step();
+        auto q_frag = [&](int ks, uint32_t(&f)[4]) {
+            if constexpr (Sh::kQInRegs) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = qf[ks][i];
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(s_q + (ks * 32 + lane) * 4);
+                f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+            }
+        };
         float slope0 = 0.0f, slope1 = 0.0f;
-        if (a.slopes) {
-            slope0 = r0 < rows ? __ldg(a.slopes + head0 + r0) : 0.0f;
-            slope1 = r1 < rows ? __ldg(a.slopes + head0 + r1) : 0.0f;
+        if constexpr (MODS) {
+            if (a.slopes) {
+                slope0 = r0 < rows ? __ldg(a.slopes + head0 + (r0 - t0 * in_block)) : 0.0f;
+                slope1 = r1 < rows ? __ldg(a.slopes + head0 + (r1 - t1 * in_block)) : 0.0f;
+            }
         }
+        // positions every row of the block sees, and each row's own
+        const int64_t all_hi = pos0, all_lo = pos0 + w.span.tokens - a.split.window;
+        const int64_t own0 = pos0 + t0, own1 = pos0 + t1;
+        auto sees = [&](int64_t own, int64_t p) { return p <= own && p > own - a.split.window; };
 
         float acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        const uint32_t mat = lane >> 3, mrow = lane & 7u;
+        const int64_t p_first = (int64_t)(w.span.tile0 + w.first) * kTile + warp * kSlice;
 
-        for (uint32_t k = 0; k < slices; ++k) {
-            if (k + Sh::kStages - 1 < slices) issue(k + Sh::kStages - 1);
-            cp_commit();
-            cp_wait<Sh::kStages - 1>();
-            __syncwarp();
-            const uint32_t st = k % Sh::kStages;
-            const uint32_t there = s_there[warp][st];
-            const uint32_t k_src = ring_addr + st * Sh::kStage, v_src = k_src + Sh::kPlane;
-
+        // `N` slices of tiles k, k + 1, ...
+        auto slices = [&](uint32_t k, auto n_const) -> bool {
+            constexpr int N = decltype(n_const)::value;
+            RingPos<Sh::kHalves> h[2 * N];  // K and V of each
+            h[0] = at;
+#pragma unroll
+            for (int i = 1; i < 2 * N; ++i) {
+                h[i] = h[i - 1];
+                h[i].step();
+            }
+            at = h[2 * N - 1];
+            at.step();
+            float s[2 * N][4];
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+            uint32_t there[N];
             // ---- S = Q K^T
-            float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            const uint32_t mat = lane >> 3, mrow = lane & 7u;
-            auto q_frag = [&](int ks, uint32_t(&f)[4]) {
-                if constexpr (Sh::kQInRegs) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = qf[ks][i];
+            for (int i = 0; i < N; ++i) {
+                if (!ready(h[2 * i])) return false;
+                there[i] = (uint32_t)(sm.there[h[2 * i].slot] >> (warp * kSlice)) & 0xffffu;
+                const uint32_t src = ring_addr + h[2 * i].slot * Sh::kHalf;
+                const uint32_t row0 = warp * kSlice;
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        uint32_t kf[4], f[4];
+                        ldsm4(kf, src + chunk_at<DP, FP8>(row0 + (mat >> 1) * 8 + mrow,
+                                                          2 * ks + (mat & 1)));
+                        q_frag(ks, f);
+                        mma16816<false>(s[2 * i], f, kf[0], kf[1]);
+                        mma16816<false>(s[2 * i + 1], f, kf[2], kf[3]);
+                    }
                 } else {
-                    const uint4 v = *reinterpret_cast<const uint4*>(s_q + (ks * 32 + lane) * 4);
-                    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-                }
-            };
-            if constexpr (!FP8) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t kf[4], f[4];
-                    ldsm4(kf, k_src + chunk_at<CH>((mat >> 1) * 8 + mrow, 2 * ks + (mat & 1)));
-                    q_frag(ks, f);
-                    mma16816<false>(s[0], f, kf[0], kf[1]);
-                    mma16816<false>(s[1], f, kf[2], kf[3]);
-                }
-            } else {
+                    for (int ks = 0; ks < KS; ks += 2) {
+                        uint32_t kf[4], f[4], x, y;
+                        ldsm4(kf, src + chunk_at<DP, FP8>(row0 + (mat & 1) * 8 + mrow,
+                                                          ks + (mat >> 1)));
 #pragma unroll
-                for (int ks = 0; ks < KS; ks += 2) {
-                    uint32_t kf[4], f[4];
-                    ldsm4(kf, k_src + chunk_at<CH>((mat & 1) * 8 + mrow, ks + (mat >> 1)));
-                    q_frag(ks, f);
-                    mma16816<true>(s[0], f, codes_to_f16x2(kf[0]), codes_to_f16x2(kf[0] >> 16));
-                    mma16816<true>(s[1], f, codes_to_f16x2(kf[1]), codes_to_f16x2(kf[1] >> 16));
-                    q_frag(ks + 1, f);
-                    mma16816<true>(s[0], f, codes_to_f16x2(kf[2]), codes_to_f16x2(kf[2] >> 16));
-                    mma16816<true>(s[1], f, codes_to_f16x2(kf[3]), codes_to_f16x2(kf[3] >> 16));
+                        for (int hh = 0; hh < 2; ++hh) {
+                            q_frag(ks + hh, f);
+                            codes_to_f16(kf[2 * hh], x, y);
+                            mma16816<true>(s[2 * i], f, x, y);
+                            codes_to_f16(kf[2 * hh + 1], x, y);
+                            mma16816<true>(s[2 * i + 1], f, x, y);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[h[2 * i].slot]);
+            }
+            // ---- cap, distance bias, mask
+            bool uneven[N];  // not every row sees the same positions of the slice
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int64_t p0 = p_first + (int64_t)(k + i) * kTile;
+                if constexpr (MODS) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float x = s[2 * i + n][e] * (e < 2 ? qs0 : qs1);
+                            if (a.softcap > 0.0f) {
+                                // tanh y = 1 - 2 / (e^2y + 1): absolute error of a few
+                                // 2^-24, so the capped score is off by that times the cap
+                                const float z = fast_exp2(x * a.cap_factor);
+                                x = a.softcap - __fdividef(2.0f * a.softcap, z + 1.0f);
+                            }
+                            if (a.slopes) {
+                                const int64_t j = p0 + n * 8 + 2 * in_quad + (e & 1);
+                                x -= e < 2 ? slope0 * (float)(own0 - j) : slope1 * (float)(own1 - j);
+                            }
+                            s[2 * i + n][e] = x * kLog2e;
+                        }
+                }
+                uneven[i] = p0 + kSlice - 1 > all_hi || p0 < all_lo;
+                if (there[i] != 0xffffu || uneven[i]) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t j = n * 8 + 2 * in_quad + (e & 1);
+                            if (!((there[i] >> j) & 1u) || !sees(e < 2 ? own0 : own1, p0 + j))
+                                s[2 * i + n][e] = -INFINITY;
+                        }
                 }
             }
-
-            // ---- scores in units of log2: cap, distance bias, mask
-            const uint32_t p0 = p_first + k * kTile;
+            // ---- running maximum, weights
+            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t j = n * 8 + 2 * in_quad + (e & 1);
-                    float x = s[n][e] * (e < 2 ? qs0 : qs1);
-                    if (a.softcap > 0.0f) {
-                        // tanh y = 1 - 2 / (e^2y + 1): absolute error of a few
-                        // 2^-24, so the capped score is off by that times the cap
-                        const float z = fast_exp2(x / a.softcap * (2.0f * kLog2e));
-                        x = a.softcap * (1.0f - __fdividef(2.0f, z + 1.0f));
-                    }
-                    if (a.slopes)
-                        x -= (e < 2 ? slope0 : slope1) * (float)((int64_t)pos - (int64_t)(p0 + j));
-                    s[n][e] = (there >> j) & 1u ? x * kLog2e : -INFINITY;
-                }
-            float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+            for (int i = 0; i < 2 * N; ++i) {
+                top0 = fmaxf(top0, fmaxf(s[i][0], s[i][1]));
+                top1 = fmaxf(top1, fmaxf(s[i][2], s[i][3]));
+            }
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
                 top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+            }
+            if constexpr (!MODS) {
+                top0 *= qs0;
+                top1 *= qs1;
             }
             const bool grows = top0 > m0 || top1 > m1;
             if (__any_sync(0xffffffffu, grows)) {
@@ -414,136 +619,208 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, FP8>::kCtasPerSm))
             }
             // a row that has seen no position keeps m = -inf: subtract 0
             const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
-            float p[2][4];
+            uint32_t pf[N][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int i = 0; i < N; ++i) {
+                float p[2][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[n][e] = fast_exp2(s[n][e] - (e < 2 ? b0 : b1));
-                    if (e < 2) l0 += p[n][e];
-                    else l1 += p[n][e];
-                }
-            uint32_t pf[4];
-            pf[0] = pack2<FP8>(p[0][0], p[0][1]);
-            pf[1] = pack2<FP8>(p[0][2], p[0][3]);
-            pf[2] = pack2<FP8>(p[1][0], p[1][1]);
-            pf[3] = pack2<FP8>(p[1][2], p[1][3]);
-
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = s[2 * i + n][e], b = e < 2 ? b0 : b1;
+                        p[n][e] = fast_exp2(MODS ? x - b : fmaf(x, e < 2 ? qs0 : qs1, -b));
+                        if (e < 2) l0 += p[n][e];
+                        else l1 += p[n][e];
+                    }
+                pf[i][0] = pack2<FP8>(p[0][0], p[0][1]);
+                pf[i][1] = pack2<FP8>(p[0][2], p[0][3]);
+                pf[i][2] = pack2<FP8>(p[1][0], p[1][1]);
+                pf[i][3] = pack2<FP8>(p[1][2], p[1][3]);
+            }
             // ---- O += P V
+            auto times_v = [&](uint32_t src, const uint32_t(&p)[4], auto masked, uint32_t low,
+                               uint32_t high, bool row0, bool row1) {
+                constexpr bool kMasked = decltype(masked)::value;
+                auto add = [&](float(&c)[4], uint32_t x, uint32_t y) {
+                    if constexpr (!kMasked) {
+                        mma16816<FP8>(c, p, x, y);
+                    } else {
+                        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816<FP8>(t, p, x, y);
+                        if (row0) {
+                            c[0] += t[0];
+                            c[1] += t[1];
+                        }
+                        if (row1) {
+                            c[2] += t[2];
+                            c[3] += t[3];
+                        }
+                    }
+                };
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-                uint32_t vf[4];
-                ldsm4_trans(vf, v_src + chunk_at<CH>((mat & 1) * 8 + mrow, c + (mat >> 1)));
-                if constexpr (!FP8) {  // a chunk is 8 columns
-                    mma16816<false>(acc[c], pf, vf[0], vf[1]);
-                    mma16816<false>(acc[c + 1], pf, vf[2], vf[3]);
-                } else {
-                    // a chunk is 16 columns; a word holds two columns of two
-                    // positions: even columns to one operand, odd to the next
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t vf[4];
+                    ldsm4_trans(vf, src + chunk_at<DP, FP8>(warp * kSlice + (mat & 1) * 8 + mrow,
+                                                            c + (mat >> 1)));
+                    if constexpr (kMasked) {
+                        vf[0] &= low;
+                        vf[1] &= high;
+                        vf[2] &= low;
+                        vf[3] &= high;
+                    }
+                    if constexpr (!FP8) {  // a chunk is 8 columns
+                        add(acc[c], vf[0], vf[1]);
+                        add(acc[c + 1], vf[2], vf[3]);
+                    } else {
+                        // a chunk is 16 columns; a word holds two columns of two
+                        // positions: even columns to one operand, odd to the next
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x0 = codes_to_f16x2(vf[2 * h]),
-                                       x1 = codes_to_f16x2(vf[2 * h] >> 16);
-                        const uint32_t y0 = codes_to_f16x2(vf[2 * h + 1]),
-                                       y1 = codes_to_f16x2(vf[2 * h + 1] >> 16);
-                        mma16816<true>(acc[2 * (c + h)], pf, __byte_perm(x0, x1, 0x5410),
-                                       __byte_perm(y0, y1, 0x5410));
-                        mma16816<true>(acc[2 * (c + h) + 1], pf, __byte_perm(x0, x1, 0x7632),
-                                       __byte_perm(y0, y1, 0x7632));
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t x0, x1, y0, y1;
+                            codes_to_f16(__byte_perm(vf[2 * hh], 0, 0x3120), x0, x1);
+                            codes_to_f16(__byte_perm(vf[2 * hh + 1], 0, 0x3120), y0, y1);
+                            add(acc[2 * (c + hh)], x0, y0);
+                            add(acc[2 * (c + hh) + 1], x1, y1);
+                        }
                     }
                 }
+            };
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!ready(h[2 * i + 1])) return false;
+                const uint32_t src = ring_addr + h[2 * i + 1].slot * Sh::kHalf;
+                if (there[i] == 0xffffu && !uneven[i]) {
+                    times_v(src, pf[i], std::false_type{}, 0u, 0u, true, true);
+                } else if (there[i]) {
+                    // A weight of 0 does not keep out a value that is not
+                    // finite (a row that is not there holds anything): one
+                    // token of the chunk at a time, with the values that it
+                    // does not see taken out.
+                    const int64_t p = p_first + (int64_t)(k + i) * kTile;
+#pragma unroll 1
+                    for (uint32_t ct = 0; ct < w.span.tokens; ++ct) {
+                        auto keep = [&](uint32_t j) {
+                            return ((there[i] >> j) & 1u) && sees(pos0 + ct, p + j);
+                        };
+                        auto pair = [&](uint32_t j) {
+                            return (keep(j) ? 0xffffu : 0u) | (keep(j + 1) ? 0xffff0000u : 0u);
+                        };
+                        times_v(src, pf[i], std::true_type{}, pair(2 * in_quad),
+                                pair(2 * in_quad + 8), t0 == ct, t1 == ct);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[h[2 * i + 1].slot]);
             }
-            __syncwarp();  // the stage may be filled again
-        }
-        cp_wait<0>();
-        __syncwarp();
+            return true;
+        };
+        const uint32_t count = w.last - w.first;
+        uint32_t k = 0;
+        if constexpr (NP == 2)
+            for (; alive && k + 1 < count; k += 2)
+                alive = slices(k, std::integral_constant<int, 2>{});
+        for (; alive && k < count; ++k) alive = slices(k, std::integral_constant<int, 1>{});
+        if (!alive) break;
 
-        // ---- the four warps join, in their own rings' memory
+        // ---- the four warps join, a few rows at a time
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         if (in_quad == 0) {
-            s_m[warp][r0] = m0;
-            s_m[warp][r1] = m1;
-            s_l[warp][r0] = l0;
-            s_l[warp][r1] = l1;
+            sm.m[warp][r0] = m0;
+            sm.m[warp][r1] = m1;
+            sm.l[warp][r0] = l0;
+            sm.l[warp][r1] = l1;
         }
-        float* mine = reinterpret_cast<float*>(ring);
-        constexpr int pitch = Sh::kScratchPitch;
-#pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t d = 8 * (n + i) + 2 * in_quad;
-                    *reinterpret_cast<float2*>(mine + r0 * pitch + d) =
-                        make_float2(acc[n + i][0], acc[n + i][1]);
-                    *reinterpret_cast<float2*>(mine + r1 * pitch + d) =
-                        make_float2(acc[n + i][2], acc[n + i][3]);
-                }
-            } else {
-                const uint32_t d = 8 * n + 4 * in_quad;
-                *reinterpret_cast<float4*>(mine + r0 * pitch + d) =
-                    make_float4(acc[n][0], acc[n + 1][0], acc[n][1], acc[n + 1][1]);
-                *reinterpret_cast<float4*>(mine + r1 * pitch + d) =
-                    make_float4(acc[n][2], acc[n + 1][2], acc[n][3], acc[n + 1][3]);
-            }
+        if constexpr (!Sh::kQInRegs) {  // Q's memory is free
+            alive = meet();
+            if (!alive) break;
         }
-        __syncthreads();
-        const bool whole = first == 0 && w.u + (last - first) == end;
-        float* part = slot_of<DP>(a.workspace, blockIdx.x, first == 0 ? 1 : 0);
+        const bool whole = w.whole();
+        float* part = slot_of<DP>(a.workspace, blockIdx.x, w.first == 0 ? 1 : 0);
         const uint32_t quads = a.D / 4;
-        for (uint32_t e = tid; e < rows * quads; e += kThreads) {
-            const uint32_t r = e / quads, d = (e - r * quads) * 4;
-            float top = s_m[0][r];
+        constexpr uint32_t JR = Sh::kJoinRows;
 #pragma unroll
-            for (int v = 1; v < kWarps; ++v) top = fmaxf(top, s_m[v][r]);
-            const float base = top == -INFINITY ? 0.0f : top;
-            float l = 0.0f;
-            float4 o = make_float4(0, 0, 0, 0);
+        for (uint32_t round = 0; round < kRows / JR; ++round) {
+            if (round * JR >= rows) break;
+            if ((quad / JR) == (round & (8 / JR - 1))) {
+                const bool high = round >= 8 / JR;
+                float* mine = s_join + (warp * JR + quad % JR) * DP;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                const float f = fast_exp2(s_m[v][r] - base);
-                const float4 x = *reinterpret_cast<const float4*>(
-                    smem + v * (Sh::kStages * Sh::kStage) + (r * pitch + d) * 4);
-                l += f * s_l[v][r];
-                o.x += f * x.x;
-                o.y += f * x.y;
-                o.z += f * x.z;
-                o.w += f * x.w;
-            }
-            if (whole) {
-                const uint64_t row = (uint64_t)w.t * a.Hq + head0 + r;
-                const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
-                uint2 y;
-                y.x = pack_bf16x2(o.x * inv, o.y * inv);
-                y.y = pack_bf16x2(o.z * inv, o.w * inv);
-                *reinterpret_cast<uint2*>(a.out + row * a.D + d) = y;
-                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
-            } else {
-                *reinterpret_cast<float4*>(part + r * DP + d) = o;
-                if (d == 0) {
-                    part[kRows * DP + r] = top;
-                    part[kRows * DP + kRows + r] = l;
+                for (int n = 0; n < NT; n += 2) {
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<float2*>(mine + 8 * (n + i) + 2 * in_quad) =
+                                high ? make_float2(acc[n + i][2], acc[n + i][3])
+                                     : make_float2(acc[n + i][0], acc[n + i][1]);
+                    } else {
+                        *reinterpret_cast<float4*>(mine + 8 * n + 4 * in_quad) =
+                            high ? make_float4(acc[n][2], acc[n + 1][2], acc[n][3], acc[n + 1][3])
+                                 : make_float4(acc[n][0], acc[n + 1][0], acc[n][1], acc[n + 1][1]);
+                    }
                 }
             }
+            alive = meet();
+            if (!alive) break;
+            const uint32_t here = rows - round * JR < JR ? rows - round * JR : JR;
+            for (uint32_t e = tid; e < here * quads; e += 32 * kWarps) {
+                const uint32_t rj = e / quads, d = (e - rj * quads) * 4, r = round * JR + rj;
+                float top = sm.m[0][r];
+#pragma unroll
+                for (int v = 1; v < kWarps; ++v) top = fmaxf(top, sm.m[v][r]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                float l = 0.0f;
+                float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) {
+                    const float f = fast_exp2(sm.m[v][r] - base);
+                    const float4 x =
+                        *reinterpret_cast<const float4*>(s_join + (v * JR + rj) * DP + d);
+                    l += f * sm.l[v][r];
+                    o.x += f * x.x;
+                    o.y += f * x.y;
+                    o.z += f * x.z;
+                    o.w += f * x.w;
+                }
+                if (whole) {
+                    const uint32_t ct = r / in_block;
+                    const uint64_t row = (uint64_t)(w.t + ct) * a.Hq + head0 + (r - ct * in_block);
+                    const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+                    uint2 y;
+                    y.x = pack_bf16x2(o.x * inv, o.y * inv);
+                    y.y = pack_bf16x2(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(a.out + row * a.D + d) = y;
+                    if (d == 0 && a.lse)
+                        a.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4*>(part + r * DP + d) = o;
+                    if (d == 0) {
+                        part[kRows * DP + r] = top;
+                        part[kRows * DP + kRows + r] = l;
+                    }
+                }
+            }
+            alive = meet();
+            if (!alive) break;
         }
-        if (!whole && first == 0 && tid == 0) {
-            open->end = end;
-            open->pieces = piece.pieces;
+        if (!alive) break;
+        if (!whole && w.first == 0 && tid == 0) {
+            open->end = w.end();
+            open->pieces = sm.split.start.pieces;
             open->t = w.t;
-            open->block = block;
-            open->units = piece.units;
+            open->tokens = w.span.tokens;
+            open->block = w.block;
+            open->units = sm.split.start.units;
         }
-        __syncthreads();  // scratch is read: the rings are free
-        w.advance(a.split, last - first);
+        w.next(a.split);
     }
-    if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
+    if (!alive && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
 
-// Joins a (token, row block) that piece blockIdx.x began and others went on
+// Joins a (chunk, row block) that piece blockIdx.x began and others went on
 // with: weights 2^(m_i - M) per row, then one weighted sum over the pieces in
 // their order, the pieces dealt to groups of threads and the groups' sums
 // added up in order.
@@ -558,18 +835,10 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
     if (open.units == 0) return;
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    // pieces that start before the end: a binary search, the starts ascend
-    uint32_t lo = c0 + 1, hi = open.pieces;
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (piece_start(open.units, open.pieces, mid) < open.end)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    const uint32_t n = lo - c0;
+    const uint32_t n = sharers(open, c0);
     const uint32_t kvh = open.block / a.HB, hb = open.block - kvh * a.HB;
-    const uint32_t rows = a.G - hb * kRows < kRows ? a.G - hb * kRows : kRows;
+    const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+    const uint32_t rows = open.tokens * in_block;
     const uint32_t head0 = kvh * a.G + hb * kRows;
     auto part = [&](uint32_t i) { return slot_of<DP>(a.workspace, c0 + i, i == 0 ? 1 : 0); };
 
@@ -631,7 +900,8 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
             }
         }
         if (in && g == 0) {
-            const uint64_t row = (uint64_t)open.t * a.Hq + head0 + r;
+            const uint32_t ct = r / in_block;
+            const uint64_t row = (uint64_t)(open.t + ct) * a.Hq + head0 + (r - ct * in_block);
             const float l = s_sum[r], inv = l == 0.0f ? 0.0f : a.v_scale / l;
             uint2 y;
             y.x = pack_bf16x2(o.x * inv, o.y * inv);
@@ -642,16 +912,17 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     }
 }
 
-template <int DP, bool FP8>
-cudaError_t launch(GqaArgs& a, cudaStream_t stream) {
-    using Sh = Shape<DP, FP8>;
+template <int DP, bool FP8, bool MODS, bool WITHHOLD>
+cudaError_t launch_as(GqaArgs& a, const CUtensorMap& map, cudaStream_t stream) {
+    constexpr size_t smem = sizeof(Smem<DP, FP8>);
+    static_assert(smem <= 113 * 1024, "two CTAs per SM");
     uint64_t wave = 0;
-    cudaError_t e = wave_ctas<&gqa_decode_kernel<DP, FP8>>(kThreads, Sh::kSmem, wave);
+    cudaError_t e = wave_ctas<&gqa_decode_kernel<DP, FP8, MODS, WITHHOLD>>(kThreads, smem, wave);
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
     if (wave > kMaxPieces) wave = kMaxPieces;
     a.pieces = (uint32_t)wave;
-    gqa_decode_kernel<DP, FP8><<<a.pieces, kThreads, Sh::kSmem, stream>>>(a);
+    gqa_decode_kernel<DP, FP8, MODS, WITHHOLD><<<a.pieces, kThreads, smem, stream>>>(a, map);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.pieces);
@@ -665,14 +936,21 @@ cudaError_t launch(GqaArgs& a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, gqa_join_kernel<DP>, a);
 }
 
+template <int DP, bool FP8, bool WITHHOLD>
+int launch(GqaArgs& a, const kvw_paged_cache_t* cache, uint32_t layer_idx, cudaStream_t stream) {
+    CUtensorMap map;
+    const int st = encode_cache_map(&map, cache, layer_idx, 2);
+    if (st != KVW_OK) return st;
+    const cudaError_t e = a.softcap > 0.0f || a.slopes
+                              ? launch_as<DP, FP8, true, WITHHOLD>(a, map, stream)
+                              : launch_as<DP, FP8, false, WITHHOLD>(a, map, stream);
+    return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
+}
+
 uint32_t padded_head(uint32_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-}  // namespace
-}  // namespace kvw
-
-extern "C" int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads,
-                                        uint32_t head_size, uint64_t* bytes) {
-    using namespace kvw;
+int workspace_bytes_for(uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_size,
+                        uint64_t* bytes) {
     if (!bytes || !num_q_heads || !num_kv_heads || num_q_heads % num_kv_heads) return KVW_EINVAL;
     if (head_size == 0 || head_size % 16 || head_size > 256 || num_q_heads > 4096)
         return KVW_EUNSUPPORTED;
@@ -681,20 +959,17 @@ extern "C" int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_he
     return KVW_OK;
 }
 
-extern "C" int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_t q_row_stride,
-                                    const uint32_t* input_row_offsets, uint32_t num_batches,
-                                    uint32_t tot_seq_len, uint32_t num_q_heads,
-                                    const kvw_paged_cache_t* cache, float v_scale,
-                                    uint32_t layer_idx, float sm_scale, float softcap,
-                                    uint32_t window, const float* alibi_slopes, void* workspace,
-                                    uint64_t workspace_bytes, uint32_t* err_flags,
-                                    cudaStream_t stream) {
-    using namespace kvw;
+int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
+              const uint32_t* input_row_offsets, uint32_t num_batches, uint32_t tot_seq_len,
+              uint32_t num_q_heads, const kvw_paged_cache_t* cache, float v_scale,
+              uint32_t layer_idx, float sm_scale, float softcap, uint32_t window,
+              const float* alibi_slopes, void* workspace, uint64_t workspace_bytes,
+              uint32_t* err_flags, cudaStream_t stream, bool withhold, uint64_t wait_ns) {
     const int st = check_cache(cache, layer_idx, 2);
     if (st != KVW_OK) return st;
     const uint32_t D = cache->head_size, Hk = cache->num_heads;
     uint64_t need = 0;
-    const int ws = kva_gqa_decode_workspace(num_q_heads, Hk, D, &need);
+    const int ws = workspace_bytes_for(num_q_heads, Hk, D, &need);
     if (ws != KVW_OK) return ws;
     if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20)) return KVW_EUNSUPPORTED;
     if (!value_scale_ok(cache, v_scale)) return KVW_EINVAL;
@@ -704,6 +979,7 @@ extern "C" int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_
     if (!aligned16(out) || !aligned16(q) || !aligned16(workspace) || !aligned4(lse) ||
         !aligned4(input_row_offsets) || !aligned4(alibi_slopes) || !aligned4(err_flags))
         return KVW_EINVAL;
+    if (!tma_strides_ok(cache, 2)) return KVW_EINVAL;
     if (q_row_stride < (int64_t)num_q_heads * D || q_row_stride % 8) return KVW_EINVAL;
     if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return KVW_EINVAL;
     if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return KVW_EINVAL;
@@ -717,41 +993,88 @@ extern "C" int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_
     a.G = num_q_heads / Hk;
     a.HB = (a.G + kRows - 1) / kRows;
     a.split.blocks = Hk * a.HB;
+    a.per_token = a.HB == 1 ? a.G : kRows;
+    // tokens of a chunk: as many as fit the 16 rows (a power of two)
+    while (a.HB == 1 && (2u << a.split.log_c) * a.G <= kRows) ++a.split.log_c;
     a.split.min_units = 1;
-    a.split.cap = (uint64_t)cache->max_pages_per_seq * cache->page_size;
-    if (a.split.cap > (1ull << 32)) a.split.cap = 1ull << 32;
-    a.split.window = window ? window : 1ull << 40;
+    const uint64_t reach = (uint64_t)cache->max_pages_per_seq * cache->page_size;
+    a.split.cap = reach > kMaxReach ? (int64_t)kMaxReach : (int64_t)reach;
+    a.split.window = window ? (int64_t)window : 1ll << 40;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_row_stride;
-    const int64_t esz = cache_esz(cache);
-    const bool fp8 = esz == 1;
-    a.k_base = static_cast<const unsigned char*>(cache->data) +
-               (int64_t)layer_idx * cache->stride_layer * esz;
-    a.kv_bytes = cache->stride_kv * esz;
-    a.s_page = cache->stride_page;
-    a.s_token = cache->stride_token;
-    a.s_head = cache->stride_head;
+    const bool fp8 = cache->dtype == KVW_DTYPE_FP8_E4M3;
     a.page_table = cache->page_table;
     a.slopes = alibi_slopes;
     a.err_flags = err_flags;
     a.workspace = static_cast<unsigned char*>(workspace);
     a.sm_scale = sm_scale;
     a.softcap = softcap;
+    a.cap_factor = softcap > 0.0f ? 2.0f * kLog2e / softcap : 0.0f;
     a.k_scale = fp8 ? cache->scale : 1.0f;
     a.v_scale = fp8 ? v_scale : 1.0f;
     a.Hq = num_q_heads;
-    a.Hk = Hk;
     a.D = D;
     a.num_pages = cache->num_pages;
     a.max_pages = cache->max_pages_per_seq;
     a.ps = make_fast_div(cache->page_size);
-    cudaError_t e;
+    a.copy_rows = rows_per_copy(cache->page_size);
+    a.wait_ns = wait_ns;
+    auto run = [&](auto dp, auto f8) {
+#ifdef KVW_TEST_HOOKS
+        if (withhold)
+            return launch<decltype(dp)::value, decltype(f8)::value, true>(a, cache, layer_idx,
+                                                                          stream);
+#else
+        if (withhold) return (int)KVW_EUNSUPPORTED;
+#endif
+        return launch<decltype(dp)::value, decltype(f8)::value, false>(a, cache, layer_idx, stream);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    using D256 = std::integral_constant<int, 256>;
     switch (padded_head(D)) {
-        case 64: e = fp8 ? launch<64, true>(a, stream) : launch<64, false>(a, stream); break;
-        case 128: e = fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream); break;
-        default: e = fp8 ? launch<256, true>(a, stream) : launch<256, false>(a, stream); break;
+        case 64: return fp8 ? run(D64{}, std::true_type{}) : run(D64{}, std::false_type{});
+        case 128: return fp8 ? run(D128{}, std::true_type{}) : run(D128{}, std::false_type{});
+        default: return fp8 ? run(D256{}, std::true_type{}) : run(D256{}, std::false_type{});
     }
-    return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
+
+}  // namespace
+}  // namespace kvw
+
+extern "C" int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads,
+                                        uint32_t head_size, uint64_t* bytes) {
+    return kvw::workspace_bytes_for(num_q_heads, num_kv_heads, head_size, bytes);
+}
+
+extern "C" int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_t q_row_stride,
+                                    const uint32_t* input_row_offsets, uint32_t num_batches,
+                                    uint32_t tot_seq_len, uint32_t num_q_heads,
+                                    const kvw_paged_cache_t* cache, float v_scale,
+                                    uint32_t layer_idx, float sm_scale, float softcap,
+                                    uint32_t window, const float* alibi_slopes, void* workspace,
+                                    uint64_t workspace_bytes, uint32_t* err_flags,
+                                    cudaStream_t stream) {
+    return kvw::gqa_entry(out, lse, q, q_row_stride, input_row_offsets, num_batches, tot_seq_len,
+                          num_q_heads, cache, v_scale, layer_idx, sm_scale, softcap, window,
+                          alibi_slopes, workspace, workspace_bytes, err_flags, stream, false,
+                          kvw::kWaitLimitNs);
+}
+
+#ifdef KVW_TEST_HOOKS
+// Test builds only (a separate library; the product has no such symbol): the
+// first half tile of every CTA is announced on its barrier but never copied,
+// and every wait is bounded by `wait_ns`, so the consumers' wait runs out,
+// KVW_ERR_TIMEOUT is set and the kernel returns.
+extern "C" int kva_test_gqa_decode_withheld(
+    void* out, const void* q, int64_t q_row_stride, const uint32_t* input_row_offsets,
+    uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_q_heads,
+    const kvw_paged_cache_t* cache, uint32_t layer_idx, void* workspace, uint64_t workspace_bytes,
+    uint32_t* err_flags, cudaStream_t stream, uint64_t wait_ns) {
+    return kvw::gqa_entry(out, nullptr, q, q_row_stride, input_row_offsets, num_batches,
+                          tot_seq_len, num_q_heads, cache, 1.0f, layer_idx, 0.1f, 0.0f, 0, nullptr,
+                          workspace, workspace_bytes, err_flags, stream, true, wait_ns);
+}
+#endif

@@ -1,23 +1,23 @@
 // How the attention calls of kva.h divide their work, and how the pieces
 // meet again.
 //
-// Work is counted in units: one unit is one tile of kTile cache positions for
-// one row block (a group of query heads that read the same rows) of one
-// token.  The units of all tokens in order - token, row block, tile - form
-// one long axis, cut into G pieces of equal length, one for each CTA (or CTA
-// pair).  So every CTA reads the same amount of cache whatever the lengths, a
-// CTA crosses from one token to the next where its piece does, and at most
-// two of its segments are parts of a (token, row block) that other CTAs
-// share: its first (slot 0) and its last (slot 1).  Those write their
+// A chunk is up to C consecutive new tokens of one request (C a power of two;
+// their query rows share a row block, so a cache row is read once for all of
+// them).  Work is counted in units: one unit is one tile of kTile cache
+// positions for one row block of one chunk.  The units of all chunks in
+// order - chunk, row block, tile - form one long axis, cut into equal pieces,
+// one for each CTA.  So every CTA reads the same amount of cache whatever the
+// lengths, a CTA crosses from one chunk to the next where its piece does, and
+// at most two of its segments are parts of a (chunk, row block) that other
+// CTAs share: its first (slot 0) and its last (slot 1).  Those write their
 // unnormalised sums with their running maximum and sum to a workspace whose
-// size depends on G alone, and a second kernel joins them in order, so the
-// result depends on nothing but the lengths and G.
+// size depends on the number of pieces alone, and a second kernel joins them
+// in order: the result depends on the lengths and the device only.
 //
-// The number of tiles of one token's context is needed as a prefix sum over
-// tokens.  A request's tokens have consecutive lengths, so its total is a
-// difference of two closed forms (tiles_upto), one evaluation for each
-// request; a CTA finds its start by one block-wide scan over requests and a
-// search within one request.
+// Finding a piece needs the number of tiles before a chunk, a prefix sum over
+// chunks.  Within a request the chunks' lengths rise by C, so a request's
+// prefix has a closed form (tiles_before); a CTA finds its start by one
+// block-wide scan over requests and a binary search within one.
 #pragma once
 
 #include "kva_common.cuh"
@@ -25,52 +25,83 @@
 namespace kvw {
 
 constexpr uint32_t kTile = 64;        // cache positions of one unit
-constexpr uint32_t kMaxPieces = 512;  // G, and so the workspace, is bounded by this
+constexpr uint32_t kMaxPieces = 512;  // bounds the workspace
+constexpr uint64_t kMaxReach = 0xffffff00ull;  // positions, all 32-bit, tiles included
 
 struct SplitArgs {
     const uint32_t* offsets;
     const uint32_t* cache_lengths;
     uint32_t B, T;
-    uint32_t blocks;  // row blocks per token
+    uint32_t blocks;     // row blocks per chunk
+    uint32_t log_c;      // log2 of the tokens per chunk, <= 6
     uint32_t min_units;  // a piece is at least this long (fewer pieces for little work)
-    uint64_t cap;     // positions the page tables can hold
-    uint64_t window;  // positions seen, own included (a huge number for no window)
+    int64_t cap;         // positions the page tables can hold
+    int64_t window;      // positions seen, own included (a huge number for no window)
 };
 
-// Positions a token at length `len` (its own position + 1) reads: [start, hi),
-// tiles [start / kTile, ceil(hi / kTile)).  Positions past the page table's
-// reach are left out; at least one tile is kept so that every token has an
-// owner for its output row.
-struct TokenSpan {
-    uint64_t start, hi;
-    uint32_t tile0, tiles;
+// What a chunk reads: positions [start, hi), tiles tile0 .. tile0 + tiles - 1
+// (its last token's length bounds hi, its first token's window start).
+// Positions past the page tables' reach are left out; at least one tile is
+// kept so that every token has an owner for its output row.
+struct ChunkSpan {
+    int64_t start, hi;
+    uint32_t tile0, tiles, tokens;
 };
 
-__device__ __forceinline__ TokenSpan token_span(const SplitArgs& a, uint64_t len) {
-    TokenSpan s;
-    s.start = len > a.window ? len - a.window : 0;
-    s.hi = len < a.cap ? len : a.cap;
-    const uint64_t first = s.start < s.hi ? s.start : s.hi - 1;
-    s.tile0 = (uint32_t)(first / kTile);
+// Chunk k of a request with n new tokens after len cached ones.
+__host__ __device__ __forceinline__ ChunkSpan chunk_span(const SplitArgs& a, int64_t len,
+                                                         uint32_t n, uint32_t k) {
+    ChunkSpan s;
+    const uint32_t first = k << a.log_c, left = n - first, c = 1u << a.log_c;
+    s.tokens = left < c ? left : c;
+    const int64_t begin = len + first + 1 - a.window, end = len + first + s.tokens;
+    s.start = begin > 0 ? begin : 0;
+    s.hi = end < a.cap ? end : a.cap;
+    const int64_t at = s.start < s.hi ? s.start : s.hi - 1;
+    s.tile0 = (uint32_t)(at / kTile);
     s.tiles = (uint32_t)((s.hi + kTile - 1) / kTile) - s.tile0;
     return s;
 }
 
-// Sum of token_span(l).tiles over lengths l = 1 .. x.
-__device__ __forceinline__ uint64_t tiles_upto(const SplitArgs& a, uint64_t x) {
-    // sum of ceil(min(l, cap) / kTile)
-    const uint64_t u = x < a.cap ? x : a.cap;
-    const uint64_t uq = u / kTile, ur = u % kTile;
-    uint64_t n = kTile * (uq * (uq + 1) / 2) + ur * (uq + 1);
-    n += (x - u) * ((a.cap + kTile - 1) / kTile);
-    // minus the sum of floor(min(l - window, cap - 1) / kTile) over l > window
-    if (x > a.window) {
-        const uint64_t y = x - a.window, v = y < a.cap - 1 ? y : a.cap - 1;
-        const uint64_t vq = v / kTile, vr = v % kTile;
-        n -= (vq ? kTile * (vq * (vq - 1) / 2) : 0) + vq * (vr + 1);
-        n -= (y - v) * ((a.cap - 1) / kTile);
-    }
-    return n;
+// Sum of min(ceil(l / m), top) over l = 1 .. x, m = 1 << log_m.
+__host__ __device__ __forceinline__ int64_t sum_ceil(int64_t x, uint32_t log_m, int64_t top) {
+    const int64_t flat = top << log_m, u = x < flat ? x : flat;
+    const int64_t q = u >> log_m, r = u - (q << log_m);
+    return ((q * (q + 1) / 2) << log_m) + r * (q + 1) + (x - u) * top;
+}
+
+// Sum of min(floor(l / m), top) over l = 0 .. x - 1 (nothing for x <= 0).
+__host__ __device__ __forceinline__ int64_t sum_floor(int64_t x, uint32_t log_m, int64_t top) {
+    if (x <= 0) return 0;
+    const int64_t flat = top << log_m, u = x < flat ? x : flat;
+    const int64_t q = u >> log_m, r = u - (q << log_m);
+    return (q * (q - 1) / 2) * (1ll << log_m) + r * q + (x - u) * top;
+}
+
+// Tiles of the first k chunks of a request, all of them full ones: with c =
+// 1 << log_c and m = kTile / c, chunk j ends in tile ceil((e + j + 1) / m),
+// e = ceil(len / c), and starts in tile floor((f + j) / m), f = floor((len +
+// 1 - window) / c), both cut at the page tables' reach.
+__host__ __device__ __forceinline__ int64_t tiles_before(const SplitArgs& a, int64_t len,
+                                                         uint32_t k) {
+    const uint32_t log_m = 6 - a.log_c;
+    const int64_t e = (len + (1ll << a.log_c) - 1) >> a.log_c;
+    const int64_t f = (len + 1 - a.window) >> a.log_c;  // floor, also of a negative number
+    const int64_t last = (a.cap + kTile - 1) / kTile, from = (a.cap - 1) / kTile;
+    return sum_ceil(e + k, log_m, last) - sum_ceil(e, log_m, last) -
+           sum_floor(f + k, log_m, from) + sum_floor(f, log_m, from);
+}
+
+__host__ __device__ __forceinline__ uint32_t chunks_of(const SplitArgs& a, uint32_t n) {
+    return (n >> a.log_c) + ((n & ((1u << a.log_c) - 1u)) ? 1u : 0u);
+}
+
+// All tiles of a request.
+__host__ __device__ __forceinline__ int64_t request_tiles(const SplitArgs& a, int64_t len,
+                                                          uint32_t n) {
+    if (n == 0) return 0;
+    const uint32_t k = chunks_of(a, n) - 1;
+    return tiles_before(a, len, k) + chunk_span(a, len, n, k).tiles;
 }
 
 // First unit of piece c of `pieces` over `units` units (even to one unit).
@@ -80,9 +111,10 @@ __host__ __device__ __forceinline__ uint64_t piece_start(uint64_t units, uint32_
     return q * c + (c < r ? c : r);
 }
 
-// Pieces in use: never more than `most`, and none shorter than min_units
-// unless there is only one.
-__device__ __forceinline__ uint32_t pieces_of(const SplitArgs& a, uint64_t units, uint32_t most) {
+// Pieces in use: at most `most`, none shorter than min_units unless there is
+// only one.
+__host__ __device__ __forceinline__ uint32_t pieces_of(const SplitArgs& a, uint64_t units,
+                                                       uint32_t most) {
     const uint64_t p = units / a.min_units;
     return p == 0 ? 1u : p < most ? (uint32_t)p : most;
 }
@@ -91,79 +123,81 @@ __device__ __forceinline__ uint32_t pieces_of(const SplitArgs& a, uint64_t units
 struct PieceStart {
     uint64_t units;       // of the whole call
     uint64_t u0, u1;      // the piece
-    uint64_t token_base;  // first unit of the token u0 lies in
+    uint64_t chunk_base;  // first unit of the chunk u0 lies in
     uint32_t pieces;
-    uint32_t b, i;        // that token: request and index in it
+    uint32_t b, k;        // that chunk: request and index in it
 };
 
-// All threads of the CTA call this.  Returns false (uniformly) for malformed
-// offsets.  `shared` needs THREADS / 32 + 1 uint64 and one PieceStart.
 template <int THREADS>
 struct SplitShared {
-    uint64_t warp_sum[THREADS / 32];
+    int64_t warp_sum[THREADS / 32];
     PieceStart start;
 };
 
+// All threads of the CTA call this, with the same arguments.  Returns false
+// (uniformly) for malformed offsets; else the piece is in sh.start.
 template <int THREADS>
 __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, uint32_t c,
-                                           SplitShared<THREADS>& sh, PieceStart& out) {
+                                           SplitShared<THREADS>& sh) {
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t per = (a.B + THREADS - 1) / THREADS;
     const uint32_t lo = tid * per < a.B ? tid * per : a.B;
     const uint32_t hi = lo + per < a.B ? lo + per : a.B;
-    uint64_t mine = 0;
+    int64_t mine = 0;
     int ok = 1;
     for (uint32_t r = lo; r < hi; ++r) {
         const uint32_t o0 = __ldg(a.offsets + r), o1 = __ldg(a.offsets + r + 1);
-        const uint64_t len = __ldg(a.cache_lengths + r);
+        const uint32_t len = __ldg(a.cache_lengths + r);
         if (o1 < o0 || o1 > a.T || (r == 0 && o0 != 0) || (r == a.B - 1 && o1 != a.T))
             ok = 0;
         else
-            mine += tiles_upto(a, len + (o1 - o0)) - tiles_upto(a, len);
+            mine += request_tiles(a, len, o1 - o0);
     }
-    uint64_t scan = mine;
+    int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+        const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= (uint32_t)o) scan += v;
     }
     if (lane == 31) sh.warp_sum[warp] = scan;
     if (!__syncthreads_and(ok)) return false;
-    uint64_t before = scan - mine, total = 0;
+    int64_t before = scan - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if ((uint32_t)w < warp) before += sh.warp_sum[w];
         total += sh.warp_sum[w];
     }
     PieceStart s;
-    s.units = total * a.blocks;
+    s.units = (uint64_t)total * a.blocks;
     s.pieces = pieces_of(a, s.units, most);
     const bool used = c < s.pieces;
     s.u0 = used ? piece_start(s.units, s.pieces, c) : s.units;
     s.u1 = used ? piece_start(s.units, s.pieces, c + 1) : s.units;
-    s.token_base = 0;
-    s.b = s.i = 0;
+    s.chunk_base = 0;
+    s.b = s.k = 0;
+    if (!used && tid == 0) sh.start = s;
     // the one thread whose requests hold u0 walks them
-    if (s.u0 < s.u1 && s.u0 >= before * a.blocks && s.u0 < (before + mine) * a.blocks) {
-        uint64_t base = before;
+    if (used && s.u0 >= (uint64_t)before * a.blocks &&
+        s.u0 < (uint64_t)(before + mine) * a.blocks) {
+        const uint64_t at = s.u0 / a.blocks;  // u0 in tiles: the chunk holds this tile
+        int64_t base = before;
         for (uint32_t r = lo; r < hi; ++r) {
-            const uint64_t len = __ldg(a.cache_lengths + r);
+            const uint32_t len = __ldg(a.cache_lengths + r);
             const uint32_t n = __ldg(a.offsets + r + 1) - __ldg(a.offsets + r);
-            const uint64_t at = tiles_upto(a, len);
-            const uint64_t tiles = tiles_upto(a, len + n) - at;
-            if (s.u0 < (base + tiles) * a.blocks) {
-                // largest i whose tokens before it end at or before u0
-                uint32_t i0 = 0, i1 = n;
-                while (i1 - i0 > 1u) {
-                    const uint32_t mid = i0 + (i1 - i0) / 2;
-                    if ((base + tiles_upto(a, len + mid) - at) * a.blocks <= s.u0)
-                        i0 = mid;
+            const int64_t tiles = request_tiles(a, len, n);
+            if (at < (uint64_t)(base + tiles)) {
+                // the last chunk that begins at or before it
+                uint32_t k0 = 0, k1 = chunks_of(a, n);
+                while (k1 - k0 > 1u) {
+                    const uint32_t mid = k0 + (k1 - k0) / 2;
+                    if ((uint64_t)(base + tiles_before(a, len, mid)) <= at)
+                        k0 = mid;
                     else
-                        i1 = mid;
+                        k1 = mid;
                 }
                 s.b = r;
-                s.i = i0;
-                s.token_base = (base + tiles_upto(a, len + i0) - at) * a.blocks;
+                s.k = k0;
+                s.chunk_base = (uint64_t)(base + tiles_before(a, len, k0)) * a.blocks;
                 break;
             }
             base += tiles;
@@ -171,70 +205,91 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
         sh.start = s;
     }
     __syncthreads();
-    if (s.u0 < s.u1) s = sh.start;
-    out = s;
     return true;
 }
 
-// A CTA's place on the axis of units; every thread keeps one, they agree.
+// A place on the axis of units and the segment that begins there: the rest of
+// a (chunk, row block), as far as the piece goes.
 struct Walk {
-    uint64_t u, u1, token_base;
-    uint32_t b, i, t, n;  // request, index in it, token, tokens of the request
-    uint64_t len0;        // cache_lengths[b]
-    TokenSpan span;
+    uint64_t u, u1, chunk_base;
+    uint32_t b, k, t, n;  // request, chunk in it, the chunk's first token, tokens of the request
+    uint32_t len0;        // cache_lengths[b]
+    ChunkSpan span;
+    uint32_t block, first, last;  // the segment: row block, tiles first .. last - 1 of the span
 
     __device__ __forceinline__ void load_request(const SplitArgs& a) {
         const uint32_t o = __ldg(a.offsets + b);
         n = __ldg(a.offsets + b + 1) - o;
-        t = o + i;
+        t = o + (k << a.log_c);
         len0 = __ldg(a.cache_lengths + b);
+    }
+    __device__ __forceinline__ void find_segment() {
+        const uint64_t in = u - chunk_base;
+        block = (uint32_t)(in / span.tiles);
+        first = (uint32_t)(in - (uint64_t)block * span.tiles);
+        const uint64_t left = u1 - u;
+        last = span.tiles - first < left ? span.tiles : first + (uint32_t)left;
     }
     __device__ __forceinline__ void begin(const SplitArgs& a, const PieceStart& s) {
         u = s.u0;
         u1 = s.u1;
-        token_base = s.token_base;
+        chunk_base = s.chunk_base;
         b = s.b;
-        i = s.i;
+        k = s.k;
+        block = first = last = 0;
         if (u < u1) {
             load_request(a);
-            span = token_span(a, len0 + i + 1);
+            span = chunk_span(a, len0, n, k);
+            find_segment();
         }
     }
-    // The segment at u: row block, first and last + 1 tile (counted from the
-    // token's tile0), and the unit where the (token, row block) ends.
-    __device__ __forceinline__ void segment(uint32_t& block, uint32_t& first, uint32_t& last,
-                                            uint64_t& end) const {
-        const uint64_t in = u - token_base;
-        block = (uint32_t)(in / span.tiles);
-        first = (uint32_t)(in - (uint64_t)block * span.tiles);
-        end = token_base + (uint64_t)(block + 1) * span.tiles;
-        const uint64_t stop = end < u1 ? end : u1;
-        last = first + (uint32_t)(stop - u);
+    __device__ __forceinline__ bool done() const { return u >= u1; }
+    // The unit where the segment's (chunk, row block) ends.
+    __device__ __forceinline__ uint64_t end() const {
+        return chunk_base + (uint64_t)(block + 1) * span.tiles;
     }
-    __device__ __forceinline__ void advance(const SplitArgs& a, uint32_t count) {
-        u += count;
-        if (u >= u1 || u < token_base + (uint64_t)a.blocks * span.tiles) return;
-        token_base += (uint64_t)a.blocks * span.tiles;
-        if (++i < n) {
-            ++t;
-        } else {
-            i = 0;
-            do {
-                ++b;
-                load_request(a);
-            } while (n == 0);  // u < u1: a later request has tokens
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == span.tiles; }
+    // On to the next segment.
+    __device__ __forceinline__ void next(const SplitArgs& a) {
+        u += last - first;
+        if (u >= u1) return;
+        if (u >= chunk_base + (uint64_t)a.blocks * span.tiles) {
+            chunk_base += (uint64_t)a.blocks * span.tiles;
+            if (++k < chunks_of(a, n)) {
+                t += 1u << a.log_c;
+            } else {
+                k = 0;
+                do {
+                    ++b;
+                    load_request(a);
+                } while (n == 0);  // u < u1: a later request has tokens
+            }
+            span = chunk_span(a, len0, n, k);
         }
-        span = token_span(a, len0 + i + 1);
+        find_segment();
     }
 };
 
-// What piece c left open: a (token, row block) that it began (slot 1) and
-// that pieces c + 1 .. go on with (their slot 0).  `units` 0: nothing.
+// What a piece left open: a (chunk, row block) that it began (slot 1) and that
+// the pieces after it go on with (their slot 0), up to unit `end`.  `units` 0:
+// nothing.
 struct OpenPiece {
     uint64_t units, end;
-    uint32_t pieces, t, block, pad;
+    uint32_t pieces, t, tokens, block;
 };
-
 static_assert(sizeof(OpenPiece) == 32, "workspace layout");
+
+// Pieces c0 .. c0 + n - 1 share what piece c0 left open; returns n.
+__device__ __forceinline__ uint32_t sharers(const OpenPiece& open, uint32_t c0) {
+    uint32_t lo = c0 + 1, hi = open.pieces;  // the starts ascend
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (piece_start(open.units, open.pieces, mid) < open.end)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return lo - c0;
+}
 
 }  // namespace kvw

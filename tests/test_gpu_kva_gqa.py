@@ -221,3 +221,25 @@ def test_equal_calls_give_equal_bits(kva):
     for _ in range(3):
         again, _ = run(kva, c, 8, q=q)
         assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("window", [0, 3])
+def test_a_later_tokens_row_does_not_reach_an_earlier_one(kva, dtype, window):
+    """Tokens of a request share a pass over the cache: the row of the last one
+    is NaN, and with a window so is the first position that only the first
+    token sees."""
+    c = R.Paged(47, [4, 1], [61, 5], kv_heads=1, head=64, dtype=dtype, page=8).fill()
+    nan = float("nan") if dtype == R.BF16 else 0x7F
+    at = [64] + ([61 + 1 - window] if window else [])
+    for p in at:
+        c.data[int(c.table[0, p // 8]), 1, c.layer, p % 8, 0] = nan
+    desc, store, keep = c.on()
+    q = c.normal(5, 4, 64).cuda()
+    out = torch.zeros_like(q)
+    space = torch.empty(kva.kva_gqa_decode_workspace(4, 1, 64), dtype=torch.uint8, device="cuda")
+    kva.kva_gqa_decode_paged(out, q, keep[3], desc, c.layer, 0.1, space, window=window,
+                             v_scale=c.v_scale)
+    bad = torch.isnan(out).all(-1).all(-1).tolist()
+    some = torch.isnan(out).any(-1).any(-1).tolist()
+    assert bad == some == [bool(window), False, False, True, False]
