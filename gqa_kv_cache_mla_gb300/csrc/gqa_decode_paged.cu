@@ -41,6 +41,7 @@ static_assert(kConsumerRegs + kFeederRegs <= 2 * 128, "registers of the launch")
 constexpr int kSlice = kTile / kWarps;      // positions of a tile that a warp takes
 constexpr int kRows = 16;                   // rows of a row block
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 6.0f;              // log2 of the largest weight before a rescale
 static_assert(kSlice == 16, "one m16n8k16 operand");
 
 struct GqaArgs {
@@ -56,7 +57,7 @@ struct GqaArgs {
     float sm_scale, softcap, cap_factor, k_scale, v_scale;
     uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
     uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
-    uint32_t num_pages, max_pages, pieces, copy_rows;
+    uint32_t num_pages, max_pages, pieces;
     FastDiv ps;
     uint64_t wait_ns;
 };
@@ -156,8 +157,9 @@ struct Shape {
     static constexpr int kRing = kHalves * kHalf;
     // queries stay in registers while the accumulators leave room
     static constexpr bool kQInRegs = DP <= 128;
-    static constexpr int kQBufs = kQInRegs ? 2 : 1;
-    static constexpr int kQRaw = kRows * DP * 2;
+    static constexpr int kQBufs = DP <= 64 ? 2 : 1;
+    // eight rows on distinct banks (256-wide heads have no memory left for it)
+    static constexpr int kQPitch = DP * 2 + (DP <= 128 ? 16 : 0);
     // rows that join at a time; their memory holds Q's operands in between
     // where these are not in registers
     static constexpr int kJoinRows = 1024 / (kWarps * DP / 2);
@@ -170,7 +172,7 @@ template <int DP, bool FP8>
 struct Smem {
     using Sh = Shape<DP, FP8>;
     unsigned char ring[Sh::kRing];
-    unsigned char q_raw[Sh::kQBufs][Sh::kQRaw];
+    unsigned char q_raw[Sh::kQBufs][kRows * Sh::kQPitch];
     unsigned char join[Sh::kJoin];
     uint64_t full[Sh::kHalves], empty[Sh::kHalves], q_full[2], q_empty[2], meet;
     uint64_t there[Sh::kHalves];  // of a K half: positions of the tile that are there
@@ -217,7 +219,7 @@ struct RingPos {
 
 // The feeding warp: walks the piece's tiles ahead of the arithmetic.
 template <int DP, bool FP8, bool WITHHOLD>
-__device__ __forceinline__ void feed(const GqaArgs& a, const CUtensorMap* map,
+__device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
                                      Smem<DP, FP8>& sm) {
     using Sh = Shape<DP, FP8>;
     const uint32_t lane = threadIdx.x & 31u;
@@ -227,59 +229,39 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CUtensorMap* map,
     RingPos<Sh::kQBufs> q_at;
     uint32_t bad_page = 0, issued = 0;
     bool ok = true, first_half = true;
-    const uint32_t R = a.copy_rows, copies = kTile / R;
     while (ok && !w.done()) {
         const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
-        // ---- the queries: one copy per token
+        // ---- the queries: one copy per row
         ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_ns);
         if (!ok) break;
-        if (lane == 0)
-            mbar_arrive_expect_tx(&sm.q_full[q_at.slot], w.span.tokens * in_block * a.D * 2);
+        const uint32_t rows = w.span.tokens * in_block;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * a.D * 2);
         __syncwarp();
-        if (lane < w.span.tokens)
-            bulk_load(sm.q_raw[q_at.slot] + lane * in_block * a.D * 2,
-                      a.q + (int64_t)(w.t + lane) * a.q_stride +
-                          (int64_t)(kvh * a.G + hb * kRows) * a.D,
-                      in_block * a.D * 2, &sm.q_full[q_at.slot]);
+        if (lane < rows) {
+            const uint32_t ct = lane / in_block;
+            bulk_load(sm.q_raw[q_at.slot] + lane * Sh::kQPitch,
+                      a.q + (int64_t)(w.t + ct) * a.q_stride +
+                          (int64_t)(kvh * a.G + hb * kRows + (lane - ct * in_block)) * a.D,
+                      a.D * 2, &sm.q_full[q_at.slot]);
+        }
         q_at.step();
         // ---- the tiles
         for (uint32_t i = w.first; ok && i < w.last; ++i) {
             const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
-            // lane l looks up copies l and l + 32
-            uint32_t page[2], row[2];
+            // lane l looks up units l and (of more than 32) l + 32
+            UnitCopy copy[2];
             uint64_t there = 0;
             uint32_t n = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t c = lane + 32u * h;
-                const int64_t p = p_tile + (int64_t)c * R;
-                page[h] = KVW_PAGE_UNMAPPED;
-                row[h] = 0;
-                uint64_t mine = 0;
-                if (c < copies && p < w.span.hi && p + R > w.span.start) {
-                    const uint32_t idx = fast_div((uint32_t)p, a.ps);
-                    row[h] = (uint32_t)p - idx * a.ps.d;
-                    const uint32_t id =
-                        idx < a.max_pages
-                            ? __ldg(a.page_table + (uint64_t)w.b * a.max_pages + idx)
-                            : KVW_PAGE_UNMAPPED;
-                    if (id < a.num_pages) {
-                        page[h] = id;
-                        const int64_t lo = p > w.span.start ? p : w.span.start;
-                        const int64_t hi = p + R < w.span.hi ? p + R : w.span.hi;
-                        const uint32_t len = (uint32_t)(hi - lo);
-                        mine = (len == 64 ? ~0ull : (1ull << len) - 1) << (uint32_t)(lo - p_tile);
-                    } else {
-                        bad_page = 1;
-                    }
-                }
-                n += __popc(__ballot_sync(0xffffffffu, mine != 0));
-                there |= mine;
-                if (copies <= 32) {
-                    page[1] = KVW_PAGE_UNMAPPED;
-                    break;
-                }
+                copy[h].level = 4;
+                if (h && maps.log_rows) continue;
+                copy[h] = plan_unit(maps, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
+                                    p_tile, w.span.start, w.span.hi, lane + 32u * h);
+                if (copy[h].bad_page) bad_page = 1;
+                n += __popc(__ballot_sync(0xffffffffu, copy[h].there != 0));
+                there |= copy[h].there;
             }
             const uint32_t t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
             const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
@@ -289,20 +271,22 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CUtensorMap* map,
                 if (!ok) break;
                 if (lane == 0) {
                     if (plane == 0) sm.there[at.slot] = ((uint64_t)t_hi << 32) | t_lo;
-                    mbar_arrive_expect_tx(&sm.full[at.slot], n * R * Sh::kLine * Sh::kBlocks);
+                    mbar_arrive_expect_tx(&sm.full[at.slot],
+                                          (n << maps.log_rows) * Sh::kLine * Sh::kBlocks);
                 }
                 __syncwarp();
                 if (!(WITHHOLD && first_half)) {
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (page[h] == KVW_PAGE_UNMAPPED) continue;
+                        if (copy[h].level == 4) continue;
                         const uint32_t dst = smem_addr(sm.ring + at.slot * Sh::kHalf) +
-                                             (lane + 32u * h) * R * Sh::kLine;
+                                             ((lane + 32u * h) << maps.log_rows) * Sh::kLine;
 #pragma unroll
                         for (int blk = 0; blk < Sh::kBlocks; ++blk)
-                            tma_rows(dst + blk * Sh::kBlock, map, blk * (Sh::kLine / Sh::kEsz),
-                                     kvh, row[h], page[h], plane, bar);
+                            tma_rows(dst + blk * Sh::kBlock, &maps.map[copy[h].level],
+                                     blk * (Sh::kLine / Sh::kEsz), kvh, copy[h].row, copy[h].page,
+                                     plane, bar);
                     }
                 }
                 first_half = false;
@@ -329,7 +313,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CUtensorMap* map,
 
 template <int DP, bool FP8, bool MODS, bool WITHHOLD>
 __global__ void __launch_bounds__(kThreads, 2)
-    gqa_decode_kernel(const GqaArgs a, const __grid_constant__ CUtensorMap map) {
+    gqa_decode_kernel(const GqaArgs a, const __grid_constant__ CacheMaps maps) {
     using Sh = Shape<DP, FP8>;
     constexpr int KS = DP / 16, NT = DP / 8, CH = DP * Sh::kEsz / 16, NP = Sh::kPair ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char dyn[];
@@ -351,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(&sm.meet, kWarps);
         sm.stop = 0;
         mbar_init_fence();
-        prefetch_map(&map);
+        prefetch_map(&maps.map[0]);
     }
     const bool ok = find_piece(a.split, a.pieces, blockIdx.x, sm.split);
     OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
@@ -362,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeederRegs));
-        if (warp == kWarps) feed<DP, FP8, WITHHOLD>(a, &map, sm);
+        if (warp == kWarps) feed<DP, FP8, WITHHOLD>(a, maps, sm);
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
@@ -401,24 +385,37 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t t0 = r0 / in_block, t1 = r1 / in_block;  // tokens of the chunk
         alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_ns);
         if (!alive) break;
-        const uint16_t* q0 = reinterpret_cast<const uint16_t*>(sm.q_raw[q_at.slot]) + r0 * a.D;
-        const uint16_t* q1 = q0 + 8 * a.D;
+        const unsigned char* q0 = sm.q_raw[q_at.slot] + r0 * Sh::kQPitch;
+        const unsigned char* q1 = q0 + 8 * Sh::kQPitch;
         // two neighbouring values of a row; column order of the k16 operand
         // (bf16: as the instruction has it; fp16: the order in which the
         // E4M3 codes of a lane's 4-byte word are unpacked)
-        auto q_word = [&](const uint16_t* p, uint32_t r, int ks, int half) -> uint32_t {
+        auto q_word = [&](const unsigned char* p, uint32_t r, int ks, int half) -> uint32_t {
             const uint32_t d = 16 * ks + (FP8 ? 4 * in_quad + 2 * half : 2 * in_quad + 8 * half);
-            return r < rows && d < a.D ? *reinterpret_cast<const uint32_t*>(p + d) : 0u;
+            return r < rows && d < a.D ? *reinterpret_cast<const uint32_t*>(p + 2 * d) : 0u;
         };
-        float qs0 = a.sm_scale, qs1 = a.sm_scale, up0 = 1.0f, up1 = 1.0f;
+        constexpr int kStep = Sh::kQInRegs ? 1 : kWarps;  // or one copy for the four warps
+        uint32_t qf[KS / kStep][4];
+#pragma unroll
+        for (int i = 0; i < KS / kStep; ++i) {
+            const int ks = Sh::kQInRegs ? i : i * kWarps + (int)warp;
+            qf[i][0] = q_word(q0, r0, ks, 0);
+            qf[i][1] = q_word(q1, r1, ks, 0);
+            qf[i][2] = q_word(q0, r0, ks, 1);
+            qf[i][3] = q_word(q1, r1, ks, 1);
+        }
+        float qs0 = a.sm_scale, qs1 = a.sm_scale;
         if constexpr (FP8) {
             uint32_t top0 = 0, top1 = 0;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    top0 = __vmaxu2(top0, q_word(q0, r0, ks, h) & 0x7fff7fffu);
-                    top1 = __vmaxu2(top1, q_word(q1, r1, ks, h) & 0x7fff7fffu);
+                    const uint32_t x0 = kStep == 1 ? qf[ks / kStep][2 * h] : q_word(q0, r0, ks, h);
+                    const uint32_t x1 =
+                        kStep == 1 ? qf[ks / kStep][2 * h + 1] : q_word(q1, r1, ks, h);
+                    top0 = __vmaxu2(top0, x0 & 0x7fff7fffu);
+                    top1 = __vmaxu2(top1, x1 & 0x7fff7fffu);
                 }
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
@@ -427,11 +424,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             top0 = max(top0 & 0xffffu, top0 >> 16);
             top1 = max(top1 & 0xffffu, top1 >> 16);
-            float d0, d1;
+            float up0, up1, d0, d1;
             row_power(top0, up0, d0);
             row_power(top1, up1, d1);
             qs0 = a.sm_scale * a.k_scale * d0;
             qs1 = a.sm_scale * a.k_scale * d1;
+#pragma unroll
+            for (int i = 0; i < KS / kStep; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x0 = qf[i][2 * h], x1 = qf[i][2 * h + 1];
+                    qf[i][2 * h] = pack2<true>(bf16_lo(x0) * up0, bf16_hi(x0) * up0);
+                    qf[i][2 * h + 1] = pack2<true>(bf16_lo(x1) * up1, bf16_hi(x1) * up1);
+                }
         }
         if constexpr (!MODS) {  // scores in units of log2 straight from the product
             qs0 *= kLog2e;
@@ -440,28 +445,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         // never 0: a masked score is -inf times this
         qs0 = fmaxf(qs0, 1.17549435e-38f);
         qs1 = fmaxf(qs1, 1.17549435e-38f);
-        auto q_conv = [&](uint32_t v, float up) -> uint32_t {
-            if constexpr (FP8) return pack2<true>(bf16_lo(v) * up, bf16_hi(v) * up);
-            return v;
-        };
-        uint32_t qf[Sh::kQInRegs ? KS : 1][4];
-        if constexpr (Sh::kQInRegs) {
+        if constexpr (!Sh::kQInRegs) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qf[ks][0] = q_conv(q_word(q0, r0, ks, 0), up0);
-                qf[ks][1] = q_conv(q_word(q1, r1, ks, 0), up1);
-                qf[ks][2] = q_conv(q_word(q0, r0, ks, 1), up0);
-                qf[ks][3] = q_conv(q_word(q1, r1, ks, 1), up1);
-            }
-        } else {  // one copy for the four warps, in operand order
-            for (int ks = warp; ks < KS; ks += kWarps) {
-                uint4 v;
-                v.x = q_conv(q_word(q0, r0, ks, 0), up0);
-                v.y = q_conv(q_word(q1, r1, ks, 0), up1);
-                v.z = q_conv(q_word(q0, r0, ks, 1), up0);
-                v.w = q_conv(q_word(q1, r1, ks, 1), up1);
-                *reinterpret_cast<uint4*>(s_q + (ks * 32 + lane) * 4) = v;
-            }
+            for (int i = 0; i < KS / kStep; ++i)
+                *reinterpret_cast<uint4*>(s_q + ((i * kWarps + warp) * 32 + lane) * 4) =
+                    make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
             alive = meet();
             if (!alive) break;
         }
@@ -471,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto q_frag = [&](int ks, uint32_t(&f)[4]) {
             if constexpr (Sh::kQInRegs) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = qf[ks][i];
+                for (int i = 0; i < 4; ++i) f[i] = qf[ks / kStep][i];
             } else {
                 const uint4 v = *reinterpret_cast<const uint4*>(s_q + (ks * 32 + lane) * 4);
                 f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
@@ -496,9 +484,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t mat = lane >> 3, mrow = lane & 7u;
         const int64_t p_first = (int64_t)(w.span.tile0 + w.first) * kTile + warp * kSlice;
 
-        // `N` slices of tiles k, k + 1, ...
-        auto slices = [&](uint32_t k, auto n_const) -> bool {
+        // Is every position of this warp's slice there, in the K half at x?
+        auto full_slice = [&](const RingPos<Sh::kHalves>& x) {
+            return ((uint32_t)(sm.there[x.slot] >> (warp * kSlice)) & 0xffffu) == 0xffffu;
+        };
+        // `N` slices of tiles k, k + 1, ... whose K halves have arrived; EDGE:
+        // positions may be missing, or seen by some rows only
+        auto slices = [&](uint32_t k, auto n_const, auto edge_const) -> bool {
             constexpr int N = decltype(n_const)::value;
+            constexpr bool EDGE = decltype(edge_const)::value;
             RingPos<Sh::kHalves> h[2 * N];  // K and V of each
             h[0] = at;
 #pragma unroll
@@ -511,12 +505,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             float s[2 * N][4];
 #pragma unroll
             for (int i = 0; i < 2 * N; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-            uint32_t there[N];
+            [[maybe_unused]] uint32_t there[N];
             // ---- S = Q K^T
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (!ready(h[2 * i])) return false;
-                there[i] = (uint32_t)(sm.there[h[2 * i].slot] >> (warp * kSlice)) & 0xffffu;
+                if constexpr (EDGE)
+                    there[i] = (uint32_t)(sm.there[h[2 * i].slot] >> (warp * kSlice)) & 0xffffu;
                 const uint32_t src = ring_addr + h[2 * i].slot * Sh::kHalf;
                 const uint32_t row0 = warp * kSlice;
                 if constexpr (!FP8) {
@@ -549,10 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (lane == 0) mbar_arrive(&sm.empty[h[2 * i].slot]);
             }
             // ---- cap, distance bias, mask
-            bool uneven[N];  // not every row sees the same positions of the slice
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int64_t p0 = p_first + (int64_t)(k + i) * kTile;
+                [[maybe_unused]] const int64_t p0 = p_first + (int64_t)(k + i) * kTile;
                 if constexpr (MODS) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
@@ -572,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             s[2 * i + n][e] = x * kLog2e;
                         }
                 }
-                uneven[i] = p0 + kSlice - 1 > all_hi || p0 < all_lo;
-                if (there[i] != 0xffffu || uneven[i]) {
+                if constexpr (EDGE) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -600,7 +592,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 top0 *= qs0;
                 top1 *= qs1;
             }
-            const bool grows = top0 > m0 || top1 > m1;
+            // The weights' reference m follows the maximum only when that has
+            // risen by more than 2^kSlack: any m will do that keeps the
+            // weights in range, and the accumulators are rescaled seldom.
+            const bool grows = top0 > m0 + kSlack || top1 > m1 + kSlack;
             if (__any_sync(0xffffffffu, grows)) {
                 const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
                 const float f0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0);
@@ -689,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int i = 0; i < N; ++i) {
                 if (!ready(h[2 * i + 1])) return false;
                 const uint32_t src = ring_addr + h[2 * i + 1].slot * Sh::kHalf;
-                if (there[i] == 0xffffu && !uneven[i]) {
+                if constexpr (!EDGE) {
                     times_v(src, pf[i], std::false_type{}, 0u, 0u, true, true);
                 } else if (there[i]) {
                     // A weight of 0 does not keep out a value that is not
@@ -714,12 +709,40 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             return true;
         };
+        // tiles [even0, even1) of the segment: this warp's slices are seen by
+        // every row of the block alike
         const uint32_t count = w.last - w.first;
-        uint32_t k = 0;
-        if constexpr (NP == 2)
-            for (; alive && k + 1 < count; k += 2)
-                alive = slices(k, std::integral_constant<int, 2>{});
-        for (; alive && k < count; ++k) alive = slices(k, std::integral_constant<int, 1>{});
+        const int64_t lo_gap = all_lo - p_first, hi_gap = all_hi + 1 - kSlice - p_first;
+        const uint32_t even0 = lo_gap <= 0 ? 0u : (uint32_t)((lo_gap + kTile - 1) / kTile);
+        const uint32_t even1 = hi_gap < 0 ? 0u : (uint32_t)(hi_gap / kTile) + 1;
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        for (uint32_t k = 0; alive && k < count;) {
+            alive = ready(at);
+            if (!alive) break;
+            if constexpr (NP == 2) {
+                if (k >= even0 && k + 1 < count && k + 1 < even1) {
+                    RingPos<Sh::kHalves> x = at;
+                    x.step();
+                    x.step();
+                    alive = ready(x);
+                    if (!alive) break;
+                    if (full_slice(at) && full_slice(x)) {
+                        alive = slices(k, Two{}, std::false_type{});
+                        k += 2;
+                        continue;
+                    }
+                }
+            } else {
+                if (k >= even0 && k < even1 && full_slice(at)) {
+                    alive = slices(k, One{}, std::false_type{});
+                    ++k;
+                    continue;
+                }
+            }
+            alive = slices(k, One{}, std::true_type{});
+            ++k;
+        }
         if (!alive) break;
 
         // ---- the four warps join, a few rows at a time
@@ -808,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!alive) break;
         if (!whole && w.first == 0 && tid == 0) {
-            open->end = w.end();
+            open->end = w.end(a.split);
             open->pieces = sm.split.start.pieces;
             open->t = w.t;
             open->tokens = w.span.tokens;
@@ -913,7 +936,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
 }
 
 template <int DP, bool FP8, bool MODS, bool WITHHOLD>
-cudaError_t launch_as(GqaArgs& a, const CUtensorMap& map, cudaStream_t stream) {
+cudaError_t launch_as(GqaArgs& a, const CacheMaps& maps, cudaStream_t stream) {
     constexpr size_t smem = sizeof(Smem<DP, FP8>);
     static_assert(smem <= 113 * 1024, "two CTAs per SM");
     uint64_t wave = 0;
@@ -922,7 +945,7 @@ cudaError_t launch_as(GqaArgs& a, const CUtensorMap& map, cudaStream_t stream) {
     if (wave == 0) return cudaErrorInvalidConfiguration;
     if (wave > kMaxPieces) wave = kMaxPieces;
     a.pieces = (uint32_t)wave;
-    gqa_decode_kernel<DP, FP8, MODS, WITHHOLD><<<a.pieces, kThreads, smem, stream>>>(a, map);
+    gqa_decode_kernel<DP, FP8, MODS, WITHHOLD><<<a.pieces, kThreads, smem, stream>>>(a, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.pieces);
@@ -938,12 +961,12 @@ cudaError_t launch_as(GqaArgs& a, const CUtensorMap& map, cudaStream_t stream) {
 
 template <int DP, bool FP8, bool WITHHOLD>
 int launch(GqaArgs& a, const kvw_paged_cache_t* cache, uint32_t layer_idx, cudaStream_t stream) {
-    CUtensorMap map;
-    const int st = encode_cache_map(&map, cache, layer_idx, 2);
+    CacheMaps maps;
+    const int st = encode_cache_maps(&maps, cache, layer_idx, 2);
     if (st != KVW_OK) return st;
     const cudaError_t e = a.softcap > 0.0f || a.slopes
-                              ? launch_as<DP, FP8, true, WITHHOLD>(a, map, stream)
-                              : launch_as<DP, FP8, false, WITHHOLD>(a, map, stream);
+                              ? launch_as<DP, FP8, true, WITHHOLD>(a, maps, stream)
+                              : launch_as<DP, FP8, false, WITHHOLD>(a, maps, stream);
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
@@ -997,6 +1020,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     // tokens of a chunk: as many as fit the 16 rows (a power of two)
     while (a.HB == 1 && (2u << a.split.log_c) * a.G <= kRows) ++a.split.log_c;
     a.split.min_units = 1;
+    a.split.overhead = 2;
     const uint64_t reach = (uint64_t)cache->max_pages_per_seq * cache->page_size;
     a.split.cap = reach > kMaxReach ? (int64_t)kMaxReach : (int64_t)reach;
     a.split.window = window ? (int64_t)window : 1ll << 40;
@@ -1019,7 +1043,6 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     a.num_pages = cache->num_pages;
     a.max_pages = cache->max_pages_per_seq;
     a.ps = make_fast_div(cache->page_size);
-    a.copy_rows = rows_per_copy(cache->page_size);
     a.wait_ns = wait_ns;
     auto run = [&](auto dp, auto f8) {
 #ifdef KVW_TEST_HOOKS

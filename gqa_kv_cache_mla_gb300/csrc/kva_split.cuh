@@ -4,15 +4,17 @@
 // A chunk is up to C consecutive new tokens of one request (C a power of two;
 // their query rows share a row block, so a cache row is read once for all of
 // them).  Work is counted in units: one unit is one tile of kTile cache
-// positions for one row block of one chunk.  The units of all chunks in
-// order - chunk, row block, tile - form one long axis, cut into equal pieces,
-// one for each CTA.  So every CTA reads the same amount of cache whatever the
-// lengths, a CTA crosses from one chunk to the next where its piece does, and
-// at most two of its segments are parts of a (chunk, row block) that other
-// CTAs share: its first (slot 0) and its last (slot 1).  Those write their
-// unnormalised sums with their running maximum and sum to a workspace whose
-// size depends on the number of pieces alone, and a second kernel joins them
-// in order: the result depends on the lengths and the device only.
+// positions for one row block of one chunk; `overhead` further units stand
+// before the tiles of every (chunk, row block) for what it costs to begin and
+// end one.  The units of all chunks in order - chunk, row block, tile - form
+// one long axis, cut into equal pieces, one for each CTA.  So every CTA has
+// the same work whatever the lengths, a CTA crosses from one chunk to the
+// next where its piece does, and at most two of its segments are parts of a
+// (chunk, row block) that other CTAs share: its first (slot 0) and its last
+// (slot 1).  Those write their unnormalised sums with their running maximum
+// and sum to a workspace whose size depends on the number of pieces alone,
+// and a second kernel joins them in order: the result depends on the lengths
+// and the device only.
 //
 // Finding a piece needs the number of tiles before a chunk, a prefix sum over
 // chunks.  Within a request the chunks' lengths rise by C, so a request's
@@ -35,6 +37,7 @@ struct SplitArgs {
     uint32_t blocks;     // row blocks per chunk
     uint32_t log_c;      // log2 of the tokens per chunk, <= 6
     uint32_t min_units;  // a piece is at least this long (fewer pieces for little work)
+    uint32_t overhead;   // what beginning a (chunk, row block) costs, in units
     int64_t cap;         // positions the page tables can hold
     int64_t window;      // positions seen, own included (a huge number for no window)
 };
@@ -92,22 +95,33 @@ __host__ __device__ __forceinline__ int64_t tiles_before(const SplitArgs& a, int
            sum_floor(f + k, log_m, from) + sum_floor(f, log_m, from);
 }
 
+// Units of one row block of the first k chunks.
+__host__ __device__ __forceinline__ int64_t units_before(const SplitArgs& a, int64_t len,
+                                                         uint32_t k) {
+    return tiles_before(a, len, k) + (int64_t)k * a.overhead;
+}
+
 __host__ __device__ __forceinline__ uint32_t chunks_of(const SplitArgs& a, uint32_t n) {
     return (n >> a.log_c) + ((n & ((1u << a.log_c) - 1u)) ? 1u : 0u);
 }
 
-// All tiles of a request.
-__host__ __device__ __forceinline__ int64_t request_tiles(const SplitArgs& a, int64_t len,
+// Units of one row block of a whole request.
+__host__ __device__ __forceinline__ int64_t request_units(const SplitArgs& a, int64_t len,
                                                           uint32_t n) {
     if (n == 0) return 0;
     const uint32_t k = chunks_of(a, n) - 1;
-    return tiles_before(a, len, k) + chunk_span(a, len, n, k).tiles;
+    return units_before(a, len, k) + chunk_span(a, len, n, k).tiles + a.overhead;
+}
+
+// Quotients of the axis, with the 32-bit division where it will do.
+__host__ __device__ __forceinline__ uint64_t div_units(uint64_t x, uint64_t y) {
+    return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
 
 // First unit of piece c of `pieces` over `units` units (even to one unit).
 __host__ __device__ __forceinline__ uint64_t piece_start(uint64_t units, uint32_t pieces,
                                                          uint32_t c) {
-    const uint64_t q = units / pieces, r = units % pieces;
+    const uint64_t q = div_units(units, pieces), r = units - q * pieces;
     return q * c + (c < r ? c : r);
 }
 
@@ -115,7 +129,7 @@ __host__ __device__ __forceinline__ uint64_t piece_start(uint64_t units, uint32_
 // only one.
 __host__ __device__ __forceinline__ uint32_t pieces_of(const SplitArgs& a, uint64_t units,
                                                        uint32_t most) {
-    const uint64_t p = units / a.min_units;
+    const uint64_t p = div_units(units, a.min_units);
     return p == 0 ? 1u : p < most ? (uint32_t)p : most;
 }
 
@@ -151,7 +165,7 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
         if (o1 < o0 || o1 > a.T || (r == 0 && o0 != 0) || (r == a.B - 1 && o1 != a.T))
             ok = 0;
         else
-            mine += request_tiles(a, len, o1 - o0);
+            mine += request_units(a, len, o1 - o0);
     }
     int64_t scan = mine;
 #pragma unroll
@@ -179,28 +193,28 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
     // the one thread whose requests hold u0 walks them
     if (used && s.u0 >= (uint64_t)before * a.blocks &&
         s.u0 < (uint64_t)(before + mine) * a.blocks) {
-        const uint64_t at = s.u0 / a.blocks;  // u0 in tiles: the chunk holds this tile
+        const uint64_t at = div_units(s.u0, a.blocks);  // the chunk holds this unit of a row block
         int64_t base = before;
         for (uint32_t r = lo; r < hi; ++r) {
             const uint32_t len = __ldg(a.cache_lengths + r);
             const uint32_t n = __ldg(a.offsets + r + 1) - __ldg(a.offsets + r);
-            const int64_t tiles = request_tiles(a, len, n);
-            if (at < (uint64_t)(base + tiles)) {
+            const int64_t units = request_units(a, len, n);
+            if (at < (uint64_t)(base + units)) {
                 // the last chunk that begins at or before it
                 uint32_t k0 = 0, k1 = chunks_of(a, n);
                 while (k1 - k0 > 1u) {
                     const uint32_t mid = k0 + (k1 - k0) / 2;
-                    if ((uint64_t)(base + tiles_before(a, len, mid)) <= at)
+                    if ((uint64_t)(base + units_before(a, len, mid)) <= at)
                         k0 = mid;
                     else
                         k1 = mid;
                 }
                 s.b = r;
                 s.k = k0;
-                s.chunk_base = (uint64_t)(base + tiles_before(a, len, k0)) * a.blocks;
+                s.chunk_base = (uint64_t)(base + units_before(a, len, k0)) * a.blocks;
                 break;
             }
-            base += tiles;
+            base += units;
         }
         sh.start = s;
     }
@@ -215,7 +229,9 @@ struct Walk {
     uint32_t b, k, t, n;  // request, chunk in it, the chunk's first token, tokens of the request
     uint32_t len0;        // cache_lengths[b]
     ChunkSpan span;
-    uint32_t block, first, last;  // the segment: row block, tiles first .. last - 1 of the span
+    // the segment: row block, units of the axis, tiles first .. last - 1 of
+    // the span (at least one)
+    uint32_t block, units, first, last;
 
     __device__ __forceinline__ void load_request(const SplitArgs& a) {
         const uint32_t o = __ldg(a.offsets + b);
@@ -223,38 +239,23 @@ struct Walk {
         t = o + (k << a.log_c);
         len0 = __ldg(a.cache_lengths + b);
     }
-    __device__ __forceinline__ void find_segment() {
-        const uint64_t in = u - chunk_base;
-        block = (uint32_t)(in / span.tiles);
-        first = (uint32_t)(in - (uint64_t)block * span.tiles);
-        const uint64_t left = u1 - u;
-        last = span.tiles - first < left ? span.tiles : first + (uint32_t)left;
+    __device__ __forceinline__ uint64_t chunk_units(const SplitArgs& a) const {
+        return (uint64_t)a.blocks * (span.tiles + a.overhead);
     }
-    __device__ __forceinline__ void begin(const SplitArgs& a, const PieceStart& s) {
-        u = s.u0;
-        u1 = s.u1;
-        chunk_base = s.chunk_base;
-        b = s.b;
-        k = s.k;
-        block = first = last = 0;
-        if (u < u1) {
-            load_request(a);
-            span = chunk_span(a, len0, n, k);
-            find_segment();
-        }
+    __device__ __forceinline__ void find_segment(const SplitArgs& a) {
+        const uint32_t per = span.tiles + a.overhead;
+        const uint64_t in = u - chunk_base, left = u1 - u;
+        block = (uint32_t)div_units(in, per);
+        const uint32_t from = (uint32_t)(in - (uint64_t)block * per);
+        units = per - from < left ? per - from : (uint32_t)left;
+        first = from > a.overhead ? from - a.overhead : 0;
+        last = from + units > a.overhead ? from + units - a.overhead : 0;
     }
-    __device__ __forceinline__ bool done() const { return u >= u1; }
-    // The unit where the segment's (chunk, row block) ends.
-    __device__ __forceinline__ uint64_t end() const {
-        return chunk_base + (uint64_t)(block + 1) * span.tiles;
-    }
-    __device__ __forceinline__ bool whole() const { return first == 0 && last == span.tiles; }
-    // On to the next segment.
-    __device__ __forceinline__ void next(const SplitArgs& a) {
-        u += last - first;
+    __device__ __forceinline__ void step(const SplitArgs& a) {
+        u += units;
         if (u >= u1) return;
-        if (u >= chunk_base + (uint64_t)a.blocks * span.tiles) {
-            chunk_base += (uint64_t)a.blocks * span.tiles;
+        if (u >= chunk_base + chunk_units(a)) {
+            chunk_base += chunk_units(a);
             if (++k < chunks_of(a, n)) {
                 t += 1u << a.log_c;
             } else {
@@ -266,13 +267,39 @@ struct Walk {
             }
             span = chunk_span(a, len0, n, k);
         }
-        find_segment();
+        find_segment(a);
+    }
+    __device__ __forceinline__ void begin(const SplitArgs& a, const PieceStart& s) {
+        u = s.u0;
+        u1 = s.u1;
+        chunk_base = s.chunk_base;
+        b = s.b;
+        k = s.k;
+        block = units = first = last = 0;
+        if (u < u1) {
+            load_request(a);
+            span = chunk_span(a, len0, n, k);
+            find_segment(a);
+            while (u < u1 && first == last) step(a);
+        }
+    }
+    __device__ __forceinline__ bool done() const { return u >= u1; }
+    // The unit where the segment's (chunk, row block) ends.
+    __device__ __forceinline__ uint64_t end(const SplitArgs& a) const {
+        return chunk_base + (uint64_t)(block + 1) * (span.tiles + a.overhead);
+    }
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == span.tiles; }
+    // On to the next segment that has tiles (a piece may end in units that
+    // have none).
+    __device__ __forceinline__ void next(const SplitArgs& a) {
+        do step(a);
+        while (u < u1 && first == last);
     }
 };
 
-// What a piece left open: a (chunk, row block) that it began (slot 1) and that
-// the pieces after it go on with (their slot 0), up to unit `end`.  `units` 0:
-// nothing.
+// What a piece left open: a (chunk, row block) whose first tile it has (slot 1)
+// and that the pieces after it go on with (their slot 0), up to unit `end`.
+// `units` 0: nothing.
 struct OpenPiece {
     uint64_t units, end;
     uint32_t pieces, t, tokens, block;

@@ -2,12 +2,15 @@
 // kernels of kva.h.
 //
 // The cache of one layer is a tensor (column, head, row of a page, page,
-// plane) under the descriptor's own strides.  One copy takes R rows of one
-// head of one page and 128 bytes of their columns into shared memory in
-// the 128-byte swizzle (16-byte chunk c of a row lies in place c ^ (line & 7)),
-// with columns past the head size filled with zeros.  R is the largest power
-// of two up to 64 that divides the page size, so a copy never crosses a page
-// and a tile of 64 positions is 64 / R copies for each 128 bytes of columns.
+// plane) under the descriptor's own strides.  One copy takes some rows of one
+// head of one page and 128 bytes of their columns into shared memory in the
+// 128-byte swizzle (16-byte chunk c of a row lies in place c ^ (line & 7)),
+// with columns past the head size filled with zeros.  A copy must not cross a
+// page.  With R the largest power of two up to 64 that divides the page size,
+// pages cut a tile of 64 positions at multiples of R only, so a tile is made
+// of runs of R-row units; a run is copied greedily in pieces of 16, 4 and 1
+// units, one map for each piece size (one map in all for page sizes whose R
+// is 32 or 64, and for those of 16 up to 48).
 #pragma once
 
 #include <cuda.h>
@@ -47,10 +50,16 @@ inline bool tma_strides_ok(const kvw_paged_cache_t* c, int planes) {
            ok(c->stride_page, c->num_pages) && ok(c->stride_kv, (uint64_t)planes);
 }
 
-// Map of one layer's planes; 128 bytes of columns per copy, so that a copy of
-// any number of rows starts on a 128-byte line of shared memory, as it must.
-inline int encode_cache_map(CUtensorMap* map, const kvw_paged_cache_t* c, uint32_t layer_idx,
-                            int planes) {
+// Maps of one layer's planes, map[i] for copies of R << 2i rows; 128 bytes of
+// columns per copy, so that a copy of any number of rows starts on a 128-byte
+// line of shared memory, as it must.
+struct CacheMaps {
+    CUtensorMap map[4];
+    uint32_t levels, log_rows;  // maps in use; log2 of R
+};
+
+inline int encode_cache_maps(CacheMaps* m, const kvw_paged_cache_t* c, uint32_t layer_idx,
+                             int planes) {
     const auto encode = tensor_map_encoder();
     if (!encode) return KVW_ECUDA;
     const uint64_t esz = cache_esz(c);
@@ -62,16 +71,79 @@ inline int encode_cache_map(CUtensorMap* map, const kvw_paged_cache_t* c, uint32
                                    bytes(c->stride_token, c->page_size),
                                    bytes(c->stride_page, c->num_pages),
                                    bytes(c->stride_kv, (uint64_t)planes)};
-    const cuuint32_t box[5] = {(cuuint32_t)(128 / esz), 1, rows_per_copy(c->page_size), 1, 1};
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     unsigned char* base = static_cast<unsigned char*>(c->data) +
                           (int64_t)layer_idx * (c->num_layers > 1 ? c->stride_layer : 0) *
                               (int64_t)esz;
-    const CUresult r = encode(
-        map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base,
-        dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? KVW_OK : KVW_EINVAL;
+    const uint32_t rows = rows_per_copy(c->page_size);
+    m->log_rows = 0;
+    while ((1u << m->log_rows) < rows) ++m->log_rows;
+    m->levels = 0;
+    for (uint32_t r = rows; r <= 64 && r <= c->page_size; r *= 4) {
+        const cuuint32_t box[5] = {(cuuint32_t)(128 / esz), 1, r, 1, 1};
+        if (encode(&m->map[m->levels++],
+                   esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                   base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KVW_EINVAL;
+    }
+    return KVW_OK;
+}
+
+// Does a copy begin at unit x of a run of `run` units, and with which map?
+__host__ __device__ __forceinline__ bool copy_begins(uint32_t x, uint32_t run, uint32_t levels,
+                                                     uint32_t& level) {
+    for (level = levels - 1; level > 0; --level) {
+        const uint32_t in = (run >> (2 * level)) << (2 * level);
+        if (x < in) return (x & ((1u << (2 * level)) - 1u)) == 0;
+        x -= in;
+        run -= in;
+    }
+    return true;
+}
+
+// What one lane copies for one unit of a tile.
+struct UnitCopy {
+    uint32_t page, row, level;  // level 4: nothing
+    uint64_t there;             // positions of the tile that the unit holds
+    bool bad_page;
+};
+
+// Unit c (of 64 >> log_rows) of the tile at position p_tile of request b, for
+// positions [start, hi).
+__device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m, const uint32_t* page_table,
+                                              uint32_t max_pages, uint32_t num_pages,
+                                              const FastDiv& ps, uint32_t b, int64_t p_tile,
+                                              int64_t start, int64_t hi, uint32_t c) {
+    UnitCopy u;
+    u.page = u.row = 0;
+    u.level = 4;
+    u.there = 0;
+    u.bad_page = false;
+    const int64_t p = p_tile + ((int64_t)c << m.log_rows);
+    const int64_t p_end = p + (1ll << m.log_rows);
+    if (c >= (64u >> m.log_rows) || p >= hi || p_end <= start) return u;
+    const uint32_t idx = fast_div((uint32_t)p, ps);
+    u.row = (uint32_t)p - idx * ps.d;
+    u.page = idx < max_pages ? __ldg(page_table + (uint64_t)b * max_pages + idx) : KVW_PAGE_UNMAPPED;
+    if (u.page >= num_pages) {
+        u.bad_page = true;
+        return u;
+    }
+    const int64_t lo = p > start ? p : start, top = p_end < hi ? p_end : hi;
+    const uint32_t len = (uint32_t)(top - lo);
+    u.there = (len == 64 ? ~0ull : (1ull << len) - 1) << (uint32_t)(lo - p_tile);
+    // the run of units of this page that the tile uses
+    const uint32_t u0 = start > p_tile ? (uint32_t)(start - p_tile) >> m.log_rows : 0;
+    const uint32_t past = hi - p_tile < 64 ? (uint32_t)(hi - p_tile) : 64u;
+    const uint32_t u1 = (past + (1u << m.log_rows) - 1) >> m.log_rows;
+    const uint32_t back = u.row >> m.log_rows, ahead = (ps.d - u.row) >> m.log_rows;
+    const uint32_t from = c - u0 < back ? u0 : c - back;
+    const uint32_t to = u1 - c < ahead ? u1 : c + ahead;
+    uint32_t level;
+    if (copy_begins(c - from, to - from, m.levels, level)) u.level = level;
+    return u;
 }
 
 // One copy: columns from `col` of R rows from `row` of (page, plane, head).

@@ -21,6 +21,7 @@ int main() {
         SplitArgs a = {};
         a.log_c = (uint32_t)rnd(7);
         a.cap = 1 + (int64_t)rnd(it % 3 == 0 ? 90 : it % 3 == 1 ? 1000 : 1ull << 32);
+        a.overhead = (uint32_t)rnd(4);
         a.window = rnd(3) ? 1 + (int64_t)rnd(it % 2 ? 70 : 2000) : 1ll << 40;
         const int64_t len = (int64_t)rnd(it % 5 == 0 ? 1ull << 32 : it % 2 ? 100 : 3000);
         const uint32_t n = (uint32_t)rnd(200);
@@ -51,8 +52,8 @@ int main() {
             sum += s.tiles;
             ++checks;
         }
-        if (request_tiles(a, len, n) != sum) {
-            printf("request_tiles: it %d\n", it);
+        if (request_units(a, len, n) != sum + (int64_t)chunks_of(a, n) * a.overhead) {
+            printf("request_units: it %d\n", it);
             return 1;
         }
     }
