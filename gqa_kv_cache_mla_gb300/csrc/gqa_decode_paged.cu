@@ -25,6 +25,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "kva_attention.cuh"
 #include "kva_split.cuh"
 #include "kva_tma.cuh"
 
@@ -40,7 +41,6 @@ constexpr int kConsumerRegs = 200, kFeederRegs = 56;
 static_assert(kConsumerRegs + kFeederRegs <= 2 * 128, "registers of the launch");
 constexpr int kSlice = kTile / kWarps;      // positions of a tile that a warp takes
 constexpr int kRows = 16;                   // rows of a row block
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 6.0f;              // log2 of the largest weight before a rescale
 static_assert(kSlice == 16, "one m16n8k16 operand");
 
@@ -103,45 +103,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Four E4M3 codes -> two f16x2 (low bytes first), exact.
-__device__ __forceinline__ void codes_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(codes));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        return pack_bf16x2(lo, hi);
-    }
-}
-
-// Power of two that brings a row whose largest |value| has the bf16 pattern
-// `top` to [2^14, 2^15), and its inverse; 1 for a row of zeros or one that
-// holds an infinity or a NaN.  fp16 then holds the row's bf16 values exactly
-// down to 2^-31 of the largest.
-__device__ __forceinline__ void row_power(uint32_t top, float& up, float& down) {
-    const int e = (int)(top >> 7);
-    if (top == 0 || e == 255) {
-        up = down = 1.0f;
-        return;
-    }
-    const int ue = 268 - e > 254 ? 254 : 268 - e, de = e - 14 < 1 ? 1 : e - 14;
-    up = __uint_as_float((uint32_t)ue << 23);
-    down = __uint_as_float((uint32_t)de << 23);
-}
-
 template <int DP, bool FP8>
 struct Shape {
     static constexpr int kEsz = FP8 ? 1 : 2;
@@ -186,36 +147,6 @@ template <int DP, bool FP8>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
     return (c >> 3) * Shape<DP, FP8>::kBlock + r * 128u + (((c ^ r) & 7u) << 4);
 }
-
-// Bounded wait of a whole warp that ends early when another role gave up;
-// the answer is the same for all lanes.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t* stop,
-                                           uint64_t limit_ns) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = global_ns();
-        while (!(ok = mbar_try_wait(bar, parity))) {
-            if (*reinterpret_cast<volatile uint32_t*>(stop)) break;
-            if (global_ns() - t0 > limit_ns) {
-                *reinterpret_cast<volatile uint32_t*>(stop) = 1;
-                break;
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
-// A ring position: slot and the parity of its present round.
-template <int N>
-struct RingPos {
-    uint32_t slot = 0, parity = 0;
-    __device__ __forceinline__ void step() {
-        if (++slot == (uint32_t)N) {
-            slot = 0;
-            parity ^= 1u;
-        }
-    }
-};
 
 // The feeding warp: walks the piece's tiles ahead of the arithmetic.
 template <int DP, bool FP8, bool WITHHOLD>

@@ -1,0 +1,80 @@
+// Device helpers of the attention kernels of kva.h: exponentials, the fp16
+// side of an E4M3 cache, bounded waits between the warps of a CTA.
+#pragma once
+
+#include "kva_common.cuh"
+
+namespace kvw {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four E4M3 codes -> two f16x2 (low bytes first), exact.
+__device__ __forceinline__ void codes_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_bf16x2(lo, hi);
+    }
+}
+
+// Power of two that brings a row whose largest |value| has the bf16 pattern
+// `top` to [2^14, 2^15), and its inverse; 1 for a row of zeros or one that
+// holds an infinity or a NaN.  fp16 then holds the row's bf16 values exactly
+// down to 2^-31 of the largest.
+__device__ __forceinline__ void row_power(uint32_t top, float& up, float& down) {
+    const int e = (int)(top >> 7);
+    if (top == 0 || e == 255) {
+        up = down = 1.0f;
+        return;
+    }
+    const int ue = 268 - e > 254 ? 254 : 268 - e, de = e - 14 < 1 ? 1 : e - 14;
+    up = __uint_as_float((uint32_t)ue << 23);
+    down = __uint_as_float((uint32_t)de << 23);
+}
+
+// Bounded wait of a whole warp that ends early when another role gave up;
+// the answer is the same for all lanes.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t* stop,
+                                           uint64_t limit_ns) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (*reinterpret_cast<volatile uint32_t*>(stop)) break;
+            if (global_ns() - t0 > limit_ns) {
+                *reinterpret_cast<volatile uint32_t*>(stop) = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// A ring position: slot and the parity of its present round.
+template <int N>
+struct RingPos {
+    uint32_t slot = 0, parity = 0;
+    __device__ __forceinline__ void step() {
+        if (++slot == (uint32_t)N) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+}  // namespace kvw

@@ -157,6 +157,31 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// Queries [tokens, heads, width] in bf16: copies of 64 heads x 64 columns,
+// heads past the last one filled with zeros.
+inline int encode_query_map(CUtensorMap* map, const void* q, uint32_t width, uint32_t heads,
+                            uint32_t tokens, int64_t row_stride) {
+    const auto encode = tensor_map_encoder();
+    if (!encode) return KVW_ECUDA;
+    const cuuint64_t dims[3] = {width, heads, tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)row_stride * 2};
+    const cuuint32_t box[3] = {64, 64, 1}, ones[3] = {1, 1, 1};
+    const CUresult r =
+        encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+               ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KVW_OK : KVW_EINVAL;
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t c0,
+                                       uint32_t c1, uint32_t c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

@@ -1,0 +1,888 @@
+// Attention of new tokens over the paged MLA latent cache.
+//
+// Mathematics, for one token and a block of up to 64 heads: every head reads
+// the same rows (576 wide: 512 latent, 64 rotated), so one tile of 64
+// positions serves all of them.  S = Q K^T (64 heads x 64 positions, 576
+// deep); with the running maximum m and sum l of a softmax per head, P =
+// 2^(S - m); and, turned around so that the 512 output columns fill the matrix
+// unit's lanes, O^T += V^T P^T (512 x 64, 64 positions deep), V being the
+// first 512 columns of the same tile in shared memory.  m follows the maximum
+// only when that has risen by more than 2^6, so O^T is rescaled seldom.
+//
+// Bound: 64 heads do 121 flops per byte of a bf16 row (242 with both blocks
+// of 128 heads, whose two CTAs read the same piece at the same time and meet
+// in L2), close to the ridge of the card: both HBM and the matrix unit's
+// operand bandwidth matter.  The products are tcgen05 MMAs on tiles that the
+// copy engine writes in the operands' own swizzled layout, page by page, so a
+// bf16 row goes from HBM to the matrix unit without passing a register.  An
+// E4M3 row lands as codes; four warps turn them into fp16 (exactly) in the
+// same layout.
+//
+// Shared memory (227 KB) decides the rest: Q takes 72 KB, a bf16 tile 72 KB,
+// so there are two tiles, each in five groups (the rotated columns, then four
+// times 128 latent columns) that are filled and freed one by one: the first
+// group is free after S, the others as the four row blocks of O^T complete.
+// An E4M3 cache has one fp16 tile and nine 8 KB slots of codes ahead of it.
+// O^T fills 256 of the 512 columns of tensor memory, two S tiles 128.
+//
+// Warps: 0-3 softmax, rescaling, results; 4 feeds; 5 issues the MMAs; 6-9
+// (E4M3) convert.  Every wait is bounded.
+#include <cstdint>
+#include <type_traits>
+
+#include "kva_attention.cuh"
+#include "kva_split.cuh"
+#include "kva_tcgen05.cuh"
+#include "kva_tma.cuh"
+
+namespace kvw {
+namespace {
+
+constexpr uint32_t kHeads = 64;               // rows of a row block
+constexpr uint32_t kLatent = 512, kRow = 576;
+constexpr uint32_t kPanel = kTile * 128;      // 64 columns of a 16-bit tile, or 128 codes
+constexpr uint32_t kGroups = 5;               // of a tile: rotated columns, 4 x 128 latent ones
+constexpr uint32_t kRawSlots = 9;
+constexpr uint32_t kMaxCtas = 192;
+constexpr uint32_t kTmemColumns = 512, kScoreColumn = 256;
+constexpr float kSlack = 6.0f;                // log2 of the largest weight before a rescale
+constexpr int kSoftmaxThreads = 128;
+
+struct MlaArgs {
+    SplitArgs split;
+    uint16_t* out;
+    float* lse;
+    const uint32_t* page_table;
+    uint32_t* err_flags;
+    unsigned char* workspace;
+    float scale;      // sm_scale * log2(e) * row_scale
+    float row_scale;  // what a cache element stands for: its code times this
+    uint32_t H, HB, slot_rows;  // heads, row blocks, rows of a workspace slot
+    uint32_t num_pages, max_pages, pieces;
+    FastDiv ps;
+    uint64_t wait_ns;
+};
+
+struct QMaps {
+    CUtensorMap latent, rope;
+};
+
+template <bool FP8>
+constexpr int threads_of() {
+    return FP8 ? 320 : 192;
+}
+
+template <bool FP8>
+struct Smem {
+    unsigned char q[9 * kPanel];  // rotated columns, then the latent panels
+    unsigned char kv[(FP8 ? 1 : 2) * 9 * kPanel];
+    unsigned char p[kPanel];
+    unsigned char raw[FP8 ? kRawSlots * kPanel : 16];
+    uint64_t full[2 * kGroups], empty[2 * kGroups];  // groups of the 16-bit tiles
+    uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+    uint64_t q_full, q_ready, q_free;
+    uint64_t s_full[2], s_free[2], p_full, pv_done, o_free, drained;
+    uint64_t there[8];  // of a tile: positions that are there
+    float alpha[kHeads], m[kHeads], l[kHeads], q_scale[kHeads];
+    SplitShared<threads_of<FP8>()> split;
+    uint32_t tmem, stop;
+};
+
+__device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 1u : 2u; }
+// First panel of group g within a tile.
+__device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g - 1u; }
+
+// Do any of the softmax threads say yes?
+__device__ __forceinline__ bool any_softmax(bool mine) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)mine)
+        : "memory");
+    return all != 0;
+}
+
+// A workspace slot: `rows` x 512 sums, then their maxima and sums of weights,
+// in whole 16-byte vectors.
+__host__ __device__ __forceinline__ uint32_t slot_floats(uint32_t rows) {
+    return (rows * (kLatent + 2) + 3u) & ~3u;
+}
+__device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32_t s) {
+    return reinterpret_cast<float*>(a.workspace + kMaxCtas * sizeof(OpenPiece)) +
+           (uint64_t)(2 * cta + s) * slot_floats(a.slot_rows);
+}
+
+// ---------------------------------------------------------------- feeding
+
+template <bool FP8, bool WITHHOLD>
+__device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
+                                     Smem<FP8>& sm) {
+    constexpr uint32_t kSlots = FP8 ? kRawSlots : 2 * kGroups;
+    const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
+    uint64_t* full = FP8 ? sm.raw_full : sm.full;
+    uint64_t* empty = FP8 ? sm.raw_empty : sm.empty;
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    RingPos<(int)kSlots> at;
+    uint32_t bad_page = 0, issued = 0, tile = 0, segment = 0;
+    bool ok = true;
+    while (ok && !w.done()) {
+        ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_ns);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
+        __syncwarp();
+        if (lane < 9) {
+            const uint32_t dst = smem_addr(sm.q + lane * kPanel), bar = smem_addr(&sm.q_full);
+            if (lane == 0)
+                tma_3d(dst, &qm.rope, 0, hb * kHeads, w.t, bar);
+            else
+                tma_3d(dst, &qm.latent, (lane - 1) * 64, hb * kHeads, w.t, bar);
+        }
+        ++segment;
+        for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
+            const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
+            UnitCopy copy[2];
+            uint64_t there = 0;
+            uint32_t n = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                copy[h].level = 4;
+                if (h && maps.log_rows) continue;
+                copy[h] = plan_unit(maps, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
+                                    p_tile, w.span.start, w.span.hi, lane + 32u * h);
+                if (copy[h].bad_page) bad_page = 1;
+                n += __popc(__ballot_sync(0xffffffffu, copy[h].there != 0));
+                there |= copy[h].there;
+            }
+            const uint32_t t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
+            const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+#pragma unroll 1
+            for (uint32_t g = 0; g < kGroups; ++g) {
+                ok = wait_phase(&empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
+                if (!ok) break;
+                const uint32_t panels = FP8 ? 1u : group_panels(g);
+                if (lane == 0) {
+                    if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
+                    mbar_arrive_expect_tx(&full[at.slot], (n << maps.log_rows) * 128u * panels);
+                }
+                __syncwarp();
+                if (!(WITHHOLD && issued == 0)) {
+                    const uint32_t bar = smem_addr(&full[at.slot]);
+                    const uint32_t base =
+                        FP8 ? smem_addr(sm.raw + at.slot * kPanel)
+                            : smem_addr(sm.kv + ((tile & 1u) * 9 + group_start(g)) * kPanel);
+                    const uint32_t col = g == 0 ? kLatent : (g - 1) * 128u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (copy[h].level == 4) continue;
+                        const uint32_t dst = base + ((lane + 32u * h) << maps.log_rows) * 128u;
+                        for (uint32_t x = 0; x < panels; ++x)
+                            tma_rows(dst + x * kPanel, &maps.map[copy[h].level], col + x * 64u, 0,
+                                     copy[h].row, copy[h].page, 0, bar);
+                    }
+                }
+                at.step();
+                ++issued;
+            }
+        }
+        if (ok) w.next(a.split);
+    }
+    if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
+    if (!ok) {
+        // copies still under way land in this CTA's memory: wait for them (a
+        // bounded time) before the CTA may end
+        if (lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+        const uint32_t n = issued < kSlots ? issued : kSlots;
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint32_t x = issued - 1 - i;
+            mbar_wait(&full[x % kSlots], (x / kSlots) & 1u, a.wait_ns);
+        }
+        if (segment) mbar_wait(&sm.q_full, (segment - 1) & 1u, a.wait_ns);
+    }
+}
+
+// ---------------------------------------------------------------- converting
+
+// Codes of a group -> fp16 panels in the operands' layout; positions that are
+// not there become zeros.
+__device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
+    const uint32_t lane = threadIdx.x & 31u, i0 = threadIdx.x - 192u;
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    RingPos<(int)kRawSlots> at;
+    uint32_t tile = 0;
+    bool ok = true;
+    while (ok && !w.done()) {
+        for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
+#pragma unroll 1
+            for (uint32_t g = 0; g < kGroups; ++g) {
+                ok = wait_phase(&sm.raw_full[at.slot], at.parity, &sm.stop, a.wait_ns) &&
+                     wait_phase(&sm.empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_ns);
+                if (!ok) break;
+                const uint64_t there = sm.there[tile & 7u];
+                const unsigned char* src = sm.raw + at.slot * kPanel;
+                unsigned char* dst = sm.kv + group_start(g) * kPanel;
+                const uint32_t c = i0 & 7u;
+                if (g > 0 || c < 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t r = (i0 >> 3) + 16u * k;
+                        v[k] = *reinterpret_cast<const uint4*>(src + r * 128u +
+                                                               (((c ^ r) & 7u) << 4));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t r = (i0 >> 3) + 16u * k;
+                        if (!((there >> r) & 1ull)) v[k] = make_uint4(0, 0, 0, 0);
+                        uint4 x, y;
+                        codes_to_f16(v[k].x, x.x, x.y);
+                        codes_to_f16(v[k].y, x.z, x.w);
+                        codes_to_f16(v[k].z, y.x, y.y);
+                        codes_to_f16(v[k].w, y.z, y.w);
+                        // 16 codes are two chunks of the row's line; chunks 4-7
+                        // of the codes go to the second panel and store their
+                        // odd chunk first, so that the eight lanes of a row
+                        // hit distinct banks
+                        const uint32_t o = 2u * (c & 3u), odd = c >> 2;
+                        unsigned char* line = dst + (c >> 2) * kPanel + r * 128u;
+                        *reinterpret_cast<uint4*>(line + (((o + odd) ^ (r & 7u)) << 4)) =
+                            odd ? y : x;
+                        *reinterpret_cast<uint4*>(line + (((o + (odd ^ 1u)) ^ (r & 7u)) << 4)) =
+                            odd ? x : y;
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.full[g]);
+                    mbar_arrive(&sm.raw_empty[at.slot]);
+                }
+                at.step();
+            }
+        }
+        if (ok) w.next(a.split);
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+template <bool FP8>
+__device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
+    constexpr uint32_t kBufs = FP8 ? 1 : 2;
+    const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB, tmem = sm.tmem;
+    const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
+    const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
+    const uint32_t qk_instr = f16_instr(!FP8, 0, 0, kHeads, kTile);
+    const uint32_t pv_instr = f16_instr(!FP8, 1, 0, 128, cols);
+    const uint64_t q_desc = operand_desc(smem_addr(sm.q), 0);
+    const uint64_t k_desc = operand_desc(smem_addr(sm.kv), 0);
+    const uint64_t v_desc = operand_desc(smem_addr(sm.kv), kPanel);
+    const uint64_t p_desc = operand_desc(smem_addr(sm.p), 0);
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    bool ok = true;
+    uint32_t tile = 0, segment = 0;
+
+    // S of tile n
+    auto scores = [&](uint32_t n, bool last) {
+        const uint32_t buf = n & 1u, kv = n % kBufs;
+        if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
+        fence_after_sync();
+#pragma unroll 1
+        for (uint32_t g = 0; g < kGroups; ++g) {
+            const uint32_t slot = kv * kGroups + g;
+            if (!wait_phase(&sm.full[slot], (n / kBufs) & 1u, &sm.stop, a.wait_ns)) return false;
+            fence_after_sync();
+            if (lane == 0) {
+                const uint32_t panel = group_start(g);
+                for (uint32_t x = 0; x < group_panels(g); ++x)
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(tmem + kScoreColumn + buf * kTile,
+                                   q_desc + (((panel + x) * kPanel + ks * 32u) >> 4),
+                                   k_desc + (((kv * 9 + panel + x) * kPanel + ks * 32u) >> 4),
+                                   qk_instr, g > 0 || x > 0 || ks > 0);
+                if (g == 0) mma_commit(&sm.empty[slot]);  // the rotated columns are done with
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            mma_commit(&sm.s_full[buf]);
+            if (last) mma_commit(&sm.q_free);
+        }
+        __syncwarp();
+        return true;
+    };
+    // O^T (+)= V^T P^T of tile n
+    auto values = [&](uint32_t n, bool first, uint32_t seg) {
+        const uint32_t kv = n % kBufs;
+        if (first && !wait_phase(&sm.o_free, (seg & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
+        if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_ns)) return false;
+        fence_after_sync();
+        if (lane == 0) {
+#pragma unroll 1
+            for (uint32_t j = 0; j < 4; ++j) {
+#pragma unroll
+                for (uint32_t ks = 0; ks < 4; ++ks)
+                    mma_f16_ss(tmem + j * kHeads,
+                               v_desc + (((kv * 9 + 1 + 2 * j) * kPanel + ks * 2048u) >> 4),
+                               p_desc + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
+                mma_commit(&sm.empty[kv * kGroups + 1 + j]);
+            }
+            mma_commit(&sm.pv_done);
+        }
+        __syncwarp();
+        return true;
+    };
+
+    bool pending = false, pending_first = false;
+    while (ok && !w.done()) {
+        const uint32_t count = w.last - w.first;
+        for (uint32_t i = 0; ok && i < count; ++i, ++tile) {
+            if (i == 0) {
+                if (pending) ok = values(tile - 1, pending_first, segment - 1);
+                pending = false;
+                ok = ok && wait_phase(FP8 ? &sm.q_ready : &sm.q_full, segment & 1u, &sm.stop,
+                                      a.wait_ns);
+                if (!ok) break;
+            }
+            ok = scores(tile, i + 1 == count);
+            if (!ok) break;
+            if constexpr (kBufs == 2) {
+                if (pending) ok = values(tile - 1, pending_first, segment);
+                pending = true;
+                pending_first = i == 0;
+            } else {
+                ok = values(tile, i == 0, segment);
+            }
+        }
+        ++segment;
+        w.next(a.split);
+    }
+    if (ok && pending) ok = values(tile - 1, pending_first, segment - 1);
+    if (!ok) {
+        // let what was issued finish before tensor and shared memory go
+        if (lane == 0) {
+            flag(a.err_flags, KVW_ERR_TIMEOUT);
+            mma_commit(&sm.drained);
+        }
+        __syncwarp();
+        mbar_wait(&sm.drained, 0, a.wait_ns);
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+
+// The queries of a segment from bf16 to fp16 in place, each row brought into
+// fp16's range by a power of two; two threads to a row.
+__device__ __forceinline__ void convert_queries(Smem<true>& sm) {
+    const uint32_t r = threadIdx.x >> 1, part = threadIdx.x & 1u;
+    uint32_t top = 0;
+    for (uint32_t p = 0; p < 9; ++p)
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                sm.q + p * kPanel + r * 128u + (((part * 4 + c) ^ (r & 7u)) << 4));
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top & 0xffffu, top >> 16);
+    float up, down;
+    row_power(top, up, down);
+    for (uint32_t p = 0; p < 9; ++p)
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(sm.q + p * kPanel + r * 128u +
+                                                 (((part * 4 + c) ^ (r & 7u)) << 4));
+            uint4 v = *at;
+            v.x = pack2<true>(bf16_lo(v.x) * up, bf16_hi(v.x) * up);
+            v.y = pack2<true>(bf16_lo(v.y) * up, bf16_hi(v.y) * up);
+            v.z = pack2<true>(bf16_lo(v.z) * up, bf16_hi(v.z) * up);
+            v.w = pack2<true>(bf16_lo(v.w) * up, bf16_hi(v.w) * up);
+            *at = v;
+        }
+    if (part == 0) sm.q_scale[r] = down;
+}
+
+template <bool FP8>
+__device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    const uint32_t quad = lane >> 2, in_quad = lane & 3u, hb = blockIdx.x % a.HB;
+    const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
+    const uint32_t head0 = hb * kHeads, tmem = sm.tmem + ((warp * 32u) << 16);
+    // this thread's rows of S: heads h0 and h0 + 8, 16 positions of each
+    const uint32_t h0 = warp * 16u + quad;
+    OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    bool ok = true;
+    uint32_t tile = 0, segment = 0;
+    while (!w.done()) {
+        if ((int64_t)w.len0 + w.k + 1 > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
+        float qs0 = a.scale, qs1 = a.scale;
+        if constexpr (FP8) {
+            ok = wait_phase(&sm.q_full, segment & 1u, &sm.stop, a.wait_ns);
+            if (ok) convert_queries(sm);
+            fence_async_smem();
+            if (any_softmax(!ok)) break;  // q_scale is written
+            qs0 = fmaxf(a.scale * sm.q_scale[h0], 1.17549435e-38f);
+            qs1 = fmaxf(a.scale * sm.q_scale[h0 + 8], 1.17549435e-38f);
+            if (lane == 0) mbar_arrive(&sm.q_ready);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        const uint32_t count = w.last - w.first;
+        bool stopped = false;
+        for (uint32_t i = 0; i < count; ++i, ++tile) {
+            const uint32_t buf = tile & 1u;
+            float s[32];
+            ok = ok && wait_phase(&sm.s_full[buf], (tile >> 1) & 1u, &sm.stop, a.wait_ns);
+            if (ok) {
+                fence_after_sync();
+                tmem_ld_16x64(s, tmem + kScoreColumn + buf * kTile);
+                fence_before_sync();
+                if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] = 0.0f;
+            }
+            const uint64_t there = sm.there[tile & 7u];
+            if (there != ~0ull) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const uint32_t j = 8u * (e >> 2) + 2u * in_quad + (e & 1);
+                    if (!((there >> j) & 1ull)) s[e] = -INFINITY;
+                }
+            }
+            float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                top0 = fmaxf(top0, fmaxf(s[e], s[e + 1]));
+                top1 = fmaxf(top1, fmaxf(s[e + 2], s[e + 3]));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+                top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+            }
+            top0 *= qs0;
+            top1 *= qs1;
+            if (any_softmax(!ok || top0 > m0 + kSlack || top1 > m1 + kSlack)) {
+                const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+                const float f0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0);
+                const float f1 = n1 == m1 ? 1.0f : fast_exp2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+                if (in_quad == 0) {
+                    sm.alpha[h0] = f0;
+                    sm.alpha[h0 + 8] = f1;
+                }
+                if (i > 0)
+                    ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+                if (any_softmax(!ok)) {  // the alphas are written
+                    stopped = true;
+                    break;
+                }
+                if (i > 0) {
+                    fence_after_sync();
+                    for (uint32_t c = 0; c < rows; c += 16) {
+                        float f[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = sm.alpha[c + e];
+#pragma unroll
+                        for (uint32_t j = 0; j < 4; ++j) {
+                            float o[16];
+                            tmem_ld_32x16(o, tmem + j * kHeads + c);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f[e];
+                            tmem_st_32x16(tmem + j * kHeads + c, o);
+                        }
+                    }
+                    tmem_st_wait();
+                    fence_before_sync();
+                }
+            }
+            // a row that has seen no position keeps m = -inf: subtract 0
+            const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x0 = fast_exp2(fmaf(s[4 * e], qs0, -b0));
+                const float x1 = fast_exp2(fmaf(s[4 * e + 1], qs0, -b0));
+                const float y0 = fast_exp2(fmaf(s[4 * e + 2], qs1, -b1));
+                const float y1 = fast_exp2(fmaf(s[4 * e + 3], qs1, -b1));
+                l0 += x0 + x1;
+                l1 += y0 + y1;
+                p[2 * e] = pack2<FP8>(x0, x1);
+                p[2 * e + 1] = pack2<FP8>(y0, y1);
+            }
+            if (tile > 0)  // P's memory is free
+                ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+            if (ok) {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e) {
+                    const uint32_t chunk = ((e ^ (h0 & 7u)) << 4) + in_quad * 4u;
+                    *reinterpret_cast<uint32_t*>(sm.p + h0 * 128u + chunk) = p[2 * e];
+                    *reinterpret_cast<uint32_t*>(sm.p + (h0 + 8u) * 128u + chunk) = p[2 * e + 1];
+                }
+                if constexpr (!FP8) {
+                    // a weight of 0 does not keep out what a row that is not
+                    // there may hold
+                    if (there != ~0ull) {
+                        unsigned char* kv = sm.kv + ((tile & 1u) * 9 + 1) * kPanel;
+                        for (uint32_t x = tid; x < 64 * 64; x += kSoftmaxThreads) {
+                            const uint32_t r = x >> 6, c = x & 63u;
+                            if (!((there >> r) & 1ull))
+                                *reinterpret_cast<uint4*>(kv + (c >> 3) * kPanel + r * 128u +
+                                                          (c & 7u) * 16u) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full);
+            }
+        }
+        if (stopped) break;
+        // ---- the segment's results
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+        }
+        if (in_quad == 0) {
+            sm.m[h0] = m0;
+            sm.m[h0 + 8] = m1;
+            sm.l[h0] = l0;
+            sm.l[h0 + 8] = l1;
+        }
+        ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+        if (any_softmax(!ok)) break;
+        fence_after_sync();
+        const bool whole = w.whole();
+        float* part = slot_of(a, blockIdx.x, w.first == 0 ? 1 : 0);
+        uint16_t* out = a.out + ((uint64_t)w.t * a.H + head0) * kLatent;
+        for (uint32_t c = 0; c < rows; c += 16) {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                float o[16];
+                tmem_ld_32x16(o, tmem + j * kHeads + c);
+#pragma unroll
+                for (uint32_t e = 0; e < 16; ++e) {
+                    const uint32_t h = c + e;
+                    if (h >= rows) break;
+                    const uint64_t at = (uint64_t)h * kLatent + j * 128u + tid;
+                    if (whole) {
+                        const float l = sm.l[h], inv = l == 0.0f ? 0.0f : a.row_scale / l;
+                        out[at] = (uint16_t)(pack_bf16x2(o[e] * inv, 0.0f) & 0xffffu);
+                    } else {
+                        part[at] = o[e];
+                    }
+                }
+            }
+        }
+        fence_before_sync();
+        if (tid < rows) {
+            const float l = sm.l[tid], m = sm.m[tid];
+            if (whole) {
+                if (a.lse)
+                    a.lse[(uint64_t)w.t * a.H + head0 + tid] =
+                        l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else {
+                part[(uint64_t)a.slot_rows * kLatent + tid] = m;
+                part[(uint64_t)a.slot_rows * (kLatent + 1) + tid] = l;
+            }
+        }
+        if (!whole && w.first == 0 && tid == 0) {
+            open->end = w.end(a.split);
+            open->pieces = sm.split.start.pieces;
+            open->t = w.t;
+            open->tokens = 1;
+            open->block = hb;
+            open->units = sm.split.start.units;
+        }
+        any_softmax(false);  // sm.m, sm.l are read
+        if (lane == 0) mbar_arrive(&sm.o_free);
+        ++segment;
+        w.next(a.split);
+    }
+    if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+}
+
+template <bool FP8, bool WITHHOLD>
+__global__ void __launch_bounds__((threads_of<FP8>()), 1)
+    mla_decode_kernel(const MlaArgs a, const __grid_constant__ CacheMaps maps,
+                      const __grid_constant__ QMaps qm) {
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    Smem<FP8>& sm = *reinterpret_cast<Smem<FP8>*>(dyn);
+    const uint32_t tid = threadIdx.x, warp = tid >> 5;
+    // the join of the pieces may be scheduled; it waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (uint32_t i = 0; i < 2 * kGroups; ++i) {
+            mbar_init(&sm.full[i], FP8 ? 4 : 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (uint32_t i = 0; i < kRawSlots; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], 4);
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_ready, 4);
+        mbar_init(&sm.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
+        }
+        mbar_init(&sm.p_full, 4);
+        mbar_init(&sm.pv_done, 1);
+        mbar_init(&sm.o_free, 4);
+        mbar_init(&sm.drained, 1);
+        sm.stop = 0;
+        mbar_init_fence();
+        prefetch_map(&maps.map[0]);
+        prefetch_map(&qm.latent);
+        prefetch_map(&qm.rope);
+    }
+    if (warp == 5) tmem_alloc(&sm.tmem, kTmemColumns);
+    const bool ok = find_piece(a.split, a.pieces, blockIdx.x / a.HB, sm.split);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (tid == 0) reinterpret_cast<OpenPiece*>(a.workspace)[blockIdx.x].units = 0;
+    if (!ok) {
+        if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
+    } else if (warp < 4) {
+        soften<FP8>(a, sm);
+    } else if (warp == 4) {
+        feed<FP8, WITHHOLD>(a, maps, qm, sm);
+    } else if (warp == 5) {
+        multiply<FP8>(a, sm);
+    } else {
+        if constexpr (FP8) convert(a, sm);
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 5) {
+        fence_after_sync();
+        tmem_free(sm.tmem, kTmemColumns);
+    }
+}
+
+// Joins what piece blockIdx.x / HB left open, four rows a block: weights
+// 2^(m_i - M) of the pieces, then one weighted sum in their order.
+constexpr int kJoinThreads = 512;
+constexpr uint32_t kJoinRows = 4;
+
+__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a) {
+    __shared__ float s_w[kJoinRows][kMaxCtas];
+    __shared__ float s_top[kJoinRows], s_sum[kJoinRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
+    if (open.units == 0) return;
+    const uint32_t rows = a.H - open.block * kHeads < kHeads ? a.H - open.block * kHeads : kHeads;
+    const uint32_t r0 = blockIdx.y * kJoinRows;
+    if (r0 >= rows) return;
+    const uint32_t here = rows - r0 < kJoinRows ? rows - r0 : kJoinRows;
+    const uint32_t piece = blockIdx.x / a.HB, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    const uint32_t n = sharers(open, piece);
+    auto part = [&](uint32_t i) {
+        return slot_of(a, (piece + i) * a.HB + open.block, i == 0 ? 1 : 0);
+    };
+    if (warp < here) {
+        const uint32_t r = r0 + warp;
+        float top = -INFINITY;
+        for (uint32_t i = lane; i < n; i += 32) {
+            const float m = part(i)[(uint64_t)a.slot_rows * kLatent + r];
+            s_w[warp][i] = m;
+            top = fmaxf(top, m);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        for (uint32_t i = lane; i < n; i += 32) {
+            const float f = fast_exp2(s_w[warp][i] - base);
+            s_w[warp][i] = f;
+            l += f * part(i)[(uint64_t)a.slot_rows * (kLatent + 1) + r];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+            s_top[warp] = top;
+            s_sum[warp] = l;
+        }
+    }
+    __syncthreads();
+    const uint32_t rj = tid >> 7, d = (tid & 127u) * 4u;  // 128 threads a row
+    if (rj >= here) return;
+    float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (uint32_t i = 0; i < n; ++i) {
+        const float4 x =
+            *reinterpret_cast<const float4*>(part(i) + (uint64_t)(r0 + rj) * kLatent + d);
+        const float f = s_w[rj][i];
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+    }
+    const uint64_t row = (uint64_t)open.t * a.H + open.block * kHeads + r0 + rj;
+    const float l = s_sum[rj], inv = l == 0.0f ? 0.0f : a.row_scale / l;
+    uint2 y;
+    y.x = pack_bf16x2(o.x * inv, o.y * inv);
+    y.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(a.out + row * kLatent + d) = y;
+    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (s_top[rj] + log2f(l)) * kLn2;
+}
+
+int workspace_bytes_for(uint32_t num_heads, uint64_t* bytes) {
+    if (!bytes || !num_heads) return KVW_EINVAL;
+    if (num_heads > 1024) return KVW_EUNSUPPORTED;
+    const uint32_t rows = num_heads < kHeads ? num_heads : kHeads;
+    *bytes = kMaxCtas * (sizeof(OpenPiece) + 2ull * slot_floats(rows) * sizeof(float));
+    return KVW_OK;
+}
+
+template <bool FP8, bool WITHHOLD>
+cudaError_t launch(MlaArgs& a, const CacheMaps& maps, const QMaps& qm, cudaStream_t stream) {
+    constexpr size_t smem = sizeof(Smem<FP8>);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = prepare_smem<&mla_decode_kernel<FP8, WITHHOLD>>(smem);
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    if ((e = sm_count(sms)) != cudaSuccess) return e;
+    uint32_t ctas = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
+    a.pieces = ctas / a.HB > 0 ? ctas / a.HB : 1;
+    ctas = a.pieces * a.HB;
+    mla_decode_kernel<FP8, WITHHOLD><<<ctas, threads_of<FP8>(), smem, stream>>>(a, maps, qm);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mla_join_kernel, a);
+}
+
+int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_stride,
+              const void* q_rope, int64_t q_rope_row_stride, const uint32_t* input_row_offsets,
+              uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_heads,
+              const kvw_paged_cache_t* cache, uint32_t layer_idx, float sm_scale, void* workspace,
+              uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream, bool withhold,
+              uint64_t wait_ns) {
+    const int st = check_cache(cache, layer_idx, 1);
+    if (st != KVW_OK) return st;
+    uint64_t need = 0;
+    const int ws = workspace_bytes_for(num_heads, &need);
+    if (ws != KVW_OK) return ws;
+    if (cache->num_heads != 1 || cache->head_size != kRow) return KVW_EUNSUPPORTED;
+    if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20)) return KVW_EUNSUPPORTED;
+    if (!out || !q_latent || !q_rope || !input_row_offsets || num_batches == 0 || !workspace ||
+        workspace_bytes < need)
+        return KVW_EINVAL;
+    if (!aligned16(out) || !aligned16(q_latent) || !aligned16(q_rope) || !aligned16(workspace) ||
+        !aligned4(lse) || !aligned4(input_row_offsets) || !aligned4(err_flags))
+        return KVW_EINVAL;
+    if (!tma_strides_ok(cache, 1)) return KVW_EINVAL;
+    const int64_t top = 1ll << 39;  // bytes below 2^40
+    if (q_latent_row_stride < (int64_t)num_heads * kLatent || q_latent_row_stride % 8 ||
+        q_latent_row_stride >= top || q_rope_row_stride < (int64_t)num_heads * 64 ||
+        q_rope_row_stride % 8 || q_rope_row_stride >= top)
+        return KVW_EINVAL;
+    if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return KVW_EINVAL;
+    if (tot_seq_len == 0) return KVW_OK;
+
+    const bool fp8 = cache->dtype == KVW_DTYPE_FP8_E4M3;
+    MlaArgs a = {};
+    a.split.offsets = input_row_offsets;
+    a.split.cache_lengths = cache->cache_lengths;
+    a.split.B = num_batches;
+    a.split.T = tot_seq_len;
+    a.split.blocks = 1;  // the row blocks of a token are CTAs of the same piece
+    a.split.min_units = 1;
+    a.split.overhead = 2;
+    const uint64_t reach = (uint64_t)cache->max_pages_per_seq * cache->page_size;
+    a.split.cap = reach > kMaxReach ? (int64_t)kMaxReach : (int64_t)reach;
+    a.split.window = 1ll << 40;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.page_table = cache->page_table;
+    a.err_flags = err_flags;
+    a.workspace = static_cast<unsigned char*>(workspace);
+    a.row_scale = fp8 ? cache->scale : 1.0f;
+    a.scale = sm_scale * kLog2e * a.row_scale;
+    a.H = num_heads;
+    a.HB = (num_heads + kHeads - 1) / kHeads;
+    a.slot_rows = num_heads < kHeads ? num_heads : kHeads;
+    a.num_pages = cache->num_pages;
+    a.max_pages = cache->max_pages_per_seq;
+    a.ps = make_fast_div(cache->page_size);
+    a.wait_ns = wait_ns;
+    CacheMaps maps;
+    QMaps qm;
+    int e = encode_cache_maps(&maps, cache, layer_idx, 1);
+    if (e == KVW_OK)
+        e = encode_query_map(&qm.latent, q_latent, kLatent, num_heads, tot_seq_len,
+                             q_latent_row_stride);
+    if (e == KVW_OK)
+        e = encode_query_map(&qm.rope, q_rope, 64, num_heads, tot_seq_len, q_rope_row_stride);
+    if (e != KVW_OK) return e;
+    cudaError_t r;
+#ifdef KVW_TEST_HOOKS
+    if (withhold)
+        r = fp8 ? launch<true, true>(a, maps, qm, stream) : launch<false, true>(a, maps, qm, stream);
+    else
+#else
+    if (withhold) return KVW_EUNSUPPORTED;
+#endif
+        r = fp8 ? launch<true, false>(a, maps, qm, stream)
+                : launch<false, false>(a, maps, qm, stream);
+    return r == cudaSuccess ? KVW_OK : KVW_ECUDA;
+}
+
+}  // namespace
+}  // namespace kvw
+
+extern "C" int kva_mla_decode_workspace(uint32_t num_heads, uint64_t* bytes) {
+    return kvw::workspace_bytes_for(num_heads, bytes);
+}
+
+extern "C" int kva_mla_decode_paged(void* out, float* lse, const void* q_latent,
+                                    int64_t q_latent_row_stride, const void* q_rope,
+                                    int64_t q_rope_row_stride, const uint32_t* input_row_offsets,
+                                    uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_heads,
+                                    const kvw_paged_cache_t* cache, uint32_t layer_idx,
+                                    float sm_scale, void* workspace, uint64_t workspace_bytes,
+                                    uint32_t* err_flags, cudaStream_t stream) {
+    return kvw::mla_entry(out, lse, q_latent, q_latent_row_stride, q_rope, q_rope_row_stride,
+                          input_row_offsets, num_batches, tot_seq_len, num_heads, cache, layer_idx,
+                          sm_scale, workspace, workspace_bytes, err_flags, stream, false,
+                          kvw::kWaitLimitNs);
+}
+
+#ifdef KVW_TEST_HOOKS
+// Test builds only (a separate library; the product has no such symbol): the
+// first copies of every CTA are announced on their barrier but never made, and
+// every wait is bounded by `wait_ns`, so the waits for them run out,
+// KVW_ERR_TIMEOUT is set and the kernel returns.
+extern "C" int kva_test_mla_decode_withheld(
+    void* out, const void* q_latent, int64_t q_latent_row_stride, const void* q_rope,
+    int64_t q_rope_row_stride, const uint32_t* input_row_offsets, uint32_t num_batches,
+    uint32_t tot_seq_len, uint32_t num_heads, const kvw_paged_cache_t* cache, uint32_t layer_idx,
+    void* workspace, uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream,
+    uint64_t wait_ns) {
+    return kvw::mla_entry(out, nullptr, q_latent, q_latent_row_stride, q_rope, q_rope_row_stride,
+                          input_row_offsets, num_batches, tot_seq_len, num_heads, cache, layer_idx,
+                          0.1f, workspace, workspace_bytes, err_flags, stream, true, wait_ns);
+}
+#endif

@@ -28,6 +28,9 @@ def _declare(L):
         "kva_gqa_decode_paged": [vp, vp, vp, i64, vp, u32, u32, u32, pc, f32, u32, f32, f32, u32,
                                  vp, vp, u64, vp, vp],
         "kva_gqa_decode_workspace": [u32, u32, u32, pu64],
+        "kva_mla_decode_paged": [vp, vp, vp, i64, vp, i64, vp, u32, u32, u32, pc, u32, f32, vp,
+                                 u64, vp, vp],
+        "kva_mla_decode_workspace": [u32, pu64],
     }.items():
         f = getattr(L, name)
         f.restype, f.argtypes = i, args
@@ -104,3 +107,30 @@ def kva_gqa_decode_paged(out, q, input_row_offsets, cache: PagedCacheT, layer_id
         v_scale, layer_idx, sm_scale, softcap, window, _ptr(alibi_slopes), _ptr(workspace), nb,
         _ptr(err_flags), _stream(stream))
     return _done(st, "kva_gqa_decode_paged", check)
+
+
+def kva_mla_decode_workspace(num_heads: int) -> int:
+    """Bytes of workspace :func:`kva_mla_decode_paged` needs."""
+    n = ctypes.c_uint64()
+    _done(lib.kva_mla_decode_workspace(num_heads, ctypes.byref(n)), "kva_mla_decode_workspace",
+          True)
+    return n.value
+
+
+def kva_mla_decode_paged(out, q_latent, q_rope, input_row_offsets, cache: PagedCacheT,
+                         layer_idx: int, sm_scale: float, workspace, lse=None, err_flags=None,
+                         stream=None, *, num_batches=None, tot_seq_len=None, num_heads=None,
+                         q_latent_row_stride=None, q_rope_row_stride=None, workspace_bytes=None,
+                         check=True) -> int:
+    """``out``, ``q_latent`` [tokens, heads, 512], ``q_rope`` [tokens, heads, 64]."""
+    B = input_row_offsets.shape[0] - 1 if num_batches is None else num_batches
+    T = q_latent.shape[0] if tot_seq_len is None else tot_seq_len
+    H = q_latent.shape[1] if num_heads is None else num_heads
+    ls = q_latent.stride(0) if q_latent_row_stride is None else q_latent_row_stride
+    rs = q_rope.stride(0) if q_rope_row_stride is None else q_rope_row_stride
+    nb = _size(workspace) if workspace_bytes is None else workspace_bytes
+    st = lib.kva_mla_decode_paged(
+        _ptr(out), _ptr(lse), _ptr(q_latent), ls, _ptr(q_rope), rs, _ptr(input_row_offsets), B, T,
+        H, ctypes.byref(cache), layer_idx, sm_scale, _ptr(workspace), nb, _ptr(err_flags),
+        _stream(stream))
+    return _done(st, "kva_mla_decode_paged", check)

@@ -8,19 +8,21 @@
  *                            and values to the paged cache
  *   kva_gqa_decode_paged     attention of each new token's query heads over
  *                            its request's paged keys and values
- * One step of a layer is an append followed by the decode call, on one
- * stream.
+ *   kva_mla_decode_paged     the same over the paged latent cache (absorbed
+ *                            queries, one 576-wide row for all heads)
+ * One step of a layer is append (GQA) or kvw_mla_rope_rmsnorm_quant (MLA)
+ * followed by the decode call, on one stream.
  *
  * Conventions: those of kvw.h (asynchronous, caller-owned pointers, host
  * argument errors returned before any launch, device data errors reported as
  * KVW_ERR_* bits in *err_flags, ragged batches through input_row_offsets),
- * and for the attention call:
- * - It enqueues two kernels on `stream`: the attention, split over the
+ * and for the two attention calls:
+ * - They enqueue two kernels on `stream`: the attention, split over the
  *   contexts of all tokens so that every CTA reads the same amount of cache,
  *   and a join of the pieces.  The split depends only on the lengths, the
  *   sizes and the device, so equal calls give equal bits.
  * - `workspace` (device, 16-byte aligned) holds the pieces between the two
- *   kernels.  Its size depends on the sizes alone (the *_workspace call),
+ *   kernels.  Its size depends on the sizes alone (the *_workspace calls),
  *   not on the batch or the lengths.  Its contents need no preparation and
  *   mean nothing after the call.  Calls that may run at the same time (two
  *   streams, two graphs replayed together) need a workspace each; calls
@@ -133,6 +135,39 @@ int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_t q_row_str
 /* Bytes of workspace for kva_gqa_decode_paged, into *bytes (host). */
 int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_size,
                              uint64_t* bytes);
+
+/*
+ * Attention of new tokens over the paged MLA latent cache, with queries
+ * absorbed into the latent space.  For token t at position p and head h,
+ * with row_j the 576-wide cache row of position j (code * scale for E4M3):
+ *   s_j = sm_scale * (dot(q_latent[t, h], row_j[0:512])
+ *                     + dot(q_rope[t, h], row_j[512:576]))
+ *   out[t, h] = bf16(sum_j e^s_j row_j[0:512] / sum_j e^s_j)
+ *   lse[t, h] = log(sum_j e^s_j)
+ * over positions 0 .. p.  Precision as kva_gqa_decode_paged.
+ *
+ *   out            device, bf16 [tot_seq_len, num_heads, 512]
+ *   lse            device, f32 [tot_seq_len, num_heads], or NULL
+ *   q_latent       device, bf16, token t at q_latent + t*q_latent_row_stride
+ *                  elements, its heads 512 apart (stride >= num_heads*512,
+ *                  multiple of 8)
+ *   q_rope         device, bf16, the same with 64 (the q_rope_out of
+ *                  kvw_mla_rope_rmsnorm_quant has stride num_heads*64)
+ *   cache          host pointer: bf16 or E4M3, num_heads 1, head_size 576
+ *   workspace      device, kva_mla_decode_workspace(...) bytes
+ * 1 <= num_heads <= 1024, tot_seq_len <= 2^20.  The matrix unit's stages
+ * complete through bounded waits: KVW_ERR_TIMEOUT as in kvw.h.
+ */
+int kva_mla_decode_paged(void* out, float* lse, const void* q_latent,
+                         int64_t q_latent_row_stride, const void* q_rope,
+                         int64_t q_rope_row_stride, const uint32_t* input_row_offsets,
+                         uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_heads,
+                         const kvw_paged_cache_t* cache, uint32_t layer_idx, float sm_scale,
+                         void* workspace, uint64_t workspace_bytes, uint32_t* err_flags,
+                         cudaStream_t stream);
+
+/* Bytes of workspace for kva_mla_decode_paged, into *bytes (host). */
+int kva_mla_decode_workspace(uint32_t num_heads, uint64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -29,7 +29,8 @@ def test_header_compiles_as_c(tmp_path):
         pytest.skip("no nvcc")
     src = tmp_path / "use.c"
     src.write_text('#include "kva.h"\nint main(void) { uint64_t n = 0;\n'
-                   '  return kva_gqa_decode_workspace(32, 8, 128, &n) != KVW_OK || n == 0; }\n')
+                   '  return kva_gqa_decode_workspace(32, 8, 128, &n) != KVW_OK || n == 0 ||\n'
+                   '         kva_mla_decode_workspace(128, &n) != KVW_OK; }\n')
     exe, where = str(tmp_path / "use"), os.path.dirname(kvw.LIB_PATH)
     subprocess.run([nvcc, str(src), "-I", os.path.dirname(kva.HEADER), "-L", where, "-lkvw",
                     "-Xlinker", "-rpath=" + where, "-o", exe], check=True, capture_output=True)
@@ -175,3 +176,63 @@ def test_gqa_workspace_is_exact():
             kva.kva_gqa_decode_workspace(*args)
     assert gqa(None) == kvw.KVW_EINVAL
     assert gqa(cache(dtype=kvw.DTYPE_FP8_E4M3), vs=0.0) == kvw.KVW_EINVAL
+
+
+def mla_cache(**kw):
+    d = dict(num_heads=1, head_size=576, strides=(2 * 16 * 576, 0, 16 * 576, 576, 576))
+    d.update(kw)
+    return cache(**d)
+
+
+def mla(c, **kw):
+    a = dict(out=FAKE, lse=None, ql=FAKE, qls=16 * 512, qr=FAKE, qrs=16 * 64, off=FAKE, B=2, T=0,
+             H=16, layer=1, scale=0.1, ws=FAKE, nbytes=1 << 30, err=None)
+    a.update(kw)
+    return kva.lib.kva_mla_decode_paged(
+        a["out"], a["lse"], a["ql"], a["qls"], a["qr"], a["qrs"], a["off"], a["B"], a["T"], a["H"],
+        None if c is None else ctypes.byref(c), a["layer"], a["scale"], a["ws"], a["nbytes"],
+        a["err"], 0)
+
+
+@pytest.mark.parametrize("call_kw,want", [
+    ({}, kvw.KVW_OK), ({"lse": FAKE}, kvw.KVW_OK), ({"qls": 16 * 512 + 8, "qrs": 4096}, kvw.KVW_OK),
+    ({"out": None}, kvw.KVW_EINVAL), ({"out": ODD}, kvw.KVW_EINVAL),
+    ({"ql": None}, kvw.KVW_EINVAL), ({"ql": ODD}, kvw.KVW_EINVAL),
+    ({"qr": None}, kvw.KVW_EINVAL), ({"qr": ODD}, kvw.KVW_EINVAL),
+    ({"lse": ODD4}, kvw.KVW_EINVAL), ({"off": None}, kvw.KVW_EINVAL),
+    ({"err": ODD4}, kvw.KVW_EINVAL), ({"qls": 16 * 512 - 8}, kvw.KVW_EINVAL),
+    ({"qls": 16 * 512 + 4}, kvw.KVW_EINVAL), ({"qrs": 16 * 64 - 8}, kvw.KVW_EINVAL),
+    ({"qrs": 16 * 64 + 4}, kvw.KVW_EINVAL), ({"qls": 1 << 39}, kvw.KVW_EINVAL),
+    ({"B": 0}, kvw.KVW_EINVAL), ({"B": 8193}, kvw.KVW_EUNSUPPORTED),
+    ({"T": (1 << 20) + 1}, kvw.KVW_EUNSUPPORTED), ({"H": 0}, kvw.KVW_EINVAL),
+    ({"H": 1025, "qls": 1 << 20, "qrs": 1 << 20}, kvw.KVW_EUNSUPPORTED),
+    ({"scale": 0.0}, kvw.KVW_EINVAL), ({"scale": float("nan")}, kvw.KVW_EINVAL),
+    ({"ws": None}, kvw.KVW_EINVAL), ({"ws": ODD}, kvw.KVW_EINVAL),
+    ({"nbytes": 1000}, kvw.KVW_EINVAL), ({"layer": 2}, kvw.KVW_EINVAL),
+])
+def test_mla_refusals(call_kw, want):
+    assert mla(mla_cache(), **call_kw) == want
+
+
+@pytest.mark.parametrize("cache_kw,want", CACHE_FAULTS + [
+    ({"num_heads": 2}, kvw.KVW_EUNSUPPORTED), ({"head_size": 512}, kvw.KVW_EUNSUPPORTED),
+    ({"strides": (2 * 16 * 576, 0, 16 * 576, 580, 576)}, kvw.KVW_EINVAL),
+    ({"strides": (2 * 16 * 576, 0, 16 * 576, -576, 576)}, kvw.KVW_EINVAL),
+    ({"strides": (1 << 39, 0, 16 * 576, 576, 576)}, kvw.KVW_EINVAL),
+])
+def test_mla_cache_refusals(cache_kw, want):
+    assert mla(mla_cache(**cache_kw)) == want
+
+
+def test_mla_workspace_is_exact():
+    for heads in (1, 16, 128):
+        n = kva.kva_mla_decode_workspace(heads)
+        kw = dict(H=heads, qls=heads * 512, qrs=heads * 64)
+        assert n % 16 == 0
+        assert mla(mla_cache(), nbytes=n, **kw) == kvw.KVW_OK
+        assert mla(mla_cache(), nbytes=n - 1, **kw) == kvw.KVW_EINVAL
+    assert kva.kva_mla_decode_workspace(64) == kva.kva_mla_decode_workspace(1024)
+    for heads in (0, 1025):
+        with pytest.raises(kvw.KvwError):
+            kva.kva_mla_decode_workspace(heads)
+    assert mla(None) == kvw.KVW_EINVAL
