@@ -6,15 +6,26 @@
 
 namespace kvw {
 
+// One thread of a converged warp, known to the compiler as one: what it
+// issues needs no loop over lanes (120 cycles an MMA without it, 32 to 128
+// with it).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory operand in 128-byte-swizzled lines, 8 lines to a 1024-byte
 // group.  K-major: a line holds 64 contraction elements of one row and groups
 // of 8 rows lie 1024 bytes apart (lead is not used).  MN-major: a line holds
 // 64 rows' elements of one contraction index, groups of 8 indices lie 1024
-// bytes apart, and the next 64 rows `lead` bytes away.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t smem, uint32_t lead) {
-    constexpr uint64_t kVersion = 1ull << 46, kSwizzle128 = 2ull << 61;
-    return kVersion | kSwizzle128 | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)(lead >> 4) << 16) |
-           (uint64_t)((smem & 0x3ffffu) >> 4);
+// bytes apart, and the next 64 rows `lead` bytes away.  The descriptor's low
+// word; the high one is the same for all.  An operand `bytes` further on has
+// the low word plus bytes / 16.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_low(uint32_t smem, uint32_t lead) {
+    return ((lead >> 4) << 16) | ((smem & 0x3ffffu) >> 4);
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, both operands bf16
@@ -24,13 +35,14 @@ constexpr uint32_t f16_instr(bool bf16, uint32_t a_mn, uint32_t b_mn, uint32_t m
            (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// D (+)= A B, one k16 step; one thread issues.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+// D (+)= A B, one k16 step, operands by their low words; one thread issues.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
                                            bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(instr), "r"((uint32_t)accumulate), "n"(kOperandHigh)
         : "memory");
 }
 

@@ -88,8 +88,8 @@ struct Smem {
     uint32_t tmem, stop;
 };
 
+// Panels of group g, and its first one within a tile.
 __device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 1u : 2u; }
-// First panel of group g within a tile.
 __device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g - 1u; }
 
 // Do any of the softmax threads say yes?
@@ -272,15 +272,15 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
 template <bool FP8>
 __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     constexpr uint32_t kBufs = FP8 ? 1 : 2;
-    const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB, tmem = sm.tmem;
+    const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
     const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
     const uint32_t qk_instr = f16_instr(!FP8, 0, 0, kHeads, kTile);
     const uint32_t pv_instr = f16_instr(!FP8, 1, 0, 128, cols);
-    const uint64_t q_desc = operand_desc(smem_addr(sm.q), 0);
-    const uint64_t k_desc = operand_desc(smem_addr(sm.kv), 0);
-    const uint64_t v_desc = operand_desc(smem_addr(sm.kv), kPanel);
-    const uint64_t p_desc = operand_desc(smem_addr(sm.p), 0);
+    const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
+    const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
+    const uint32_t v_op = operand_low(smem_addr(sm.kv), kPanel);
+    const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
     Walk w;
     w.begin(a.split, sm.split.start);
     bool ok = true;
@@ -291,29 +291,29 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
         const uint32_t buf = n & 1u, kv = n % kBufs;
         if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
         fence_after_sync();
-#pragma unroll 1
+        const uint32_t k_tile = k_op + ((kv * 9 * kPanel) >> 4);
+        const uint32_t d = tmem + kScoreColumn + buf * kTile;
+#pragma unroll
         for (uint32_t g = 0; g < kGroups; ++g) {
             const uint32_t slot = kv * kGroups + g;
             if (!wait_phase(&sm.full[slot], (n / kBufs) & 1u, &sm.stop, a.wait_ns)) return false;
             fence_after_sync();
-            if (lane == 0) {
-                const uint32_t panel = group_start(g);
+            if (elect_one()) {
+#pragma unroll
                 for (uint32_t x = 0; x < group_panels(g); ++x)
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(tmem + kScoreColumn + buf * kTile,
-                                   q_desc + (((panel + x) * kPanel + ks * 32u) >> 4),
-                                   k_desc + (((kv * 9 + panel + x) * kPanel + ks * 32u) >> 4),
-                                   qk_instr, g > 0 || x > 0 || ks > 0);
+                    for (uint32_t ks = 0; ks < 4; ++ks) {
+                        const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
+                        mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
+                    }
                 if (g == 0) mma_commit(&sm.empty[slot]);  // the rotated columns are done with
+                if (g == kGroups - 1) {
+                    mma_commit(&sm.s_full[buf]);
+                    if (last) mma_commit(&sm.q_free);
+                }
             }
             __syncwarp();
         }
-        if (lane == 0) {
-            mma_commit(&sm.s_full[buf]);
-            if (last) mma_commit(&sm.q_free);
-        }
-        __syncwarp();
         return true;
     };
     // O^T (+)= V^T P^T of tile n
@@ -322,14 +322,14 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
         if (first && !wait_phase(&sm.o_free, (seg & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
         if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_ns)) return false;
         fence_after_sync();
-        if (lane == 0) {
-#pragma unroll 1
+        if (elect_one()) {
+            const uint32_t v_tile = v_op + (((kv * 9 + 1) * kPanel) >> 4);
+#pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
 #pragma unroll
                 for (uint32_t ks = 0; ks < 4; ++ks)
-                    mma_f16_ss(tmem + j * kHeads,
-                               v_desc + (((kv * 9 + 1 + 2 * j) * kPanel + ks * 2048u) >> 4),
-                               p_desc + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
+                    mma_f16_ss(tmem + j * kHeads, v_tile + ((2 * j * kPanel + ks * 2048u) >> 4),
+                               p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
                 mma_commit(&sm.empty[kv * kGroups + 1 + j]);
             }
             mma_commit(&sm.pv_done);
@@ -365,7 +365,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     if (ok && pending) ok = values(tile - 1, pending_first, segment - 1);
     if (!ok) {
         // let what was issued finish before tensor and shared memory go
-        if (lane == 0) {
+        if (elect_one()) {
             flag(a.err_flags, KVW_ERR_TIMEOUT);
             mma_commit(&sm.drained);
         }
@@ -561,28 +561,40 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
             sm.l[h0] = l0;
             sm.l[h0 + 8] = l1;
         }
+        const bool whole = w.whole();
+        if (in_quad == 0) {  // what the sums are multiplied by
+            sm.alpha[h0] = l0 == 0.0f ? 0.0f : whole ? a.row_scale / l0 : 1.0f;
+            sm.alpha[h0 + 8] = l1 == 0.0f ? 0.0f : whole ? a.row_scale / l1 : 1.0f;
+        }
         ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
         if (any_softmax(!ok)) break;
         fence_after_sync();
-        const bool whole = w.whole();
         float* part = slot_of(a, blockIdx.x, w.first == 0 ? 1 : 0);
         uint16_t* out = a.out + ((uint64_t)w.t * a.H + head0) * kLatent;
+        const bool odd = lane & 1u;
+#pragma unroll 1
         for (uint32_t c = 0; c < rows; c += 16) {
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = sm.alpha[c + e];
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) {
                 float o[16];
                 tmem_ld_32x16(o, tmem + j * kHeads + c);
+                // a lane has one column (its own) of 16 heads: neighbours swap,
+                // so that each has two columns of every other head
 #pragma unroll
-                for (uint32_t e = 0; e < 16; ++e) {
-                    const uint32_t h = c + e;
-                    if (h >= rows) break;
-                    const uint64_t at = (uint64_t)h * kLatent + j * 128u + tid;
-                    if (whole) {
-                        const float l = sm.l[h], inv = l == 0.0f ? 0.0f : a.row_scale / l;
-                        out[at] = (uint16_t)(pack_bf16x2(o[e] * inv, 0.0f) & 0xffffu);
-                    } else {
-                        part[at] = o[e];
-                    }
+                for (uint32_t e = 0; e < 16; e += 2) {
+                    const float x = o[e] * f[e], y = o[e + 1] * f[e + 1];
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                    const uint32_t h = c + e + odd;
+                    if (h >= rows) continue;
+                    const uint64_t at = (uint64_t)h * kLatent + j * 128u + (tid & ~1u);
+                    const float lo = odd ? got : x, hi = odd ? y : got;
+                    if (whole)
+                        *reinterpret_cast<uint32_t*>(out + at) = pack_bf16x2(lo, hi);
+                    else
+                        *reinterpret_cast<float2*>(part + at) = make_float2(lo, hi);
                 }
             }
         }
