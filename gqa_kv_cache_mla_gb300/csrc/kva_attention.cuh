@@ -65,6 +65,20 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
     return __all_sync(0xffffffffu, ok);
 }
 
+// Has the phase of parity `parity` completed?  (Does not wait; one answer for
+// the warp.)
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+}
+
 // A ring position: slot and the parity of its present round.
 template <int N>
 struct RingPos {

@@ -35,6 +35,28 @@ constexpr uint32_t f16_instr(bool bf16, uint32_t a_mn, uint32_t b_mn, uint32_t m
            (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// The same with 64-byte-swizzled lines, 8 lines to a 512-byte group.
+constexpr uint32_t kOperandHigh64 = (512u >> 4) | (1u << 14) | (4u << 29);
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, both operands
+// E4M3, K-major.
+constexpr uint32_t e4m3_instr(uint32_t m, uint32_t n) {
+    return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D (+)= A B, one k32 step of E4M3 operands; A_HIGH: A's high word.
+template <uint32_t A_HIGH>
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(instr), "r"((uint32_t)accumulate), "n"(A_HIGH),
+        "n"(kOperandHigh)
+        : "memory");
+}
+
 // D (+)= A B, one k16 step, operands by their low words; one thread issues.
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
                                            bool accumulate) {

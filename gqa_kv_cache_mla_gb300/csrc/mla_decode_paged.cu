@@ -14,16 +14,24 @@
 // in L2), close to the ridge of the card: both HBM and the matrix unit's
 // operand bandwidth matter.  The products are tcgen05 MMAs on tiles that the
 // copy engine writes in the operands' own swizzled layout, page by page, so a
-// bf16 row goes from HBM to the matrix unit without passing a register.  An
-// E4M3 row lands as codes; four warps turn them into fp16 (exactly) in the
-// same layout.
+// bf16 row goes from HBM to the matrix unit without passing a register.
 //
-// Shared memory (227 KB) decides the rest: Q takes 72 KB, a bf16 tile 72 KB,
-// so there are two tiles, each in five groups (the rotated columns, then four
-// times 128 latent columns) that are filled and freed one by one: the first
-// group is free after S, the others as the four row blocks of O^T complete.
-// An E4M3 cache has one fp16 tile and nine 8 KB slots of codes ahead of it.
-// O^T fills 256 of the 512 columns of tensor memory, two S tiles 128.
+// An E4M3 cache keeps its codes for S: the query row, scaled by a power of
+// two, is the sum of two E4M3 numbers (4 + 4 significant bits are bf16's 8),
+// x = q1 + q2 / 16, so q1 fills rows 32w .. 32w + 15 and q2 rows 32w + 16 ..
+// 32w + 31 of one 128-row operand and S = S1 + S2 / 16; products of two E4M3
+// numbers are exact in fp32.  The sum is exact down to 2^-21 of the row's
+// largest value.  Weights need more than E4M3 has, so four warps turn the
+// value columns into fp16 (exactly) for O^T.
+//
+// Shared memory (227 KB) decides the rest.  bf16: Q 72 KB and two tiles of 72
+// KB, each in five groups (the rotated columns, then four times 128 latent
+// columns) that are filled and freed one by one: the first group is free after
+// S, the others as the four row blocks of O^T complete.  E4M3: Q's two parts
+// 72 KB, two tiles of codes 80 KB, one fp16 tile of values 64 KB in four
+// groups.  P 8 KB.  O^T fills 256 of the 512 columns of tensor memory, two S
+// tiles 128.  The MMA warp takes what is ready first, the next S or the next
+// O^T, so that neither a late tile nor a late softmax holds up the other.
 //
 // Warps: 0-3 softmax, rescaling, results; 4 feeds; 5 issues the MMAs; 6-9
 // (E4M3) convert.  Every wait is bounded.
@@ -42,7 +50,6 @@ constexpr uint32_t kHeads = 64;               // rows of a row block
 constexpr uint32_t kLatent = 512, kRow = 576;
 constexpr uint32_t kPanel = kTile * 128;      // 64 columns of a 16-bit tile, or 128 codes
 constexpr uint32_t kGroups = 5;               // of a tile: rotated columns, 4 x 128 latent ones
-constexpr uint32_t kRawSlots = 9;
 constexpr uint32_t kMaxCtas = 192;
 constexpr uint32_t kTmemColumns = 512, kScoreColumn = 256;
 constexpr float kSlack = 6.0f;                // log2 of the largest weight before a rescale
@@ -52,6 +59,8 @@ struct MlaArgs {
     SplitArgs split;
     uint16_t* out;
     float* lse;
+    const uint16_t *q_latent, *q_rope;
+    int64_t q_latent_stride, q_rope_stride;
     const uint32_t* page_table;
     uint32_t* err_flags;
     unsigned char* workspace;
@@ -74,12 +83,15 @@ constexpr int threads_of() {
 
 template <bool FP8>
 struct Smem {
-    unsigned char q[9 * kPanel];  // rotated columns, then the latent panels
-    unsigned char kv[(FP8 ? 1 : 2) * 9 * kPanel];
+    // bf16: Q as nine panels, rotated columns first.  E4M3: four panels of 128
+    // rows x 128 codes, then 128 rows x 64 rotated columns in 64-byte lines.
+    unsigned char q[9 * kPanel];
     unsigned char p[kPanel];
-    unsigned char raw[FP8 ? kRawSlots * kPanel : 16];
-    uint64_t full[2 * kGroups], empty[2 * kGroups];  // groups of the 16-bit tiles
-    uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+    // two tiles as they come: nine panels each, or five of codes
+    unsigned char kv[2 * (FP8 ? kGroups : 9) * kPanel];
+    unsigned char values[FP8 ? 8 * kPanel : 16];  // E4M3: the value columns in fp16
+    uint64_t full[2 * kGroups], empty[2 * kGroups];  // groups of the two tiles
+    uint64_t v_full[4], v_empty[4];                  // groups of `values`
     uint64_t q_full, q_ready, q_free;
     uint64_t s_full[2], s_free[2], p_full, pv_done, o_free, drained;
     uint64_t there[8];  // of a tile: positions that are there
@@ -119,26 +131,26 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 template <bool FP8, bool WITHHOLD>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
-    constexpr uint32_t kSlots = FP8 ? kRawSlots : 2 * kGroups;
+    constexpr uint32_t kSlots = 2 * kGroups;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
-    uint64_t* full = FP8 ? sm.raw_full : sm.full;
-    uint64_t* empty = FP8 ? sm.raw_empty : sm.empty;
     Walk w;
     w.begin(a.split, sm.split.start);
     RingPos<(int)kSlots> at;
     uint32_t bad_page = 0, issued = 0, tile = 0, segment = 0;
     bool ok = true;
     while (ok && !w.done()) {
-        ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_ns);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
-        __syncwarp();
-        if (lane < 9) {
-            const uint32_t dst = smem_addr(sm.q + lane * kPanel), bar = smem_addr(&sm.q_full);
-            if (lane == 0)
-                tma_3d(dst, &qm.rope, 0, hb * kHeads, w.t, bar);
-            else
-                tma_3d(dst, &qm.latent, (lane - 1) * 64, hb * kHeads, w.t, bar);
+        if constexpr (!FP8) {
+            ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_ns);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
+            __syncwarp();
+            if (lane < 9) {
+                const uint32_t dst = smem_addr(sm.q + lane * kPanel), bar = smem_addr(&sm.q_full);
+                if (lane == 0)
+                    tma_3d(dst, &qm.rope, 0, hb * kHeads, w.t, bar);
+                else
+                    tma_3d(dst, &qm.latent, (lane - 1) * 64, hb * kHeads, w.t, bar);
+            }
         }
         ++segment;
         for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
@@ -160,19 +172,18 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
 #pragma unroll 1
             for (uint32_t g = 0; g < kGroups; ++g) {
-                ok = wait_phase(&empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
+                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
                 if (!ok) break;
                 const uint32_t panels = FP8 ? 1u : group_panels(g);
                 if (lane == 0) {
                     if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
-                    mbar_arrive_expect_tx(&full[at.slot], (n << maps.log_rows) * 128u * panels);
+                    mbar_arrive_expect_tx(&sm.full[at.slot], (n << maps.log_rows) * 128u * panels);
                 }
                 __syncwarp();
                 if (!(WITHHOLD && issued == 0)) {
-                    const uint32_t bar = smem_addr(&full[at.slot]);
-                    const uint32_t base =
-                        FP8 ? smem_addr(sm.raw + at.slot * kPanel)
-                            : smem_addr(sm.kv + ((tile & 1u) * 9 + group_start(g)) * kPanel);
+                    const uint32_t bar = smem_addr(&sm.full[at.slot]);
+                    const uint32_t base = smem_addr(
+                        sm.kv + (FP8 ? at.slot : (tile & 1u) * 9 + group_start(g)) * kPanel);
                     const uint32_t col = g == 0 ? kLatent : (g - 1) * 128u;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -197,70 +208,66 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
         const uint32_t n = issued < kSlots ? issued : kSlots;
         for (uint32_t i = 0; i < n; ++i) {
             const uint32_t x = issued - 1 - i;
-            mbar_wait(&full[x % kSlots], (x / kSlots) & 1u, a.wait_ns);
+            mbar_wait(&sm.full[x % kSlots], (x / kSlots) & 1u, a.wait_ns);
         }
-        if (segment) mbar_wait(&sm.q_full, (segment - 1) & 1u, a.wait_ns);
+        if (!FP8 && segment) mbar_wait(&sm.q_full, (segment - 1) & 1u, a.wait_ns);
     }
 }
 
 // ---------------------------------------------------------------- converting
 
-// Codes of a group -> fp16 panels in the operands' layout; positions that are
-// not there become zeros.
+// Codes of the value columns -> fp16 panels in the operands' layout; positions
+// that are not there become zeros.
 __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
-    const uint32_t lane = threadIdx.x & 31u, i0 = threadIdx.x - 192u;
+    const uint32_t lane = threadIdx.x & 31u, i0 = threadIdx.x - 192u, c = i0 & 7u;
     Walk w;
     w.begin(a.split, sm.split.start);
-    RingPos<(int)kRawSlots> at;
     uint32_t tile = 0;
     bool ok = true;
     while (ok && !w.done()) {
         for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
+            const uint32_t buf = tile & 1u;
 #pragma unroll 1
-            for (uint32_t g = 0; g < kGroups; ++g) {
-                ok = wait_phase(&sm.raw_full[at.slot], at.parity, &sm.stop, a.wait_ns) &&
-                     wait_phase(&sm.empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_ns);
+            for (uint32_t g = 0; g < 4; ++g) {
+                const uint32_t slot = buf * kGroups + 1 + g;
+                ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_ns);
                 if (!ok) break;
                 const uint64_t there = sm.there[tile & 7u];
-                const unsigned char* src = sm.raw + at.slot * kPanel;
-                unsigned char* dst = sm.kv + group_start(g) * kPanel;
-                const uint32_t c = i0 & 7u;
-                if (g > 0 || c < 4) {
-                    uint4 v[4];
+                const unsigned char* src = sm.kv + slot * kPanel;
+                uint4 v[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t r = (i0 >> 3) + 16u * k;
-                        v[k] = *reinterpret_cast<const uint4*>(src + r * 128u +
-                                                               (((c ^ r) & 7u) << 4));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t r = (i0 >> 3) + 16u * k;
+                    v[k] = *reinterpret_cast<const uint4*>(src + r * 128u + (((c ^ r) & 7u) << 4));
+                }
+                ok = wait_phase(&sm.v_empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_ns);
+                if (!ok) break;
+                unsigned char* dst = sm.values + 2 * g * kPanel;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t r = (i0 >> 3) + 16u * k;
-                        if (!((there >> r) & 1ull)) v[k] = make_uint4(0, 0, 0, 0);
-                        uint4 x, y;
-                        codes_to_f16(v[k].x, x.x, x.y);
-                        codes_to_f16(v[k].y, x.z, x.w);
-                        codes_to_f16(v[k].z, y.x, y.y);
-                        codes_to_f16(v[k].w, y.z, y.w);
-                        // 16 codes are two chunks of the row's line; chunks 4-7
-                        // of the codes go to the second panel and store their
-                        // odd chunk first, so that the eight lanes of a row
-                        // hit distinct banks
-                        const uint32_t o = 2u * (c & 3u), odd = c >> 2;
-                        unsigned char* line = dst + (c >> 2) * kPanel + r * 128u;
-                        *reinterpret_cast<uint4*>(line + (((o + odd) ^ (r & 7u)) << 4)) =
-                            odd ? y : x;
-                        *reinterpret_cast<uint4*>(line + (((o + (odd ^ 1u)) ^ (r & 7u)) << 4)) =
-                            odd ? x : y;
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t r = (i0 >> 3) + 16u * k;
+                    if (!((there >> r) & 1ull)) v[k] = make_uint4(0, 0, 0, 0);
+                    uint4 x, y;
+                    codes_to_f16(v[k].x, x.x, x.y);
+                    codes_to_f16(v[k].y, x.z, x.w);
+                    codes_to_f16(v[k].z, y.x, y.y);
+                    codes_to_f16(v[k].w, y.z, y.w);
+                    // 16 codes are two chunks of the row's line; chunks 4-7 of
+                    // the codes go to the second panel and store their odd
+                    // chunk first, so that the eight lanes of a row hit
+                    // distinct banks
+                    const uint32_t o = 2u * (c & 3u), odd = c >> 2;
+                    unsigned char* line = dst + (c >> 2) * kPanel + r * 128u;
+                    *reinterpret_cast<uint4*>(line + (((o + odd) ^ (r & 7u)) << 4)) = odd ? y : x;
+                    *reinterpret_cast<uint4*>(line + (((o + (odd ^ 1u)) ^ (r & 7u)) << 4)) =
+                        odd ? x : y;
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sm.full[g]);
-                    mbar_arrive(&sm.raw_empty[at.slot]);
+                    mbar_arrive(&sm.v_full[g]);
+                    mbar_arrive(&sm.empty[slot]);
                 }
-                at.step();
             }
         }
         if (ok) w.next(a.split);
@@ -271,98 +278,148 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
 
 template <bool FP8>
 __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
-    constexpr uint32_t kBufs = FP8 ? 1 : 2;
     const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
     const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
-    const uint32_t qk_instr = f16_instr(!FP8, 0, 0, kHeads, kTile);
+    constexpr uint32_t qk_instr =
+        FP8 ? e4m3_instr(128, kTile) : f16_instr(true, 0, 0, kHeads, kTile);
     const uint32_t pv_instr = f16_instr(!FP8, 1, 0, 128, cols);
     const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
     const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
-    const uint32_t v_op = operand_low(smem_addr(sm.kv), kPanel);
+    const uint32_t v_op = operand_low(smem_addr(FP8 ? sm.values : sm.kv), kPanel);
     const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
     Walk w;
     w.begin(a.split, sm.split.start);
     bool ok = true;
-    uint32_t tile = 0, segment = 0;
 
     // S of tile n
     auto scores = [&](uint32_t n, bool last) {
-        const uint32_t buf = n & 1u, kv = n % kBufs;
+        const uint32_t buf = n & 1u;
         if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
         fence_after_sync();
-        const uint32_t k_tile = k_op + ((kv * 9 * kPanel) >> 4);
+        const uint32_t k_tile = k_op + ((buf * (FP8 ? kGroups : 9) * kPanel) >> 4);
         const uint32_t d = tmem + kScoreColumn + buf * kTile;
 #pragma unroll
         for (uint32_t g = 0; g < kGroups; ++g) {
-            const uint32_t slot = kv * kGroups + g;
-            if (!wait_phase(&sm.full[slot], (n / kBufs) & 1u, &sm.stop, a.wait_ns)) return false;
+            const uint32_t slot = buf * kGroups + g;
+            if (!wait_phase(&sm.full[slot], (n >> 1) & 1u, &sm.stop, a.wait_ns)) return false;
             fence_after_sync();
             if (elect_one()) {
+                if constexpr (FP8) {
+                    const uint32_t k_at = k_tile + ((g * kPanel) >> 4);
+                    if (g == 0) {  // rotated columns: 64-byte lines of Q behind its panels
 #pragma unroll
-                for (uint32_t x = 0; x < group_panels(g); ++x)
+                        for (uint32_t ks = 0; ks < 2; ++ks)
+                            mma_e4m3_ss<kOperandHigh64>(d, q_op + ((8 * kPanel + ks * 32u) >> 4),
+                                                        k_at + ((ks * 32u) >> 4), qk_instr, ks > 0);
+                    } else {
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 4; ++ks) {
-                        const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
-                        mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
+                        for (uint32_t ks = 0; ks < 4; ++ks)
+                            mma_e4m3_ss<kOperandHigh>(
+                                d, q_op + (((g - 1) * 2 * kPanel + ks * 32u) >> 4),
+                                k_at + ((ks * 32u) >> 4), qk_instr, true);
                     }
-                if (g == 0) mma_commit(&sm.empty[slot]);  // the rotated columns are done with
+                    mma_commit(&sm.empty[slot]);
+                } else {
+#pragma unroll
+                    for (uint32_t x = 0; x < group_panels(g); ++x)
+#pragma unroll
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
+                            mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
+                        }
+                    if (g == 0) mma_commit(&sm.empty[slot]);  // the rotated columns are done with
+                }
                 if (g == kGroups - 1) {
                     mma_commit(&sm.s_full[buf]);
-                    if (last) mma_commit(&sm.q_free);
+                    if (!FP8 && last) mma_commit(&sm.q_free);
                 }
             }
             __syncwarp();
         }
         return true;
     };
-    // O^T (+)= V^T P^T of tile n
-    auto values = [&](uint32_t n, bool first, uint32_t seg) {
-        const uint32_t kv = n % kBufs;
-        if (first && !wait_phase(&sm.o_free, (seg & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
+    // O^T (+)= V^T P^T of tile n, the `first` of a segment or not; `odd`: the
+    // segment's parity
+    auto values = [&](uint32_t n, bool first, uint32_t odd) {
+        const uint32_t buf = n & 1u;
+        if (first && !wait_phase(&sm.o_free, odd ^ 1u, &sm.stop, a.wait_ns)) return false;
         if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_ns)) return false;
         fence_after_sync();
-        if (elect_one()) {
-            const uint32_t v_tile = v_op + (((kv * 9 + 1) * kPanel) >> 4);
+        const uint32_t v_tile = FP8 ? v_op : v_op + (((buf * 9 + 1) * kPanel) >> 4);
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
+        for (uint32_t j = 0; j < 4; ++j) {
+            if constexpr (FP8) {
+                if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_ns)) return false;
+                fence_after_sync();
+            }
+            if (elect_one()) {
 #pragma unroll
                 for (uint32_t ks = 0; ks < 4; ++ks)
                     mma_f16_ss(tmem + j * kHeads, v_tile + ((2 * j * kPanel + ks * 2048u) >> 4),
                                p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
-                mma_commit(&sm.empty[kv * kGroups + 1 + j]);
+                mma_commit(FP8 ? &sm.v_empty[j] : &sm.empty[buf * kGroups + 1 + j]);
+                if (j == 3) mma_commit(&sm.pv_done);
             }
-            mma_commit(&sm.pv_done);
+            __syncwarp();
         }
-        __syncwarp();
         return true;
     };
 
-    bool pending = false, pending_first = false;
-    while (ok && !w.done()) {
-        const uint32_t count = w.last - w.first;
-        for (uint32_t i = 0; ok && i < count; ++i, ++tile) {
-            if (i == 0) {
-                if (pending) ok = values(tile - 1, pending_first, segment - 1);
-                pending = false;
-                ok = ok && wait_phase(FP8 ? &sm.q_ready : &sm.q_full, segment & 1u, &sm.stop,
-                                      a.wait_ns);
-                if (!ok) break;
+    // S runs at most two tiles ahead of O^T (its two buffers).  Whichever is
+    // ready goes first.
+    uint32_t s_tile = 0, o_tile = 0, s_segment = 0, i = 0;
+    // of the tiles between S and O^T, by the parity of the tile: is it the
+    // first of its segment, and the parity of that
+    uint32_t firsts = 0, odd_segments = 0;
+    uint64_t* q_bar = FP8 ? &sm.q_ready : &sm.q_full;
+    while (ok && (!w.done() || o_tile < s_tile)) {
+        const uint32_t pending = s_tile - o_tile;
+        bool take_s = !w.done() && pending < 2;
+        if (take_s && pending > 0) {
+            // both are possible: wait for either
+            const uint32_t slot = (s_tile & 1u) * kGroups + kGroups - 1;
+            const uint64_t t0 = global_ns();
+            while (true) {
+                if (phase_done(&sm.p_full, o_tile & 1u)) {
+                    take_s = false;
+                    break;
+                }
+                if (phase_done(&sm.full[slot], (s_tile >> 1) & 1u) &&
+                    phase_done(&sm.s_free[s_tile & 1u], ((s_tile >> 1) & 1u) ^ 1u) &&
+                    (i > 0 || phase_done(q_bar, s_segment & 1u)))
+                    break;
+                bool give_up = *reinterpret_cast<volatile uint32_t*>(&sm.stop) != 0;
+                if (global_ns() - t0 > a.wait_ns) {
+                    *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+                    give_up = true;
+                }
+                if (__any_sync(0xffffffffu, give_up)) {
+                    ok = false;
+                    break;
+                }
             }
-            ok = scores(tile, i + 1 == count);
             if (!ok) break;
-            if constexpr (kBufs == 2) {
-                if (pending) ok = values(tile - 1, pending_first, segment);
-                pending = true;
-                pending_first = i == 0;
-            } else {
-                ok = values(tile, i == 0, segment);
-            }
         }
-        ++segment;
-        w.next(a.split);
+        if (take_s) {
+            if (i == 0) ok = wait_phase(q_bar, s_segment & 1u, &sm.stop, a.wait_ns);
+            if (!ok) break;
+            const uint32_t count = w.last - w.first;
+            ok = scores(s_tile, i + 1 == count);
+            const uint32_t bit = 1u << (s_tile & 1u);
+            firsts = i == 0 ? firsts | bit : firsts & ~bit;
+            odd_segments = s_segment & 1u ? odd_segments | bit : odd_segments & ~bit;
+            ++s_tile;
+            if (++i == count) {
+                i = 0;
+                ++s_segment;
+                w.next(a.split);
+            }
+        } else {
+            ok = values(o_tile, (firsts >> (o_tile & 1u)) & 1u, (odd_segments >> (o_tile & 1u)) & 1u);
+            ++o_tile;
+        }
     }
-    if (ok && pending) ok = values(tile - 1, pending_first, segment - 1);
     if (!ok) {
         // let what was issued finish before tensor and shared memory go
         if (elect_one()) {
@@ -376,36 +433,77 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
 
 // ---------------------------------------------------------------- softmax
 
-// The queries of a segment from bf16 to fp16 in place, each row brought into
-// fp16's range by a power of two; two threads to a row.
-__device__ __forceinline__ void convert_queries(Smem<true>& sm) {
-    const uint32_t r = threadIdx.x >> 1, part = threadIdx.x & 1u;
-    uint32_t top = 0;
-    for (uint32_t p = 0; p < 9; ++p)
+// The queries of a segment as two E4M3 parts: row h scaled by a power of two
+// so that its largest value lies in [128, 256), x = q1 + q2 / 16 with q1 the
+// nearest E4M3 number and q2 the remainder, exact while q1's step is not
+// below E4M3's smallest (2^-9).  A row with an infinity or a NaN becomes NaN
+// (E4M3 has no infinity; its scores are not finite either way).  A warp takes
+// 16 heads, four at a time, its lanes the 72 chunks of 8 values of a row.
+__device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, uint32_t t,
+                                              uint32_t head0, uint32_t rows) {
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    constexpr int kAtOnce = 4;
+    for (uint32_t i0 = 0; i0 < 16; i0 += kAtOnce) {
+        uint4 v[kAtOnce][3];
 #pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                sm.q + p * kPanel + r * 128u + (((part * 4 + c) ^ (r & 7u)) << 4));
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-        }
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top & 0xffffu, top >> 16);
-    float up, down;
-    row_power(top, up, down);
-    for (uint32_t p = 0; p < 9; ++p)
+        for (int n = 0; n < kAtOnce; ++n) {
+            const uint32_t h = warp * 16 + i0 + n;
+            const uint16_t* ql = a.q_latent + (int64_t)t * a.q_latent_stride +
+                                 (int64_t)(head0 + h) * kLatent;
+            const uint16_t* qr = a.q_rope + (int64_t)t * a.q_rope_stride + (int64_t)(head0 + h) * 64;
 #pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(sm.q + p * kPanel + r * 128u +
-                                                 (((part * 4 + c) ^ (r & 7u)) << 4));
-            uint4 v = *at;
-            v.x = pack2<true>(bf16_lo(v.x) * up, bf16_hi(v.x) * up);
-            v.y = pack2<true>(bf16_lo(v.y) * up, bf16_hi(v.y) * up);
-            v.z = pack2<true>(bf16_lo(v.z) * up, bf16_hi(v.z) * up);
-            v.w = pack2<true>(bf16_lo(v.w) * up, bf16_hi(v.w) * up);
-            *at = v;
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t c = lane + 32u * k;
+                v[n][k] = make_uint4(0, 0, 0, 0);
+                if (h < rows && c < 72)
+                    v[n][k] = __ldg(reinterpret_cast<const uint4*>(c < 64 ? ql + c * 8
+                                                                          : qr + (c - 64) * 8));
+            }
         }
-    if (part == 0) sm.q_scale[r] = down;
+#pragma unroll
+        for (int n = 0; n < kAtOnce; ++n) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[n][k].x & 0x7fff7fffu, v[n][k].y & 0x7fff7fffu),
+                                             __vmaxu2(v[n][k].z & 0x7fff7fffu, v[n][k].w & 0x7fff7fffu)));
+            top = max(top & 0xffffu, top >> 16);
+            top = __reduce_max_sync(0xffffffffu, top);
+            float up, down;
+            row_power(top, up, down);  // to [2^14, 2^15)
+            const bool finite = (top >> 7) != 255u;
+            up *= 0x1p-7f;
+            down *= 0x1p7f;
+            const uint32_t h = warp * 16 + i0 + n, r1 = 32u * warp + i0 + n, r2 = r1 + 16u;
+            if (lane == 0) sm.q_scale[h] = down;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t c = lane + 32u * k;
+                if (c >= 72) continue;
+                float x[8], y[8], z[8];
+                unpack8(v[n][k], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = finite ? x[e] * up : __int_as_float(0x7fffffff);
+                const uint2 q1 = pack8_e4m3(x);
+                unpack8_e4m3(q1, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = (x[e] - y[e]) * 16.0f;
+                const uint2 q2 = pack8_e4m3(z);
+                // 8 codes: half of a 16-byte chunk
+                if (c < 64) {
+                    unsigned char* at = sm.q + (c >> 4) * 2 * kPanel;
+                    const uint32_t chunk = (c >> 1) & 7u, half = (c & 1u) * 8u;
+                    *reinterpret_cast<uint2*>(at + r1 * 128u + ((chunk ^ (r1 & 7u)) << 4) + half) = q1;
+                    *reinterpret_cast<uint2*>(at + r2 * 128u + ((chunk ^ (r2 & 7u)) << 4) + half) = q2;
+                } else {
+                    unsigned char* at = sm.q + 8 * kPanel;
+                    const uint32_t chunk = (c - 64) >> 1, half = (c & 1u) * 8u;
+                    *reinterpret_cast<uint2*>(at + r1 * 64u + ((chunk ^ ((r1 >> 1) & 3u)) << 4) + half) = q1;
+                    *reinterpret_cast<uint2*>(at + r2 * 64u + ((chunk ^ ((r2 >> 1) & 3u)) << 4) + half) = q2;
+                }
+            }
+        }
+    }
 }
 
 template <bool FP8>
@@ -425,10 +523,10 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
         if ((int64_t)w.len0 + w.k + 1 > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
         float qs0 = a.scale, qs1 = a.scale;
         if constexpr (FP8) {
-            ok = wait_phase(&sm.q_full, segment & 1u, &sm.stop, a.wait_ns);
-            if (ok) convert_queries(sm);
+            // the last S of the segment before has been read: Q is free
+            split_queries(a, sm, w.t, head0, rows);
             fence_async_smem();
-            if (any_softmax(!ok)) break;  // q_scale is written
+            any_softmax(false);  // q_scale is written
             qs0 = fmaxf(a.scale * sm.q_scale[h0], 1.17549435e-38f);
             qs1 = fmaxf(a.scale * sm.q_scale[h0 + 8], 1.17549435e-38f);
             if (lane == 0) mbar_arrive(&sm.q_ready);
@@ -443,6 +541,12 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
             if (ok) {
                 fence_after_sync();
                 tmem_ld_16x64(s, tmem + kScoreColumn + buf * kTile);
+                if constexpr (FP8) {
+                    float s2[32];
+                    tmem_ld_16x64(s2, tmem + (16u << 16) + kScoreColumn + buf * kTile);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[e] = fmaf(s2[e], 0.0625f, s[e]);
+                }
                 fence_before_sync();
                 if (lane == 0) mbar_arrive(&sm.s_free[buf]);
             } else {
@@ -637,12 +741,13 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
         for (uint32_t i = 0; i < 2 * kGroups; ++i) {
-            mbar_init(&sm.full[i], FP8 ? 4 : 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.full[i], 1);
+            // E4M3: value columns go to the matrix unit and to four converting warps
+            mbar_init(&sm.empty[i], FP8 && i % kGroups ? 5 : 1);
         }
-        for (uint32_t i = 0; i < kRawSlots; ++i) {
-            mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], 4);
+        for (uint32_t i = 0; i < 4; ++i) {
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_empty[i], 1);
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_ready, 4);
@@ -828,6 +933,10 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
     a.split.window = 1ll << 40;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
+    a.q_latent = static_cast<const uint16_t*>(q_latent);
+    a.q_rope = static_cast<const uint16_t*>(q_rope);
+    a.q_latent_stride = q_latent_row_stride;
+    a.q_rope_stride = q_rope_row_stride;
     a.page_table = cache->page_table;
     a.err_flags = err_flags;
     a.workspace = static_cast<unsigned char*>(workspace);
