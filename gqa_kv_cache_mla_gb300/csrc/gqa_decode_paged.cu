@@ -59,7 +59,7 @@ struct GqaArgs {
     uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
     uint32_t num_pages, max_pages, pieces;
     FastDiv ps;
-    uint64_t wait_ns;
+    int64_t wait_limit;  // cycles
 };
 
 template <int DP>
@@ -164,7 +164,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
         const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
         // ---- the queries: one copy per row
-        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_ns);
+        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_limit);
         if (!ok) break;
         const uint32_t rows = w.span.tokens * in_block;
         if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * a.D * 2);
@@ -198,7 +198,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
             const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
 #pragma unroll 1
             for (uint32_t plane = 0; plane < 2; ++plane) {
-                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
+                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 if (lane == 0) {
                     if (plane == 0) sm.there[at.slot] = ((uint64_t)t_hi << 32) | t_lo;
@@ -208,17 +208,15 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
                 __syncwarp();
                 if (!(WITHHOLD && first_half)) {
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (copy[h].level == 4) continue;
-                        const uint32_t dst = smem_addr(sm.ring + at.slot * Sh::kHalf) +
-                                             ((lane + 32u * h) << maps.log_rows) * Sh::kLine;
+                    const uint32_t base = smem_addr(sm.ring + at.slot * Sh::kHalf);
+                    each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
+                                              const CUtensorMap* map) {
+                        const uint32_t dst = base + (unit << maps.log_rows) * Sh::kLine;
 #pragma unroll
                         for (int blk = 0; blk < Sh::kBlocks; ++blk)
-                            tma_rows(dst + blk * Sh::kBlock, &maps.map[copy[h].level],
-                                     blk * (Sh::kLine / Sh::kEsz), kvh, copy[h].row, copy[h].page,
-                                     plane, bar);
-                    }
+                            tma_rows(dst + blk * Sh::kBlock, map, blk * (Sh::kLine / Sh::kEsz), kvh,
+                                     row, page, plane, bar);
+                    });
                 }
                 first_half = false;
                 at.step();
@@ -235,10 +233,10 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
         const uint32_t n = issued < (uint32_t)Sh::kHalves ? issued : (uint32_t)Sh::kHalves;
         for (uint32_t i = 0; i < n; ++i) {
             const uint32_t x = issued - 1 - i;
-            mbar_wait(&sm.full[x % Sh::kHalves], (x / Sh::kHalves) & 1u, a.wait_ns);
+            drain_phase(&sm.full[x % Sh::kHalves], (x / Sh::kHalves) & 1u, a.wait_limit);
         }
         for (uint32_t i = 0; i < (uint32_t)Sh::kQBufs; ++i)
-            mbar_wait(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_ns);
+            drain_phase(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_limit);
     }
 }
 
@@ -290,13 +288,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     RingPos<Sh::kQBufs> q_at;
     uint32_t meet_parity = 0;
     auto ready = [&](const RingPos<Sh::kHalves>& x) {
-        return wait_phase(&sm.full[x.slot], x.parity, &sm.stop, a.wait_ns);
+        return wait_phase(&sm.full[x.slot], x.parity, &sm.stop, a.wait_limit);
     };
     // the consumers meet (bounded, so that one that gave up strands nobody)
     auto meet = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.meet);
-        const bool met = wait_phase(&sm.meet, meet_parity, &sm.stop, a.wait_ns);
+        const bool met = wait_phase(&sm.meet, meet_parity, &sm.stop, a.wait_limit);
         meet_parity ^= 1u;
         return met;
     };
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---- queries: A operands, fp16 rows brought into range by 2^x
         const uint32_t r0 = quad, r1 = quad + 8;
         const uint32_t t0 = r0 / in_block, t1 = r1 / in_block;  // tokens of the chunk
-        alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_ns);
+        alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_limit);
         if (!alive) break;
         const unsigned char* q0 = sm.q_raw[q_at.slot] + r0 * Sh::kQPitch;
         const unsigned char* q1 = q0 + 8 * Sh::kQPitch;
@@ -974,7 +972,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     a.num_pages = cache->num_pages;
     a.max_pages = cache->max_pages_per_seq;
     a.ps = make_fast_div(cache->page_size);
-    a.wait_ns = wait_ns;
+    a.wait_limit = wait_cycles(wait_ns);
     auto run = [&](auto dp, auto f8) {
 #ifdef KVW_TEST_HOOKS
         if (withhold)

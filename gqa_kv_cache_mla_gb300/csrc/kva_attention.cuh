@@ -47,16 +47,28 @@ __device__ __forceinline__ void row_power(uint32_t top, float& up, float& down) 
     down = __uint_as_float((uint32_t)de << 23);
 }
 
+// One thread of a converged warp, known to the compiler as one: what it
+// issues needs no loop over lanes (an MMA or a copy takes 120 cycles to issue
+// without it).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // Bounded wait of a whole warp that ends early when another role gave up;
-// the answer is the same for all lanes.
+// the answer is the same for all lanes.  The limit is in cycles of the SM's
+// clock, which is read in a few of them; the global timer takes about a
+// microsecond, as long as most of these waits.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t* stop,
-                                           uint64_t limit_ns) {
+                                           int64_t limit_cycles) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
-        const uint64_t t0 = global_ns();
+        const int64_t t0 = clock64();
         while (!(ok = mbar_try_wait(bar, parity))) {
             if (*reinterpret_cast<volatile uint32_t*>(stop)) break;
-            if (global_ns() - t0 > limit_ns) {
+            if (clock64() - t0 > limit_cycles) {
                 *reinterpret_cast<volatile uint32_t*>(stop) = 1;
                 break;
             }
@@ -64,6 +76,16 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
     }
     return __all_sync(0xffffffffu, ok);
 }
+
+// The same without early end, for what has to land before a CTA may go.
+__device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity, int64_t limit_cycles) {
+    const int64_t t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > limit_cycles) return;
+}
+
+// Cycles of a limit in nanoseconds (the clock runs at 2.07 GHz at most).
+inline int64_t wait_cycles(uint64_t ns) { return (int64_t)(ns * 2); }
 
 // Has the phase of parity `parity` completed?  (Does not wait; one answer for
 // the warp.)

@@ -6,16 +6,6 @@
 
 namespace kvw {
 
-// One thread of a converged warp, known to the compiler as one: what it
-// issues needs no loop over lanes (120 cycles an MMA without it, 32 to 128
-// with it).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(p));
-    return p != 0;
-}
-
 // Shared-memory operand in 128-byte-swizzled lines, 8 lines to a 1024-byte
 // group.  K-major: a line holds 64 contraction elements of one row and groups
 // of 8 rows lie 1024 bytes apart (lead is not used).  MN-major: a line holds

@@ -16,7 +16,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "kva_common.cuh"
+#include "kva_attention.cuh"
 
 namespace kvw {
 
@@ -155,6 +155,28 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
         "[%1, {%2, %3, %4, %5, %6}], [%7];"
         ::"r"(dst), "l"(map), "r"(col), "r"(head), "r"(row), "r"(page), "r"(plane), "r"(bar)
         : "memory");
+}
+
+// Calls issue(unit, row, page, map) for every copy that the lanes planned.  A
+// tile of one copy is issued with the same arguments in all lanes, by one
+// elected thread; of several copies every lane issues its own (the hardware
+// takes them one by one, faster than a loop that hands them round).
+template <class Issue>
+__device__ __forceinline__ void each_copy(const CacheMaps& m, const UnitCopy (&copy)[2],
+                                          Issue&& issue) {
+    if (m.log_rows == 6) {
+        const uint32_t level = __shfl_sync(0xffffffffu, copy[0].level, 0);
+        const uint32_t row = __shfl_sync(0xffffffffu, copy[0].row, 0);
+        const uint32_t page = __shfl_sync(0xffffffffu, copy[0].page, 0);
+        if (level != 4 && elect_one()) issue(0u, row, page, &m.map[0]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (copy[h].level != 4)
+                issue((threadIdx.x & 31u) + 32u * h, copy[h].row, copy[h].page,
+                      &m.map[copy[h].level]);
+    }
+    __syncwarp();
 }
 
 // Queries [tokens, heads, width] in bf16: copies of 64 heads x 64 columns,

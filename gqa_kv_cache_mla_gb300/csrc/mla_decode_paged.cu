@@ -69,7 +69,7 @@ struct MlaArgs {
     uint32_t H, HB, slot_rows;  // heads, row blocks, rows of a workspace slot
     uint32_t num_pages, max_pages, pieces;
     FastDiv ps;
-    uint64_t wait_ns;
+    int64_t wait_limit;  // cycles
 };
 
 struct QMaps {
@@ -140,7 +140,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
     bool ok = true;
     while (ok && !w.done()) {
         if constexpr (!FP8) {
-            ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_ns);
+            ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
             __syncwarp();
@@ -172,7 +172,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
 #pragma unroll 1
             for (uint32_t g = 0; g < kGroups; ++g) {
-                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_ns);
+                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 const uint32_t panels = FP8 ? 1u : group_panels(g);
                 if (lane == 0) {
@@ -185,14 +185,13 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                     const uint32_t base = smem_addr(
                         sm.kv + (FP8 ? at.slot : (tile & 1u) * 9 + group_start(g)) * kPanel);
                     const uint32_t col = g == 0 ? kLatent : (g - 1) * 128u;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (copy[h].level == 4) continue;
-                        const uint32_t dst = base + ((lane + 32u * h) << maps.log_rows) * 128u;
-                        for (uint32_t x = 0; x < panels; ++x)
-                            tma_rows(dst + x * kPanel, &maps.map[copy[h].level], col + x * 64u, 0,
-                                     copy[h].row, copy[h].page, 0, bar);
-                    }
+                    each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
+                                              const CUtensorMap* map) {
+                        const uint32_t dst = base + (unit << maps.log_rows) * 128u;
+                        tma_rows(dst, map, col, 0, row, page, 0, bar);
+                        if (panels == 2)
+                            tma_rows(dst + kPanel, map, col + 64u, 0, row, page, 0, bar);
+                    });
                 }
                 at.step();
                 ++issued;
@@ -208,9 +207,9 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
         const uint32_t n = issued < kSlots ? issued : kSlots;
         for (uint32_t i = 0; i < n; ++i) {
             const uint32_t x = issued - 1 - i;
-            mbar_wait(&sm.full[x % kSlots], (x / kSlots) & 1u, a.wait_ns);
+            drain_phase(&sm.full[x % kSlots], (x / kSlots) & 1u, a.wait_limit);
         }
-        if (!FP8 && segment) mbar_wait(&sm.q_full, (segment - 1) & 1u, a.wait_ns);
+        if (!FP8 && segment) drain_phase(&sm.q_full, (segment - 1) & 1u, a.wait_limit);
     }
 }
 
@@ -230,7 +229,7 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
 #pragma unroll 1
             for (uint32_t g = 0; g < 4; ++g) {
                 const uint32_t slot = buf * kGroups + 1 + g;
-                ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_ns);
+                ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 const uint64_t there = sm.there[tile & 7u];
                 const unsigned char* src = sm.kv + slot * kPanel;
@@ -240,7 +239,7 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
                     const uint32_t r = (i0 >> 3) + 16u * k;
                     v[k] = *reinterpret_cast<const uint4*>(src + r * 128u + (((c ^ r) & 7u) << 4));
                 }
-                ok = wait_phase(&sm.v_empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_ns);
+                ok = wait_phase(&sm.v_empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 unsigned char* dst = sm.values + 2 * g * kPanel;
 #pragma unroll
@@ -292,18 +291,19 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     w.begin(a.split, sm.split.start);
     bool ok = true;
 
-    // S of tile n
+    // S of tile n.  (Fences only where tensor memory passes between threads,
+    // about 140 cycles each: operands in shared memory come with their
+    // barriers.)
     auto scores = [&](uint32_t n, bool last) {
         const uint32_t buf = n & 1u;
-        if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_ns)) return false;
+        if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit)) return false;
         fence_after_sync();
         const uint32_t k_tile = k_op + ((buf * (FP8 ? kGroups : 9) * kPanel) >> 4);
         const uint32_t d = tmem + kScoreColumn + buf * kTile;
 #pragma unroll
         for (uint32_t g = 0; g < kGroups; ++g) {
             const uint32_t slot = buf * kGroups + g;
-            if (!wait_phase(&sm.full[slot], (n >> 1) & 1u, &sm.stop, a.wait_ns)) return false;
-            fence_after_sync();
+            if (!wait_phase(&sm.full[slot], (n >> 1) & 1u, &sm.stop, a.wait_limit)) return false;
             if (elect_one()) {
                 if constexpr (FP8) {
                     const uint32_t k_at = k_tile + ((g * kPanel) >> 4);
@@ -343,15 +343,14 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     // segment's parity
     auto values = [&](uint32_t n, bool first, uint32_t odd) {
         const uint32_t buf = n & 1u;
-        if (first && !wait_phase(&sm.o_free, odd ^ 1u, &sm.stop, a.wait_ns)) return false;
-        if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_ns)) return false;
+        if (first && !wait_phase(&sm.o_free, odd ^ 1u, &sm.stop, a.wait_limit)) return false;
+        if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_limit)) return false;
         fence_after_sync();
         const uint32_t v_tile = FP8 ? v_op : v_op + (((buf * 9 + 1) * kPanel) >> 4);
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
             if constexpr (FP8) {
-                if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_ns)) return false;
-                fence_after_sync();
+                if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_limit)) return false;
             }
             if (elect_one()) {
 #pragma unroll
@@ -379,7 +378,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
         if (take_s && pending > 0) {
             // both are possible: wait for either
             const uint32_t slot = (s_tile & 1u) * kGroups + kGroups - 1;
-            const uint64_t t0 = global_ns();
+            const int64_t t0 = clock64();
             while (true) {
                 if (phase_done(&sm.p_full, o_tile & 1u)) {
                     take_s = false;
@@ -390,7 +389,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
                     (i > 0 || phase_done(q_bar, s_segment & 1u)))
                     break;
                 bool give_up = *reinterpret_cast<volatile uint32_t*>(&sm.stop) != 0;
-                if (global_ns() - t0 > a.wait_ns) {
+                if (clock64() - t0 > a.wait_limit) {
                     *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
                     give_up = true;
                 }
@@ -402,7 +401,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
             if (!ok) break;
         }
         if (take_s) {
-            if (i == 0) ok = wait_phase(q_bar, s_segment & 1u, &sm.stop, a.wait_ns);
+            if (i == 0) ok = wait_phase(q_bar, s_segment & 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
             const uint32_t count = w.last - w.first;
             ok = scores(s_tile, i + 1 == count);
@@ -427,7 +426,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
             mma_commit(&sm.drained);
         }
         __syncwarp();
-        mbar_wait(&sm.drained, 0, a.wait_ns);
+        drain_phase(&sm.drained, 0, a.wait_limit);
     }
 }
 
@@ -537,7 +536,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
         for (uint32_t i = 0; i < count; ++i, ++tile) {
             const uint32_t buf = tile & 1u;
             float s[32];
-            ok = ok && wait_phase(&sm.s_full[buf], (tile >> 1) & 1u, &sm.stop, a.wait_ns);
+            ok = ok && wait_phase(&sm.s_full[buf], (tile >> 1) & 1u, &sm.stop, a.wait_limit);
             if (ok) {
                 fence_after_sync();
                 tmem_ld_16x64(s, tmem + kScoreColumn + buf * kTile);
@@ -587,7 +586,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                     sm.alpha[h0 + 8] = f1;
                 }
                 if (i > 0)
-                    ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+                    ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_limit);
                 if (any_softmax(!ok)) {  // the alphas are written
                     stopped = true;
                     break;
@@ -626,7 +625,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                 p[2 * e + 1] = pack2<FP8>(y0, y1);
             }
             if (tile > 0)  // P's memory is free
-                ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+                ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_limit);
             if (ok) {
 #pragma unroll
                 for (uint32_t e = 0; e < 8; ++e) {
@@ -670,7 +669,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
             sm.alpha[h0] = l0 == 0.0f ? 0.0f : whole ? a.row_scale / l0 : 1.0f;
             sm.alpha[h0 + 8] = l1 == 0.0f ? 0.0f : whole ? a.row_scale / l1 : 1.0f;
         }
-        ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_ns);
+        ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_limit);
         if (any_softmax(!ok)) break;
         fence_after_sync();
         float* part = slot_of(a, blockIdx.x, w.first == 0 ? 1 : 0);
@@ -948,7 +947,7 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
     a.num_pages = cache->num_pages;
     a.max_pages = cache->max_pages_per_seq;
     a.ps = make_fast_div(cache->page_size);
-    a.wait_ns = wait_ns;
+    a.wait_limit = wait_cycles(wait_ns);
     CacheMaps maps;
     QMaps qm;
     int e = encode_cache_maps(&maps, cache, layer_idx, 1);
