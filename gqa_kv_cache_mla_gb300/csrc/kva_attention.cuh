@@ -87,8 +87,22 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity, int6
 // Cycles of a limit in nanoseconds (the clock runs at 2.07 GHz at most).
 inline int64_t wait_cycles(uint64_t ns) { return (int64_t)(ns * 2); }
 
-// Has the phase of parity `parity` completed?  (Does not wait; one answer for
-// the warp.)
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t* stop,
+                                         int64_t limit_cycles) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const int64_t t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile uint32_t*>(stop)) return false;
+        if (clock64() - t0 > limit_cycles) {
+            *reinterpret_cast<volatile uint32_t*>(stop) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// Has the phase of parity `parity` completed?  (Does not wait.)
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -98,7 +112,7 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
         : "=r"(done)
         : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
-    return __all_sync(0xffffffffu, done != 0);
+    return done != 0;
 }
 
 // A ring position: slot and the parity of its present round.

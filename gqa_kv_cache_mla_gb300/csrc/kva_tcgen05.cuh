@@ -88,7 +88,9 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The loads wait for their data.  16 lanes x 64 columns: thread t gets, for i = 0..7, columns 8i + 2(t%4) and
+// The loads wait for their data in the same statement: until the wait the
+// registers belong to the load, and the compiler must not move or reuse them.
+// 16 lanes x 64 columns: thread t gets, for i = 0..7, columns 8i + 2(t%4) and
 // + 1 of lane t/4 (r[4i], r[4i+1]) and of lane t/4 + 8 (r[4i+2], r[4i+3]).
 __device__ __forceinline__ void tmem_ld_16x64(float (&r)[32], uint32_t addr) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);

@@ -25,16 +25,16 @@
 // value columns into fp16 (exactly) for O^T.
 //
 // Shared memory (227 KB) decides the rest.  bf16: Q 72 KB and two tiles of 72
-// KB, each in five groups (the rotated columns, then four times 128 latent
-// columns) that are filled and freed one by one: the first group is free after
-// S, the others as the four row blocks of O^T complete.  E4M3: Q's two parts
-// 72 KB, two tiles of codes 80 KB, one fp16 tile of values 64 KB in four
-// groups.  P 8 KB.  O^T fills 256 of the 512 columns of tensor memory, two S
-// tiles 128.  The MMA warp takes what is ready first, the next S or the next
-// O^T, so that neither a late tile nor a late softmax holds up the other.
+// KB, each in four groups (128 latent columns; the first with the rotated
+// columns) that are filled one by one and freed as the four row blocks of O^T
+// complete.  E4M3: Q's two parts 72 KB, two tiles of codes 80 KB, one fp16
+// tile of values 64 KB in four groups.  P 8 KB.  O^T fills 256 of the 512
+// columns of tensor memory, two S tiles 128.  The MMA thread takes what is
+// ready first, the next S or the next O^T, so that neither a late tile nor a
+// late softmax holds up the other.
 //
 // Warps: 0-3 softmax, rescaling, results; 4 feeds; 5 issues the MMAs; 6-9
-// (E4M3) convert.  Every wait is bounded.
+// (E4M3) convert values.  Every wait is bounded.
 #include <cstdint>
 #include <type_traits>
 
@@ -49,7 +49,8 @@ namespace {
 constexpr uint32_t kHeads = 64;               // rows of a row block
 constexpr uint32_t kLatent = 512, kRow = 576;
 constexpr uint32_t kPanel = kTile * 128;      // 64 columns of a 16-bit tile, or 128 codes
-constexpr uint32_t kGroups = 5;               // of a tile: rotated columns, 4 x 128 latent ones
+constexpr uint32_t kGroups = 4;               // of a bf16 tile: 128 latent columns each
+constexpr uint32_t kCodePanels = 5;           // of an E4M3 tile: 64 rotated columns, 4 x 128 latent ones
 constexpr uint32_t kMaxCtas = 192;
 constexpr uint32_t kTmemColumns = 512, kScoreColumn = 256;
 constexpr float kSlack = 6.0f;                // log2 of the largest weight before a rescale
@@ -88,10 +89,11 @@ struct Smem {
     unsigned char q[9 * kPanel];
     unsigned char p[kPanel];
     // two tiles as they come: nine panels each, or five of codes
-    unsigned char kv[2 * (FP8 ? kGroups : 9) * kPanel];
+    unsigned char kv[2 * (FP8 ? kCodePanels : 9) * kPanel];
     unsigned char values[FP8 ? 8 * kPanel : 16];  // E4M3: the value columns in fp16
-    uint64_t full[2 * kGroups], empty[2 * kGroups];  // groups of the two tiles
-    uint64_t v_full[4], v_empty[4];                  // groups of `values`
+    // groups of the two tiles: four of bf16 columns, or the five panels of codes
+    uint64_t full[2 * kCodePanels], empty[2 * kCodePanels];
+    uint64_t v_full[4], v_empty[4];  // groups of `values`
     uint64_t q_full, q_ready, q_free;
     uint64_t s_full[2], s_free[2], p_full, pv_done, o_free, drained;
     uint64_t there[8];  // of a tile: positions that are there
@@ -100,9 +102,10 @@ struct Smem {
     uint32_t tmem, stop;
 };
 
-// Panels of group g, and its first one within a tile.
-__device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 1u : 2u; }
-__device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g - 1u; }
+// The panels of a bf16 tile: rotated columns, then eight of the latent ones.
+// Group g: its first panel and their number.
+__device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g + 1u; }
+__device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 3u : 2u; }
 
 // Do any of the softmax threads say yes?
 __device__ __forceinline__ bool any_softmax(bool mine) {
@@ -131,7 +134,7 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 template <bool FP8, bool WITHHOLD>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
-    constexpr uint32_t kSlots = 2 * kGroups;
+    constexpr uint32_t kTileGroups = FP8 ? kCodePanels : kGroups, kSlots = 2 * kTileGroups;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -171,7 +174,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             const uint32_t t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
             const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
 #pragma unroll 1
-            for (uint32_t g = 0; g < kGroups; ++g) {
+            for (uint32_t g = 0; g < kTileGroups; ++g) {
                 ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 const uint32_t panels = FP8 ? 1u : group_panels(g);
@@ -184,13 +187,20 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
                     const uint32_t base = smem_addr(
                         sm.kv + (FP8 ? at.slot : (tile & 1u) * 9 + group_start(g)) * kPanel);
-                    const uint32_t col = g == 0 ? kLatent : (g - 1) * 128u;
                     each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
                                               const CUtensorMap* map) {
                         const uint32_t dst = base + (unit << maps.log_rows) * 128u;
-                        tma_rows(dst, map, col, 0, row, page, 0, bar);
-                        if (panels == 2)
-                            tma_rows(dst + kPanel, map, col + 64u, 0, row, page, 0, bar);
+                        if constexpr (FP8) {
+                            tma_rows(dst, map, g == 0 ? kLatent : (g - 1) * 128u, 0, row, page, 0,
+                                     bar);
+                        } else if (g == 0) {
+                            tma_rows(dst, map, kLatent, 0, row, page, 0, bar);
+                            tma_rows(dst + kPanel, map, 0, 0, row, page, 0, bar);
+                            tma_rows(dst + 2 * kPanel, map, 64, 0, row, page, 0, bar);
+                        } else {
+                            tma_rows(dst, map, g * 128u, 0, row, page, 0, bar);
+                            tma_rows(dst + kPanel, map, g * 128u + 64u, 0, row, page, 0, bar);
+                        }
                     });
                 }
                 at.step();
@@ -228,7 +238,7 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
             const uint32_t buf = tile & 1u;
 #pragma unroll 1
             for (uint32_t g = 0; g < 4; ++g) {
-                const uint32_t slot = buf * kGroups + 1 + g;
+                const uint32_t slot = buf * kCodePanels + 1 + g;
                 ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 const uint64_t there = sm.there[tile & 7u];
@@ -275,65 +285,173 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
 
 // ---------------------------------------------------------------- products
 
-template <bool FP8>
-__device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
+// The products of a bf16 cache: one thread issues every MMA.  (Fences only where tensor memory passes
+// between threads: operands in shared memory come with their barriers.)
+__device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
     const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
     const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
-    constexpr uint32_t qk_instr =
-        FP8 ? e4m3_instr(128, kTile) : f16_instr(true, 0, 0, kHeads, kTile);
-    const uint32_t pv_instr = f16_instr(!FP8, 1, 0, 128, cols);
+    constexpr uint32_t qk_instr = f16_instr(true, 0, 0, kHeads, kTile);
+    const uint32_t pv_instr = f16_instr(true, 1, 0, 128, cols);
     const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
     const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
-    const uint32_t v_op = operand_low(smem_addr(FP8 ? sm.values : sm.kv), kPanel);
+    const uint32_t v_op = operand_low(smem_addr(sm.kv), kPanel);
+    const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return wait_one(bar, parity & 1u, &sm.stop, a.wait_limit);
+    };
+
+    // S of tile n.  Its buffer is free: S of tile n - 2 was read before the
+    // weights of that tile were written, and those have been waited for.
+    auto scores = [&](uint32_t n, bool last) {
+        const uint32_t buf = n & 1u;
+        const uint32_t k_tile = k_op + ((buf * 9 * kPanel) >> 4);
+        const uint32_t d = tmem + kScoreColumn + buf * kTile;
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; ++g) {
+            if (!wait(&sm.full[buf * kGroups + g], n >> 1)) return false;
+#pragma unroll
+            for (uint32_t x = 0; x < group_panels(g); ++x)
+#pragma unroll
+                for (uint32_t ks = 0; ks < 4; ++ks) {
+                    const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
+                    mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
+                }
+        }
+        mma_commit(&sm.s_full[buf]);
+        if (last) mma_commit(&sm.q_free);
+        return true;
+    };
+    // O^T (+)= V^T P^T of tile n, the `first` of a segment or not; `odd`: the
+    // segment's parity
+    auto values = [&](uint32_t n, bool first, uint32_t odd) {
+        const uint32_t buf = n & 1u;
+        if (first && !wait(&sm.o_free, odd ^ 1u)) return false;
+        if (!wait(&sm.p_full, n)) return false;
+        fence_after_sync();
+        const uint32_t v_tile = v_op + (((buf * 9 + 1) * kPanel) >> 4);
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+#pragma unroll
+            for (uint32_t ks = 0; ks < 4; ++ks)
+                mma_f16_ss(tmem + j * kHeads, v_tile + ((2 * j * kPanel + ks * 2048u) >> 4),
+                           p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
+            mma_commit(&sm.empty[buf * kGroups + j]);
+        }
+        mma_commit(&sm.pv_done);
+        return true;
+    };
+
+    if (elect_one()) {
+        Walk w;
+        w.begin(a.split, sm.split.start);
+        bool ok = true;
+        // S runs at most two tiles ahead of O^T (its two buffers).  Whichever
+        // is ready goes first.
+        uint32_t s_tile = 0, o_tile = 0, s_segment = 0, i = 0;
+        // of the tiles between S and O^T, by the parity of the tile: is it the
+        // first of its segment, and the parity of that
+        uint32_t firsts = 0, odd_segments = 0;
+        while (ok && (!w.done() || o_tile < s_tile)) {
+            const uint32_t pending = s_tile - o_tile;
+            bool take_s = !w.done() && pending < 2;
+            if (take_s && pending > 0) {
+                // both are possible: wait for either
+                uint64_t* full = &sm.full[(s_tile & 1u) * kGroups + kGroups - 1];
+                const int64_t t0 = clock64();
+                while (true) {
+                    if (phase_done(&sm.p_full, o_tile & 1u)) {
+                        take_s = false;
+                        break;
+                    }
+                    if (phase_done(full, (s_tile >> 1) & 1u) &&
+                        (i > 0 || phase_done(&sm.q_full, s_segment & 1u)))
+                        break;
+                    if (clock64() - t0 > a.wait_limit)
+                        *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+                    if (*reinterpret_cast<volatile uint32_t*>(&sm.stop)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (take_s) {
+                if (i == 0) ok = wait(&sm.q_full, s_segment);
+                if (!ok) break;
+                const uint32_t count = w.last - w.first;
+                ok = scores(s_tile, i + 1 == count);
+                const uint32_t bit = 1u << (s_tile & 1u);
+                firsts = i == 0 ? firsts | bit : firsts & ~bit;
+                odd_segments = s_segment & 1u ? odd_segments | bit : odd_segments & ~bit;
+                ++s_tile;
+                if (++i == count) {
+                    i = 0;
+                    ++s_segment;
+                    w.next(a.split);
+                }
+            } else {
+                ok = values(o_tile, (firsts >> (o_tile & 1u)) & 1u,
+                            (odd_segments >> (o_tile & 1u)) & 1u);
+                ++o_tile;
+            }
+        }
+        if (!ok) {
+            // let what was issued finish before tensor and shared memory go
+            flag(a.err_flags, KVW_ERR_TIMEOUT);
+            mma_commit(&sm.drained);
+            drain_phase(&sm.drained, 0, a.wait_limit);
+        }
+    }
+    __syncwarp();
+}
+
+// The products of an E4M3 cache: a warp whose elected thread issues.
+__device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm) {
+    const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
+    const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
+    const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
+    constexpr uint32_t qk_instr = e4m3_instr(128, kTile);
+    const uint32_t pv_instr = f16_instr(false, 1, 0, 128, cols);
+    const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
+    const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
+    const uint32_t v_op = operand_low(smem_addr(sm.values), kPanel);
     const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
     Walk w;
     w.begin(a.split, sm.split.start);
     bool ok = true;
 
+    auto all_done = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, phase_done(bar, parity)) != 0;
+    };
     // S of tile n.  (Fences only where tensor memory passes between threads,
     // about 140 cycles each: operands in shared memory come with their
     // barriers.)
-    auto scores = [&](uint32_t n, bool last) {
+    auto scores = [&](uint32_t n) {
         const uint32_t buf = n & 1u;
         if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit)) return false;
         fence_after_sync();
-        const uint32_t k_tile = k_op + ((buf * (FP8 ? kGroups : 9) * kPanel) >> 4);
+        const uint32_t k_tile = k_op + ((buf * kCodePanels * kPanel) >> 4);
         const uint32_t d = tmem + kScoreColumn + buf * kTile;
 #pragma unroll
-        for (uint32_t g = 0; g < kGroups; ++g) {
-            const uint32_t slot = buf * kGroups + g;
+        for (uint32_t g = 0; g < kCodePanels; ++g) {
+            const uint32_t slot = buf * kCodePanels + g;
             if (!wait_phase(&sm.full[slot], (n >> 1) & 1u, &sm.stop, a.wait_limit)) return false;
             if (elect_one()) {
-                if constexpr (FP8) {
-                    const uint32_t k_at = k_tile + ((g * kPanel) >> 4);
-                    if (g == 0) {  // rotated columns: 64-byte lines of Q behind its panels
+                const uint32_t k_at = k_tile + ((g * kPanel) >> 4);
+                if (g == 0) {  // rotated columns: 64-byte lines of Q behind its panels
 #pragma unroll
-                        for (uint32_t ks = 0; ks < 2; ++ks)
-                            mma_e4m3_ss<kOperandHigh64>(d, q_op + ((8 * kPanel + ks * 32u) >> 4),
-                                                        k_at + ((ks * 32u) >> 4), qk_instr, ks > 0);
-                    } else {
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks)
-                            mma_e4m3_ss<kOperandHigh>(
-                                d, q_op + (((g - 1) * 2 * kPanel + ks * 32u) >> 4),
-                                k_at + ((ks * 32u) >> 4), qk_instr, true);
-                    }
-                    mma_commit(&sm.empty[slot]);
+                    for (uint32_t ks = 0; ks < 2; ++ks)
+                        mma_e4m3_ss<kOperandHigh64>(d, q_op + ((8 * kPanel + ks * 32u) >> 4),
+                                                    k_at + ((ks * 32u) >> 4), qk_instr, ks > 0);
                 } else {
 #pragma unroll
-                    for (uint32_t x = 0; x < group_panels(g); ++x)
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks) {
-                            const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
-                            mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
-                        }
-                    if (g == 0) mma_commit(&sm.empty[slot]);  // the rotated columns are done with
+                    for (uint32_t ks = 0; ks < 4; ++ks)
+                        mma_e4m3_ss<kOperandHigh>(d, q_op + (((g - 1) * 2 * kPanel + ks * 32u) >> 4),
+                                                  k_at + ((ks * 32u) >> 4), qk_instr, true);
                 }
-                if (g == kGroups - 1) {
-                    mma_commit(&sm.s_full[buf]);
-                    if (!FP8 && last) mma_commit(&sm.q_free);
-                }
+                mma_commit(&sm.empty[slot]);
+                if (g == kCodePanels - 1) mma_commit(&sm.s_full[buf]);
             }
             __syncwarp();
         }
@@ -342,22 +460,18 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     // O^T (+)= V^T P^T of tile n, the `first` of a segment or not; `odd`: the
     // segment's parity
     auto values = [&](uint32_t n, bool first, uint32_t odd) {
-        const uint32_t buf = n & 1u;
         if (first && !wait_phase(&sm.o_free, odd ^ 1u, &sm.stop, a.wait_limit)) return false;
         if (!wait_phase(&sm.p_full, n & 1u, &sm.stop, a.wait_limit)) return false;
         fence_after_sync();
-        const uint32_t v_tile = FP8 ? v_op : v_op + (((buf * 9 + 1) * kPanel) >> 4);
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-            if constexpr (FP8) {
-                if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_limit)) return false;
-            }
+            if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_limit)) return false;
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t ks = 0; ks < 4; ++ks)
-                    mma_f16_ss(tmem + j * kHeads, v_tile + ((2 * j * kPanel + ks * 2048u) >> 4),
+                    mma_f16_ss(tmem + j * kHeads, v_op + ((2 * j * kPanel + ks * 2048u) >> 4),
                                p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
-                mma_commit(FP8 ? &sm.v_empty[j] : &sm.empty[buf * kGroups + 1 + j]);
+                mma_commit(&sm.v_empty[j]);
                 if (j == 3) mma_commit(&sm.pv_done);
             }
             __syncwarp();
@@ -371,22 +485,21 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
     // of the tiles between S and O^T, by the parity of the tile: is it the
     // first of its segment, and the parity of that
     uint32_t firsts = 0, odd_segments = 0;
-    uint64_t* q_bar = FP8 ? &sm.q_ready : &sm.q_full;
     while (ok && (!w.done() || o_tile < s_tile)) {
         const uint32_t pending = s_tile - o_tile;
         bool take_s = !w.done() && pending < 2;
         if (take_s && pending > 0) {
             // both are possible: wait for either
-            const uint32_t slot = (s_tile & 1u) * kGroups + kGroups - 1;
+            const uint32_t slot = (s_tile & 1u) * kCodePanels + kCodePanels - 1;
             const int64_t t0 = clock64();
             while (true) {
-                if (phase_done(&sm.p_full, o_tile & 1u)) {
+                if (all_done(&sm.p_full, o_tile & 1u)) {
                     take_s = false;
                     break;
                 }
-                if (phase_done(&sm.full[slot], (s_tile >> 1) & 1u) &&
-                    phase_done(&sm.s_free[s_tile & 1u], ((s_tile >> 1) & 1u) ^ 1u) &&
-                    (i > 0 || phase_done(q_bar, s_segment & 1u)))
+                if (all_done(&sm.full[slot], (s_tile >> 1) & 1u) &&
+                    all_done(&sm.s_free[s_tile & 1u], ((s_tile >> 1) & 1u) ^ 1u) &&
+                    (i > 0 || all_done(&sm.q_ready, s_segment & 1u)))
                     break;
                 bool give_up = *reinterpret_cast<volatile uint32_t*>(&sm.stop) != 0;
                 if (clock64() - t0 > a.wait_limit) {
@@ -401,15 +514,14 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<FP8>& sm) {
             if (!ok) break;
         }
         if (take_s) {
-            if (i == 0) ok = wait_phase(q_bar, s_segment & 1u, &sm.stop, a.wait_limit);
+            if (i == 0) ok = wait_phase(&sm.q_ready, s_segment & 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
-            const uint32_t count = w.last - w.first;
-            ok = scores(s_tile, i + 1 == count);
+            ok = scores(s_tile);
             const uint32_t bit = 1u << (s_tile & 1u);
             firsts = i == 0 ? firsts | bit : firsts & ~bit;
             odd_segments = s_segment & 1u ? odd_segments | bit : odd_segments & ~bit;
             ++s_tile;
-            if (++i == count) {
+            if (++i == w.last - w.first) {
                 i = 0;
                 ++s_segment;
                 w.next(a.split);
@@ -546,8 +658,10 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) s[e] = fmaf(s2[e], 0.0625f, s[e]);
                 }
-                fence_before_sync();
-                if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+                if constexpr (FP8) {
+                    fence_before_sync();
+                    if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) s[e] = 0.0f;
@@ -607,7 +721,6 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                         }
                     }
                     tmem_st_wait();
-                    fence_before_sync();
                 }
             }
             // a row that has seen no position keeps m = -inf: subtract 0
@@ -647,6 +760,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                     }
                 }
                 fence_async_smem();
+                fence_before_sync();  // S has been read, O^T may have been rescaled
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full);
             }
@@ -674,9 +788,12 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
         fence_after_sync();
         float* part = slot_of(a, blockIdx.x, w.first == 0 ? 1 : 0);
         uint16_t* out = a.out + ((uint64_t)w.t * a.H + head0) * kLatent;
-        const bool odd = lane & 1u;
-#pragma unroll 1
-        for (uint32_t c = 0; c < rows; c += 16) {
+        // A lane has one column (its own) of 16 heads at a time: neighbours
+        // swap, so that each has two columns of every other head.
+        const uint32_t odd = lane & 1u;
+        uint16_t* out_at = out + (uint64_t)odd * kLatent + (tid & ~1u);
+        float* part_at = part + (uint64_t)odd * kLatent + (tid & ~1u);
+        auto store = [&](auto whole_const, uint32_t c) {
             float f[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] = sm.alpha[c + e];
@@ -684,22 +801,27 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
             for (uint32_t j = 0; j < 4; ++j) {
                 float o[16];
                 tmem_ld_32x16(o, tmem + j * kHeads + c);
-                // a lane has one column (its own) of 16 heads: neighbours swap,
-                // so that each has two columns of every other head
 #pragma unroll
                 for (uint32_t e = 0; e < 16; e += 2) {
                     const float x = o[e] * f[e], y = o[e + 1] * f[e + 1];
                     const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-                    const uint32_t h = c + e + odd;
-                    if (h >= rows) continue;
-                    const uint64_t at = (uint64_t)h * kLatent + j * 128u + (tid & ~1u);
                     const float lo = odd ? got : x, hi = odd ? y : got;
-                    if (whole)
-                        *reinterpret_cast<uint32_t*>(out + at) = pack_bf16x2(lo, hi);
-                    else
-                        *reinterpret_cast<float2*>(part + at) = make_float2(lo, hi);
+                    if (c + e + odd < rows) {
+                        const uint64_t at = (uint64_t)(c + e) * kLatent + j * 128u;
+                        if constexpr (decltype(whole_const)::value)
+                            *reinterpret_cast<uint32_t*>(out_at + at) = pack_bf16x2(lo, hi);
+                        else
+                            *reinterpret_cast<float2*>(part_at + at) = make_float2(lo, hi);
+                    }
                 }
             }
+        };
+#pragma unroll 1
+        for (uint32_t c = 0; c < rows; c += 16) {
+            if (whole)
+                store(std::true_type{}, c);
+            else
+                store(std::false_type{}, c);
         }
         fence_before_sync();
         if (tid < rows) {
@@ -739,10 +861,10 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        for (uint32_t i = 0; i < 2 * kGroups; ++i) {
+        for (uint32_t i = 0; i < 2 * kCodePanels; ++i) {
             mbar_init(&sm.full[i], 1);
-            // E4M3: value columns go to the matrix unit and to four converting warps
-            mbar_init(&sm.empty[i], FP8 && i % kGroups ? 5 : 1);
+            // E4M3: latent columns go to the matrix unit and to four warps
+            mbar_init(&sm.empty[i], FP8 && i % kCodePanels ? 5 : 1);
         }
         for (uint32_t i = 0; i < 4; ++i) {
             mbar_init(&sm.v_full[i], 4);
@@ -778,7 +900,10 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     } else if (warp == 4) {
         feed<FP8, WITHHOLD>(a, maps, qm, sm);
     } else if (warp == 5) {
-        multiply<FP8>(a, sm);
+        if constexpr (FP8)
+            multiply_codes(a, sm);
+        else
+            multiply(a, sm);
     } else {
         if constexpr (FP8) convert(a, sm);
     }
