@@ -28,7 +28,7 @@
 // KB, each in four groups (128 latent columns; the first with the rotated
 // columns) that are filled one by one and freed as the four row blocks of O^T
 // complete.  E4M3: Q's two parts 72 KB, two tiles of codes 80 KB, one fp16
-// tile of values 64 KB in four groups.  P 8 KB.  O^T fills 256 of the 512
+// tile of values 64 KB in two halves.  P 8 KB.  O^T fills 256 of the 512
 // columns of tensor memory, two S tiles 128.  The MMA thread takes what is
 // ready first, the next S or the next O^T, so that neither a late tile nor a
 // late softmax holds up the other.
@@ -51,6 +51,7 @@ constexpr uint32_t kLatent = 512, kRow = 576;
 constexpr uint32_t kPanel = kTile * 128;      // 64 columns of a 16-bit tile, or 128 codes
 constexpr uint32_t kGroups = 4;               // of a bf16 tile: 128 latent columns each
 constexpr uint32_t kCodePanels = 5;           // of an E4M3 tile: 64 rotated columns, 4 x 128 latent ones
+constexpr uint32_t kCodeGroups = 2;           // panels 0 - 2 and 3, 4
 constexpr uint32_t kMaxCtas = 192;
 constexpr uint32_t kTmemColumns = 512, kScoreColumn = 256;
 constexpr float kSlack = 6.0f;                // log2 of the largest weight before a rescale
@@ -91,19 +92,18 @@ struct Smem {
     // two tiles as they come: nine panels each, or five of codes
     unsigned char kv[2 * (FP8 ? kCodePanels : 9) * kPanel];
     unsigned char values[FP8 ? 8 * kPanel : 16];  // E4M3: the value columns in fp16
-    // groups of the two tiles: four of bf16 columns, or the five panels of codes
-    uint64_t full[2 * kCodePanels], empty[2 * kCodePanels];
-    uint64_t v_full[4], v_empty[4];  // groups of `values`
+    uint64_t full[2 * kGroups], empty[2 * kGroups];  // groups of the two tiles
+    uint64_t v_full[2], v_empty[2];                  // halves of `values`
     uint64_t q_full, q_ready, q_free;
-    uint64_t s_full[2], s_free[2], p_full, pv_done, o_free, drained;
+    uint64_t s_full[2], p_full, pv_done, o_free, drained;
     uint64_t there[8];  // of a tile: positions that are there
     float alpha[kHeads], m[kHeads], l[kHeads], q_scale[kHeads];
     SplitShared<threads_of<FP8>()> split;
     uint32_t tmem, stop;
 };
 
-// The panels of a bf16 tile: rotated columns, then eight of the latent ones.
-// Group g: its first panel and their number.
+// The panels of a tile: rotated columns, then eight (codes: four) of the
+// latent ones.  Group g: its first panel and their number.
 __device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g + 1u; }
 __device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 3u : 2u; }
 
@@ -134,7 +134,7 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 template <bool FP8, bool WITHHOLD>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
-    constexpr uint32_t kTileGroups = FP8 ? kCodePanels : kGroups, kSlots = 2 * kTileGroups;
+    constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups, kSlots = 2 * kTileGroups;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -177,7 +177,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             for (uint32_t g = 0; g < kTileGroups; ++g) {
                 ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
-                const uint32_t panels = FP8 ? 1u : group_panels(g);
+                const uint32_t panels = group_panels(g);
                 if (lane == 0) {
                     if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
                     mbar_arrive_expect_tx(&sm.full[at.slot], (n << maps.log_rows) * 128u * panels);
@@ -186,13 +186,19 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 if (!(WITHHOLD && issued == 0)) {
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
                     const uint32_t base = smem_addr(
-                        sm.kv + (FP8 ? at.slot : (tile & 1u) * 9 + group_start(g)) * kPanel);
+                        sm.kv + ((tile & 1u) * (FP8 ? kCodePanels : 9) + group_start(g)) * kPanel);
                     each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
                                               const CUtensorMap* map) {
                         const uint32_t dst = base + (unit << maps.log_rows) * 128u;
                         if constexpr (FP8) {
-                            tma_rows(dst, map, g == 0 ? kLatent : (g - 1) * 128u, 0, row, page, 0,
-                                     bar);
+                            if (g == 0) {
+                                tma_rows(dst, map, kLatent, 0, row, page, 0, bar);
+                                tma_rows(dst + kPanel, map, 0, 0, row, page, 0, bar);
+                                tma_rows(dst + 2 * kPanel, map, 128, 0, row, page, 0, bar);
+                            } else {
+                                tma_rows(dst, map, 256, 0, row, page, 0, bar);
+                                tma_rows(dst + kPanel, map, 384, 0, row, page, 0, bar);
+                            }
                         } else if (g == 0) {
                             tma_rows(dst, map, kLatent, 0, row, page, 0, bar);
                             tma_rows(dst + kPanel, map, 0, 0, row, page, 0, bar);
@@ -237,19 +243,21 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
         for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
             const uint32_t buf = tile & 1u;
 #pragma unroll 1
-            for (uint32_t g = 0; g < 4; ++g) {
-                const uint32_t slot = buf * kCodePanels + 1 + g;
-                ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_limit);
+            for (uint32_t g = 0; g < 4; ++g) {  // 128 columns each
+                const uint32_t slot = buf * kCodeGroups + (g >> 1);
+                if (!(g & 1u))
+                    ok = wait_phase(&sm.full[slot], (tile >> 1) & 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 const uint64_t there = sm.there[tile & 7u];
-                const unsigned char* src = sm.kv + slot * kPanel;
+                const unsigned char* src = sm.kv + (buf * kCodePanels + 1 + g) * kPanel;
                 uint4 v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t r = (i0 >> 3) + 16u * k;
                     v[k] = *reinterpret_cast<const uint4*>(src + r * 128u + (((c ^ r) & 7u) << 4));
                 }
-                ok = wait_phase(&sm.v_empty[g], (tile & 1u) ^ 1u, &sm.stop, a.wait_limit);
+                if (!(g & 1u))
+                    ok = wait_phase(&sm.v_empty[g >> 1], (tile & 1u) ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 unsigned char* dst = sm.values + 2 * g * kPanel;
 #pragma unroll
@@ -271,11 +279,13 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
                     *reinterpret_cast<uint4*>(line + (((o + (odd ^ 1u)) ^ (r & 7u)) << 4)) =
                         odd ? x : y;
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.v_full[g]);
-                    mbar_arrive(&sm.empty[slot]);
+                if (g & 1u) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.v_full[g >> 1]);
+                        mbar_arrive(&sm.empty[slot]);
+                    }
                 }
             }
         }
@@ -424,34 +434,31 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
     auto all_done = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, phase_done(bar, parity)) != 0;
     };
-    // S of tile n.  (Fences only where tensor memory passes between threads,
-    // about 140 cycles each: operands in shared memory come with their
-    // barriers.)
+    // S of tile n (its buffer is free as in multiply)
     auto scores = [&](uint32_t n) {
         const uint32_t buf = n & 1u;
-        if (!wait_phase(&sm.s_free[buf], ((n >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit)) return false;
-        fence_after_sync();
         const uint32_t k_tile = k_op + ((buf * kCodePanels * kPanel) >> 4);
         const uint32_t d = tmem + kScoreColumn + buf * kTile;
 #pragma unroll
-        for (uint32_t g = 0; g < kCodePanels; ++g) {
-            const uint32_t slot = buf * kCodePanels + g;
+        for (uint32_t g = 0; g < kCodeGroups; ++g) {
+            const uint32_t slot = buf * kCodeGroups + g;
             if (!wait_phase(&sm.full[slot], (n >> 1) & 1u, &sm.stop, a.wait_limit)) return false;
             if (elect_one()) {
-                const uint32_t k_at = k_tile + ((g * kPanel) >> 4);
                 if (g == 0) {  // rotated columns: 64-byte lines of Q behind its panels
 #pragma unroll
                     for (uint32_t ks = 0; ks < 2; ++ks)
                         mma_e4m3_ss<kOperandHigh64>(d, q_op + ((8 * kPanel + ks * 32u) >> 4),
-                                                    k_at + ((ks * 32u) >> 4), qk_instr, ks > 0);
-                } else {
+                                                    k_tile + ((ks * 32u) >> 4), qk_instr, ks > 0);
+                }
+#pragma unroll
+                for (uint32_t x = 0; x < 2; ++x)
 #pragma unroll
                     for (uint32_t ks = 0; ks < 4; ++ks)
-                        mma_e4m3_ss<kOperandHigh>(d, q_op + (((g - 1) * 2 * kPanel + ks * 32u) >> 4),
-                                                  k_at + ((ks * 32u) >> 4), qk_instr, true);
-                }
+                        mma_e4m3_ss<kOperandHigh>(
+                            d, q_op + (((2 * g + x) * 2 * kPanel + ks * 32u) >> 4),
+                            k_tile + (((1 + 2 * g + x) * kPanel + ks * 32u) >> 4), qk_instr, true);
                 mma_commit(&sm.empty[slot]);
-                if (g == kCodePanels - 1) mma_commit(&sm.s_full[buf]);
+                if (g == kCodeGroups - 1) mma_commit(&sm.s_full[buf]);
             }
             __syncwarp();
         }
@@ -465,13 +472,15 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
         fence_after_sync();
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-            if (!wait_phase(&sm.v_full[j], n & 1u, &sm.stop, a.wait_limit)) return false;
+            if (!(j & 1u) &&
+                !wait_phase(&sm.v_full[j >> 1], n & 1u, &sm.stop, a.wait_limit))
+                return false;
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t ks = 0; ks < 4; ++ks)
                     mma_f16_ss(tmem + j * kHeads, v_op + ((2 * j * kPanel + ks * 2048u) >> 4),
                                p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
-                mma_commit(&sm.v_empty[j]);
+                if (j & 1u) mma_commit(&sm.v_empty[j >> 1]);
                 if (j == 3) mma_commit(&sm.pv_done);
             }
             __syncwarp();
@@ -490,7 +499,7 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
         bool take_s = !w.done() && pending < 2;
         if (take_s && pending > 0) {
             // both are possible: wait for either
-            const uint32_t slot = (s_tile & 1u) * kCodePanels + kCodePanels - 1;
+            const uint32_t slot = (s_tile & 1u) * kCodeGroups + kCodeGroups - 1;
             const int64_t t0 = clock64();
             while (true) {
                 if (all_done(&sm.p_full, o_tile & 1u)) {
@@ -498,7 +507,6 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
                     break;
                 }
                 if (all_done(&sm.full[slot], (s_tile >> 1) & 1u) &&
-                    all_done(&sm.s_free[s_tile & 1u], ((s_tile >> 1) & 1u) ^ 1u) &&
                     (i > 0 || all_done(&sm.q_ready, s_segment & 1u)))
                     break;
                 bool give_up = *reinterpret_cast<volatile uint32_t*>(&sm.stop) != 0;
@@ -549,13 +557,13 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
 // nearest E4M3 number and q2 the remainder, exact while q1's step is not
 // below E4M3's smallest (2^-9).  A row with an infinity or a NaN becomes NaN
 // (E4M3 has no infinity; its scores are not finite either way).  A warp takes
-// 16 heads, four at a time, its lanes the 72 chunks of 8 values of a row.
+// 16 heads, four at a time with the next four on their way, its lanes the 72
+// chunks of 8 values of a row.
 __device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, uint32_t t,
                                               uint32_t head0, uint32_t rows) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     constexpr int kAtOnce = 4;
-    for (uint32_t i0 = 0; i0 < 16; i0 += kAtOnce) {
-        uint4 v[kAtOnce][3];
+    auto load = [&](uint32_t i0, uint4(&v)[kAtOnce][3]) {
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n) {
             const uint32_t h = warp * 16 + i0 + n;
@@ -571,6 +579,17 @@ __device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, 
                                                                           : qr + (c - 64) * 8));
             }
         }
+    };
+    uint4 ahead[kAtOnce][3];
+    load(0, ahead);
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < 16; i0 += kAtOnce) {
+        uint4 v[kAtOnce][3];
+#pragma unroll
+        for (int n = 0; n < kAtOnce; ++n)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[n][k] = ahead[n][k];
+        if (i0 + kAtOnce < 16) load(i0 + kAtOnce, ahead);
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n) {
             uint32_t top = 0;
@@ -657,10 +676,6 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                     tmem_ld_16x64(s2, tmem + (16u << 16) + kScoreColumn + buf * kTile);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) s[e] = fmaf(s2[e], 0.0625f, s[e]);
-                }
-                if constexpr (FP8) {
-                    fence_before_sync();
-                    if (lane == 0) mbar_arrive(&sm.s_free[buf]);
                 }
             } else {
 #pragma unroll
@@ -861,22 +876,19 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        for (uint32_t i = 0; i < 2 * kCodePanels; ++i) {
+        for (uint32_t i = 0; i < 2 * kGroups; ++i) {
             mbar_init(&sm.full[i], 1);
-            // E4M3: latent columns go to the matrix unit and to four warps
-            mbar_init(&sm.empty[i], FP8 && i % kCodePanels ? 5 : 1);
+            // E4M3: codes go to the matrix unit and to four warps
+            mbar_init(&sm.empty[i], FP8 ? 5 : 1);
         }
-        for (uint32_t i = 0; i < 4; ++i) {
+        for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.v_empty[i], 1);
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_ready, 4);
         mbar_init(&sm.q_free, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_free[i], 4);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.p_full, 4);
         mbar_init(&sm.pv_done, 1);
         mbar_init(&sm.o_free, 4);
