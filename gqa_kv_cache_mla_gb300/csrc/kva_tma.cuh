@@ -157,6 +157,14 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// The same columns and rows into L2 only.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, uint32_t col, uint32_t head,
+                                             uint32_t row, uint32_t page, uint32_t plane) {
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];"
+                 ::"l"(map), "r"(col), "r"(head), "r"(row), "r"(page), "r"(plane)
+                 : "memory");
+}
+
 // Calls issue(unit, row, page, map) for every copy that the lanes planned.  A
 // tile of one copy is issued with the same arguments in all lanes, by one
 // elected thread; of several copies every lane issues its own (the hardware

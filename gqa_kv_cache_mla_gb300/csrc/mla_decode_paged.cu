@@ -135,6 +135,7 @@ template <bool FP8, bool WITHHOLD>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
     constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups, kSlots = 2 * kTileGroups;
+    constexpr uint32_t kTilePanels = FP8 ? kCodePanels : 9;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -156,23 +157,27 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             }
         }
         ++segment;
-        for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
-            const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
-            UnitCopy copy[2];
+        UnitCopy copy[2];
+        uint32_t n = 0, t_lo = 0, t_hi = 0;
+        auto plan = [&](uint32_t i) {
             uint64_t there = 0;
-            uint32_t n = 0;
+            n = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 copy[h].level = 4;
                 if (h && maps.log_rows) continue;
                 copy[h] = plan_unit(maps, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
-                                    p_tile, w.span.start, w.span.hi, lane + 32u * h);
+                                    (int64_t)(w.span.tile0 + i) * kTile, w.span.start, w.span.hi,
+                                    lane + 32u * h);
                 if (copy[h].bad_page) bad_page = 1;
                 n += __popc(__ballot_sync(0xffffffffu, copy[h].there != 0));
                 there |= copy[h].there;
             }
-            const uint32_t t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
-            const uint32_t t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+            t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
+            t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+        };
+        plan(w.first);
+        for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
 #pragma unroll 1
             for (uint32_t g = 0; g < kTileGroups; ++g) {
                 ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
@@ -186,7 +191,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 if (!(WITHHOLD && issued == 0)) {
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
                     const uint32_t base = smem_addr(
-                        sm.kv + ((tile & 1u) * (FP8 ? kCodePanels : 9) + group_start(g)) * kPanel);
+                        sm.kv + ((tile & 1u) * kTilePanels + group_start(g)) * kPanel);
                     each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
                                               const CUtensorMap* map) {
                         const uint32_t dst = base + (unit << maps.log_rows) * 128u;
@@ -211,6 +216,19 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 }
                 at.step();
                 ++issued;
+            }
+            if (ok && i + 1 < w.last) {
+                // The next tile's place is taken for a while yet: into L2 with
+                // it (256 requests, 128 heads, bf16: 472 -> 453 us; a tile of
+                // codes, half as large, gains nothing: 478 and 480 us).
+                plan(i + 1);
+                if (!FP8 && ((i & 1u) == hb || a.HB == 1))
+                    each_copy(maps, copy, [&](uint32_t, uint32_t row, uint32_t page,
+                                              const CUtensorMap* map) {
+#pragma unroll
+                        for (uint32_t x = 0; x < kTilePanels; ++x)
+                            tma_prefetch(map, x * (FP8 ? 128u : 64u), 0, row, page, 0);
+                    });
             }
         }
         if (ok) w.next(a.split);
