@@ -112,10 +112,12 @@ struct UnitCopy {
 
 // Unit c (of 64 >> log_rows) of the tile at position p_tile of request b, for
 // positions [start, hi).
-__device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m, const uint32_t* page_table,
-                                              uint32_t max_pages, uint32_t num_pages,
-                                              const FastDiv& ps, uint32_t b, int64_t p_tile,
-                                              int64_t start, int64_t hi, uint32_t c) {
+__host__ __device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m,
+                                                       const uint32_t* page_table,
+                                                       uint32_t max_pages, uint32_t num_pages,
+                                                       const FastDiv& ps, uint32_t b,
+                                                       int64_t p_tile, int64_t start, int64_t hi,
+                                                       uint32_t c) {
     UnitCopy u;
     u.page = u.row = 0;
     u.level = 4;
@@ -126,7 +128,15 @@ __device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m, const uint32_t
     if (c >= (64u >> m.log_rows) || p >= hi || p_end <= start) return u;
     const uint32_t idx = fast_div((uint32_t)p, ps);
     u.row = (uint32_t)p - idx * ps.d;
-    u.page = idx < max_pages ? __ldg(page_table + (uint64_t)b * max_pages + idx) : KVW_PAGE_UNMAPPED;
+    u.page = KVW_PAGE_UNMAPPED;
+    if (idx < max_pages) {
+        const uint32_t* id = page_table + (uint64_t)b * max_pages + idx;
+#ifdef __CUDA_ARCH__
+        u.page = __ldg(id);
+#else
+        u.page = *id;
+#endif
+    }
     if (u.page >= num_pages) {
         u.bad_page = true;
         return u;

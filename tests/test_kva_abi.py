@@ -236,3 +236,29 @@ def test_mla_workspace_is_exact():
         with pytest.raises(kvw.KvwError):
             kva.kva_mla_decode_workspace(heads)
     assert mla(None) == kvw.KVW_EINVAL
+
+
+# (page, kv, layer, token, head): a copy of the cache walks page, plane, token
+# and head with positive strides below 2^40 bytes; one index needs no stride
+@pytest.mark.parametrize("at,stride,want", [
+    (0, -65536, kvw.KVW_EINVAL), (0, 0, kvw.KVW_EINVAL), (0, 1 << 39, kvw.KVW_EINVAL),
+    (1, -32768, kvw.KVW_EINVAL), (1, 0, kvw.KVW_EINVAL), (1, 1 << 39, kvw.KVW_EINVAL),
+    (3, -1024, kvw.KVW_EINVAL), (3, 0, kvw.KVW_EINVAL), (3, 1 << 39, kvw.KVW_EINVAL),
+    (4, -128, kvw.KVW_EINVAL), (4, 0, kvw.KVW_EINVAL), (4, 1 << 39, kvw.KVW_EINVAL),
+    (2, -16384, kvw.KVW_OK), (2, 0, kvw.KVW_OK), (2, 1 << 45, kvw.KVW_OK),
+    (0, (1 << 39) - 8, kvw.KVW_OK),
+])
+def test_gqa_strides(at, stride, want):
+    strides = [65536, 32768, 16384, 1024, 128]
+    strides[at] = stride
+    assert gqa(cache(strides=tuple(strides))) == want
+    one = {0: "num_pages", 4: "num_heads"}.get(at)
+    if one and stride % 8 == 0:
+        assert gqa(cache(strides=tuple(strides), **{one: 1})) == kvw.KVW_OK
+
+
+def test_query_strides():
+    top = 1 << 39  # bytes of a row stride of the latent queries stay below 2^40
+    assert mla(mla_cache(), qls=top - 8, qrs=top - 8) == kvw.KVW_OK
+    assert mla(mla_cache(), qls=top - 8, qrs=top) == kvw.KVW_EINVAL
+    assert gqa(cache(), qs=1 << 45) == kvw.KVW_OK
