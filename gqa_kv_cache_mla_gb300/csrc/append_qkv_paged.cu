@@ -23,6 +23,13 @@
 // of one token and `passes` passes of 32 / TL rows; the rows' vectors are
 // loaded two passes ahead of their use.  CTAs are persistent and stage the
 // ragged tables once.
+//
+// Measured, 32 ragged requests of up to 2048 new tokens, 32 + 2 x 8 heads of
+// 128 (780 MB): 130 us, 6.0 TB/s, 88 % of the card's copy rate; E4M3 cache
+// 133 us, with norms 133 us.  Three CTAs per SM (80 registers, a few scalars
+// spilled): with two, 131, 151 and 142 us; with four (64 registers) 138, 129
+// and 190 us.  One pass ahead instead of two: 134, 140 and 136 us.  One token:
+// 2.4 us on the device.
 #include <cstdint>
 
 #include "kva_common.cuh"
@@ -63,7 +70,7 @@ struct TokenSlot {
 };
 
 template <int TL, bool INTERLEAVED, bool FP8, bool MROPE>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a) {
     extern __shared__ uint32_t s_tables[];
     uint32_t* s_off = s_tables;
     uint32_t* s_clen = s_tables + a.B + 1;
