@@ -31,11 +31,20 @@
  *   and attends to the positions max(0, p - window + 1) .. p, its own
  *   included: its key and value (its latent row) are in the cache already.
  *   Any mix of new tokens per request is right; the split is made for few
- *   (each token reads its context by itself, shared reads meet in L2).
+ *   (neighbouring tokens of a request share a GQA pass over their contexts
+ *   where their rows fit 16 to a key-value head, and read them one by one
+ *   otherwise; shared reads meet in L2).
+ * - A page table reaches max_pages_per_seq * page_size positions, at most
+ *   2^32 - 256.  A position past that has no valid page.
  * - A position whose slot has no valid page takes no part in the softmax,
  *   as if masked, and sets KVW_ERR_PAGE.  A token left with no position at
  *   all gets a row of zeros and lse = -infinity.
  * - Malformed offsets set KVW_ERR_OFFSETS; out and lse are left as they were.
+ * - The cache is read by the copy engine, whose stages complete through
+ *   bounded waits: KVW_ERR_TIMEOUT as in kvw.h, out and lse are then partly
+ *   written.  It takes strides that are positive, multiples of 16 bytes and
+ *   below 2^40 bytes in every dimension of more than one index (pages,
+ *   planes, tokens, heads; the layer stride is free): KVW_EINVAL for others.
  * - Cache rows behind a token's last position are never used, whatever they
  *   hold (NaN included).  A NaN or an infinity in a used row or in a query
  *   propagates as the formula has it.
@@ -108,9 +117,9 @@ int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const void* qkv,
  * over the positions j named above (window = 0: from 0).  Scores, softmax
  * statistics and sums are fp32; the products take bf16 operands with a bf16
  * cache and fp16 operands with an E4M3 cache (codes are exact in fp16; each
- * query row is brought into fp16's range by a power of two, exactly unless
- * the row's values span more than 2^25 in magnitude), and the weights e^s
- * are rounded to that type, relative to the row's running maximum.
+ * query row is brought into fp16's range by a power of two, which loses only
+ * what is below 2^-39 of the row's largest value), and the weights e^s are
+ * rounded to that type, relative to the row's running maximum.
  *
  *   out            device, bf16 [tot_seq_len, num_q_heads, head_size]
  *   lse            device, f32 [tot_seq_len, num_q_heads], or NULL
@@ -144,7 +153,10 @@ int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads, uint32
  *                     + dot(q_rope[t, h], row_j[512:576]))
  *   out[t, h] = bf16(sum_j e^s_j row_j[0:512] / sum_j e^s_j)
  *   lse[t, h] = log(sum_j e^s_j)
- * over positions 0 .. p.  Precision as kva_gqa_decode_paged.
+ * over positions 0 .. p.  Precision as kva_gqa_decode_paged, except that the
+ * scores of an E4M3 cache come from its codes and each query row as two E4M3
+ * parts (the row's values to within 2^-21 of its largest); a row that holds
+ * an infinity or a NaN gives NaN.
  *
  *   out            device, bf16 [tot_seq_len, num_heads, 512]
  *   lse            device, f32 [tot_seq_len, num_heads], or NULL
@@ -155,8 +167,7 @@ int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads, uint32
  *                  kvw_mla_rope_rmsnorm_quant has stride num_heads*64)
  *   cache          host pointer: bf16 or E4M3, num_heads 1, head_size 576
  *   workspace      device, kva_mla_decode_workspace(...) bytes
- * 1 <= num_heads <= 1024, tot_seq_len <= 2^20.  The matrix unit's stages
- * complete through bounded waits: KVW_ERR_TIMEOUT as in kvw.h.
+ * 1 <= num_heads <= 1024, tot_seq_len <= 2^20, query row strides below 2^39.
  */
 int kva_mla_decode_paged(void* out, float* lse, const void* q_latent,
                          int64_t q_latent_row_stride, const void* q_rope,
