@@ -79,8 +79,12 @@ struct QMaps {
 };
 
 template <bool FP8>
+constexpr uint32_t feeders_of() {
+    return FP8 ? 1 : 2;
+}
+template <bool FP8>
 constexpr int threads_of() {
-    return FP8 ? 320 : 192;
+    return 32 * ((FP8 ? 9 : 5) + feeders_of<FP8>());
 }
 
 template <bool FP8>
@@ -131,34 +135,45 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 
 // ---------------------------------------------------------------- feeding
 
-template <bool FP8, bool WITHHOLD>
+// Two warps feed, each half of the groups of every tile: one needs about 400
+// cycles to issue a group and 1200 to look up the next tile's page and fetch
+// it ahead, which together were most of a tile's time.
+template <bool FP8, bool WITHHOLD, uint32_t WHICH>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
-    constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups, kSlots = 2 * kTileGroups;
+    constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups;
     constexpr uint32_t kTilePanels = FP8 ? kCodePanels : 9;
+    constexpr int kUnroll = FP8 ? 8 : 1;
+    constexpr uint32_t kEach = kTileGroups / feeders_of<FP8>(), kFrom = WHICH * kEach;
+    constexpr uint32_t kTo = kFrom + kEach;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
+    auto column = [](uint32_t panel) {
+        return panel == 0 ? kLatent : (panel - 1) * (FP8 ? 128u : 64u);
+    };
     Walk w;
     w.begin(a.split, sm.split.start);
-    RingPos<(int)kSlots> at;
-    uint32_t bad_page = 0, issued = 0, tile = 0, segment = 0;
+    uint32_t bad_page = 0, tile = 0, segment = 0;
+    uint32_t stopped_at = kFrom;  // the group whose place was not free in time
     bool ok = true;
     while (ok && !w.done()) {
-        if constexpr (!FP8) {
+        if constexpr (!FP8 && WHICH == feeders_of<FP8>() - 1) {
             ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
-            __syncwarp();
-            if (lane < 9) {
-                const uint32_t dst = smem_addr(sm.q + lane * kPanel), bar = smem_addr(&sm.q_full);
-                if (lane == 0)
-                    tma_3d(dst, &qm.rope, 0, hb * kHeads, w.t, bar);
-                else
-                    tma_3d(dst, &qm.latent, (lane - 1) * 64, hb * kHeads, w.t, bar);
+            if (elect_one()) {
+                const uint32_t bar = smem_addr(&sm.q_full);
+                mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
+                tma_3d(smem_addr(sm.q), &qm.rope, 0, hb * kHeads, w.t, bar);
+#pragma unroll kUnroll
+                for (uint32_t x = 0; x < 8; ++x)
+                    tma_3d(smem_addr(sm.q + (x + 1) * kPanel), &qm.latent, x * 64, hb * kHeads, w.t,
+                           bar);
             }
+            __syncwarp();
+            ++segment;
         }
-        ++segment;
         UnitCopy copy[2];
         uint32_t n = 0, t_lo = 0, t_hi = 0;
+        uint32_t row = 0, page = 0;  // of a tile that is one copy
         auto plan = [&](uint32_t i) {
             uint64_t there = 0;
             n = 0;
@@ -175,59 +190,68 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             }
             t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
             t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+            row = __shfl_sync(0xffffffffu, copy[0].row, 0);
+            page = __shfl_sync(0xffffffffu, copy[0].page, 0);
         };
         plan(w.first);
-        for (uint32_t i = w.first; ok && i < w.last; ++i, ++tile) {
-#pragma unroll 1
-            for (uint32_t g = 0; g < kTileGroups; ++g) {
-                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
-                if (!ok) break;
-                const uint32_t panels = group_panels(g);
-                if (lane == 0) {
-                    if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
-                    mbar_arrive_expect_tx(&sm.full[at.slot], (n << maps.log_rows) * 128u * panels);
+        for (uint32_t i = w.first; ok && i < w.last; ++i) {
+#pragma unroll kUnroll
+            for (uint32_t g = kFrom; g < kTo; ++g) {
+                uint64_t* full = &sm.full[(tile & 1u) * kTileGroups + g];
+                if (ok) {
+                    stopped_at = g;
+                    ok = wait_phase(&sm.empty[(tile & 1u) * kTileGroups + g],
+                                    ((tile >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit);
                 }
-                __syncwarp();
-                if (!(WITHHOLD && issued == 0)) {
-                    const uint32_t bar = smem_addr(&sm.full[at.slot]);
-                    const uint32_t base = smem_addr(
-                        sm.kv + ((tile & 1u) * kTilePanels + group_start(g)) * kPanel);
-                    each_copy(maps, copy, [&](uint32_t unit, uint32_t row, uint32_t page,
-                                              const CUtensorMap* map) {
-                        const uint32_t dst = base + (unit << maps.log_rows) * 128u;
-                        if constexpr (FP8) {
-                            if (g == 0) {
-                                tma_rows(dst, map, kLatent, 0, row, page, 0, bar);
-                                tma_rows(dst + kPanel, map, 0, 0, row, page, 0, bar);
-                                tma_rows(dst + 2 * kPanel, map, 128, 0, row, page, 0, bar);
-                            } else {
-                                tma_rows(dst, map, 256, 0, row, page, 0, bar);
-                                tma_rows(dst + kPanel, map, 384, 0, row, page, 0, bar);
-                            }
-                        } else if (g == 0) {
-                            tma_rows(dst, map, kLatent, 0, row, page, 0, bar);
-                            tma_rows(dst + kPanel, map, 0, 0, row, page, 0, bar);
-                            tma_rows(dst + 2 * kPanel, map, 64, 0, row, page, 0, bar);
-                        } else {
-                            tma_rows(dst, map, g * 128u, 0, row, page, 0, bar);
-                            tma_rows(dst + kPanel, map, g * 128u + 64u, 0, row, page, 0, bar);
+                if (!ok) continue;
+                const uint32_t bytes = (n << maps.log_rows) * 128u * group_panels(g);
+                const uint32_t bar = smem_addr(full);
+                const uint32_t base = smem_addr(
+                    sm.kv + ((tile & 1u) * kTilePanels + group_start(g)) * kPanel);
+                const bool withheld = WITHHOLD && tile == 0 && g == 0;
+                if (maps.log_rows == 6) {  // one copy per panel
+                    if (elect_one()) {
+                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
+                        mbar_arrive_expect_tx(full, bytes);
+                        if (n && !withheld) {
+#pragma unroll kUnroll
+                            for (uint32_t x = 0; x < group_panels(g); ++x)
+                                tma_rows(base + x * kPanel, &maps.map[0],
+                                         column(group_start(g) + x), 0, row, page, 0, bar);
                         }
-                    });
+                    }
+                    __syncwarp();
+                } else {
+                    if (lane == 0) {
+                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
+                        mbar_arrive_expect_tx(full, bytes);
+                    }
+                    __syncwarp();
+                    if (!withheld)
+                        each_copy(maps, copy, [&](uint32_t unit, uint32_t r, uint32_t id,
+                                                  const CUtensorMap* map) {
+#pragma unroll kUnroll
+                            for (uint32_t x = 0; x < group_panels(g); ++x)
+                                tma_rows(base + x * kPanel + (unit << maps.log_rows) * 128u, map,
+                                         column(group_start(g) + x), 0, r, id, 0, bar);
+                        });
                 }
-                at.step();
-                ++issued;
             }
-            if (ok && i + 1 < w.last) {
+            if (!ok) break;
+            ++tile;
+            stopped_at = kFrom;
+            if (i + 1 < w.last) {
                 // The next tile's place is taken for a while yet: into L2 with
                 // it (256 requests, 128 heads, bf16: 472 -> 453 us; a tile of
                 // codes, half as large, gains nothing: 478 and 480 us).
                 plan(i + 1);
                 if (!FP8 && ((i & 1u) == hb || a.HB == 1))
-                    each_copy(maps, copy, [&](uint32_t, uint32_t row, uint32_t page,
+                    each_copy(maps, copy, [&](uint32_t, uint32_t r, uint32_t id,
                                               const CUtensorMap* map) {
-#pragma unroll
-                        for (uint32_t x = 0; x < kTilePanels; ++x)
-                            tma_prefetch(map, x * (FP8 ? 128u : 64u), 0, row, page, 0);
+#pragma unroll kUnroll
+                        for (uint32_t x = group_start(kFrom);
+                             x < group_start(kTo - 1) + group_panels(kTo - 1); ++x)
+                            tma_prefetch(map, column(x), 0, r, id, 0);
                     });
             }
         }
@@ -238,11 +262,14 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
         // copies still under way land in this CTA's memory: wait for them (a
         // bounded time) before the CTA may end
         if (lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
-        const uint32_t n = issued < kSlots ? issued : kSlots;
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint32_t x = issued - 1 - i;
-            drain_phase(&sm.full[x % kSlots], (x / kSlots) & 1u, a.wait_limit);
-        }
+#pragma unroll 1
+        for (uint32_t buf = 0; buf < 2; ++buf)
+#pragma unroll 1
+            for (uint32_t g = kFrom; g < kTo; ++g) {
+                const uint32_t issued = (tile + (g < stopped_at) + 1 - buf) >> 1;  // into this place
+                if (issued)
+                    drain_phase(&sm.full[buf * kTileGroups + g], (issued - 1) & 1u, a.wait_limit);
+            }
         if (!FP8 && segment) drain_phase(&sm.q_full, (segment - 1) & 1u, a.wait_limit);
     }
 }
@@ -313,8 +340,45 @@ __device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
 
 // ---------------------------------------------------------------- products
 
-// The products of a bf16 cache: one thread issues every MMA.  (Fences only where tensor memory passes
-// between threads: operands in shared memory come with their barriers.)
+// What the issuing thread of a bf16 cache keeps of its place: the next
+// group of S and the next O^T.  O^T goes first: it frees a tile's place, S only
+// takes one.  S runs at most two tiles ahead of O^T (its two buffers).  One
+// loop with one copy of either product: with the MMAs of a tile unrolled, and
+// more so with several copies of O^T, the loop's time was that of fetching its
+// instructions.
+struct Products {
+    Walk w;
+    uint32_t s_tile = 0, o_tile = 0, group = 0, i = 0, s_segment = 0;
+    // of the tiles between S and O^T, by the parity of the tile: is it the
+    // first of its segment, and the parity of that
+    uint32_t firsts = 0, odd_segments = 0;
+
+    __device__ __forceinline__ bool more(const MlaArgs&) const {
+        return !w.done() || o_tile < s_tile;
+    }
+    __device__ __forceinline__ bool s_next() const { return !w.done() && s_tile - o_tile < 2; }
+    __device__ __forceinline__ bool last_of_segment() const { return i + 1 == w.last - w.first; }
+    __device__ __forceinline__ void s_done(const MlaArgs& a) {
+        const uint32_t bit = 1u << (s_tile & 1u);
+        firsts = i == 0 ? firsts | bit : firsts & ~bit;
+        odd_segments = s_segment & 1u ? odd_segments | bit : odd_segments & ~bit;
+        ++s_tile;
+        group = 0;
+        if (last_of_segment()) {
+            i = 0;
+            ++s_segment;
+            w.next(a.split);
+        } else {
+            ++i;
+        }
+    }
+    __device__ __forceinline__ bool first() const { return (firsts >> (o_tile & 1u)) & 1u; }
+    __device__ __forceinline__ uint32_t odd() const { return (odd_segments >> (o_tile & 1u)) & 1u; }
+};
+
+// The products of a bf16 cache: one thread issues every MMA.  (Fences only
+// where tensor memory passes between threads: operands in shared memory come
+// with their barriers.)
 __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
     const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
@@ -323,105 +387,65 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
     const uint32_t pv_instr = f16_instr(true, 1, 0, 128, cols);
     const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
     const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
-    const uint32_t v_op = operand_low(smem_addr(sm.kv), kPanel);
+    const uint32_t v_op = operand_low(smem_addr(sm.kv + kPanel), kPanel);
     const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wait_one(bar, parity & 1u, &sm.stop, a.wait_limit);
-    };
-
-    // S of tile n.  Its buffer is free: S of tile n - 2 was read before the
-    // weights of that tile were written, and those have been waited for.
-    auto scores = [&](uint32_t n, bool last) {
-        const uint32_t buf = n & 1u;
-        const uint32_t k_tile = k_op + ((buf * 9 * kPanel) >> 4);
-        const uint32_t d = tmem + kScoreColumn + buf * kTile;
-#pragma unroll
-        for (uint32_t g = 0; g < kGroups; ++g) {
-            if (!wait(&sm.full[buf * kGroups + g], n >> 1)) return false;
-#pragma unroll
-            for (uint32_t x = 0; x < group_panels(g); ++x)
-#pragma unroll
-                for (uint32_t ks = 0; ks < 4; ++ks) {
-                    const uint32_t at = ((group_start(g) + x) * kPanel + ks * 32u) >> 4;
-                    mma_f16_ss(d, q_op + at, k_tile + at, qk_instr, g > 0 || x > 0 || ks > 0);
-                }
-        }
-        mma_commit(&sm.s_full[buf]);
-        if (last) mma_commit(&sm.q_free);
-        return true;
-    };
-    // O^T (+)= V^T P^T of tile n, the `first` of a segment or not; `odd`: the
-    // segment's parity
-    auto values = [&](uint32_t n, bool first, uint32_t odd) {
-        const uint32_t buf = n & 1u;
-        if (first && !wait(&sm.o_free, odd ^ 1u)) return false;
-        if (!wait(&sm.p_full, n)) return false;
-        fence_after_sync();
-        const uint32_t v_tile = v_op + (((buf * 9 + 1) * kPanel) >> 4);
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-#pragma unroll
-            for (uint32_t ks = 0; ks < 4; ++ks)
-                mma_f16_ss(tmem + j * kHeads, v_tile + ((2 * j * kPanel + ks * 2048u) >> 4),
-                           p_op + ((ks * 32u) >> 4), pv_instr, !first || ks > 0);
-            mma_commit(&sm.empty[buf * kGroups + j]);
-        }
-        mma_commit(&sm.pv_done);
-        return true;
-    };
-
     if (elect_one()) {
-        Walk w;
-        w.begin(a.split, sm.split.start);
+        Products x;
+        x.w.begin(a.split, sm.split.start);
         bool ok = true;
-        // S runs at most two tiles ahead of O^T (its two buffers).  Whichever
-        // is ready goes first.
-        uint32_t s_tile = 0, o_tile = 0, s_segment = 0, i = 0;
-        // of the tiles between S and O^T, by the parity of the tile: is it the
-        // first of its segment, and the parity of that
-        uint32_t firsts = 0, odd_segments = 0;
-        while (ok && (!w.done() || o_tile < s_tile)) {
-            const uint32_t pending = s_tile - o_tile;
-            bool take_s = !w.done() && pending < 2;
-            if (take_s && pending > 0) {
-                // both are possible: wait for either
-                uint64_t* full = &sm.full[(s_tile & 1u) * kGroups + kGroups - 1];
-                const int64_t t0 = clock64();
-                while (true) {
-                    if (phase_done(&sm.p_full, o_tile & 1u)) {
-                        take_s = false;
-                        break;
-                    }
-                    if (phase_done(full, (s_tile >> 1) & 1u) &&
-                        (i > 0 || phase_done(&sm.q_full, s_segment & 1u)))
-                        break;
-                    if (clock64() - t0 > a.wait_limit)
-                        *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
-                    if (*reinterpret_cast<volatile uint32_t*>(&sm.stop)) {
-                        ok = false;
-                        break;
-                    }
+        int64_t t0 = 0;
+        uint32_t tries = 0;
+        while (ok && x.more(a)) {
+            if (x.o_tile < x.s_tile && phase_done(&sm.p_full, x.o_tile & 1u)) {
+                // O^T (+)= V^T P^T
+                const uint32_t buf = x.o_tile & 1u;
+                if (x.first())
+                    ok = wait_one(&sm.o_free, x.odd() ^ 1u, &sm.stop, a.wait_limit);
+                fence_after_sync();
+                uint32_t d = tmem, v = v_op + ((buf * 9 * kPanel) >> 4);
+                uint64_t* empty = &sm.empty[buf * kGroups];
+                const bool add = !x.first();
+#pragma unroll 1
+                for (uint32_t j = 0; ok && j < 4; ++j) {
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(d, v + ((ks * 2048u) >> 4), p_op + ((ks * 32u) >> 4), pv_instr,
+                                   add || ks > 0);
+                    mma_commit(empty++);
+                    d += kHeads;
+                    v += (2 * kPanel) >> 4;
                 }
-                if (!ok) break;
-            }
-            if (take_s) {
-                if (i == 0) ok = wait(&sm.q_full, s_segment);
-                if (!ok) break;
-                const uint32_t count = w.last - w.first;
-                ok = scores(s_tile, i + 1 == count);
-                const uint32_t bit = 1u << (s_tile & 1u);
-                firsts = i == 0 ? firsts | bit : firsts & ~bit;
-                odd_segments = s_segment & 1u ? odd_segments | bit : odd_segments & ~bit;
-                ++s_tile;
-                if (++i == count) {
-                    i = 0;
-                    ++s_segment;
-                    w.next(a.split);
+                mma_commit(&sm.pv_done);
+                ++x.o_tile;
+                tries = 0;
+            } else if (x.s_next() &&
+                       phase_done(&sm.full[(x.s_tile & 1u) * kGroups + x.group],
+                                  (x.s_tile >> 1) & 1u) &&
+                       (x.i > 0 || phase_done(&sm.q_full, x.s_segment & 1u))) {
+                // a group of S.  Its buffer is free: S of tile n - 2 was read
+                // before the weights of that tile were written, and those have
+                // been waited for.
+                const uint32_t buf = x.s_tile & 1u, d = tmem + kScoreColumn + buf * kTile;
+                uint32_t at = (group_start(x.group) * kPanel) >> 4;
+                const uint32_t k = k_op + ((buf * 9 * kPanel) >> 4);
+                const uint32_t end = at + ((group_panels(x.group) * kPanel) >> 4);
+#pragma unroll 1
+                for (; at < end; at += kPanel >> 4)
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(d, q_op + at + ks * 2u, k + at + ks * 2u, qk_instr,
+                                   at > 0 || ks > 0);
+                if (++x.group == kGroups) {
+                    mma_commit(&sm.s_full[buf]);
+                    if (x.last_of_segment()) mma_commit(&sm.q_free);
+                    x.s_done(a);
                 }
-            } else {
-                ok = values(o_tile, (firsts >> (o_tile & 1u)) & 1u,
-                            (odd_segments >> (o_tile & 1u)) & 1u);
-                ++o_tile;
+                tries = 0;
+            } else if ((++tries & 63u) == 0) {
+                if (tries == 64u) t0 = clock64();
+                if (clock64() - t0 > a.wait_limit)
+                    *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+                if (*reinterpret_cast<volatile uint32_t*>(&sm.stop)) ok = false;
             }
         }
         if (!ok) {
@@ -928,14 +952,16 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     } else if (warp < 4) {
         soften<FP8>(a, sm);
     } else if (warp == 4) {
-        feed<FP8, WITHHOLD>(a, maps, qm, sm);
+        feed<FP8, WITHHOLD, 0>(a, maps, qm, sm);
     } else if (warp == 5) {
         if constexpr (FP8)
             multiply_codes(a, sm);
         else
             multiply(a, sm);
-    } else {
-        if constexpr (FP8) convert(a, sm);
+    } else if constexpr (FP8) {
+        convert(a, sm);
+    } else if constexpr (feeders_of<FP8>() > 1) {
+        feed<FP8, WITHHOLD, 1>(a, maps, qm, sm);
     }
     fence_before_sync();
     __syncthreads();
