@@ -25,11 +25,10 @@
 // ragged tables once.
 //
 // Measured, 32 ragged requests of up to 2048 new tokens, 32 + 2 x 8 heads of
-// 128 (780 MB): 130 us, 6.0 TB/s, 88 % of the card's copy rate; E4M3 cache
-// 133 us, with norms 133 us.  Three CTAs per SM (80 registers, a few scalars
-// spilled): with two, 131, 151 and 142 us; with four (64 registers) 138, 129
-// and 190 us.  One pass ahead instead of two: 134, 140 and 136 us.  One token:
-// 2.4 us on the device.
+// 128 (780 MB): 127 us, 6.1 TB/s, 90 % of the card's copy rate.  Three CTAs per SM (80 registers, a few scalars
+// spilled) against two and four (64 registers): bf16 130, 131, 138 us; E4M3
+// 133, 151, 129 us; with norms 133, 142, 190 us.  One pass ahead instead of
+// two: 134, 140 and 136 us.  One token: 2.3 us on the device.
 #include <cstdint>
 
 #include "kva_common.cuh"
@@ -98,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a)
             v[0] = v[1] = make_uint4(0, 0, 0, 0);
         }
     };
+    wait_for_stream();
     RaggedLoads ragged;
     ragged.issue(a.offsets, a.cache_lengths, a.B);
     if (item < a.items) {
@@ -260,8 +260,8 @@ cudaError_t launch(AppendArgs& a, cudaStream_t stream) {
     a.chunk_div = make_fast_div(a.chunks);
     uint64_t grid = ((uint64_t)a.items + kWarps - 1) / kWarps;
     if (grid > wave) grid = wave;
-    append_kernel<TL, IL, FP8, MROPE><<<(unsigned)grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(&append_kernel<TL, IL, FP8, MROPE>, dim3((unsigned)grid), kThreads, smem,
+                        stream, a);
 }
 
 template <int TL, bool IL>

@@ -266,6 +266,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init_fence();
         prefetch_map(&maps.map[0]);
     }
+    // All that touches global memory comes after the kernel before this one in
+    // the stream; its launch and the lines above do not (calls in a row,
+    // one token over 901 positions 14.4 -> 12.3 us).
+    wait_for_stream();
     const bool ok = find_piece(a.split, a.pieces, blockIdx.x, sm.split);
     OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
     if (tid == 0) open->units = 0;
@@ -783,7 +787,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     __shared__ float s_w[kRows][kMaxPieces];
     __shared__ float s_top[kRows], s_sum[kRows];
     __shared__ float4 s_acc[kJoinThreads];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
     if (open.units == 0) return;
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -874,18 +878,10 @@ cudaError_t launch_as(GqaArgs& a, const CacheMaps& maps, cudaStream_t stream) {
     if (wave == 0) return cudaErrorInvalidConfiguration;
     if (wave > kMaxPieces) wave = kMaxPieces;
     a.pieces = (uint32_t)wave;
-    gqa_decode_kernel<DP, FP8, MODS, WITHHOLD><<<a.pieces, kThreads, smem, stream>>>(a, maps);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.pieces);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gqa_join_kernel<DP>, a);
+    e = launch_early(&gqa_decode_kernel<DP, FP8, MODS, WITHHOLD>, dim3(a.pieces), kThreads, smem,
+                     stream, a, maps);
+    if (e != cudaSuccess) return e;
+    return launch_early(&gqa_join_kernel<DP>, dim3(a.pieces), kJoinThreads, 0, stream, a);
 }
 
 template <int DP, bool FP8, bool WITHHOLD>

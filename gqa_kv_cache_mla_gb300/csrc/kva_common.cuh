@@ -35,6 +35,29 @@ inline int check_cache(const kvw_paged_cache_t* c, uint32_t layer_idx, int plane
     return KVW_OK;
 }
 
+// Launches a kernel that may be scheduled before the one before it in the
+// stream has ended; it calls wait_for_stream before it touches global memory.
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Until what came before this kernel in the stream has ended and is visible.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The value scale of an E4M3 cache (a bf16 cache ignores it).
 inline bool value_scale_ok(const kvw_paged_cache_t* c, float v_scale) {
     return c->dtype != KVW_DTYPE_FP8_E4M3 || (v_scale > 0.0f && std::isfinite(v_scale));

@@ -87,6 +87,7 @@ __host__ __device__ __forceinline__ int64_t sum_floor(int64_t x, uint32_t log_m,
 // 1 - window) / c), both cut at the page tables' reach.
 __host__ __device__ __forceinline__ int64_t tiles_before(const SplitArgs& a, int64_t len,
                                                          uint32_t k) {
+    if (k == 0) return 0;  // single tokens, the usual case
     const uint32_t log_m = 6 - a.log_c;
     const int64_t e = (len + (1ll << a.log_c) - 1) >> a.log_c;
     const int64_t f = (len + 1 - a.window) >> a.log_c;  // floor, also of a negative number

@@ -942,6 +942,10 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
         prefetch_map(&qm.rope);
     }
     if (warp == 5) tmem_alloc(&sm.tmem, kTmemColumns);
+    // All that touches global memory comes after the kernel before this one in
+    // the stream; its launch and the lines above do not (calls in a row,
+    // one token, 16 heads, 1501 positions 18.5 -> 15.5 us).
+    wait_for_stream();
     const bool ok = find_piece(a.split, a.pieces, blockIdx.x / a.HB, sm.split);
     fence_before_sync();
     __syncthreads();
@@ -979,7 +983,7 @@ constexpr uint32_t kJoinRows = 4;
 __global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a) {
     __shared__ float s_w[kJoinRows][kMaxCtas];
     __shared__ float s_top[kJoinRows], s_sum[kJoinRows];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
     if (open.units == 0) return;
     const uint32_t rows = a.H - open.block * kHeads < kHeads ? a.H - open.block * kHeads : kHeads;
@@ -1057,18 +1061,11 @@ cudaError_t launch(MlaArgs& a, const CacheMaps& maps, const QMaps& qm, cudaStrea
     uint32_t ctas = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
     a.pieces = ctas / a.HB > 0 ? ctas / a.HB : 1;
     ctas = a.pieces * a.HB;
-    mla_decode_kernel<FP8, WITHHOLD><<<ctas, threads_of<FP8>(), smem, stream>>>(a, maps, qm);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_join_kernel, a);
+    e = launch_early(&mla_decode_kernel<FP8, WITHHOLD>, dim3(ctas), threads_of<FP8>(), smem, stream,
+                     a, maps, qm);
+    if (e != cudaSuccess) return e;
+    return launch_early(&mla_join_kernel, dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows),
+                        kJoinThreads, 0, stream, a);
 }
 
 int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_stride,
