@@ -161,8 +161,10 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
     uint32_t bad_page = 0, issued = 0;
     bool ok = true, first_half = true;
     while (ok && !w.done()) {
-        const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
+        const uint32_t kvh = a.HB == 1 ? w.block : w.block / a.HB, hb = w.block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        prefetch_page(maps, a.page_table, a.max_pages, a.ps, w.b,
+                      (int64_t)(w.span.tile0 + w.first) * kTile, lane);
         // ---- the queries: one copy per row
         ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_limit);
         if (!ok) break;
@@ -170,7 +172,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
         if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * a.D * 2);
         __syncwarp();
         if (lane < rows) {
-            const uint32_t ct = lane / in_block;
+            const uint32_t ct = w.span.tokens == 1 ? 0 : lane / in_block;
             bulk_load(sm.q_raw[q_at.slot] + lane * Sh::kQPitch,
                       a.q + (int64_t)(w.t + ct) * a.q_stride +
                           (int64_t)(kvh * a.G + hb * kRows + (lane - ct * in_block)) * a.D,
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (tid == 0) {
+    if (tid == kThreads - 32) {  // not a thread that the division of the work waits for
         for (int i = 0; i < Sh::kHalves; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], kWarps);
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     w.begin(a.split, sm.split.start);
     bool alive = true;
     while (!w.done()) {
-        const uint32_t kvh = w.block / a.HB, hb = w.block - kvh * a.HB;
+        const uint32_t kvh = a.HB == 1 ? w.block : w.block / a.HB, hb = w.block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
         const uint32_t rows = w.span.tokens * in_block;
         const uint32_t head0 = kvh * a.G + hb * kRows;
@@ -315,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
         // ---- queries: A operands, fp16 rows brought into range by 2^x
         const uint32_t r0 = quad, r1 = quad + 8;
-        const uint32_t t0 = r0 / in_block, t1 = r1 / in_block;  // tokens of the chunk
+        const uint32_t t0 = w.span.tokens == 1 ? 0 : r0 / in_block;  // tokens of the chunk
+        const uint32_t t1 = w.span.tokens == 1 ? 0 : r1 / in_block;
         alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_limit);
         if (!alive) break;
         const unsigned char* q0 = sm.q_raw[q_at.slot] + r0 * Sh::kQPitch;

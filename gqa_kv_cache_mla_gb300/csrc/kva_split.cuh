@@ -130,7 +130,7 @@ __host__ __device__ __forceinline__ uint64_t piece_start(uint64_t units, uint32_
 // only one.
 __host__ __device__ __forceinline__ uint32_t pieces_of(const SplitArgs& a, uint64_t units,
                                                        uint32_t most) {
-    const uint64_t p = div_units(units, a.min_units);
+    const uint64_t p = a.min_units == 1 ? units : div_units(units, a.min_units);
     return p == 0 ? 1u : p < most ? (uint32_t)p : most;
 }
 
@@ -141,6 +141,7 @@ struct PieceStart {
     uint64_t chunk_base;  // first unit of the chunk u0 lies in
     uint32_t pieces;
     uint32_t b, k;        // that chunk: request and index in it
+    uint32_t first, n, len;  // the request's first token, tokens and cache length
 };
 
 template <int THREADS>
@@ -160,9 +161,11 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
     const uint32_t hi = lo + per < a.B ? lo + per : a.B;
     int64_t mine = 0;
     int ok = 1;
+    uint32_t o0 = 0, o1 = 0, len = 0;  // of the thread's last request, usually its only one
     for (uint32_t r = lo; r < hi; ++r) {
-        const uint32_t o0 = __ldg(a.offsets + r), o1 = __ldg(a.offsets + r + 1);
-        const uint32_t len = __ldg(a.cache_lengths + r);
+        o0 = __ldg(a.offsets + r);
+        o1 = __ldg(a.offsets + r + 1);
+        len = __ldg(a.cache_lengths + r);
         if (o1 < o0 || o1 > a.T || (r == 0 && o0 != 0) || (r == a.B - 1 && o1 != a.T))
             ok = 0;
         else
@@ -186,37 +189,45 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
     s.units = (uint64_t)total * a.blocks;
     s.pieces = pieces_of(a, s.units, most);
     const bool used = c < s.pieces;
-    s.u0 = used ? piece_start(s.units, s.pieces, c) : s.units;
-    s.u1 = used ? piece_start(s.units, s.pieces, c + 1) : s.units;
+    const uint64_t q = div_units(s.units, s.pieces), rest = s.units - q * s.pieces;
+    s.u0 = used ? q * c + (c < rest ? c : rest) : s.units;  // as piece_start has it
+    s.u1 = used ? s.u0 + q + (c < rest ? 1 : 0) : s.units;
     s.chunk_base = 0;
-    s.b = s.k = 0;
+    s.b = s.k = s.first = s.n = s.len = 0;
     if (!used && tid == 0) sh.start = s;
     // the one thread whose requests hold u0 walks them
     if (used && s.u0 >= (uint64_t)before * a.blocks &&
         s.u0 < (uint64_t)(before + mine) * a.blocks) {
-        const uint64_t at = div_units(s.u0, a.blocks);  // the chunk holds this unit of a row block
         int64_t base = before;
-        for (uint32_t r = lo; r < hi; ++r) {
-            const uint32_t len = __ldg(a.cache_lengths + r);
-            const uint32_t n = __ldg(a.offsets + r + 1) - __ldg(a.offsets + r);
-            const int64_t units = request_units(a, len, n);
-            if (at < (uint64_t)(base + units)) {
-                // the last chunk that begins at or before it
-                uint32_t k0 = 0, k1 = chunks_of(a, n);
-                while (k1 - k0 > 1u) {
-                    const uint32_t mid = k0 + (k1 - k0) / 2;
-                    if ((uint64_t)(base + units_before(a, len, mid)) <= at)
-                        k0 = mid;
-                    else
-                        k1 = mid;
-                }
-                s.b = r;
-                s.k = k0;
-                s.chunk_base = (uint64_t)(base + units_before(a, len, k0)) * a.blocks;
-                break;
+        uint32_t r = lo;
+        if (hi - lo > 1) {
+            for (;; ++r) {
+                o0 = __ldg(a.offsets + r);
+                o1 = __ldg(a.offsets + r + 1);
+                len = __ldg(a.cache_lengths + r);
+                const int64_t units = request_units(a, len, o1 - o0);
+                if (r + 1 == hi || s.u0 < (uint64_t)(base + units) * a.blocks) break;
+                base += units;
             }
-            base += units;
         }
+        // the last chunk that begins at or before u0
+        uint32_t k0 = 0, k1 = chunks_of(a, o1 - o0);
+        if (k1 > 1u) {
+            const uint64_t at = div_units(s.u0, a.blocks);  // the chunk holds this unit of a row block
+            while (k1 - k0 > 1u) {
+                const uint32_t mid = k0 + (k1 - k0) / 2;
+                if ((uint64_t)(base + units_before(a, len, mid)) <= at)
+                    k0 = mid;
+                else
+                    k1 = mid;
+            }
+        }
+        s.b = r;
+        s.k = k0;
+        s.first = o0;
+        s.n = o1 - o0;
+        s.len = len;
+        s.chunk_base = (uint64_t)(base + units_before(a, len, k0)) * a.blocks;
         sh.start = s;
     }
     __syncthreads();
@@ -246,7 +257,7 @@ struct Walk {
     __device__ __forceinline__ void find_segment(const SplitArgs& a) {
         const uint32_t per = span.tiles + a.overhead;
         const uint64_t in = u - chunk_base, left = u1 - u;
-        block = (uint32_t)div_units(in, per);
+        block = in < per ? 0 : (uint32_t)div_units(in, per);
         const uint32_t from = (uint32_t)(in - (uint64_t)block * per);
         units = per - from < left ? per - from : (uint32_t)left;
         first = from > a.overhead ? from - a.overhead : 0;
@@ -278,7 +289,9 @@ struct Walk {
         k = s.k;
         block = units = first = last = 0;
         if (u < u1) {
-            load_request(a);
+            n = s.n;
+            t = s.first + (k << a.log_c);
+            len0 = s.len;
             span = chunk_span(a, len0, n, k);
             find_segment(a);
             while (u < u1 && first == last) step(a);

@@ -156,6 +156,15 @@ __host__ __device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m,
     return u;
 }
 
+// The page id that plan_unit will look up for unit `lane`, on its way to L1.
+__device__ __forceinline__ void prefetch_page(const CacheMaps& m, const uint32_t* page_table,
+                                              uint32_t max_pages, const FastDiv& ps, uint32_t b,
+                                              int64_t p_tile, uint32_t lane) {
+    const uint32_t idx = fast_div((uint32_t)p_tile + (lane << m.log_rows), ps);
+    if (lane < (64u >> m.log_rows) && idx < max_pages)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(page_table + (uint64_t)b * max_pages + idx));
+}
+
 // One copy: columns from `col` of R rows from `row` of (page, plane, head).
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t col,
                                          uint32_t head, uint32_t row, uint32_t page,

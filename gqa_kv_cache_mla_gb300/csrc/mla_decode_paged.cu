@@ -156,6 +156,8 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
     uint32_t stopped_at = kFrom;  // the group whose place was not free in time
     bool ok = true;
     while (ok && !w.done()) {
+        prefetch_page(maps, a.page_table, a.max_pages, a.ps, w.b,
+                      (int64_t)(w.span.tile0 + w.first) * kTile, lane);
         if constexpr (!FP8 && WHICH == feeders_of<FP8>() - 1) {
             ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) {
+    if (tid == 128) {  // not a thread that the division of the work waits for
         for (uint32_t i = 0; i < 2 * kGroups; ++i) {
             mbar_init(&sm.full[i], 1);
             // E4M3: codes go to the matrix unit and to four warps
