@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     wait_for_stream();
     const bool ok = find_piece(a.split, a.pieces, blockIdx.x, sm.split);
     OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
-    if (tid == 0) open->units = 0;
+    if (tid == 0) open->n = 0;
     if (!ok) {
         if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
         return;
@@ -314,6 +314,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t head0 = kvh * a.G + hb * kRows;
         const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
         if (pos0 + w.span.tokens > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
+
+        const uint32_t shared_by = w.first == 0 && !w.whole()
+                                       ? sharers(a.split, sm.split.start, w, blockIdx.x)
+                                       : 0;
 
         // ---- queries: A operands, fp16 rows brought into range by 2^x
         const uint32_t r0 = quad, r1 = quad + 8;
@@ -766,13 +770,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!alive) break;
         }
         if (!alive) break;
-        if (!whole && w.first == 0 && tid == 0) {
-            open->end = w.end(a.split);
-            open->pieces = sm.split.start.pieces;
-            open->t = w.t;
-            open->tokens = w.span.tokens;
-            open->block = w.block;
-            open->units = sm.split.start.units;
+        if (shared_by && tid == 0) {
+            OpenPiece x;
+            x.n = shared_by;
+            x.t = w.t;
+            x.tokens = w.span.tokens;
+            x.block = w.block;
+            *open = x;
         }
         w.next(a.split);
     }
@@ -792,17 +796,18 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     __shared__ float4 s_acc[kJoinThreads];
     wait_for_stream();
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
-    if (open.units == 0) return;
+    if (open.n == 0) return;
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    const uint32_t n = sharers(open, c0);
-    const uint32_t kvh = open.block / a.HB, hb = open.block - kvh * a.HB;
+    const uint32_t n = open.n, kvh = a.HB == 1 ? open.block : open.block / a.HB;
+    const uint32_t hb = open.block - kvh * a.HB;
     const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
     const uint32_t rows = open.tokens * in_block;
     const uint32_t head0 = kvh * a.G + hb * kRows;
     auto part = [&](uint32_t i) { return slot_of<DP>(a.workspace, c0 + i, i == 0 ? 1 : 0); };
 
     for (uint32_t r = warp; r < rows; r += kJoinThreads / 32) {
-        float top = -INFINITY;
+        float top = -INFINITY, l_first = 0.0f;  // of the lane's first piece
+        if (lane < n) l_first = part(lane)[kRows * DP + kRows + r];
         for (uint32_t i = lane; i < n; i += 32) {
             const float m = part(i)[kRows * DP + r];
             s_w[r][i] = m;
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
         for (uint32_t i = lane; i < n; i += 32) {
             const float f = fast_exp2(s_w[r][i] - base);
             s_w[r][i] = f;
-            l += f * part(i)[kRows * DP + kRows + r];
+            l += f * (i == lane ? l_first : part(i)[kRows * DP + kRows + r]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

@@ -311,26 +311,24 @@ struct Walk {
     }
 };
 
-// What a piece left open: a (chunk, row block) whose first tile it has (slot 1)
-// and that the pieces after it go on with (their slot 0), up to unit `end`.
-// `units` 0: nothing.
-struct OpenPiece {
-    uint64_t units, end;
-    uint32_t pieces, t, tokens, block;
-};
-static_assert(sizeof(OpenPiece) == 32, "workspace layout");
+// The piece (of `pieces`) that holds unit u.
+__host__ __device__ __forceinline__ uint32_t piece_of(uint64_t units, uint32_t pieces, uint64_t u) {
+    const uint64_t q = div_units(units, pieces), r = units - q * pieces;  // r pieces have q + 1
+    const uint64_t longer = (q + 1) * r;
+    return (uint32_t)(u < longer ? div_units(u, q + 1) : r + div_units(u - longer, q));
+}
 
-// Pieces c0 .. c0 + n - 1 share what piece c0 left open; returns n.
-__device__ __forceinline__ uint32_t sharers(const OpenPiece& open, uint32_t c0) {
-    uint32_t lo = c0 + 1, hi = open.pieces;  // the starts ascend
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (piece_start(open.units, open.pieces, mid) < open.end)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo - c0;
+// What a piece left open: a (chunk, row block) whose first tile it has (slot 1)
+// and that the next n - 1 pieces go on with (their slot 0).  n 0: nothing.
+struct __align__(16) OpenPiece {
+    uint32_t n, t, tokens, block;
+};
+static_assert(sizeof(OpenPiece) == 16, "workspace layout");
+
+// Pieces that share the segment at w, which piece c of s begins.
+__device__ __forceinline__ uint32_t sharers(const SplitArgs& a, const PieceStart& s, const Walk& w,
+                                            uint32_t c) {
+    return piece_of(s.units, s.pieces, w.end(a) - 1) - c + 1;
 }
 
 }  // namespace kvw

@@ -695,6 +695,9 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
     uint32_t tile = 0, segment = 0;
     while (!w.done()) {
         if ((int64_t)w.len0 + w.k + 1 > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
+        const uint32_t shared_by = w.first == 0 && !w.whole()
+                                       ? sharers(a.split, sm.split.start, w, blockIdx.x / a.HB)
+                                       : 0;
         float qs0 = a.scale, qs1 = a.scale;
         if constexpr (FP8) {
             // the last S of the segment before has been read: Q is free
@@ -894,13 +897,13 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                 part[(uint64_t)a.slot_rows * (kLatent + 1) + tid] = l;
             }
         }
-        if (!whole && w.first == 0 && tid == 0) {
-            open->end = w.end(a.split);
-            open->pieces = sm.split.start.pieces;
-            open->t = w.t;
-            open->tokens = 1;
-            open->block = hb;
-            open->units = sm.split.start.units;
+        if (shared_by && tid == 0) {
+            OpenPiece x;
+            x.n = shared_by;
+            x.t = w.t;
+            x.tokens = 1;
+            x.block = hb;
+            *open = x;
         }
         any_softmax(false);  // sm.m, sm.l are read
         if (lane == 0) mbar_arrive(&sm.o_free);
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (tid == 0) reinterpret_cast<OpenPiece*>(a.workspace)[blockIdx.x].units = 0;
+    if (tid == 0) reinterpret_cast<OpenPiece*>(a.workspace)[blockIdx.x].n = 0;
     if (!ok) {
         if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
     } else if (warp < 4) {
@@ -987,19 +990,20 @@ __global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a)
     __shared__ float s_top[kJoinRows], s_sum[kJoinRows];
     wait_for_stream();
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
-    if (open.units == 0) return;
+    if (open.n == 0) return;
     const uint32_t rows = a.H - open.block * kHeads < kHeads ? a.H - open.block * kHeads : kHeads;
     const uint32_t r0 = blockIdx.y * kJoinRows;
     if (r0 >= rows) return;
     const uint32_t here = rows - r0 < kJoinRows ? rows - r0 : kJoinRows;
     const uint32_t piece = blockIdx.x / a.HB, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    const uint32_t n = sharers(open, piece);
+    const uint32_t n = open.n;
     auto part = [&](uint32_t i) {
         return slot_of(a, (piece + i) * a.HB + open.block, i == 0 ? 1 : 0);
     };
     if (warp < here) {
         const uint32_t r = r0 + warp;
-        float top = -INFINITY;
+        float top = -INFINITY, l_first = 0.0f;  // of the lane's first piece
+        if (lane < n) l_first = part(lane)[(uint64_t)a.slot_rows * (kLatent + 1) + r];
         for (uint32_t i = lane; i < n; i += 32) {
             const float m = part(i)[(uint64_t)a.slot_rows * kLatent + r];
             s_w[warp][i] = m;
@@ -1012,7 +1016,7 @@ __global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a)
         for (uint32_t i = lane; i < n; i += 32) {
             const float f = fast_exp2(s_w[warp][i] - base);
             s_w[warp][i] = f;
-            l += f * part(i)[(uint64_t)a.slot_rows * (kLatent + 1) + r];
+            l += f * (i == lane ? l_first : part(i)[(uint64_t)a.slot_rows * (kLatent + 1) + r]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

@@ -69,6 +69,9 @@ int main() {
             const uint64_t size = piece_start(units, p, c + 1) - piece_start(units, p, c);
             if (size < 1 || size < units / p || size > units / p + 1) return printf("cut\n"), 1;
             if (p > 1 && size < a.min_units) return printf("short piece\n"), 1;
+            const uint64_t u = piece_start(units, p, c);
+            if (piece_of(units, p, u) != c || piece_of(units, p, u + size - 1) != c)
+                return printf("piece_of\n"), 1;
         }
         ++checks;
     }
