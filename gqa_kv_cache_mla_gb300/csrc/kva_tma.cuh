@@ -91,6 +91,47 @@ inline int encode_cache_maps(CacheMaps* m, const kvw_paged_cache_t* c, uint32_t 
     return KVW_OK;
 }
 
+// For pages of whole tiles and one head: a map whose copies take 64 rows of
+// `panels` neighbouring 128-byte panels of columns at once, each panel as one
+// copy of its own would leave it (rows 128 bytes apart, panels 8 KB).  Only
+// the columns of whole panels are in it.
+inline int encode_panel_map(CUtensorMap* map, const kvw_paged_cache_t* c, uint32_t layer_idx,
+                            uint32_t panels) {
+    const auto encode = tensor_map_encoder();
+    if (!encode) return KVW_ECUDA;
+    const uint64_t esz = cache_esz(c);
+    const cuuint64_t dims[4] = {128 / esz, c->page_size, c->head_size * esz / 128, c->num_pages};
+    const cuuint64_t strides[3] = {
+        c->page_size > 1 ? (cuuint64_t)c->stride_token * esz : (cuuint64_t)16, 128,
+        c->num_pages > 1 ? (cuuint64_t)c->stride_page * esz : (cuuint64_t)16};
+    const cuuint32_t box[4] = {(cuuint32_t)(128 / esz), 64, panels, 1}, ones[4] = {1, 1, 1, 1};
+    unsigned char* base = static_cast<unsigned char*>(c->data) +
+                          (int64_t)layer_idx * (c->num_layers > 1 ? c->stride_layer : 0) *
+                              (int64_t)esz;
+    const CUresult r = encode(
+        map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base,
+        dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KVW_OK : KVW_EINVAL;
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, uint32_t c0,
+                                       uint32_t c1, uint32_t c2, uint32_t c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// The same columns and rows into L2 only.
+__device__ __forceinline__ void tma_4d_prefetch(const CUtensorMap* map, uint32_t c0, uint32_t c1,
+                                                uint32_t c2, uint32_t c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
+                 ::"l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
 // Does a copy begin at unit x of a run of `run` units, and with which map?
 __host__ __device__ __forceinline__ bool copy_begins(uint32_t x, uint32_t run, uint32_t levels,
                                                      uint32_t& level) {

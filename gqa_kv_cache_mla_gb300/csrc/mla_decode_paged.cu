@@ -25,9 +25,8 @@
 // value columns into fp16 (exactly) for O^T.
 //
 // Shared memory (227 KB) decides the rest.  bf16: Q 72 KB and two tiles of 72
-// KB, each in four groups (128 latent columns; the first with the rotated
-// columns) that are filled one by one and freed as the four row blocks of O^T
-// complete.  E4M3: Q's two parts 72 KB, two tiles of codes 80 KB, one fp16
+// KB, each in three groups of panels that are filled one by one and freed as
+// the row blocks of O^T complete.  E4M3: Q's two parts 72 KB, two tiles of codes 80 KB, one fp16
 // tile of values 64 KB in two halves.  P 8 KB.  O^T fills 256 of the 512
 // columns of tensor memory, two S tiles 128.  The MMA thread takes what is
 // ready first, the next S or the next O^T, so that neither a late tile nor a
@@ -49,7 +48,7 @@ namespace {
 constexpr uint32_t kHeads = 64;               // rows of a row block
 constexpr uint32_t kLatent = 512, kRow = 576;
 constexpr uint32_t kPanel = kTile * 128;      // 64 columns of a 16-bit tile, or 128 codes
-constexpr uint32_t kGroups = 4;               // of a bf16 tile: 128 latent columns each
+constexpr uint32_t kGroups = 3;               // of a bf16 tile: three of its nine panels each
 constexpr uint32_t kCodePanels = 5;           // of an E4M3 tile: 64 rotated columns, 4 x 128 latent ones
 constexpr uint32_t kCodeGroups = 2;           // panels 0 - 2 and 3, 4
 constexpr uint32_t kMaxCtas = 192;
@@ -75,7 +74,7 @@ struct MlaArgs {
 };
 
 struct QMaps {
-    CUtensorMap latent, rope;
+    CUtensorMap latent, rope, panels;
 };
 
 template <bool FP8>
@@ -89,7 +88,7 @@ constexpr int threads_of() {
 
 template <bool FP8>
 struct Smem {
-    // bf16: Q as nine panels, rotated columns first.  E4M3: four panels of 128
+    // bf16: Q as nine panels, rotated columns last.  E4M3: four panels of 128
     // rows x 128 codes, then 128 rows x 64 rotated columns in 64-byte lines.
     unsigned char q[9 * kPanel];
     unsigned char p[kPanel];
@@ -106,10 +105,13 @@ struct Smem {
     uint32_t tmem, stop;
 };
 
-// The panels of a tile: rotated columns, then eight (codes: four) of the
-// latent ones.  Group g: its first panel and their number.
-__device__ __forceinline__ uint32_t group_start(uint32_t g) { return g == 0 ? 0u : 2u * g + 1u; }
-__device__ __forceinline__ uint32_t group_panels(uint32_t g) { return g == 0 ? 3u : 2u; }
+// The panels of a tile: eight of the latent columns, then the rotated ones;
+// of codes the rotated columns, then four of the latent ones.  Group g: its
+// first panel and their number.
+template <bool FP8>
+__device__ __forceinline__ uint32_t group_start(uint32_t g) { return 3u * g; }
+template <bool FP8>
+__device__ __forceinline__ uint32_t group_panels(uint32_t g) { return FP8 && g ? 2u : 3u; }
 
 // Do any of the softmax threads say yes?
 __device__ __forceinline__ bool any_softmax(bool mine) {
@@ -135,20 +137,22 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 
 // ---------------------------------------------------------------- feeding
 
-// Two warps feed, each half of the groups of every tile: one needs about 400
-// cycles to issue a group and 1200 to look up the next tile's page and fetch
-// it ahead, which together were most of a tile's time.
+// With a bf16 cache two warps feed, groups 0 and 1 and group 2 of every tile:
+// small pages make many copies (pages of 16, 256 requests, 128 heads: 548 us,
+// 772 with one warp).  Of pages of whole tiles a group is one copy of three
+// panels; three copies of one panel each took 433 us instead of 411.
 template <bool FP8, bool WITHHOLD, uint32_t WHICH>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8>& sm) {
     constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups;
     constexpr uint32_t kTilePanels = FP8 ? kCodePanels : 9;
     constexpr int kUnroll = FP8 ? 8 : 1;
-    constexpr uint32_t kEach = kTileGroups / feeders_of<FP8>(), kFrom = WHICH * kEach;
-    constexpr uint32_t kTo = kFrom + kEach;
+    // one of two: groups 0 and 1, or 2
+    constexpr uint32_t kFrom = WHICH ? 2 : 0;
+    constexpr uint32_t kTo = WHICH || feeders_of<FP8>() == 1 ? kTileGroups : 2;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
     auto column = [](uint32_t panel) {
-        return panel == 0 ? kLatent : (panel - 1) * (FP8 ? 128u : 64u);
+        return FP8 ? (panel == 0 ? kLatent : (panel - 1) * 128u) : panel * 64u;
     };
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -164,10 +168,10 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             if (elect_one()) {
                 const uint32_t bar = smem_addr(&sm.q_full);
                 mbar_arrive_expect_tx(&sm.q_full, 9 * kPanel);
-                tma_3d(smem_addr(sm.q), &qm.rope, 0, hb * kHeads, w.t, bar);
+                tma_3d(smem_addr(sm.q + 8 * kPanel), &qm.rope, 0, hb * kHeads, w.t, bar);
 #pragma unroll kUnroll
                 for (uint32_t x = 0; x < 8; ++x)
-                    tma_3d(smem_addr(sm.q + (x + 1) * kPanel), &qm.latent, x * 64, hb * kHeads, w.t,
+                    tma_3d(smem_addr(sm.q + x * kPanel), &qm.latent, x * 64, hb * kHeads, w.t,
                            bar);
             }
             __syncwarp();
@@ -206,20 +210,24 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                                     ((tile >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit);
                 }
                 if (!ok) continue;
-                const uint32_t bytes = (n << maps.log_rows) * 128u * group_panels(g);
+                const uint32_t bytes = (n << maps.log_rows) * 128u * group_panels<FP8>(g);
                 const uint32_t bar = smem_addr(full);
                 const uint32_t base = smem_addr(
-                    sm.kv + ((tile & 1u) * kTilePanels + group_start(g)) * kPanel);
+                    sm.kv + ((tile & 1u) * kTilePanels + group_start<FP8>(g)) * kPanel);
                 const bool withheld = WITHHOLD && tile == 0 && g == 0;
                 if (maps.log_rows == 6) {  // one copy per panel
                     if (elect_one()) {
                         if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
                         mbar_arrive_expect_tx(full, bytes);
                         if (n && !withheld) {
-#pragma unroll kUnroll
-                            for (uint32_t x = 0; x < group_panels(g); ++x)
-                                tma_rows(base + x * kPanel, &maps.map[0],
-                                         column(group_start(g) + x), 0, row, page, 0, bar);
+                            if constexpr (!FP8) {
+                                tma_4d(base, &qm.panels, 0, row, 3 * g, page, bar);
+                            } else {
+                                if (g == 0)
+                                    tma_rows(base, &maps.map[0], kLatent, 0, row, page, 0, bar);
+                                tma_4d(base + (g == 0 ? kPanel : 0), &qm.panels, 0, row, 2 * g,
+                                       page, bar);
+                            }
                         }
                     }
                     __syncwarp();
@@ -233,9 +241,9 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                         each_copy(maps, copy, [&](uint32_t unit, uint32_t r, uint32_t id,
                                                   const CUtensorMap* map) {
 #pragma unroll kUnroll
-                            for (uint32_t x = 0; x < group_panels(g); ++x)
+                            for (uint32_t x = 0; x < group_panels<FP8>(g); ++x)
                                 tma_rows(base + x * kPanel + (unit << maps.log_rows) * 128u, map,
-                                         column(group_start(g) + x), 0, r, id, 0, bar);
+                                         column(group_start<FP8>(g) + x), 0, r, id, 0, bar);
                         });
                 }
             }
@@ -244,17 +252,28 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             stopped_at = kFrom;
             if (i + 1 < w.last) {
                 // The next tile's place is taken for a while yet: into L2 with
-                // it (256 requests, 128 heads, bf16: 472 -> 453 us; a tile of
-                // codes, half as large, gains nothing: 478 and 480 us).
+                // it (256 requests, 128 heads, bf16: 472 -> 453 us when it was
+                // added; a tile of codes, half as large, gains nothing; two
+                // tiles ahead is no better than one).
                 plan(i + 1);
-                if (!FP8 && ((i & 1u) == hb || a.HB == 1))
-                    each_copy(maps, copy, [&](uint32_t, uint32_t r, uint32_t id,
-                                              const CUtensorMap* map) {
-#pragma unroll kUnroll
-                        for (uint32_t x = group_start(kFrom);
-                             x < group_start(kTo - 1) + group_panels(kTo - 1); ++x)
-                            tma_prefetch(map, column(x), 0, r, id, 0);
-                    });
+                if (!FP8 && ((i & 1u) == hb || a.HB == 1)) {
+                    if (maps.log_rows == 6) {
+                        if (n && elect_one()) {
+#pragma unroll 1
+                            for (uint32_t g = kFrom; g < kTo; ++g)
+                                tma_4d_prefetch(&qm.panels, 0, row, 3 * g, page);
+                        }
+                        __syncwarp();
+                    } else {
+                        each_copy(maps, copy, [&](uint32_t, uint32_t r, uint32_t id,
+                                                  const CUtensorMap* map) {
+#pragma unroll 1
+                            for (uint32_t x = group_start<FP8>(kFrom);
+                                 x < group_start<FP8>(kTo - 1) + group_panels<FP8>(kTo - 1); ++x)
+                                tma_prefetch(map, column(x), 0, r, id, 0);
+                        });
+                    }
+                }
             }
         }
         if (ok) w.next(a.split);
@@ -389,7 +408,7 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
     const uint32_t pv_instr = f16_instr(true, 1, 0, 128, cols);
     const uint32_t q_op = operand_low(smem_addr(sm.q), 0);
     const uint32_t k_op = operand_low(smem_addr(sm.kv), 0);
-    const uint32_t v_op = operand_low(smem_addr(sm.kv + kPanel), kPanel);
+    const uint32_t v_op = operand_low(smem_addr(sm.kv), kPanel);
     const uint32_t p_op = operand_low(smem_addr(sm.p), 0);
     if (elect_one()) {
         Products x;
@@ -413,7 +432,8 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
                     for (uint32_t ks = 0; ks < 4; ++ks)
                         mma_f16_ss(d, v + ((ks * 2048u) >> 4), p_op + ((ks * 32u) >> 4), pv_instr,
                                    add || ks > 0);
-                    mma_commit(empty++);
+                    // panels 0-2, 3-5, 6-8: block j takes 2j and 2j + 1
+                    if (j > 0) mma_commit(empty++);
                     d += kHeads;
                     v += (2 * kPanel) >> 4;
                 }
@@ -428,9 +448,9 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
                 // before the weights of that tile were written, and those have
                 // been waited for.
                 const uint32_t buf = x.s_tile & 1u, d = tmem + kScoreColumn + buf * kTile;
-                uint32_t at = (group_start(x.group) * kPanel) >> 4;
+                uint32_t at = (group_start<false>(x.group) * kPanel) >> 4;
                 const uint32_t k = k_op + ((buf * 9 * kPanel) >> 4);
-                const uint32_t end = at + ((group_panels(x.group) * kPanel) >> 4);
+                const uint32_t end = at + ((group_panels<false>(x.group) * kPanel) >> 4);
 #pragma unroll 1
                 for (; at < end; at += kPanel >> 4)
 #pragma unroll
@@ -812,7 +832,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
                     // a weight of 0 does not keep out what a row that is not
                     // there may hold
                     if (there != ~0ull) {
-                        unsigned char* kv = sm.kv + ((tile & 1u) * 9 + 1) * kPanel;
+                        unsigned char* kv = sm.kv + (tile & 1u) * 9 * kPanel;
                         for (uint32_t x = tid; x < 64 * 64; x += kSoftmaxThreads) {
                             const uint32_t r = x >> 6, c = x & 63u;
                             if (!((there >> r) & 1ull))
@@ -945,6 +965,7 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
         prefetch_map(&maps.map[0]);
         prefetch_map(&qm.latent);
         prefetch_map(&qm.rope);
+        prefetch_map(&qm.panels);
     }
     if (warp == 5) tmem_alloc(&sm.tmem, kTmemColumns);
     // All that touches global memory comes after the kernel before this one in
@@ -1140,6 +1161,9 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
                              q_latent_row_stride);
     if (e == KVW_OK)
         e = encode_query_map(&qm.rope, q_rope, 64, num_heads, tot_seq_len, q_rope_row_stride);
+    qm.panels = qm.rope;
+    if (e == KVW_OK && maps.log_rows == 6)
+        e = encode_panel_map(&qm.panels, cache, layer_idx, fp8 ? 2 : 3);
     if (e != KVW_OK) return e;
     cudaError_t r;
 #ifdef KVW_TEST_HOOKS
