@@ -256,12 +256,14 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 // added; a tile of codes, half as large, gains nothing; two
                 // tiles ahead is no better than one).
                 plan(i + 1);
-                if (!FP8 && ((i & 1u) == hb || a.HB == 1)) {
+                if ((i & 1u) == hb || a.HB == 1) {
                     if (maps.log_rows == 6) {
                         if (n && elect_one()) {
 #pragma unroll 1
                             for (uint32_t g = kFrom; g < kTo; ++g)
-                                tma_4d_prefetch(&qm.panels, 0, row, 3 * g, page);
+                                tma_4d_prefetch(&qm.panels, 0, row, (FP8 ? 2 : 3) * g, page);
+                            if constexpr (FP8)
+                                tma_prefetch(&maps.map[0], kLatent, 0, row, page, 0);
                         }
                         __syncwarp();
                     } else {
