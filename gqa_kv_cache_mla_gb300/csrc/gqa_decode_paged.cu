@@ -54,7 +54,8 @@ struct GqaArgs {
     const float* slopes;
     uint32_t* err_flags;
     unsigned char* workspace;
-    float sm_scale, softcap, cap_factor, k_scale, v_scale;
+    float sm_scale, k_scale, v_scale;
+    float softcap, cap_factor;  // in units of log2; 2 log2(e) / the cap
     uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
     uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
     uint32_t num_pages, max_pages, pieces;
@@ -378,10 +379,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     qf[i][2 * h + 1] = pack2<true>(bf16_lo(x1) * up1, bf16_hi(x1) * up1);
                 }
         }
-        if constexpr (!MODS) {  // scores in units of log2 straight from the product
-            qs0 *= kLog2e;
-            qs1 *= kLog2e;
-        }
+        // scores in units of log2 straight from the product, or 2 log2(e) / cap
+        // of them
+        qs0 *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
+        qs1 *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
         // never 0: a masked score is -inf times this
         qs0 = fmaxf(qs0, 1.17549435e-38f);
         qs1 = fmaxf(qs1, 1.17549435e-38f);
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         float slope0 = 0.0f, slope1 = 0.0f;
         if constexpr (MODS) {
             if (a.slopes) {
-                slope0 = r0 < rows ? __ldg(a.slopes + head0 + (r0 - t0 * in_block)) : 0.0f;
-                slope1 = r1 < rows ? __ldg(a.slopes + head0 + (r1 - t1 * in_block)) : 0.0f;
+                slope0 = r0 < rows ? kLog2e * __ldg(a.slopes + head0 + (r0 - t0 * in_block)) : 0.0f;
+                slope1 = r1 < rows ? kLog2e * __ldg(a.slopes + head0 + (r1 - t1 * in_block)) : 0.0f;
             }
         }
         // positions every row of the block sees, and each row's own
@@ -486,24 +487,36 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 [[maybe_unused]] const int64_t p0 = p_first + (int64_t)(k + i) * kTile;
-                if constexpr (MODS) {
+                if constexpr (MODS) {  // into units of log2
+                    if (a.softcap > 0.0f) {
+                        // tanh y = 1 - 2 / (e^2y + 1): absolute error of a few
+                        // 2^-24, so the capped score is off by that times the cap
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = s[2 * i + n][e] * (e < 2 ? qs0 : qs1);
-                            if (a.softcap > 0.0f) {
-                                // tanh y = 1 - 2 / (e^2y + 1): absolute error of a few
-                                // 2^-24, so the capped score is off by that times the cap
-                                const float z = fast_exp2(x * a.cap_factor);
-                                x = a.softcap - __fdividef(2.0f * a.softcap, z + 1.0f);
+                            for (int e = 0; e < 4; ++e) {
+                                const float z = fast_exp2(s[2 * i + n][e] * (e < 2 ? qs0 : qs1));
+                                s[2 * i + n][e] =
+                                    a.softcap - __fdividef(2.0f * a.softcap, z + 1.0f);
                             }
-                            if (a.slopes) {
-                                const int64_t j = p0 + n * 8 + 2 * in_quad + (e & 1);
-                                x -= e < 2 ? slope0 * (float)(own0 - j) : slope1 * (float)(own1 - j);
+                    }
+                    if (a.slopes) {
+                        // slope * (offset in the slice - distance of its start)
+                        const float f0 = a.softcap > 0.0f ? 1.0f : qs0;
+                        const float f1 = a.softcap > 0.0f ? 1.0f : qs1;
+                        const int64_t from = p0 + 2 * in_quad;
+                        const float away0 = slope0 * (float)(own0 - from);
+                        const float away1 = slope1 * (float)(own1 - from);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float bias = fmaf(e < 2 ? slope0 : slope1,
+                                                        (float)(n * 8 + (e & 1)),
+                                                        e < 2 ? -away0 : -away1);
+                                s[2 * i + n][e] = fmaf(s[2 * i + n][e], e < 2 ? f0 : f1, bias);
                             }
-                            s[2 * i + n][e] = x * kLog2e;
-                        }
+                    }
                 }
                 if constexpr (EDGE) {
 #pragma unroll
@@ -967,7 +980,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     a.err_flags = err_flags;
     a.workspace = static_cast<unsigned char*>(workspace);
     a.sm_scale = sm_scale;
-    a.softcap = softcap;
+    a.softcap = softcap * kLog2e;
     a.cap_factor = softcap > 0.0f ? 2.0f * kLog2e / softcap : 0.0f;
     a.k_scale = fp8 ? cache->scale : 1.0f;
     a.v_scale = fp8 ? v_scale : 1.0f;
