@@ -197,6 +197,82 @@ __host__ __device__ __forceinline__ UnitCopy plan_unit(const CacheMaps& m,
     return u;
 }
 
+// The same for a tile whose 64 positions all lie in [start, hi), in 32 bits:
+// level 4 and no page where the page is not valid or no copy begins.
+__host__ __device__ __forceinline__ UnitCopy plan_inner_unit(const CacheMaps& m,
+                                                             const uint32_t* page_table,
+                                                             uint32_t max_pages,
+                                                             uint32_t num_pages,
+                                                             const FastDiv& ps, uint32_t b,
+                                                             uint32_t p_tile, uint32_t c) {
+    UnitCopy u;
+    u.level = 4;
+    u.there = 0;
+    const uint32_t units = 64u >> m.log_rows, p = p_tile + (c << m.log_rows);
+    const uint32_t idx = fast_div(p, ps);
+    u.row = p - idx * ps.d;
+    u.page = KVW_PAGE_UNMAPPED;
+    if (c < units && idx < max_pages) {
+        const uint32_t* id = page_table + (uint64_t)b * max_pages + idx;
+#ifdef __CUDA_ARCH__
+        u.page = __ldg(id);
+#else
+        u.page = *id;
+#endif
+    }
+    u.bad_page = c < units && u.page >= num_pages;
+    if (c >= units || u.bad_page) return u;
+    const uint32_t back = u.row >> m.log_rows, ahead = (ps.d - u.row) >> m.log_rows;
+    const uint32_t from = c < back ? 0 : c - back, to = units - c < ahead ? units : c + ahead;
+    uint32_t level;
+    if (copy_begins(c - from, to - from, m.levels, level)) u.level = level;
+    return u;
+}
+
+// What a warp copies for a tile: lane l units l and (of more than 32) l + 32.
+struct TilePlan {
+    UnitCopy copy[2];
+    uint32_t n, t_lo, t_hi;  // units and positions that are there
+};
+
+// Sets bad_page where a position of the tile has no valid page.
+__device__ __forceinline__ void plan_tile(const CacheMaps& m, const uint32_t* page_table,
+                                          uint32_t max_pages, uint32_t num_pages,
+                                          const FastDiv& ps, uint32_t b, int64_t p_tile,
+                                          int64_t start, int64_t hi, TilePlan& t,
+                                          uint32_t& bad_page) {
+    const uint32_t lane = threadIdx.x & 31u, units = 64u >> m.log_rows;
+    t.copy[1].level = 4;
+    if (units <= 32 && start <= p_tile && p_tile + 64 <= hi) {
+        // nearly all tiles: a feeding warp's instructions are what small pages
+        // cost most (GQA, pages of 16, E4M3, 256 requests: 488 -> 449 us)
+        t.copy[0] = plan_inner_unit(m, page_table, max_pages, num_pages, ps, b, (uint32_t)p_tile,
+                                    lane);
+        if (!__any_sync(0xffffffffu, t.copy[0].bad_page)) {
+            t.n = units;
+            t.t_lo = t.t_hi = ~0u;
+            return;
+        }
+    }
+    uint64_t there = 0;
+    t.n = 0;
+#pragma unroll 1
+    for (uint32_t h = 0; h < 2; ++h) {
+        UnitCopy u = plan_unit(m, page_table, max_pages, num_pages, ps, b, p_tile, start, hi,
+                               lane + 32u * h);
+        if (u.bad_page) bad_page = 1;
+        t.n += __popc(__ballot_sync(0xffffffffu, u.there != 0));
+        there |= u.there;
+        if (h == 0)
+            t.copy[0] = u;
+        else
+            t.copy[1] = u;
+        if (units <= 32) break;
+    }
+    t.t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
+    t.t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
+}
+
 // The page id that plan_unit will look up for unit `lane`, on its way to L1.
 __device__ __forceinline__ void prefetch_page(const CacheMaps& m, const uint32_t* page_table,
                                               uint32_t max_pages, const FastDiv& ps, uint32_t b,
@@ -225,25 +301,40 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, uint32_t co
                  : "memory");
 }
 
-// Calls issue(unit, row, page, map) for every copy that the lanes planned.  A
-// tile of one copy is issued with the same arguments in all lanes, by one
-// elected thread; of several copies every lane issues its own (the hardware
-// takes them one by one, faster than a loop that hands them round).
+// The plan of a tile that lies in one page (log_rows 6), the same in all lanes.
+struct PagePlan {
+    uint32_t row, page;
+    bool valid;
+    uint64_t there;
+};
+
+__device__ __forceinline__ PagePlan plan_page(const uint32_t* page_table, uint32_t max_pages,
+                                              uint32_t num_pages, const FastDiv& ps, uint32_t b,
+                                              uint32_t p_tile, int64_t start, int64_t hi) {
+    PagePlan t;
+    const uint32_t idx = fast_div(p_tile, ps);
+    t.page = idx < max_pages ? __ldg(page_table + (uint64_t)b * max_pages + idx)
+                             : KVW_PAGE_UNMAPPED;
+    t.row = p_tile - idx * ps.d;
+    t.valid = t.page < num_pages;
+    const int64_t before = start - p_tile, left = hi - p_tile;
+    t.there = t.valid ? ~0ull : 0ull;
+    if (left < 64) t.there &= (1ull << (uint32_t)left) - 1;
+    if (before > 0) t.there &= ~0ull << (uint32_t)before;
+    return t;
+}
+
+// Calls issue(unit, row, page, map) for every copy that the lanes planned,
+// every lane its own: the hardware takes them one by one, faster than a loop
+// that hands them round to one elected thread (GQA, pages of 16, E4M3: 488 us
+// against 513).
 template <class Issue>
-__device__ __forceinline__ void each_copy(const CacheMaps& m, const UnitCopy (&copy)[2],
-                                          Issue&& issue) {
-    if (m.log_rows == 6) {
-        const uint32_t level = __shfl_sync(0xffffffffu, copy[0].level, 0);
-        const uint32_t row = __shfl_sync(0xffffffffu, copy[0].row, 0);
-        const uint32_t page = __shfl_sync(0xffffffffu, copy[0].page, 0);
-        if (level != 4 && elect_one()) issue(0u, row, page, &m.map[0]);
-    } else {
+__device__ __forceinline__ void each_copy(const CacheMaps& m, const TilePlan& t, Issue&& issue) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (copy[h].level != 4)
-                issue((threadIdx.x & 31u) + 32u * h, copy[h].row, copy[h].page,
-                      &m.map[copy[h].level]);
-    }
+    for (int h = 0; h < 2; ++h)
+        if (t.copy[h].level != 4)
+            issue((threadIdx.x & 31u) + 32u * h, t.copy[h].row, t.copy[h].page,
+                  &m.map[t.copy[h].level]);
     __syncwarp();
 }
 

@@ -177,27 +177,13 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             __syncwarp();
             ++segment;
         }
-        UnitCopy copy[2];
-        uint32_t n = 0, t_lo = 0, t_hi = 0;
+        TilePlan t;
         uint32_t row = 0, page = 0;  // of a tile that is one copy
         auto plan = [&](uint32_t i) {
-            uint64_t there = 0;
-            n = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                copy[h].level = 4;
-                if (h && maps.log_rows) continue;
-                copy[h] = plan_unit(maps, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
-                                    (int64_t)(w.span.tile0 + i) * kTile, w.span.start, w.span.hi,
-                                    lane + 32u * h);
-                if (copy[h].bad_page) bad_page = 1;
-                n += __popc(__ballot_sync(0xffffffffu, copy[h].there != 0));
-                there |= copy[h].there;
-            }
-            t_lo = __reduce_or_sync(0xffffffffu, (uint32_t)there);
-            t_hi = __reduce_or_sync(0xffffffffu, (uint32_t)(there >> 32));
-            row = __shfl_sync(0xffffffffu, copy[0].row, 0);
-            page = __shfl_sync(0xffffffffu, copy[0].page, 0);
+            plan_tile(maps, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
+                      (int64_t)(w.span.tile0 + i) * kTile, w.span.start, w.span.hi, t, bad_page);
+            row = __shfl_sync(0xffffffffu, t.copy[0].row, 0);
+            page = __shfl_sync(0xffffffffu, t.copy[0].page, 0);
         };
         plan(w.first);
         for (uint32_t i = w.first; ok && i < w.last; ++i) {
@@ -210,16 +196,16 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                                     ((tile >> 1) & 1u) ^ 1u, &sm.stop, a.wait_limit);
                 }
                 if (!ok) continue;
-                const uint32_t bytes = (n << maps.log_rows) * 128u * group_panels<FP8>(g);
+                const uint32_t bytes = (t.n << maps.log_rows) * 128u * group_panels<FP8>(g);
                 const uint32_t bar = smem_addr(full);
                 const uint32_t base = smem_addr(
                     sm.kv + ((tile & 1u) * kTilePanels + group_start<FP8>(g)) * kPanel);
                 const bool withheld = WITHHOLD && tile == 0 && g == 0;
                 if (maps.log_rows == 6) {  // one copy per panel
                     if (elect_one()) {
-                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
+                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t.t_hi << 32) | t.t_lo;
                         mbar_arrive_expect_tx(full, bytes);
-                        if (n && !withheld) {
+                        if (t.n && !withheld) {
                             if constexpr (!FP8) {
                                 tma_4d(base, &qm.panels, 0, row, 3 * g, page, bar);
                             } else {
@@ -233,12 +219,12 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                     __syncwarp();
                 } else {
                     if (lane == 0) {
-                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t_hi << 32) | t_lo;
+                        if (g == 0) sm.there[tile & 7u] = ((uint64_t)t.t_hi << 32) | t.t_lo;
                         mbar_arrive_expect_tx(full, bytes);
                     }
                     __syncwarp();
                     if (!withheld)
-                        each_copy(maps, copy, [&](uint32_t unit, uint32_t r, uint32_t id,
+                        each_copy(maps, t, [&](uint32_t unit, uint32_t r, uint32_t id,
                                                   const CUtensorMap* map) {
 #pragma unroll kUnroll
                             for (uint32_t x = 0; x < group_panels<FP8>(g); ++x)
@@ -258,7 +244,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 plan(i + 1);
                 if ((i & 1u) == hb || a.HB == 1) {
                     if (maps.log_rows == 6) {
-                        if (n && elect_one()) {
+                        if (t.n && elect_one()) {
 #pragma unroll 1
                             for (uint32_t g = kFrom; g < kTo; ++g)
                                 tma_4d_prefetch(&qm.panels, 0, row, (FP8 ? 2 : 3) * g, page);
@@ -267,7 +253,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                         }
                         __syncwarp();
                     } else {
-                        each_copy(maps, copy, [&](uint32_t, uint32_t r, uint32_t id,
+                        each_copy(maps, t, [&](uint32_t, uint32_t r, uint32_t id,
                                                   const CUtensorMap* map) {
 #pragma unroll 1
                             for (uint32_t x = group_start<FP8>(kFrom);

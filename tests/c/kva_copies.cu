@@ -51,6 +51,12 @@ int main() {
         for (uint32_t c = 0; c < 64; ++c) {
             const UnitCopy u =
                 plan_unit(m, table.data(), width, num_pages, ps, b, p_tile, start, hi, c);
+            if (start <= p_tile && p_tile + 64 <= hi && rows > 1) {  // the short way agrees
+                const UnitCopy x = plan_inner_unit(m, table.data(), width, num_pages, ps, b,
+                                                   (uint32_t)p_tile, c);
+                NEED(x.level == u.level && x.bad_page == u.bad_page);
+                NEED(x.level == 4 || (x.page == u.page && x.row == u.row));
+            }
             if (u.there) announced += rows;
             NEED(!(there & u.there));
             there |= u.there;
