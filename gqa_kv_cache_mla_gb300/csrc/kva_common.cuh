@@ -50,7 +50,9 @@ inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, si
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by the caller's next call
+    return e;
 }
 
 // Until what came before this kernel in the stream has ended and is visible.

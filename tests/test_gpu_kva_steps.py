@@ -132,6 +132,100 @@ def test_graphs_with_workspaces_of_their_own_replay_together(kva, dtype):
         x.check()
 
 
+@pytest.mark.parametrize("joined", [False, True])
+@pytest.mark.parametrize("make", MAKE)
+def test_captured_behind_other_work(kva, make, joined):
+    """A call that follows a copy on its stream, and one that follows a join
+    with another stream, inside a graph and outside: the kernels may be
+    launched early, what they read may not."""
+    x = make(kva, 95, R.BF16)
+    real, queries = x.store.clone(), x.dq if isinstance(x.dq, list) else [x.dq]
+    given = [q.clone() for q in queries]
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        x.store.copy_(real)
+        if joined:
+            side.wait_stream(s)
+            with torch.cuda.stream(side):
+                for q, g in zip(queries, given):
+                    torch.add(g, 0, out=q)
+            s.wait_stream(side)
+        x.call(stream=s)
+        x.store.zero_()
+        for q in queries:
+            if joined:
+                q.zero_()
+
+    with torch.cuda.stream(s):
+        work()
+    torch.cuda.synchronize()
+    x.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        work()
+    for _ in range(3):
+        x.out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        x.check()
+
+
+def test_append_captured_behind_other_work(kva):
+    c = R.Paged(96, [40, 1], [0, 9], kv_heads=2, head=64)
+    desc, store, keep = c.on()
+    qkv, freqs = c.normal(c.T, 8 * 64), R.freqs_table(64, 64)
+    (wq, wk, wv), (eq, ek, ev) = R.append(c, qkv, 4, freqs)
+    real, dqkv, dfreqs = qkv.cuda(), torch.zeros_like(qkv).cuda(), freqs.cuda()
+    q = torch.empty(c.T, 4, 64, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+
+    def work():
+        torch.mul(real, 1, out=dqkv)
+        kva.kva_append_qkv_paged(q, dqkv, keep[3], desc, dfreqs, c.layer, stream=s)
+        dqkv.zero_()
+
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        work()
+    for _ in range(3):
+        q.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        R.check(q, wq, R.HALF_STEP[R.BF16] * wq.abs() * (1 + 2.0 ** -8) + eq, "q")
+
+
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+def test_most_requests(kva, kind):
+    """As many requests as a call takes, many without a new token."""
+    n = 8192
+    new = [(i * 5) % 3 % 2 for i in range(n)]
+    prior = [(i * 7) % 5 for i in range(n)]
+    kw = dict(page=4, layers=1, layer=0, table_extra=0)
+    x = Gqa(kva, 97, new, prior, heads=2, kv_heads=1, head=16, **kw) if kind == "gqa" else \
+        Mla(kva, 97, new, prior, heads=1, **kw)
+    x.call()
+    torch.cuda.synchronize()
+    x.check()
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+def test_requests_share_pages(kva, kind, dtype):
+    """A common prefix: the same pages in several tables, and twice in one."""
+    make = Gqa if kind == "gqa" else Mla
+    x = make(kva, 98, [1, 1, 2], [200, 150, 170], dtype=dtype, page=16)
+    c = x.c
+    c.table[1, :6] = c.table[0, :6]
+    c.table[2, 2:5] = c.table[0, 3:6]
+    c.table[2, 7] = c.table[2, 1]
+    x.keep[1].copy_(c.table)
+    x.call()
+    torch.cuda.synchronize()
+    x.check()
+
+
 def test_calls_of_one_stream_share_a_workspace(kva):
     a, b, m = MAKE[0](kva, 86, R.BF16), MAKE[0](kva, 87, R.E4M3), MAKE[1](kva, 88, R.E4M3)
     space = space_of(max(x.space.numel() for x in (a, b, m)))
