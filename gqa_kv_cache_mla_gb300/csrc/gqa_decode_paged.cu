@@ -898,14 +898,25 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
         const bool in = e < all && g < groups;
         const uint32_t r = in ? e / quads : 0, d = in ? (e - r * quads) * 4 : 0;
         if (in) {
-#pragma unroll 4
-            for (uint32_t i = g; i < n; i += groups) {
-                const float4 x = *reinterpret_cast<const float4*>(part(i) + r * DP + d);
-                const float f = s_w[r][i];
-                o.x += f * x.x;
-                o.y += f * x.y;
-                o.z += f * x.z;
-                o.w += f * x.w;
+            constexpr uint32_t kAtOnce = 8;  // loads in flight
+            for (uint32_t i0 = g; i0 < n; i0 += kAtOnce * groups) {
+                float4 x[kAtOnce];
+#pragma unroll
+                for (uint32_t k = 0; k < kAtOnce; ++k) {
+                    const uint32_t i = i0 + k * groups;
+                    if (i < n) x[k] = load_part(part(i) + r * DP + d);
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kAtOnce; ++k) {
+                    const uint32_t i = i0 + k * groups;
+                    if (i < n) {
+                        const float f = s_w[r][i];
+                        o.x += f * x[k].x;
+                        o.y += f * x[k].y;
+                        o.z += f * x[k].z;
+                        o.w += f * x[k].w;
+                    }
+                }
             }
         }
         if (groups > 1) {

@@ -115,6 +115,16 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
     return done != 0;
 }
 
+// Four floats of a workspace slot.  Volatile, so that a batch of them is in
+// flight before the first is used: the compiler else takes them one by one.
+__device__ __forceinline__ float4 load_part(const float* p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // A ring position: slot and the parity of its present round.
 template <int N>
 struct RingPos {

@@ -77,16 +77,21 @@ struct QMaps {
     CUtensorMap latent, rope, panels;
 };
 
-template <bool FP8>
+// WHOLE: a tile lies in one page (64 divides the page size).
+// Feeding warps: small pages make many copies, and issuing them was most of a
+// tile's time (256 requests, 128 heads, pages of 16: bf16 with three warps 441
+// us, two 535, one 772; E4M3 with two 491, one 540).  Of whole tiles two (bf16)
+// or one (E4M3) are enough, and more warps cost (bf16: three 413 us, two 407).
+template <bool FP8, bool WHOLE>
 constexpr uint32_t feeders_of() {
-    return FP8 ? 1 : 2;
+    return FP8 ? (WHOLE ? 1 : 2) : WHOLE ? 2 : 3;
 }
-template <bool FP8>
+template <bool FP8, bool WHOLE>
 constexpr int threads_of() {
-    return 32 * ((FP8 ? 9 : 5) + feeders_of<FP8>());
+    return 32 * ((FP8 ? 9 : 5) + feeders_of<FP8, WHOLE>());
 }
 
-template <bool FP8>
+template <bool FP8, bool WHOLE>
 struct Smem {
     // bf16: Q as nine panels, rotated columns last.  E4M3: four panels of 128
     // rows x 128 codes, then 128 rows x 64 rotated columns in 64-byte lines.
@@ -101,7 +106,7 @@ struct Smem {
     uint64_t s_full[2], p_full, pv_done, o_free, drained;
     uint64_t there[8];  // of a tile: positions that are there
     float alpha[kHeads], m[kHeads], l[kHeads], q_scale[kHeads];
-    SplitShared<threads_of<FP8>()> split;
+    SplitShared<threads_of<FP8, WHOLE>()> split;
     uint32_t tmem, stop;
 };
 
@@ -137,19 +142,19 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 
 // ---------------------------------------------------------------- feeding
 
-// With a bf16 cache two warps feed, groups 0 and 1 and group 2 of every tile:
-// small pages make many copies (pages of 16, 256 requests, 128 heads: 548 us,
-// 772 with one warp).  Of pages of whole tiles a group is one copy of three
-// panels; three copies of one panel each took 433 us instead of 411.
-template <bool FP8, bool WITHHOLD, uint32_t WHICH>
+// Of pages of whole tiles a group is one copy of three panels; three copies of
+// one panel each took 433 us instead of 411.
+template <bool FP8, bool WHOLE, bool WITHHOLD, uint32_t WHICH>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
-                                     Smem<FP8>& sm) {
+                                     Smem<FP8, WHOLE>& sm) {
     constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups;
     constexpr uint32_t kTilePanels = FP8 ? kCodePanels : 9;
     constexpr int kUnroll = FP8 ? 8 : 1;
-    // one of two: groups 0 and 1, or 2
-    constexpr uint32_t kFrom = WHICH ? 2 : 0;
-    constexpr uint32_t kTo = WHICH || feeders_of<FP8>() == 1 ? kTileGroups : 2;
+    // of one warp all groups, of as many as groups one each, of two for three
+    // groups the first two and the last
+    constexpr uint32_t kWarps = feeders_of<FP8, WHOLE>();
+    constexpr uint32_t kFrom = WHICH == 0 ? 0 : WHICH + kTileGroups - kWarps;
+    constexpr uint32_t kTo = WHICH + 1 + kTileGroups - kWarps;
     const uint32_t lane = threadIdx.x & 31u, hb = blockIdx.x % a.HB;
     auto column = [](uint32_t panel) {
         return FP8 ? (panel == 0 ? kLatent : (panel - 1) * 128u) : panel * 64u;
@@ -162,7 +167,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
     while (ok && !w.done()) {
         prefetch_page(maps, a.page_table, a.max_pages, a.ps, w.b,
                       (int64_t)(w.span.tile0 + w.first) * kTile, lane);
-        if constexpr (!FP8 && WHICH == feeders_of<FP8>() - 1) {
+        if constexpr (!FP8 && WHICH == kWarps - 1) {
             ok = wait_phase(&sm.q_free, (segment & 1u) ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
             if (elect_one()) {
@@ -201,7 +206,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 const uint32_t base = smem_addr(
                     sm.kv + ((tile & 1u) * kTilePanels + group_start<FP8>(g)) * kPanel);
                 const bool withheld = WITHHOLD && tile == 0 && g == 0;
-                if (maps.log_rows == 6) {  // one copy per panel
+                if constexpr (WHOLE) {
                     if (elect_one()) {
                         if (g == 0) sm.there[tile & 7u] = ((uint64_t)t.t_hi << 32) | t.t_lo;
                         mbar_arrive_expect_tx(full, bytes);
@@ -243,7 +248,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 // tiles ahead is no better than one).
                 plan(i + 1);
                 if ((i & 1u) == hb || a.HB == 1) {
-                    if (maps.log_rows == 6) {
+                    if constexpr (WHOLE) {
                         if (t.n && elect_one()) {
 #pragma unroll 1
                             for (uint32_t g = kFrom; g < kTo; ++g)
@@ -287,7 +292,8 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
 
 // Codes of the value columns -> fp16 panels in the operands' layout; positions
 // that are not there become zeros.
-__device__ __forceinline__ void convert(const MlaArgs& a, Smem<true>& sm) {
+template <bool WHOLE>
+__device__ __forceinline__ void convert(const MlaArgs& a, Smem<true, WHOLE>& sm) {
     const uint32_t lane = threadIdx.x & 31u, i0 = threadIdx.x - 192u, c = i0 & 7u;
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -388,7 +394,8 @@ struct Products {
 // The products of a bf16 cache: one thread issues every MMA.  (Fences only
 // where tensor memory passes between threads: operands in shared memory come
 // with their barriers.)
-__device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
+template <bool WHOLE>
+__device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false, WHOLE>& sm) {
     const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
     const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
@@ -469,7 +476,8 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false>& sm) {
 }
 
 // The products of an E4M3 cache: a warp whose elected thread issues.
-__device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm) {
+template <bool WHOLE>
+__device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true, WHOLE>& sm) {
     const uint32_t hb = blockIdx.x % a.HB, tmem = sm.tmem;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
     const uint32_t cols = (rows + 15u) & ~15u;  // of O^T
@@ -604,21 +612,36 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true>& sm)
 
 // ---------------------------------------------------------------- softmax
 
+// Two scaled bf16 values in fp16 -> their E4M3 parts, two codes each: x = q1 +
+// q2 / 16.  In fp16 all of it is exact but the two roundings to E4M3.
+__device__ __forceinline__ void split_pair(uint32_t x, uint32_t& q1, uint32_t& q2) {
+    asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 y, z;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 y, a;\n\t"
+        "mul.rn.f16x2 z, %2, %3;\n\t"
+        "fma.rn.f16x2 z, y, %4, z;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 b, z;\n\t"
+        "cvt.u32.u16 %0, a;\n\tcvt.u32.u16 %1, b;\n\t}"
+        : "=r"(q1), "=r"(q2)
+        : "r"(x), "r"(0x4c004c00u), "r"(0xcc00cc00u));  // 16, -16
+}
+
 // The queries of a segment as two E4M3 parts: row h scaled by a power of two
 // so that its largest value lies in [128, 256), x = q1 + q2 / 16 with q1 the
 // nearest E4M3 number and q2 the remainder, exact while q1's step is not
 // below E4M3's smallest (2^-9).  A row with an infinity or a NaN becomes NaN
-// (E4M3 has no infinity; its scores are not finite either way).  A warp takes
-// 16 heads, four at a time with the next four on their way, its lanes the 72
-// chunks of 8 values of a row.
-__device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, uint32_t t,
+// (E4M3 has no infinity; its scores are not finite either way).  The heads go
+// round the warps, a warp taking four of them at a time with the next four on
+// their way, its lanes the 72 chunks of 8 values of a row.
+template <bool WHOLE>
+__device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true, WHOLE>& sm, uint32_t t,
                                               uint32_t head0, uint32_t rows) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     constexpr int kAtOnce = 4;
-    auto load = [&](uint32_t i0, uint4(&v)[kAtOnce][3]) {
+    auto load = [&](uint32_t h0, uint4(&v)[kAtOnce][3]) {
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n) {
-            const uint32_t h = warp * 16 + i0 + n;
+            const uint32_t h = h0 + n;
             const uint16_t* ql = a.q_latent + (int64_t)t * a.q_latent_stride +
                                  (int64_t)(head0 + h) * kLatent;
             const uint16_t* qr = a.q_rope + (int64_t)t * a.q_rope_stride + (int64_t)(head0 + h) * 64;
@@ -633,15 +656,15 @@ __device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, 
         }
     };
     uint4 ahead[kAtOnce][3];
-    load(0, ahead);
+    load(warp * kAtOnce, ahead);
 #pragma unroll 1
-    for (uint32_t i0 = 0; i0 < 16; i0 += kAtOnce) {
+    for (uint32_t h0 = warp * kAtOnce; h0 < rows; h0 += 4 * kAtOnce) {
         uint4 v[kAtOnce][3];
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n)
 #pragma unroll
             for (int k = 0; k < 3; ++k) v[n][k] = ahead[n][k];
-        if (i0 + kAtOnce < 16) load(i0 + kAtOnce, ahead);
+        load(h0 + 4 * kAtOnce, ahead);
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n) {
             uint32_t top = 0;
@@ -653,24 +676,28 @@ __device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, 
             top = __reduce_max_sync(0xffffffffu, top);
             float up, down;
             row_power(top, up, down);  // to [2^14, 2^15)
-            const bool finite = (top >> 7) != 255u;
-            up *= 0x1p-7f;
+            up = (top >> 7) == 255u ? __int_as_float(0x7fffffff) : up * 0x1p-7f;
             down *= 0x1p7f;
-            const uint32_t h = warp * 16 + i0 + n, r1 = 32u * warp + i0 + n, r2 = r1 + 16u;
+            const uint32_t h = h0 + n;  // below 64: rows past the last head are zeros
+            const uint32_t r1 = 32u * (h >> 4) + (h & 15u), r2 = r1 + 16u;
             if (lane == 0) sm.q_scale[h] = down;
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 const uint32_t c = lane + 32u * k;
                 if (c >= 72) continue;
-                float x[8], y[8], z[8];
-                unpack8(v[n][k], x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = finite ? x[e] * up : __int_as_float(0x7fffffff);
-                const uint2 q1 = pack8_e4m3(x);
-                unpack8_e4m3(q1, y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = (x[e] - y[e]) * 16.0f;
-                const uint2 q2 = pack8_e4m3(z);
+                auto part = [&](uint32_t x, uint32_t& q1, uint32_t& q2) {
+                    split_pair(pack2<true>(bf16_lo(x) * up, bf16_hi(x) * up), q1, q2);
+                };
+                uint32_t lo1, lo2, hi1, hi2;
+                uint2 q1, q2;
+                part(v[n][k].x, lo1, lo2);
+                part(v[n][k].y, hi1, hi2);
+                q1.x = lo1 | (hi1 << 16);
+                q2.x = lo2 | (hi2 << 16);
+                part(v[n][k].z, lo1, lo2);
+                part(v[n][k].w, hi1, hi2);
+                q1.y = lo1 | (hi1 << 16);
+                q2.y = lo2 | (hi2 << 16);
                 // 8 codes: half of a 16-byte chunk
                 if (c < 64) {
                     unsigned char* at = sm.q + (c >> 4) * 2 * kPanel;
@@ -688,8 +715,8 @@ __device__ __forceinline__ void split_queries(const MlaArgs& a, Smem<true>& sm, 
     }
 }
 
-template <bool FP8>
-__device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
+template <bool FP8, bool WHOLE>
+__device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8, WHOLE>& sm) {
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const uint32_t quad = lane >> 2, in_quad = lane & 3u, hb = blockIdx.x % a.HB;
     const uint32_t rows = a.H - hb * kHeads < kHeads ? a.H - hb * kHeads : kHeads;
@@ -701,6 +728,13 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
     w.begin(a.split, sm.split.start);
     bool ok = true;
     uint32_t tile = 0, segment = 0;
+    if constexpr (FP8) {
+        // rows of Q past the last head stay zeros
+        for (uint32_t i = tid; i < sizeof(sm.q) / 16; i += kSoftmaxThreads)
+            reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
+        if (tid < kHeads) sm.q_scale[tid] = 1.0f;
+        any_softmax(false);
+    }
     while (!w.done()) {
         if ((int64_t)w.len0 + w.k + 1 > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
         const uint32_t shared_by = w.first == 0 && !w.whole()
@@ -921,12 +955,12 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8>& sm) {
     if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
 
-template <bool FP8, bool WITHHOLD>
-__global__ void __launch_bounds__((threads_of<FP8>()), 1)
+template <bool FP8, bool WHOLE, bool WITHHOLD>
+__global__ void __launch_bounds__((threads_of<FP8, WHOLE>()), 1)
     mla_decode_kernel(const MlaArgs a, const __grid_constant__ CacheMaps maps,
                       const __grid_constant__ QMaps qm) {
     extern __shared__ __align__(1024) unsigned char dyn[];
-    Smem<FP8>& sm = *reinterpret_cast<Smem<FP8>*>(dyn);
+    Smem<FP8, WHOLE>& sm = *reinterpret_cast<Smem<FP8, WHOLE>*>(dyn);
     const uint32_t tid = threadIdx.x, warp = tid >> 5;
     // the join of the pieces may be scheduled; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -968,18 +1002,20 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
     if (!ok) {
         if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
     } else if (warp < 4) {
-        soften<FP8>(a, sm);
+        soften<FP8, WHOLE>(a, sm);
     } else if (warp == 4) {
-        feed<FP8, WITHHOLD, 0>(a, maps, qm, sm);
+        feed<FP8, WHOLE, WITHHOLD, 0>(a, maps, qm, sm);
     } else if (warp == 5) {
         if constexpr (FP8)
             multiply_codes(a, sm);
         else
             multiply(a, sm);
-    } else if constexpr (FP8) {
-        convert(a, sm);
-    } else if constexpr (feeders_of<FP8>() > 1) {
-        feed<FP8, WITHHOLD, 1>(a, maps, qm, sm);
+    } else if (FP8 && warp < 10) {
+        if constexpr (FP8) convert(a, sm);
+    } else if (warp == (FP8 ? 10 : 6)) {
+        if constexpr (feeders_of<FP8, WHOLE>() > 1) feed<FP8, WHOLE, WITHHOLD, 1>(a, maps, qm, sm);
+    } else {
+        if constexpr (feeders_of<FP8, WHOLE>() > 2) feed<FP8, WHOLE, WITHHOLD, 2>(a, maps, qm, sm);
     }
     fence_before_sync();
     __syncthreads();
@@ -990,11 +1026,18 @@ __global__ void __launch_bounds__((threads_of<FP8>()), 1)
 }
 
 // Joins what piece blockIdx.x / HB left open, four rows a block: weights
-// 2^(m_i - M) of the pieces, then one weighted sum in their order.
+// 2^(m_i - M) of the pieces, then one weighted sum in their order.  Of up to
+// AT_ONCE pieces each thread loads all that it needs at once, of more AT_ONCE
+// at a time.  With many requests every piece has a join of a few neighbours,
+// and what counts is blocks per SM (3 loads, four blocks: 64 requests 118 us,
+// with 8 loads and two blocks 127); with few requests it is loads in flight
+// (one context of 24598 positions 43 and 38 us).
 constexpr int kJoinThreads = 512;
 constexpr uint32_t kJoinRows = 4;
 
-__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a) {
+template <uint32_t AT_ONCE>
+__global__ void __launch_bounds__(kJoinThreads, AT_ONCE > 4 ? 2 : 4)
+    mla_join_kernel(const MlaArgs a) {
     __shared__ float s_w[kJoinRows][kMaxCtas];
     __shared__ float s_top[kJoinRows], s_sum[kJoinRows];
     wait_for_stream();
@@ -1009,52 +1052,86 @@ __global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const MlaArgs a)
     auto part = [&](uint32_t i) {
         return slot_of(a, (piece + i) * a.HB + open.block, i == 0 ? 1 : 0);
     };
-    if (warp < here) {
-        const uint32_t r = r0 + warp;
-        float top = -INFINITY, l_first = 0.0f;  // of the lane's first piece
-        if (lane < n) l_first = part(lane)[(uint64_t)a.slot_rows * (kLatent + 1) + r];
-        for (uint32_t i = lane; i < n; i += 32) {
-            const float m = part(i)[(uint64_t)a.slot_rows * kLatent + r];
-            s_w[warp][i] = m;
-            top = fmaxf(top, m);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
-        for (uint32_t i = lane; i < n; i += 32) {
-            const float f = fast_exp2(s_w[warp][i] - base);
-            s_w[warp][i] = f;
-            l += f * (i == lane ? l_first : part(i)[(uint64_t)a.slot_rows * (kLatent + 1) + r]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) {
-            s_top[warp] = top;
-            s_sum[warp] = l;
-        }
-    }
-    __syncthreads();
+    const uint64_t tops = (uint64_t)a.slot_rows * kLatent, sums = tops + a.slot_rows;
     const uint32_t rj = tid >> 7, d = (tid & 127u) * 4u;  // 128 threads a row
-    if (rj >= here) return;
     float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-    for (uint32_t i = 0; i < n; ++i) {
-        const float4 x =
-            *reinterpret_cast<const float4*>(part(i) + (uint64_t)(r0 + rj) * kLatent + d);
-        const float f = s_w[rj][i];
+    float top = -INFINITY, l = 0.0f;
+    auto add = [&](float f, const float4& x) {
         o.x += f * x.x;
         o.y += f * x.y;
         o.z += f * x.z;
         o.w += f * x.w;
+    };
+    if (n <= AT_ONCE) {
+        if (rj >= here) return;
+        float4 x[AT_ONCE];
+        float m[AT_ONCE], s[AT_ONCE];
+#pragma unroll
+        for (uint32_t k = 0; k < AT_ONCE; ++k) {
+            m[k] = -INFINITY;
+            s[k] = 0.0f;
+            if (k < n) {
+                const float* p = part(k);
+                x[k] = load_part(p + (uint64_t)(r0 + rj) * kLatent + d);
+                m[k] = p[tops + r0 + rj];
+                s[k] = p[sums + r0 + rj];
+                top = fmaxf(top, m[k]);
+            }
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (uint32_t k = 0; k < AT_ONCE; ++k)
+            if (k < n) {
+                const float f = fast_exp2(m[k] - base);
+                l += f * s[k];
+                add(f, x[k]);
+            }
+    } else {
+        if (warp < here) {
+            const uint32_t r = r0 + warp;
+            float s_first = 0.0f;  // of the lane's first piece
+            if (lane < n) s_first = part(lane)[sums + r];
+            for (uint32_t i = lane; i < n; i += 32) {
+                const float m = part(i)[tops + r];
+                s_w[warp][i] = m;
+                top = fmaxf(top, m);
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            const float base = top == -INFINITY ? 0.0f : top;
+            for (uint32_t i = lane; i < n; i += 32) {
+                const float f = fast_exp2(s_w[warp][i] - base);
+                s_w[warp][i] = f;
+                l += f * (i == lane ? s_first : part(i)[sums + r]);
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+            if (lane == 0) {
+                s_top[warp] = top;
+                s_sum[warp] = l;
+            }
+        }
+        __syncthreads();
+        if (rj >= here) return;
+        top = s_top[rj];
+        l = s_sum[rj];
+        for (uint32_t i0 = 0; i0 < n; i0 += AT_ONCE) {
+            float4 x[AT_ONCE];
+#pragma unroll
+            for (uint32_t k = 0; k < AT_ONCE; ++k)
+                if (i0 + k < n) x[k] = load_part(part(i0 + k) + (uint64_t)(r0 + rj) * kLatent + d);
+#pragma unroll
+            for (uint32_t k = 0; k < AT_ONCE; ++k)
+                if (i0 + k < n) add(s_w[rj][i0 + k], x[k]);
+        }
     }
     const uint64_t row = (uint64_t)open.t * a.H + open.block * kHeads + r0 + rj;
-    const float l = s_sum[rj], inv = l == 0.0f ? 0.0f : a.row_scale / l;
+    const float inv = l == 0.0f ? 0.0f : a.row_scale / l;
     uint2 y;
     y.x = pack_bf16x2(o.x * inv, o.y * inv);
     y.y = pack_bf16x2(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2*>(a.out + row * kLatent + d) = y;
-    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (s_top[rj] + log2f(l)) * kLn2;
+    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 int workspace_bytes_for(uint32_t num_heads, uint64_t* bytes) {
@@ -1065,22 +1142,25 @@ int workspace_bytes_for(uint32_t num_heads, uint64_t* bytes) {
     return KVW_OK;
 }
 
-template <bool FP8, bool WITHHOLD>
+template <bool FP8, bool WHOLE, bool WITHHOLD>
 cudaError_t launch(MlaArgs& a, const CacheMaps& maps, const QMaps& qm, cudaStream_t stream) {
-    constexpr size_t smem = sizeof(Smem<FP8>);
+    constexpr size_t smem = sizeof(Smem<FP8, WHOLE>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = prepare_smem<&mla_decode_kernel<FP8, WITHHOLD>>(smem);
+    cudaError_t e = prepare_smem<&mla_decode_kernel<FP8, WHOLE, WITHHOLD>>(smem);
     if (e != cudaSuccess) return e;
     int sms = 0;
     if ((e = sm_count(sms)) != cudaSuccess) return e;
     uint32_t ctas = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
     a.pieces = ctas / a.HB > 0 ? ctas / a.HB : 1;
     ctas = a.pieces * a.HB;
-    e = launch_early(&mla_decode_kernel<FP8, WITHHOLD>, dim3(ctas), threads_of<FP8>(), smem, stream,
+    e = launch_early(&mla_decode_kernel<FP8, WHOLE, WITHHOLD>, dim3(ctas), threads_of<FP8, WHOLE>(), smem, stream,
                      a, maps, qm);
     if (e != cudaSuccess) return e;
-    return launch_early(&mla_join_kernel, dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows),
-                        kJoinThreads, 0, stream, a);
+    // few tokens: many pieces each
+    const dim3 joins(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows);
+    return a.pieces > 4 * a.split.T
+               ? launch_early(&mla_join_kernel<8>, joins, kJoinThreads, 0, stream, a)
+               : launch_early(&mla_join_kernel<3>, joins, kJoinThreads, 0, stream, a);
 }
 
 int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_stride,
@@ -1154,15 +1234,20 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
         e = encode_panel_map(&qm.panels, cache, layer_idx, fp8 ? 2 : 3);
     if (e != KVW_OK) return e;
     cudaError_t r;
+    auto run = [&](auto held) {
+        constexpr bool kHeld = decltype(held)::value;
+        if (maps.log_rows == 6)
+            return fp8 ? launch<true, true, kHeld>(a, maps, qm, stream)
+                       : launch<false, true, kHeld>(a, maps, qm, stream);
+        return fp8 ? launch<true, false, kHeld>(a, maps, qm, stream)
+                   : launch<false, false, kHeld>(a, maps, qm, stream);
+    };
 #ifdef KVW_TEST_HOOKS
-    if (withhold)
-        r = fp8 ? launch<true, true>(a, maps, qm, stream) : launch<false, true>(a, maps, qm, stream);
-    else
+    r = withhold ? run(std::true_type{}) : run(std::false_type{});
 #else
     if (withhold) return KVW_EUNSUPPORTED;
+    r = run(std::false_type{});
 #endif
-        r = fp8 ? launch<true, false>(a, maps, qm, stream)
-                : launch<false, false>(a, maps, qm, stream);
     return r == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
