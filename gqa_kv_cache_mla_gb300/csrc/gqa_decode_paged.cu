@@ -18,6 +18,12 @@
 // four until a segment ends, where they join in shared memory.  96 KB of ring
 // per CTA keep up to 190 KB in flight per SM.
 //
+// Measured, 32 query and 8 key-value heads of 128: 8 requests of up to 131072
+// positions, bf16 301 us (6.7 TB/s, 99 % of the card's copy rate); 256 of up to
+// 8192, E4M3 329 us (6.6 TB/s, 97 %), pages of 16 449 us; 32 of up to 4096,
+// bf16 53 us (5.2 TB/s, some 12 us of it before the first and after the last
+// byte); one token over 901 positions 10.4 us.
+//
 // CTAs of neighbouring key-value heads walk the same piece side by side
 // (`lanes`): a token's heads lie next to each other, so what one CTA reads
 // completes the DRAM rows and L2 lines that the others read at that time.  In

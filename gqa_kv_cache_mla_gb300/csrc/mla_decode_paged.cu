@@ -26,14 +26,25 @@
 //
 // Shared memory (227 KB) decides the rest.  bf16: Q 72 KB and two tiles of 72
 // KB, each in three groups of panels that are filled one by one and freed as
-// the row blocks of O^T complete.  E4M3: Q's two parts 72 KB, two tiles of codes 80 KB, one fp16
-// tile of values 64 KB in two halves.  P 8 KB.  O^T fills 256 of the 512
-// columns of tensor memory, two S tiles 128.  The MMA thread takes what is
-// ready first, the next S or the next O^T, so that neither a late tile nor a
-// late softmax holds up the other.
+// the row blocks of O^T complete.  E4M3: Q's two parts 72 KB, two tiles of
+// codes 80 KB, one fp16 tile of values 64 KB in two halves.  P 8 KB.  O^T
+// fills 256 of the 512 columns of tensor memory, two S tiles 128.  What is
+// ready goes first, the next S or the next O^T, so that neither a late tile nor
+// a late softmax holds up the other.
 //
-// Warps: 0-3 softmax, rescaling, results; 4 feeds; 5 issues the MMAs; 6-9
-// (E4M3) convert values.  Every wait is bounded.
+// Measured, contexts of up to 8192 positions: 256 requests, 128 heads, bf16
+// 411 us (716 TF/s, 38 % of the card's matrix rate), E4M3 463 us; 64 heads,
+// bf16 230 us (5.4 TB/s, 80 % of its copy rate); one token, 16 heads, 1501
+// positions 14.6 us.  A tile of 64 positions takes some 3700 cycles, of which
+// the products fill 1900: with 64 rows a 16-deep step of S reads 2 KB of Q and
+// 2 KB of K from shared memory at 128 bytes a cycle, and a step of O^T 4 KB
+// and 2 KB.  The rest is the round of a tile's place (copy 1600 cycles, S 1400,
+// softmax 1250, O^T 900, two places), and for E4M3 the round of the values'
+// (conversion 1900, O^T 1200, one place).  Steps of 32 positions, four places,
+// took 581 and 658 us: S costs as much for 32 as for 64.
+//
+// Warps: 0-3 softmax, rescaling, results; 5 issues the MMAs; 4 and (several)
+// the last ones feed; 6-9 (E4M3) convert values.  Every wait is bounded.
 #include <cstdint>
 #include <type_traits>
 
