@@ -243,3 +243,48 @@ def test_a_later_tokens_row_does_not_reach_an_earlier_one(kva, dtype, window):
     bad = torch.isnan(out).all(-1).all(-1).tolist()
     some = torch.isnan(out).any(-1).any(-1).tolist()
     assert bad == some == [bool(window), False, False, True, False]
+
+
+# tiles within a page are fed in a way of their own
+WHOLE = [64, 128, 192]
+
+
+@pytest.mark.parametrize("softcap,window,alibi", [
+    (0.0, 0, False), (5.0, 0, False), (0.0, 1, False), (0.0, 65, False), (0.0, 100, True),
+    (3.0, 200, True)])
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("q_heads", [8, 24])
+def test_whole_pages_with_modifiers(kva, dtype, q_heads, softcap, window, alibi):
+    for page in WHOLE:
+        c = R.Paged(50, [1, 2, 1, 0, 1, 9], [0, 62, 63, 7, 130, 500], kv_heads=2, head=64,
+                    dtype=dtype, page=page).fill()
+        run(kva, c, q_heads, softcap=softcap, window=window, alibi=alibi, q_std=4.0)
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+def test_whole_pages_that_are_not_valid(kva, dtype, window):
+    for page in WHOLE:
+        c = R.Paged(51, *lengths(3 * page, 33, 2 * page + 7, 20), kv_heads=2, head=64, dtype=dtype,
+                    page=page).fill()
+        c.table[0, 2 if window else 1] = R.UNMAPPED
+        c.table[2, 0] = c.pages + 5
+        c.table[2, 2] = R.UNMAPPED  # the last page: the token's own row
+        c.table[3, :] = R.UNMAPPED  # nothing left
+        got, _ = run(kva, c, 4, bad_flags=1, window=window)
+        assert bool((got[3] == 0).all())
+
+
+@pytest.mark.parametrize("window", [0, 70])
+def test_contexts_past_a_table_of_whole_pages(kva, window):
+    c = R.Paged(52, [2, 1], [290, 10], kv_heads=1, head=64, page=64).fill()
+    c.table = c.table[:, :3].contiguous()  # 192 positions
+    run(kva, c, 2, bad_flags=1, window=window)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads", [(5, 5), (28, 7), (16, 16), (34, 2), (51, 3)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_heads_side_by_side(kva, q_heads, kv_heads, page):
+    c = R.Paged(53, [1, 3, 1, 1], [2000, 70, 64, 700], kv_heads=kv_heads, head=64, page=page,
+                layers=1, layer=0).fill()
+    run(kva, c, q_heads)

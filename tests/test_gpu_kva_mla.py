@@ -191,3 +191,31 @@ def test_equal_calls_give_equal_bits(kva, dtype):
     for _ in range(3):
         again, _ = run(kva, c, 128, q=q)
         assert torch.equal(first, again)
+
+
+# tiles within a page are copied in a way of their own
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("page", [64, 128, 192])
+def test_whole_pages(kva, dtype, heads, page):
+    run(kva, batch(74, [1, 2, 1, 0, 1, 3], [0, 62, 63, 7, 130, 500], dtype=dtype, page=page,
+                   head_pad=16, token_pad=32), heads, pad=(8, 16))
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("page", [64, 128])
+def test_whole_pages_that_are_not_valid(kva, dtype, page):
+    c = batch(75, *lengths(3 * page, 33, 2 * page + 7, 20), dtype=dtype, page=page)
+    c.table[0, 1] = R.UNMAPPED
+    c.table[2, 0] = c.pages + 5
+    c.table[2, 2] = R.UNMAPPED  # the last page: the token's own row
+    c.table[3, :] = R.UNMAPPED  # nothing left
+    got, _ = run(kva, c, 16, bad_flags=1)
+    assert bool((got[3] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+def test_contexts_past_a_table_of_whole_pages(kva, dtype):
+    c = batch(76, [2, 1], [290, 10], dtype=dtype, page=64)
+    c.table = c.table[:, :3].contiguous()  # 192 positions
+    run(kva, c, 16, bad_flags=1)

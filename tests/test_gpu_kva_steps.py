@@ -371,3 +371,42 @@ def test_mla_write_then_attention(kva, cache_dtype):
     assert bool(torch.isfinite(want).all())
     R.check(out, want, tol, "out")
     R.check(lse, want_lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("kind,dtype", [("gqa", R.BF16), ("gqa", R.E4M3), ("mla", R.BF16),
+                                        ("mla", R.E4M3)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_past_32_bit_offsets(kva, kind, dtype, page):
+    """The same pages at the far end of a cache of more than 2^32 elements
+    give the same bits; appending to them writes the same rows."""
+    from gqa_kv_cache_mla_gb300 import kvw
+
+    kw = dict(dtype=dtype, page=page, layers=1, layer=0)
+    x = Gqa(kva, 99, [1, 2], [150, 700], head=128, **kw) if kind == "gqa" else \
+        Mla(kva, 99, [1, 2], [150, 700], **kw)
+    c = x.c
+    one = c.store[0].numel()
+    pages = (1 << 32) // one + 8 + c.pages
+    big = torch.empty((pages, one), dtype=c.store.dtype, device="cuda")
+    far = pages - c.pages
+    big[far:] = x.store.reshape(c.pages, one)
+    table = torch.where(x.keep[1] >= 0, x.keep[1] + far, x.keep[1])
+    st = c.data.stride()
+    desc = kvw.paged_cache(big, dtype, table, x.keep[2], pages, 1, page, c.kv_heads, c.head, st[:5],
+                           scale=c.k_scale)
+    if kind == "gqa":
+        qkv, freqs = c.normal(c.T, 12 * 128).cuda(), R.freqs_table(1024, 128).cuda()
+        q = [torch.empty(c.T, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        for y, d in zip(q, (x.desc, desc)):
+            kva.kva_append_qkv_paged(y, qkv, x.keep[3], d, freqs, 0, v_scale=c.v_scale,
+                                     err_flags=x.flags)
+        assert torch.equal(*q)
+        assert torch.equal(big[far:].view(torch.uint8),
+                           x.store.reshape(c.pages, one).view(torch.uint8))
+    x.call()
+    near = x.out.clone()
+    x.out.fill_(7.0)
+    x.desc = desc
+    x.call()
+    torch.cuda.synchronize()
+    assert int(x.flags) == 0 and torch.equal(x.out, near)
