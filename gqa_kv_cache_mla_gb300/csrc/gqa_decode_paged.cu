@@ -432,9 +432,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         // of them
         qs0 *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
         qs1 *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
-        // never 0: a masked score is -inf times this
-        qs0 = fmaxf(qs0, 1.17549435e-38f);
-        qs1 = fmaxf(qs1, 1.17549435e-38f);
+        // never 0, a masked score is -inf times this, and never infinite (a tiny
+        // cap), as a score may be 0
+        qs0 = fminf(fmaxf(qs0, 1.17549435e-38f), 3.4028234e38f);
+        qs1 = fminf(fmaxf(qs1, 1.17549435e-38f), 3.4028234e38f);
         if constexpr (!Sh::kQInRegs) {
 #pragma unroll
             for (int i = 0; i < KS / kStep; ++i)

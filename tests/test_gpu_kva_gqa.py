@@ -288,3 +288,13 @@ def test_heads_side_by_side(kva, q_heads, kv_heads, page):
     c = R.Paged(53, [1, 3, 1, 1], [2000, 70, 64, 700], kv_heads=kv_heads, head=64, page=page,
                 layers=1, layer=0).fill()
     run(kva, c, q_heads)
+
+
+@pytest.mark.parametrize("softcap", [1e-38, 1e-3, 1000.0])
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+def test_extreme_caps(kva, dtype, softcap):
+    """A tiny cap makes every weight nearly the same, a huge one changes little."""
+    c = R.Paged(54, *lengths(3, 130), kv_heads=1, head=64, dtype=dtype).fill()
+    q = c.normal(2, 4, 64)
+    q[:, 0] = 0  # scores of 0
+    run(kva, c, 4, q=q, softcap=softcap)

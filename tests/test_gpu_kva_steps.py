@@ -410,3 +410,23 @@ def test_pages_past_32_bit_offsets(kva, kind, dtype, page):
     x.call()
     torch.cuda.synchronize()
     assert int(x.flags) == 0 and torch.equal(x.out, near)
+
+
+@pytest.mark.parametrize("length", [0x7FFFFFFF, 0x80000000, 0xFFFFFFFF])
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_the_longest_lengths(kva, kind, length, page):
+    """Positions past the page table have no page: what the table reaches is
+    seen, and the flag set."""
+    make = Gqa if kind == "gqa" else Mla
+    x = make(kva, 100, [1, 1], [191, 30], page=page, table_extra=0)
+    x.call()
+    torch.cuda.synchronize()
+    x.check()
+    all_seen = x.out.clone()
+    x.keep[2][0] = length - (1 << 32) if length >> 31 else length
+    x.out.fill_(7.0)
+    x.call()
+    torch.cuda.synchronize()
+    assert int(x.flags) == 1
+    assert torch.equal(x.out, all_seen)
