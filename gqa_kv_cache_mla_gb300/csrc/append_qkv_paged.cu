@@ -25,10 +25,14 @@
 // ragged tables once.
 //
 // Measured, 32 ragged requests of up to 2048 new tokens, 32 + 2 x 8 heads of
-// 128 (780 MB): 127 us, 6.1 TB/s, 90 % of the card's copy rate.  Three CTAs per SM (80 registers, a few scalars
-// spilled) against two and four (64 registers): bf16 130, 131, 138 us; E4M3
-// 133, 151, 129 us; with norms 133, 142, 190 us.  One pass ahead instead of
-// two: 134, 140 and 136 us.  One token: 2.3 us on the device.
+// 128 (780 MB): 127 us, 6.1 TB/s, 90 % of the card's copy rate.  Three CTAs
+// per SM (80 registers, a few scalars spilled) against two and four (64
+// registers): bf16 130, 131, 138 us; E4M3 133, 151, 129 us; with norms 133,
+// 142, 190 us.  One pass ahead instead of two: 134, 140 and 136 us; the next
+// item's first rows loaded before an item ends: 143, 154, 146 us (spills).  One
+// token: 2.3 us on the device.  With few rows a token (4 + 2 x 1 heads of 96)
+// the lookups of a token are most of its work: 47 k tokens 60 us, a quarter of
+// the copy rate.
 #include <cstdint>
 
 #include "kva_common.cuh"
