@@ -1048,7 +1048,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     const uint32_t fit = per_request * a.G <= 8 ? 8 : kRows;
     while (a.HB == 1 && (2u << a.split.log_c) * a.G <= fit) ++a.split.log_c;
     a.split.min_units = 1;
-    a.split.overhead = 2;
+    a.split.overhead = 3;  // a segment's cost beside its tiles, in tiles (1 to 5: within 2 %)
     const uint64_t reach = (uint64_t)cache->max_pages_per_seq * cache->page_size;
     a.split.cap = reach > kMaxReach ? (int64_t)kMaxReach : (int64_t)reach;
     a.split.window = window ? (int64_t)window : 1ll << 40;

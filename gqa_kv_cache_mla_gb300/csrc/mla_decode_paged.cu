@@ -33,8 +33,8 @@
 // a late softmax holds up the other.
 //
 // Measured, contexts of up to 8192 positions: 256 requests, 128 heads, bf16
-// 411 us (716 TF/s, 38 % of the card's matrix rate), E4M3 463 us; 64 heads,
-// bf16 230 us (5.4 TB/s, 80 % of its copy rate); one token, 16 heads, 1501
+// 411 us (716 TF/s, 38 % of the card's matrix rate), E4M3 453 us; 64 heads,
+// bf16 225 us (5.5 TB/s, 82 % of its copy rate); one token, 16 heads, 1501
 // positions 14.6 us.  A tile of 64 positions takes some 3700 cycles, of which
 // the products fill 1900: with 64 rows a 16-deep step of S reads 2 KB of Q and
 // 2 KB of K from shared memory at 128 bytes a cycle, and a step of O^T 4 KB
@@ -1210,7 +1210,11 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
     a.split.T = tot_seq_len;
     a.split.blocks = 1;  // the row blocks of a token are CTAs of the same piece
     a.split.min_units = 1;
-    a.split.overhead = 2;
+    // What a segment costs beside its tiles, in tiles: with E4M3 the queries are
+    // split (2, 4, 6: 174 requests of up to 1266 positions, 64 heads 74, 71, 68
+    // us; 206 of up to 2249, 16 heads 73, 72, 75); bf16 168 requests of 2 tokens,
+    // 8 heads 47, 52, 56 us.
+    a.split.overhead = fp8 ? 5 : 2;
     const uint64_t reach = (uint64_t)cache->max_pages_per_seq * cache->page_size;
     a.split.cap = reach > kMaxReach ? (int64_t)kMaxReach : (int64_t)reach;
     a.split.window = 1ll << 40;
