@@ -7,14 +7,15 @@
 // positions for one row block of one chunk; `overhead` further units stand
 // before the tiles of every (chunk, row block) for what it costs to begin and
 // end one.  The units of all chunks in order - chunk, row block, tile - form
-// one long axis, cut into equal pieces, one for each CTA.  So every CTA has
-// the same work whatever the lengths, a CTA crosses from one chunk to the
-// next where its piece does, and at most two of its segments are parts of a
-// (chunk, row block) that other CTAs share: its first (slot 0) and its last
-// (slot 1).  Those write their unnormalised sums with their running maximum
-// and sum to a workspace whose size depends on the number of pieces alone,
-// and a second kernel joins them in order: the result depends on the lengths
-// and the device only.
+// one long axis, cut into equal pieces, one for each CTA (or for each of
+// several CTAs that take row blocks side by side; those are then not part of
+// the axis).  So every CTA has the same work whatever the lengths, a CTA
+// crosses from one chunk to the next where its piece does, and at most two of
+// its segments are parts of a (chunk, row block) that other CTAs share: its
+// first (slot 0) and its last (slot 1).  Those write their unnormalised sums
+// with their running maximum and sum to a workspace whose size depends on the
+// number of pieces alone, and a second kernel joins them in order: the result
+// depends on the lengths and the device only.
 //
 // Finding a piece needs the number of tiles before a chunk, a prefix sum over
 // chunks.  Within a request the chunks' lengths rise by C, so a request's
@@ -119,12 +120,23 @@ __host__ __device__ __forceinline__ uint64_t div_units(uint64_t x, uint64_t y) {
     return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
 
-// First unit of piece c of `pieces` over `units` units (even to one unit).
-__host__ __device__ __forceinline__ uint64_t piece_start(uint64_t units, uint32_t pieces,
-                                                         uint32_t c) {
-    const uint64_t q = div_units(units, pieces), r = units - q * pieces;
-    return q * c + (c < r ? c : r);
-}
+// `units` units cut into `pieces` pieces, even to one unit: the first r pieces
+// have q + 1, the others q.
+struct Cut {
+    uint64_t q, r;
+    __host__ __device__ __forceinline__ Cut(uint64_t units, uint32_t pieces) {
+        q = div_units(units, pieces);
+        r = units - q * pieces;
+    }
+    // First unit of piece c, and the piece that holds unit u.
+    __host__ __device__ __forceinline__ uint64_t start(uint32_t c) const {
+        return q * c + (c < r ? c : r);
+    }
+    __host__ __device__ __forceinline__ uint32_t piece_of(uint64_t u) const {
+        const uint64_t longer = (q + 1) * r;
+        return (uint32_t)(u < longer ? div_units(u, q + 1) : r + div_units(u - longer, q));
+    }
+};
 
 // Pieces in use: at most `most`, none shorter than min_units unless there is
 // only one.
@@ -189,9 +201,9 @@ __device__ __forceinline__ bool find_piece(const SplitArgs& a, uint32_t most, ui
     s.units = (uint64_t)total * a.blocks;
     s.pieces = pieces_of(a, s.units, most);
     const bool used = c < s.pieces;
-    const uint64_t q = div_units(s.units, s.pieces), rest = s.units - q * s.pieces;
-    s.u0 = used ? q * c + (c < rest ? c : rest) : s.units;  // as piece_start has it
-    s.u1 = used ? s.u0 + q + (c < rest ? 1 : 0) : s.units;
+    const Cut cut(s.units, s.pieces);
+    s.u0 = used ? cut.start(c) : s.units;
+    s.u1 = used ? cut.start(c + 1) : s.units;
     s.chunk_base = 0;
     s.b = s.k = s.first = s.n = s.len = 0;
     if (!used && tid == 0) sh.start = s;
@@ -311,13 +323,6 @@ struct Walk {
     }
 };
 
-// The piece (of `pieces`) that holds unit u.
-__host__ __device__ __forceinline__ uint32_t piece_of(uint64_t units, uint32_t pieces, uint64_t u) {
-    const uint64_t q = div_units(units, pieces), r = units - q * pieces;  // r pieces have q + 1
-    const uint64_t longer = (q + 1) * r;
-    return (uint32_t)(u < longer ? div_units(u, q + 1) : r + div_units(u - longer, q));
-}
-
 // What a piece left open: a (chunk, row block) whose first tile it has (slot 1)
 // and that the next n - 1 pieces go on with (their slot 0).  n 0: nothing.
 struct __align__(16) OpenPiece {
@@ -328,7 +333,7 @@ static_assert(sizeof(OpenPiece) == 16, "workspace layout");
 // Pieces that share the segment at w, which piece c of s begins.
 __device__ __forceinline__ uint32_t sharers(const SplitArgs& a, const PieceStart& s, const Walk& w,
                                             uint32_t c) {
-    return piece_of(s.units, s.pieces, w.end(a) - 1) - c + 1;
+    return Cut(s.units, s.pieces).piece_of(w.end(a) - 1) - c + 1;
 }
 
 }  // namespace kvw

@@ -62,15 +62,16 @@ int main() {
         SplitArgs a = {};
         a.min_units = 1 + (uint32_t)rnd(8);
         const uint32_t most = 1 + (uint32_t)rnd(512), p = pieces_of(a, units, most);
-        if (p < 1 || p > most || p > units || piece_start(units, p, 0) != 0 ||
-            piece_start(units, p, p) != units)
+        const Cut cut(units, p);
+        if (p < 1 || p > most || p > units || cut.start(0) != 0 ||
+            cut.start(p) != units)
             return printf("pieces\n"), 1;
         for (uint32_t c = 0; c < p; ++c) {
-            const uint64_t size = piece_start(units, p, c + 1) - piece_start(units, p, c);
+            const uint64_t size = cut.start(c + 1) - cut.start(c);
             if (size < 1 || size < units / p || size > units / p + 1) return printf("cut\n"), 1;
             if (p > 1 && size < a.min_units) return printf("short piece\n"), 1;
-            const uint64_t u = piece_start(units, p, c);
-            if (piece_of(units, p, u) != c || piece_of(units, p, u + size - 1) != c)
+            const uint64_t u = cut.start(c);
+            if (cut.piece_of(u) != c || cut.piece_of(u + size - 1) != c)
                 return printf("piece_of\n"), 1;
         }
         ++checks;
