@@ -894,11 +894,15 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8, WHOLE>& sm) {
             sm.l[h0 + 8] = l1;
         }
         const bool whole = w.whole();
-        if (in_quad == 0) {  // what the sums are multiplied by
+        ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_limit);
+        // What the sums are multiplied by.  Not before the wait: a warp behind
+        // this one may still rescale by the alphas of the last tile, which it
+        // has read when it arrives on p_full, and pv_done follows all four.
+        // The vote makes the new ones visible.
+        if (ok && in_quad == 0) {
             sm.alpha[h0] = l0 == 0.0f ? 0.0f : whole ? a.row_scale / l0 : 1.0f;
             sm.alpha[h0 + 8] = l1 == 0.0f ? 0.0f : whole ? a.row_scale / l1 : 1.0f;
         }
-        ok = ok && wait_phase(&sm.pv_done, (tile - 1) & 1u, &sm.stop, a.wait_limit);
         if (any_softmax(!ok)) break;
         fence_after_sync();
         float* part = slot_of(a, blockIdx.x, w.first == 0 ? 1 : 0);

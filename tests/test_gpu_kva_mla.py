@@ -219,3 +219,23 @@ def test_contexts_past_a_table_of_whole_pages(kva, dtype):
     c = batch(76, [2, 1], [290, 10], dtype=dtype, page=64)
     c.table = c.table[:, :3].contiguous()  # 192 positions
     run(kva, c, 16, bad_flags=1)
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("page", [16, 64])
+def test_last_tile_raises_the_maximum(kva, dtype, heads, page):
+    """The token's own row, in the last tile of its segment, lifts the scores of
+    most heads far above those before: O^T is rescaled there, and right after it
+    the segment's results are taken."""
+    n = 400
+    total = [65 + (i * 37) % 190 for i in range(n)]
+    c = batch(77, *lengths(*total), dtype=dtype, page=page, layers=1, layer=0)
+    for b in range(n):
+        p = total[b] - 1
+        row = c.data[int(c.table[b, p // page]), 0, 0, p % page, 0]
+        row[0] = 60.0 if dtype == R.BF16 else \
+            torch.tensor(60.0 / c.k_scale).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = c.normal(n, heads, 512, std=0.5), c.normal(n, heads, 64, std=0.5)
+    q[0][:, :, 0] = torch.linspace(-1.0, 6.0, heads)
+    run(kva, c, heads, q=q, sm_scale=0.2)
