@@ -164,7 +164,7 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
 }
 
 // The feeding warp: walks the piece's tiles ahead of the arithmetic.
-template <int DP, bool FP8, bool WITHHOLD>
+template <int DP, bool FP8, Hook HOOK>
 __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
                                      Smem<DP, FP8>& sm) {
     using Sh = Shape<DP, FP8>;
@@ -219,7 +219,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
                         if (plane == 0) sm.there[at.slot] = t.there;
                         mbar_arrive_expect_tx(full, t.valid ? Sh::kHalf : 0);
                         const uint32_t dst = smem_addr(sm.ring + at.slot * Sh::kHalf);
-                        if (t.valid && !(WITHHOLD && first_half)) {
+                        if (t.valid && !(HOOK == Hook::kWithheld && first_half)) {
 #pragma unroll
                             for (int blk = 0; blk < Sh::kBlocks; ++blk)
                                 tma_rows(dst + blk * Sh::kBlock, &maps.map[0],
@@ -251,7 +251,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
                                           (t.n << maps.log_rows) * Sh::kLine * Sh::kBlocks);
                 }
                 __syncwarp();
-                if (!(WITHHOLD && first_half)) {
+                if (!(HOOK == Hook::kWithheld && first_half)) {
                     const uint32_t bar = smem_addr(&sm.full[at.slot]);
                     const uint32_t base = smem_addr(sm.ring + at.slot * Sh::kHalf);
                     each_copy(maps, t, [&](uint32_t unit, uint32_t row, uint32_t page,
@@ -271,24 +271,24 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
         if (ok) w.next(a.split);
     }
     if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
-    if (!ok) {
-        // copies still under way land in this CTA's memory: wait for them (a
-        // bounded time) before the CTA may end
-        if (lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
-        const uint32_t n = issued < (uint32_t)Sh::kHalves ? issued : (uint32_t)Sh::kHalves;
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint32_t x = issued - 1 - i;
-            drain_phase(&sm.full[x % Sh::kHalves], (x / Sh::kHalves) & 1u, a.wait_limit);
-        }
-        for (uint32_t i = 0; i < (uint32_t)Sh::kQBufs; ++i)
-            drain_phase(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_limit);
+    if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+    // Whether or not this warp had to wait in vain: it leaves when the last copy
+    // into each place has landed, or after a bounded time.
+    const uint32_t n = issued < (uint32_t)Sh::kHalves ? issued : (uint32_t)Sh::kHalves;
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t x = issued - 1 - i;
+        leave_phase<HOOK>(&sm.full[x % Sh::kHalves], (x / Sh::kHalves) & 1u, a.wait_limit,
+                          a.err_flags);
     }
+    for (uint32_t i = 0; i < (uint32_t)Sh::kQBufs; ++i)
+        leave_phase<HOOK>(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_limit,
+                          a.err_flags);
 }
 
 // HIGH: a row block may have more than 8 rows; without it the upper half of
 // every operand is constant zeros and nothing is computed for it (256 requests,
 // E4M3, groups of 4: 383 -> 374 us, with distance bias 435 -> 400 us).
-template <int DP, bool FP8, bool MODS, bool HIGH, bool WITHHOLD>
+template <int DP, bool FP8, bool MODS, bool HIGH, Hook HOOK>
 __global__ void __launch_bounds__(kThreads, 2)
     gqa_decode_kernel(const GqaArgs a, const __grid_constant__ CacheMaps maps) {
     using Sh = Shape<DP, FP8>;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeederRegs));
-        if (warp == kWarps) feed<DP, FP8, WITHHOLD>(a, maps, sm);
+        if (warp == kWarps) feed<DP, FP8, HOOK>(a, maps, sm);
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
@@ -354,7 +354,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     Walk w;
     w.begin(a.split, sm.split.start);
     bool alive = true;
-    while (!w.done()) {
+    if constexpr (HOOK == Hook::kAbandoned) {
+        *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+        alive = false;
+    }
+    while (alive && !w.done()) {
         const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
         const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
@@ -957,12 +961,12 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     }
 }
 
-template <int DP, bool FP8, bool MODS, bool HIGH, bool WITHHOLD>
+template <int DP, bool FP8, bool MODS, bool HIGH, Hook HOOK>
 cudaError_t launch_as(GqaArgs& a, const CacheMaps& maps, cudaStream_t stream) {
     constexpr size_t smem = sizeof(Smem<DP, FP8>);
     static_assert(smem <= 113 * 1024, "two CTAs per SM");
     uint64_t wave = 0;
-    cudaError_t e = wave_ctas<&gqa_decode_kernel<DP, FP8, MODS, HIGH, WITHHOLD>>(kThreads, smem, wave);
+    cudaError_t e = wave_ctas<&gqa_decode_kernel<DP, FP8, MODS, HIGH, HOOK>>(kThreads, smem, wave);
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
     if (wave > kMaxPieces) wave = kMaxPieces;
@@ -973,7 +977,7 @@ cudaError_t launch_as(GqaArgs& a, const CacheMaps& maps, cudaStream_t stream) {
     a.split.blocks = blocks / a.lanes;
     a.pieces = (uint32_t)wave / a.lanes;
     const uint32_t ctas = a.pieces * a.lanes;
-    e = launch_early(&gqa_decode_kernel<DP, FP8, MODS, HIGH, WITHHOLD>, dim3(ctas), kThreads, smem,
+    e = launch_early(&gqa_decode_kernel<DP, FP8, MODS, HIGH, HOOK>, dim3(ctas), kThreads, smem,
                      stream, a, maps);
     if (e != cudaSuccess) return e;
     // where a join may be of more than 48 pieces on average, eight blocks take
@@ -982,16 +986,16 @@ cudaError_t launch_as(GqaArgs& a, const CacheMaps& maps, cudaStream_t stream) {
     return launch_early(&gqa_join_kernel<DP>, dim3(ctas, y), kJoinThreads, 0, stream, a);
 }
 
-template <int DP, bool FP8, bool WITHHOLD>
+template <int DP, bool FP8, Hook HOOK>
 int launch(GqaArgs& a, const kvw_paged_cache_t* cache, uint32_t layer_idx, cudaStream_t stream) {
     CacheMaps maps;
     const int st = encode_cache_maps(&maps, cache, layer_idx, 2);
     if (st != KVW_OK) return st;
     const bool mods = a.softcap > 0.0f || a.slopes, high = (a.per_token << a.split.log_c) > 8;
-    const cudaError_t e = mods ? (high ? launch_as<DP, FP8, true, true, WITHHOLD>(a, maps, stream)
-                                       : launch_as<DP, FP8, true, false, WITHHOLD>(a, maps, stream))
-                          : high ? launch_as<DP, FP8, false, true, WITHHOLD>(a, maps, stream)
-                                 : launch_as<DP, FP8, false, false, WITHHOLD>(a, maps, stream);
+    const cudaError_t e = mods ? (high ? launch_as<DP, FP8, true, true, HOOK>(a, maps, stream)
+                                       : launch_as<DP, FP8, true, false, HOOK>(a, maps, stream))
+                          : high ? launch_as<DP, FP8, false, true, HOOK>(a, maps, stream)
+                                 : launch_as<DP, FP8, false, false, HOOK>(a, maps, stream);
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
@@ -1012,7 +1016,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
               uint32_t num_q_heads, const kvw_paged_cache_t* cache, float v_scale,
               uint32_t layer_idx, float sm_scale, float softcap, uint32_t window,
               const float* alibi_slopes, void* workspace, uint64_t workspace_bytes,
-              uint32_t* err_flags, cudaStream_t stream, bool withhold, uint64_t wait_ns) {
+              uint32_t* err_flags, cudaStream_t stream, Hook hook, uint64_t wait_ns) {
     const int st = check_cache(cache, layer_idx, 2);
     if (st != KVW_OK) return st;
     const uint32_t D = cache->head_size, Hk = cache->num_heads;
@@ -1074,13 +1078,17 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     a.wait_limit = wait_cycles(wait_ns);
     auto run = [&](auto dp, auto f8) {
 #ifdef KVW_TEST_HOOKS
-        if (withhold)
-            return launch<decltype(dp)::value, decltype(f8)::value, true>(a, cache, layer_idx,
-                                                                          stream);
+        if (hook == Hook::kWithheld)
+            return launch<decltype(dp)::value, decltype(f8)::value, Hook::kWithheld>(
+                a, cache, layer_idx, stream);
+        if (hook == Hook::kAbandoned)
+            return launch<decltype(dp)::value, decltype(f8)::value, Hook::kAbandoned>(
+                a, cache, layer_idx, stream);
 #else
-        if (withhold) return (int)KVW_EUNSUPPORTED;
+        if (hook != Hook::kNone) return (int)KVW_EUNSUPPORTED;
 #endif
-        return launch<decltype(dp)::value, decltype(f8)::value, false>(a, cache, layer_idx, stream);
+        return launch<decltype(dp)::value, decltype(f8)::value, Hook::kNone>(a, cache, layer_idx,
+                                                                            stream);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
@@ -1110,8 +1118,8 @@ extern "C" int kva_gqa_decode_paged(void* out, float* lse, const void* q, int64_
                                     cudaStream_t stream) {
     return kvw::gqa_entry(out, lse, q, q_row_stride, input_row_offsets, num_batches, tot_seq_len,
                           num_q_heads, cache, v_scale, layer_idx, sm_scale, softcap, window,
-                          alibi_slopes, workspace, workspace_bytes, err_flags, stream, false,
-                          kvw::kWaitLimitNs);
+                          alibi_slopes, workspace, workspace_bytes, err_flags, stream,
+                          kvw::Hook::kNone, kvw::kWaitLimitNs);
 }
 
 #ifdef KVW_TEST_HOOKS
@@ -1126,6 +1134,20 @@ extern "C" int kva_test_gqa_decode_withheld(
     uint32_t* err_flags, cudaStream_t stream, uint64_t wait_ns) {
     return kvw::gqa_entry(out, nullptr, q, q_row_stride, input_row_offsets, num_batches,
                           tot_seq_len, num_q_heads, cache, 1.0f, layer_idx, 0.1f, 0.0f, 0, nullptr,
-                          workspace, workspace_bytes, err_flags, stream, true, wait_ns);
+                          workspace, workspace_bytes, err_flags, stream, kvw::Hook::kWithheld,
+                          wait_ns);
+}
+
+// The consumers leave at once, so nobody waits for the copies; err_flags[1]
+// counts places whose last copy had not landed when the feeding warp left.
+extern "C" int kva_test_gqa_decode_abandoned(
+    void* out, const void* q, int64_t q_row_stride, const uint32_t* input_row_offsets,
+    uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_q_heads,
+    const kvw_paged_cache_t* cache, uint32_t layer_idx, void* workspace, uint64_t workspace_bytes,
+    uint32_t* err_flags, cudaStream_t stream, uint64_t wait_ns) {
+    return kvw::gqa_entry(out, nullptr, q, q_row_stride, input_row_offsets, num_batches,
+                          tot_seq_len, num_q_heads, cache, 1.0f, layer_idx, 0.1f, 0.0f, 0, nullptr,
+                          workspace, workspace_bytes, err_flags, stream, kvw::Hook::kAbandoned,
+                          wait_ns);
 }
 #endif

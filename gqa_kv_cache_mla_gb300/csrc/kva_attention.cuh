@@ -84,6 +84,34 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity, int6
         if (clock64() - t0 > limit_cycles) return;
 }
 
+// Has the phase of parity `parity` completed?  (Does not wait.)
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// What a kernel of a test build does on purpose: announce its first copies but
+// never issue them, or leave its tiles to nobody (the consumers go at once).
+enum class Hook { kNone, kWithheld, kAbandoned };
+
+// The last phase of a place that copies land in, before its CTA may go: copies
+// that nobody waits for (a consumer that gave up) would land in the shared
+// memory of another CTA.  The test build counts those still under way after it.
+template <Hook HOOK>
+__device__ __forceinline__ void leave_phase(uint64_t* bar, uint32_t parity, int64_t limit_cycles,
+                                            uint32_t* err_flags) {
+    drain_phase(bar, parity, limit_cycles);
+    if constexpr (HOOK == Hook::kAbandoned)
+        if ((threadIdx.x & 31u) == 0 && !phase_done(bar, parity)) atomicAdd(err_flags + 1, 1u);
+}
+
 // Cycles of a limit in nanoseconds (the clock runs at 2.07 GHz at most).
 inline int64_t wait_cycles(uint64_t ns) { return (int64_t)(ns * 2); }
 
@@ -100,19 +128,6 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_
         }
     }
     return true;
-}
-
-// Has the phase of parity `parity` completed?  (Does not wait.)
-__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
 }
 
 // Four floats of a workspace slot.  Volatile, so that a batch of them is in

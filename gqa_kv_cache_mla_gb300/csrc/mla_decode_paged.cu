@@ -155,7 +155,7 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 
 // Of pages of whole tiles a group is one copy of three panels; three copies of
 // one panel each took 433 us instead of 411.
-template <bool FP8, bool WHOLE, bool WITHHOLD, uint32_t WHICH>
+template <bool FP8, bool WHOLE, Hook HOOK, uint32_t WHICH>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8, WHOLE>& sm) {
     constexpr uint32_t kTileGroups = FP8 ? kCodeGroups : kGroups;
@@ -216,7 +216,7 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
                 const uint32_t bar = smem_addr(full);
                 const uint32_t base = smem_addr(
                     sm.kv + ((tile & 1u) * kTilePanels + group_start<FP8>(g)) * kPanel);
-                const bool withheld = WITHHOLD && tile == 0 && g == 0;
+                const bool withheld = HOOK == Hook::kWithheld && tile == 0 && g == 0;
                 if constexpr (WHOLE) {
                     if (elect_one()) {
                         if (g == 0) sm.there[tile & 7u] = ((uint64_t)t.t_hi << 32) | t.t_lo;
@@ -283,20 +283,20 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
         if (ok) w.next(a.split);
     }
     if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
-    if (!ok) {
-        // copies still under way land in this CTA's memory: wait for them (a
-        // bounded time) before the CTA may end
-        if (lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+    if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+    // Whether or not this warp had to wait in vain: it leaves when the last copy
+    // into each place has landed, or after a bounded time.
 #pragma unroll 1
-        for (uint32_t buf = 0; buf < 2; ++buf)
+    for (uint32_t buf = 0; buf < 2; ++buf)
 #pragma unroll 1
-            for (uint32_t g = kFrom; g < kTo; ++g) {
-                const uint32_t issued = (tile + (g < stopped_at) + 1 - buf) >> 1;  // into this place
-                if (issued)
-                    drain_phase(&sm.full[buf * kTileGroups + g], (issued - 1) & 1u, a.wait_limit);
-            }
-        if (!FP8 && segment) drain_phase(&sm.q_full, (segment - 1) & 1u, a.wait_limit);
-    }
+        for (uint32_t g = kFrom; g < kTo; ++g) {
+            const uint32_t issued = (tile + (g < stopped_at) + 1 - buf) >> 1;  // into this place
+            if (issued)
+                leave_phase<HOOK>(&sm.full[buf * kTileGroups + g], (issued - 1) & 1u,
+                                  a.wait_limit, a.err_flags);
+        }
+    if (!FP8 && segment)
+        leave_phase<HOOK>(&sm.q_full, (segment - 1) & 1u, a.wait_limit, a.err_flags);
 }
 
 // ---------------------------------------------------------------- converting
@@ -476,12 +476,11 @@ __device__ __forceinline__ void multiply(const MlaArgs& a, Smem<false, WHOLE>& s
                 if (*reinterpret_cast<volatile uint32_t*>(&sm.stop)) ok = false;
             }
         }
-        if (!ok) {
-            // let what was issued finish before tensor and shared memory go
-            flag(a.err_flags, KVW_ERR_TIMEOUT);
-            mma_commit(&sm.drained);
-            drain_phase(&sm.drained, 0, a.wait_limit);
-        }
+        if (!ok) flag(a.err_flags, KVW_ERR_TIMEOUT);
+        // what was issued finishes before tensor and shared memory go, also where
+        // the softmax warps, who wait for it, gave up
+        mma_commit(&sm.drained);
+        drain_phase(&sm.drained, 0, a.wait_limit);
     }
     __syncwarp();
 }
@@ -610,15 +609,14 @@ __device__ __forceinline__ void multiply_codes(const MlaArgs& a, Smem<true, WHOL
             ++o_tile;
         }
     }
-    if (!ok) {
-        // let what was issued finish before tensor and shared memory go
-        if (elect_one()) {
-            flag(a.err_flags, KVW_ERR_TIMEOUT);
-            mma_commit(&sm.drained);
-        }
-        __syncwarp();
-        drain_phase(&sm.drained, 0, a.wait_limit);
+    // what was issued finishes before tensor and shared memory go, also where the
+    // softmax warps, who wait for it, gave up
+    if (elect_one()) {
+        if (!ok) flag(a.err_flags, KVW_ERR_TIMEOUT);
+        mma_commit(&sm.drained);
     }
+    __syncwarp();
+    drain_phase(&sm.drained, 0, a.wait_limit);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -970,7 +968,7 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8, WHOLE>& sm) {
     if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
 
-template <bool FP8, bool WHOLE, bool WITHHOLD>
+template <bool FP8, bool WHOLE, Hook HOOK>
 __global__ void __launch_bounds__((threads_of<FP8, WHOLE>()), 1)
     mla_decode_kernel(const MlaArgs a, const __grid_constant__ CacheMaps maps,
                       const __grid_constant__ QMaps qm) {
@@ -1017,9 +1015,12 @@ __global__ void __launch_bounds__((threads_of<FP8, WHOLE>()), 1)
     if (!ok) {
         if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
     } else if (warp < 4) {
-        soften<FP8, WHOLE>(a, sm);
+        if constexpr (HOOK == Hook::kAbandoned)
+            *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+        else
+            soften<FP8, WHOLE>(a, sm);
     } else if (warp == 4) {
-        feed<FP8, WHOLE, WITHHOLD, 0>(a, maps, qm, sm);
+        feed<FP8, WHOLE, HOOK, 0>(a, maps, qm, sm);
     } else if (warp == 5) {
         if constexpr (FP8)
             multiply_codes(a, sm);
@@ -1028,9 +1029,9 @@ __global__ void __launch_bounds__((threads_of<FP8, WHOLE>()), 1)
     } else if (FP8 && warp < 10) {
         if constexpr (FP8) convert(a, sm);
     } else if (warp == (FP8 ? 10 : 6)) {
-        if constexpr (feeders_of<FP8, WHOLE>() > 1) feed<FP8, WHOLE, WITHHOLD, 1>(a, maps, qm, sm);
+        if constexpr (feeders_of<FP8, WHOLE>() > 1) feed<FP8, WHOLE, HOOK, 1>(a, maps, qm, sm);
     } else {
-        if constexpr (feeders_of<FP8, WHOLE>() > 2) feed<FP8, WHOLE, WITHHOLD, 2>(a, maps, qm, sm);
+        if constexpr (feeders_of<FP8, WHOLE>() > 2) feed<FP8, WHOLE, HOOK, 2>(a, maps, qm, sm);
     }
     fence_before_sync();
     __syncthreads();
@@ -1157,18 +1158,18 @@ int workspace_bytes_for(uint32_t num_heads, uint64_t* bytes) {
     return KVW_OK;
 }
 
-template <bool FP8, bool WHOLE, bool WITHHOLD>
+template <bool FP8, bool WHOLE, Hook HOOK>
 cudaError_t launch(MlaArgs& a, const CacheMaps& maps, const QMaps& qm, cudaStream_t stream) {
     constexpr size_t smem = sizeof(Smem<FP8, WHOLE>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = prepare_smem<&mla_decode_kernel<FP8, WHOLE, WITHHOLD>>(smem);
+    cudaError_t e = prepare_smem<&mla_decode_kernel<FP8, WHOLE, HOOK>>(smem);
     if (e != cudaSuccess) return e;
     int sms = 0;
     if ((e = sm_count(sms)) != cudaSuccess) return e;
     uint32_t ctas = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
     a.pieces = ctas / a.HB > 0 ? ctas / a.HB : 1;
     ctas = a.pieces * a.HB;
-    e = launch_early(&mla_decode_kernel<FP8, WHOLE, WITHHOLD>, dim3(ctas), threads_of<FP8, WHOLE>(), smem, stream,
+    e = launch_early(&mla_decode_kernel<FP8, WHOLE, HOOK>, dim3(ctas), threads_of<FP8, WHOLE>(), smem, stream,
                      a, maps, qm);
     if (e != cudaSuccess) return e;
     // few tokens: many pieces each
@@ -1182,7 +1183,7 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
               const void* q_rope, int64_t q_rope_row_stride, const uint32_t* input_row_offsets,
               uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_heads,
               const kvw_paged_cache_t* cache, uint32_t layer_idx, float sm_scale, void* workspace,
-              uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream, bool withhold,
+              uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream, Hook hook,
               uint64_t wait_ns) {
     const int st = check_cache(cache, layer_idx, 1);
     if (st != KVW_OK) return st;
@@ -1253,19 +1254,21 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
         e = encode_panel_map(&qm.panels, cache, layer_idx, fp8 ? 2 : 3);
     if (e != KVW_OK) return e;
     cudaError_t r;
-    auto run = [&](auto held) {
-        constexpr bool kHeld = decltype(held)::value;
+    auto run = [&](auto with) {
+        constexpr Hook kHook = decltype(with)::value;
         if (maps.log_rows == 6)
-            return fp8 ? launch<true, true, kHeld>(a, maps, qm, stream)
-                       : launch<false, true, kHeld>(a, maps, qm, stream);
-        return fp8 ? launch<true, false, kHeld>(a, maps, qm, stream)
-                   : launch<false, false, kHeld>(a, maps, qm, stream);
+            return fp8 ? launch<true, true, kHook>(a, maps, qm, stream)
+                       : launch<false, true, kHook>(a, maps, qm, stream);
+        return fp8 ? launch<true, false, kHook>(a, maps, qm, stream)
+                   : launch<false, false, kHook>(a, maps, qm, stream);
     };
 #ifdef KVW_TEST_HOOKS
-    r = withhold ? run(std::true_type{}) : run(std::false_type{});
+    r = hook == Hook::kWithheld    ? run(std::integral_constant<Hook, Hook::kWithheld>{})
+        : hook == Hook::kAbandoned ? run(std::integral_constant<Hook, Hook::kAbandoned>{})
+                                   : run(std::integral_constant<Hook, Hook::kNone>{});
 #else
-    if (withhold) return KVW_EUNSUPPORTED;
-    r = run(std::false_type{});
+    if (hook != Hook::kNone) return KVW_EUNSUPPORTED;
+    r = run(std::integral_constant<Hook, Hook::kNone>{});
 #endif
     return r == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
@@ -1286,8 +1289,8 @@ extern "C" int kva_mla_decode_paged(void* out, float* lse, const void* q_latent,
                                     uint32_t* err_flags, cudaStream_t stream) {
     return kvw::mla_entry(out, lse, q_latent, q_latent_row_stride, q_rope, q_rope_row_stride,
                           input_row_offsets, num_batches, tot_seq_len, num_heads, cache, layer_idx,
-                          sm_scale, workspace, workspace_bytes, err_flags, stream, false,
-                          kvw::kWaitLimitNs);
+                          sm_scale, workspace, workspace_bytes, err_flags, stream,
+                          kvw::Hook::kNone, kvw::kWaitLimitNs);
 }
 
 #ifdef KVW_TEST_HOOKS
@@ -1303,6 +1306,22 @@ extern "C" int kva_test_mla_decode_withheld(
     uint64_t wait_ns) {
     return kvw::mla_entry(out, nullptr, q_latent, q_latent_row_stride, q_rope, q_rope_row_stride,
                           input_row_offsets, num_batches, tot_seq_len, num_heads, cache, layer_idx,
-                          0.1f, workspace, workspace_bytes, err_flags, stream, true, wait_ns);
+                          0.1f, workspace, workspace_bytes, err_flags, stream, kvw::Hook::kWithheld,
+                          wait_ns);
+}
+
+// The softmax warps leave at once, so nobody waits for the last copies;
+// err_flags[1] counts places whose last copy had not landed when their feeding
+// warp left.
+extern "C" int kva_test_mla_decode_abandoned(
+    void* out, const void* q_latent, int64_t q_latent_row_stride, const void* q_rope,
+    int64_t q_rope_row_stride, const uint32_t* input_row_offsets, uint32_t num_batches,
+    uint32_t tot_seq_len, uint32_t num_heads, const kvw_paged_cache_t* cache, uint32_t layer_idx,
+    void* workspace, uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream,
+    uint64_t wait_ns) {
+    return kvw::mla_entry(out, nullptr, q_latent, q_latent_row_stride, q_rope, q_rope_row_stride,
+                          input_row_offsets, num_batches, tot_seq_len, num_heads, cache, layer_idx,
+                          0.1f, workspace, workspace_bytes, err_flags, stream,
+                          kvw::Hook::kAbandoned, wait_ns);
 }
 #endif
