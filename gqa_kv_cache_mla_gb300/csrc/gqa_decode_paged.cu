@@ -54,7 +54,6 @@ constexpr int kConsumerRegs = 200, kFeederRegs = 56;
 static_assert(kConsumerRegs + kFeederRegs <= 2 * 128, "registers of the launch");
 constexpr int kSlice = kTile / kWarps;      // positions of a tile that a warp takes
 constexpr int kRows = 16;                   // rows of a row block
-constexpr float kSlack = 6.0f;              // log2 of the largest weight before a rescale
 static_assert(kSlice == 16, "one m16n8k16 operand");
 
 struct GqaArgs {
@@ -599,12 +598,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 top0 *= qs0;
                 top1 *= qs1;
             }
-            // The weights' reference m follows the maximum only when that has
-            // risen by more than 2^kSlack: any m will do that keeps the
-            // weights in range, and the accumulators are rescaled seldom.
-            const bool grows = top0 > m0 + kSlack || (HIGH && top1 > m1 + kSlack);
+            constexpr float kLift = weight_lift<FP8>();
+            const bool grows =
+                top0 > m0 + (kSlack + kLift) || (HIGH && top1 > m1 + (kSlack + kLift));
             if (__any_sync(0xffffffffu, grows)) {
-                const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+                const float n0 = fmaxf(m0, top0 - kLift), n1 = fmaxf(m1, top1 - kLift);
                 const float f0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0);
                 const float f1 = n1 == m1 ? 1.0f : fast_exp2(m1 - n1);
                 m0 = n0;

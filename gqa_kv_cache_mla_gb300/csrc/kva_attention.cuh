@@ -8,6 +8,20 @@ namespace kvw {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Weights are 2^(s - m) with a reference m that follows the row's maximum only
+// when a weight would pass 2^(kSlack + lift): any m will do that keeps the
+// weights in range, and the sums are rescaled seldom.  fp16 weights (an E4M3
+// cache) lie a further 2^9 higher, the largest between 2^9 and 2^15: fp16 has
+// nothing below 2^-25, and at 2^0 that dropped whatever was 2^-25 of the
+// largest, while the sum of the weights, in fp32, counted it (one position 18
+// above 8191 others: 29 % of what they hold).  Up there each weight is off by
+// 2^-11 of itself or 2^-34 of the largest.
+constexpr float kSlack = 6.0f;
+template <bool F16>
+constexpr float weight_lift() {
+    return F16 ? 9.0f : 0.0f;
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -7,7 +7,8 @@
 // 2^(S - m); and, turned around so that the 512 output columns fill the matrix
 // unit's lanes, O^T += V^T P^T (512 x 64, 64 positions deep), V being the
 // first 512 columns of the same tile in shared memory.  m follows the maximum
-// only when that has risen by more than 2^6, so O^T is rescaled seldom.
+// only when that has risen by more than 2^6, so O^T is rescaled seldom, and
+// stays 2^9 below it for the fp16 weights of an E4M3 cache (kva_attention.cuh).
 //
 // Bound: 64 heads do 121 flops per byte of a bf16 row (242 with both blocks
 // of 128 heads, whose two CTAs read the same piece at the same time and meet
@@ -64,7 +65,6 @@ constexpr uint32_t kCodePanels = 5;           // of an E4M3 tile: 64 rotated col
 constexpr uint32_t kCodeGroups = 2;           // panels 0 - 2 and 3, 4
 constexpr uint32_t kMaxCtas = 192;
 constexpr uint32_t kTmemColumns = 512, kScoreColumn = 256;
-constexpr float kSlack = 6.0f;                // log2 of the largest weight before a rescale
 constexpr int kSoftmaxThreads = 128;
 
 struct MlaArgs {
@@ -800,8 +800,10 @@ __device__ __forceinline__ void soften(const MlaArgs& a, Smem<FP8, WHOLE>& sm) {
             }
             top0 *= qs0;
             top1 *= qs1;
-            if (any_softmax(!ok || top0 > m0 + kSlack || top1 > m1 + kSlack)) {
-                const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+            constexpr float kLift = weight_lift<FP8>();
+            if (any_softmax(!ok || top0 > m0 + (kSlack + kLift) ||
+                            top1 > m1 + (kSlack + kLift))) {
+                const float n0 = fmaxf(m0, top0 - kLift), n1 = fmaxf(m1, top1 - kLift);
                 const float f0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0);
                 const float f1 = n1 == m1 ? 1.0f : fast_exp2(m1 - n1);
                 m0 = n0;

@@ -120,7 +120,8 @@ int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const void* qkv,
  * cache and fp16 operands with an E4M3 cache (codes are exact in fp16; each
  * query row is brought into fp16's range by a power of two, which loses only
  * what is below 2^-39 of the row's largest value), and the weights e^s are
- * rounded to that type, relative to the row's running maximum.
+ * rounded to that type: by 2^-8 (bf16) or 2^-11 (fp16) of each at most, or, for
+ * fp16 ones below 2^-23 of the row's largest, by 2^-34 of that.
  *
  *   out            device, bf16 [tot_seq_len, num_q_heads, head_size]
  *   lse            device, f32 [tot_seq_len, num_q_heads], or NULL
