@@ -308,19 +308,29 @@ struct PagePlan {
     uint64_t there;
 };
 
-__device__ __forceinline__ PagePlan plan_page(const uint32_t* page_table, uint32_t max_pages,
-                                              uint32_t num_pages, const FastDiv& ps, uint32_t b,
-                                              uint32_t p_tile, int64_t start, int64_t hi) {
+__host__ __device__ __forceinline__ PagePlan plan_page(const uint32_t* page_table,
+                                                       uint32_t max_pages, uint32_t num_pages,
+                                                       const FastDiv& ps, uint32_t b,
+                                                       uint32_t p_tile, int64_t start,
+                                                       int64_t hi) {
     PagePlan t;
     const uint32_t idx = fast_div(p_tile, ps);
-    t.page = idx < max_pages ? __ldg(page_table + (uint64_t)b * max_pages + idx)
-                             : KVW_PAGE_UNMAPPED;
+    t.page = KVW_PAGE_UNMAPPED;
+    if (idx < max_pages) {
+        const uint32_t* id = page_table + (uint64_t)b * max_pages + idx;
+#ifdef __CUDA_ARCH__
+        t.page = __ldg(id);
+#else
+        t.page = *id;
+#endif
+    }
     t.row = p_tile - idx * ps.d;
     t.valid = t.page < num_pages;
     const int64_t before = start - p_tile, left = hi - p_tile;
     t.there = t.valid ? ~0ull : 0ull;
     if (left < 64) t.there &= (1ull << (uint32_t)left) - 1;
-    if (before > 0) t.there &= ~0ull << (uint32_t)before;
+    // a window past the page table's end begins behind the tile
+    if (before > 0) t.there = before < 64 ? t.there & (~0ull << (uint32_t)before) : 0ull;
     return t;
 }
 
