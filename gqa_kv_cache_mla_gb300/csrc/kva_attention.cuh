@@ -47,18 +47,23 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Power of two that brings a row whose largest |value| has the bf16 pattern
-// `top` to [2^14, 2^15), and its inverse; 1 for a row of zeros or one that
-// holds an infinity or a NaN.  fp16 then holds the row's bf16 values exactly
-// down to 2^-31 of the largest.
+// `top` to [2^14, 2^15), and its inverse, as exponents of fp32; both 127 (1.0)
+// for a row of zeros or one that holds an infinity or a NaN.  fp16 then holds
+// the row's bf16 values exactly down to 2^-31 of the largest.  Rows below
+// 2^-112 stop at 2^126, whose inverse is the smallest normal number: they stay
+// below 2^14, every bf16 value of theirs exact all the same.
+__host__ __device__ __forceinline__ void row_exponents(uint32_t top, uint32_t& up,
+                                                       uint32_t& down) {
+    const uint32_t e = top >> 7;
+    up = top == 0 || e == 255 ? 127u : e < 15 ? 253u : 268u - e;
+    down = 254u - up;
+}
+
 __device__ __forceinline__ void row_power(uint32_t top, float& up, float& down) {
-    const int e = (int)(top >> 7);
-    if (top == 0 || e == 255) {
-        up = down = 1.0f;
-        return;
-    }
-    const int ue = 268 - e > 254 ? 254 : 268 - e, de = e - 14 < 1 ? 1 : e - 14;
-    up = __uint_as_float((uint32_t)ue << 23);
-    down = __uint_as_float((uint32_t)de << 23);
+    uint32_t u, d;
+    row_exponents(top, u, d);
+    up = __uint_as_float(u << 23);
+    down = __uint_as_float(d << 23);
 }
 
 // One thread of a converged warp, known to the compiler as one: what it

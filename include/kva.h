@@ -158,8 +158,8 @@ int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads, uint32
  *   lse[t, h] = log(sum_j e^s_j)
  * over positions 0 .. p.  Precision as kva_gqa_decode_paged, except that the
  * scores of an E4M3 cache come from its codes and each query row as two E4M3
- * parts (the row's values to within 2^-21 of its largest); a row that holds
- * an infinity or a NaN gives NaN.
+ * parts (the row's values to within 2^-21 of its largest, or 2^-133); a row
+ * that holds an infinity or a NaN gives NaN.
  *
  *   out            device, bf16 [tot_seq_len, num_heads, 512]
  *   lse            device, f32 [tot_seq_len, num_heads], or NULL

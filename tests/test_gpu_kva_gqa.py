@@ -298,3 +298,10 @@ def test_extreme_caps(kva, dtype, softcap):
     q = c.normal(2, 4, 64)
     q[:, 0] = 0  # scores of 0
     run(kva, c, 4, q=q, softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("low", [-110, -113, -116, -119])
+def test_tiny_queries_and_a_large_scale(kva, dtype, low):
+    c = R.Paged(55, *lengths(3, 70, 130), kv_heads=1, head=64, dtype=dtype).fill()
+    run(kva, c, 4, q=c.normal(3, 4, 64, std=2.0 ** low), sm_scale=2.0 ** (-2 - low))

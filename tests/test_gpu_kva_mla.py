@@ -239,3 +239,11 @@ def test_last_tile_raises_the_maximum(kva, dtype, heads, page):
     q = c.normal(n, heads, 512, std=0.5), c.normal(n, heads, 64, std=0.5)
     q[0][:, :, 0] = torch.linspace(-1.0, 6.0, heads)
     run(kva, c, heads, q=q, sm_scale=0.2)
+
+
+@pytest.mark.parametrize("dtype", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("low", [-110, -113, -116, -119])
+def test_tiny_queries_and_a_large_scale(kva, dtype, low):
+    c = batch(78, *lengths(3, 70, 130), dtype=dtype)
+    q = c.normal(3, 16, 512, std=2.0 ** low), c.normal(3, 16, 64, std=2.0 ** low)
+    run(kva, c, 16, q=q, sm_scale=2.0 ** (-4 - low))
