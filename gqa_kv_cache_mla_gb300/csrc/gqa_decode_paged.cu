@@ -55,6 +55,11 @@ static_assert(kConsumerRegs + kFeederRegs <= 2 * 128, "registers of the launch")
 constexpr int kSlice = kTile / kWarps;      // positions of a tile that a warp takes
 constexpr int kRows = 16;                   // rows of a row block
 static_assert(kSlice == 16, "one m16n8k16 operand");
+// tanh y for u = 2 log2(e) y: the series' coefficients in u^2, and u at y = 1/4
+constexpr float kHalfLn2 = 0.5f * kLn2, kTanh3 = kHalfLn2 * kHalfLn2 / 3.0f;
+constexpr float kTanh5 = 2.0f / 15.0f * kHalfLn2 * kHalfLn2 * kHalfLn2 * kHalfLn2;
+constexpr float kTanh7 = 17.0f / 42.0f * kTanh5 * kHalfLn2 * kHalfLn2, kTanhNear = 0.5f * kLog2e;
+constexpr float kMostCap = 0x1p64f;  // a cap above it is none
 
 struct GqaArgs {
     SplitArgs split;
@@ -67,7 +72,7 @@ struct GqaArgs {
     uint32_t* err_flags;
     unsigned char* workspace;
     float sm_scale, k_scale, v_scale;
-    float softcap, cap_factor;  // in units of log2; 2 log2(e) / the cap
+    float softcap, cap_factor, cap_half;  // in units of log2; 2 log2(e) / the cap; half the cap
     uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
     uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
     uint32_t num_pages, max_pages, pieces;
@@ -542,15 +547,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                 [[maybe_unused]] const int64_t p0 = p_first + (int64_t)(k + i) * kTile;
                 if constexpr (MODS) {  // into units of log2
                     if (a.softcap > 0.0f) {
-                        // tanh y = 1 - 2 / (e^2y + 1): absolute error of a few
-                        // 2^-24, so the capped score is off by that times the cap
+                        // With u = 2 log2(e) y: tanh y = 1 - 2 / (2^u + 1), off by
+                        // 1.6 * 2^-22 of the cap, which is 2^-19 of the capped
+                        // score from y = 1/4 on; below, where a cap far above
+                        // the scores would lose them in that, the odd series
+                        // y - y^3/3 + 2 y^5/15 - 17 y^7/315, off by 2^-21 of
+                        // itself there (256 requests, E4M3: 353 -> 363 us; bf16
+                        // with cap and window the same).
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
 #pragma unroll
                             for (int e = 0; e < kEach; ++e) {
-                                const float z = fast_exp2(s[2 * i + n][e] * (e < 2 ? qs0 : qs1));
-                                s[2 * i + n][e] =
-                                    a.softcap - __fdividef(2.0f * a.softcap, z + 1.0f);
+                                const float u = s[2 * i + n][e] * (e < 2 ? qs0 : qs1), w = u * u;
+                                const float near =
+                                    a.cap_half * u *
+                                    fmaf(w, fmaf(w, fmaf(w, -kTanh7, kTanh5), -kTanh3), 1.0f);
+                                const float far =
+                                    a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
+                                s[2 * i + n][e] = fabsf(u) < kTanhNear ? near : far;
                             }
                     }
                     if (a.slopes) {
@@ -1034,6 +1048,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return KVW_EINVAL;
     if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return KVW_EINVAL;
     if (tot_seq_len == 0) return KVW_OK;
+    if (softcap > kMostCap) softcap = 0.0f;
 
     GqaArgs a = {};
     a.split.offsets = input_row_offsets;
@@ -1066,6 +1081,7 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     a.sm_scale = sm_scale;
     a.softcap = softcap * kLog2e;
     a.cap_factor = softcap > 0.0f ? 2.0f * kLog2e / softcap : 0.0f;
+    a.cap_half = 0.5f * softcap;
     a.k_scale = fp8 ? cache->scale : 1.0f;
     a.v_scale = fp8 ? v_scale : 1.0f;
     a.Hq = num_q_heads;

@@ -129,8 +129,8 @@ int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const void* qkv,
  *                  (>= num_q_heads*head_size, multiple of 8)
  *   cache          host pointer: bf16 or E4M3 (scale > 0, v_scale > 0),
  *                  head_size a multiple of 16 and <= 256
- *   sm_scale       finite, > 0;  softcap finite, >= 0 (0: none); a capped
- *                  score is off by a few 2^-24 of the cap
+ *   sm_scale       finite, > 0;  softcap finite, >= 0 (0: none, and so is one
+ *                  above 2^64); a capped score is off by 2^-19 of itself
  *   window         0: none; else the number of positions seen, own included
  *   alibi_slopes   device, f32 [num_q_heads], or NULL
  *   workspace      device, kva_gqa_decode_workspace(...) bytes
