@@ -65,13 +65,6 @@ struct AppendArgs {
     FastDiv ps, chunk_div;
 };
 
-// Four positions' worth of work of one warp: which token, where it goes.
-struct TokenSlot {
-    uint64_t pos;
-    int64_t slot;      // element offset of the token's row in a plane, -1: no valid page
-    bool position_ok;
-};
-
 template <int TL, bool INTERLEAVED, bool FP8, bool MROPE>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a) {
     extern __shared__ uint32_t s_tables[];
