@@ -62,3 +62,16 @@ def test_power_of_a_query_row(tmp_path):
                    capture_output=True, text=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "0 mismatches" in r.stdout, r.stdout
+
+
+def test_split_with_costly_segments(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("no nvcc")
+    exe = str(tmp_path / "kva_split_costs")
+    subprocess.run([nvcc, "-O2", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I",
+                    os.path.join(ROOT, "gqa_kv_cache_mla_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "c", "kva_split_costs.cu"), "-o", exe], check=True,
+                   capture_output=True, text=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "0 mismatches" in r.stdout, r.stdout
