@@ -38,7 +38,8 @@
  *   2^32 - 256.  A position past that has no valid page.
  * - A position whose slot has no valid page takes no part in the softmax,
  *   as if masked, and sets KVW_ERR_PAGE.  A token left with no position at
- *   all gets a row of zeros and lse = -infinity.
+ *   all, or whose every score is -infinity, gets a row of zeros and lse =
+ *   -infinity.
  * - Malformed offsets set KVW_ERR_OFFSETS; out and lse are left as they were.
  * - The cache is read by the copy engine, whose stages complete through
  *   bounded waits: KVW_ERR_TIMEOUT as in kvw.h, out and lse are then partly
@@ -48,7 +49,8 @@
  * - The attention calls only read the cache: page tables may share pages.
  * - Cache rows behind a token's last position are never used, whatever they
  *   hold (NaN included).  A NaN or an infinity in a used row or in a query
- *   propagates as the formula has it.
+ *   propagates as the formula has it.  The sums of weights times values are
+ *   fp32 before their division: bf16 values above 2^100 may overflow them.
  * - out and lse must not overlap any input.
  */
 #ifndef KVA_H
@@ -160,6 +162,10 @@ int kva_gqa_decode_workspace(uint32_t num_q_heads, uint32_t num_kv_heads, uint32
  * scores of an E4M3 cache come from its codes and each query row as two E4M3
  * parts (the row's values to within 2^-21 of its largest, or 2^-133); a row
  * that holds an infinity or a NaN gives NaN.
+ * An E4M3 cache halves the memory, not the time: the values are converted to
+ * fp16 on the way, and a decode step takes about a tenth longer than over a
+ * bf16 cache (256 contexts of up to 8192 positions: 128 heads 455 and 407 us,
+ * 16 heads 219 and 204).
  *
  *   out            device, bf16 [tot_seq_len, num_heads, 512]
  *   lse            device, f32 [tot_seq_len, num_heads], or NULL
