@@ -1035,7 +1035,8 @@ int gqa_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     uint64_t need = 0;
     const int ws = workspace_bytes_for(num_q_heads, Hk, D, &need);
     if (ws != KVW_OK) return ws;
-    if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20)) return KVW_EUNSUPPORTED;
+    if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20) || !tma_sizes_ok(cache))
+        return KVW_EUNSUPPORTED;
     if (!value_scale_ok(cache, v_scale)) return KVW_EINVAL;
     if (!out || !q || !input_row_offsets || num_batches == 0 || !workspace ||
         workspace_bytes < need)

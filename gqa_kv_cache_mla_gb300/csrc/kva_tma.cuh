@@ -50,6 +50,12 @@ inline bool tma_strides_ok(const kvw_paged_cache_t* c, int planes) {
            ok(c->stride_page, c->num_pages) && ok(c->stride_kv, (uint64_t)planes);
 }
 
+// A copy's coordinates (page, row of a page) are signed 32-bit: from 2^31 on it
+// would read zeros.
+inline bool tma_sizes_ok(const kvw_paged_cache_t* c) {
+    return c->num_pages <= (1u << 31) && c->page_size <= (1u << 31);
+}
+
 // Maps of one layer's planes, map[i] for copies of R << 2i rows; 128 bytes of
 // columns per copy, so that a copy of any number of rows starts on a 128-byte
 // line of shared memory, as it must.

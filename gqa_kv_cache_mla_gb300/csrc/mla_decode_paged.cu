@@ -1193,7 +1193,8 @@ int mla_entry(void* out, float* lse, const void* q_latent, int64_t q_latent_row_
     const int ws = workspace_bytes_for(num_heads, &need);
     if (ws != KVW_OK) return ws;
     if (cache->num_heads != 1 || cache->head_size != kRow) return KVW_EUNSUPPORTED;
-    if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20)) return KVW_EUNSUPPORTED;
+    if (num_batches > KVW_MAX_BATCHES || tot_seq_len > (1u << 20) || !tma_sizes_ok(cache))
+        return KVW_EUNSUPPORTED;
     if (!out || !q_latent || !q_rope || !input_row_offsets || num_batches == 0 || !workspace ||
         workspace_bytes < need)
         return KVW_EINVAL;

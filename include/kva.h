@@ -45,7 +45,8 @@
  *   bounded waits: KVW_ERR_TIMEOUT as in kvw.h, out and lse are then partly
  *   written.  It takes strides that are positive, multiples of 16 bytes and
  *   below 2^40 bytes in every dimension of more than one index (pages,
- *   planes, tokens, heads; the layer stride is free): KVW_EINVAL for others.
+ *   planes, tokens, heads; the layer stride is free): KVW_EINVAL for others,
+ *   and at most 2^31 pages and rows of a page: KVW_EUNSUPPORTED beyond.
  * - The attention calls only read the cache: page tables may share pages.
  * - Cache rows behind a token's last position are never used, whatever they
  *   hold (NaN included).  A NaN or an infinity in a used row or in a query

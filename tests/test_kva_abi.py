@@ -262,3 +262,13 @@ def test_query_strides():
     assert mla(mla_cache(), qls=top - 8, qrs=top - 8) == kvw.KVW_OK
     assert mla(mla_cache(), qls=top - 8, qrs=top) == kvw.KVW_EINVAL
     assert gqa(cache(), qs=1 << 45) == kvw.KVW_OK
+
+
+# the copies' coordinates are signed 32-bit
+@pytest.mark.parametrize("name", ["num_pages", "page_size"])
+def test_most_pages_and_rows(name):
+    for count, want in ((1 << 31, kvw.KVW_OK), ((1 << 31) + 1, kvw.KVW_EUNSUPPORTED),
+                        (2 ** 32 - 1, kvw.KVW_EUNSUPPORTED)):
+        assert gqa(cache(**{name: count})) == want
+        assert mla(mla_cache(**{name: count})) == want
+        assert append(cache(**{name: count}), q_out=FAKE + 16) == kvw.KVW_OK
