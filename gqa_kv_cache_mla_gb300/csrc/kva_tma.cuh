@@ -8,9 +8,9 @@
 // with columns past the head size filled with zeros.  A copy must not cross a
 // page.  With R the largest power of two up to 64 that divides the page size,
 // pages cut a tile of 64 positions at multiples of R only, so a tile is made
-// of runs of R-row units; a run is copied greedily in pieces of 16, 4 and 1
-// units, one map for each piece size (one map in all for page sizes whose R
-// is 32 or 64, and for those of 16 up to 48).
+// of runs of R-row units; a run is copied greedily in pieces of 64, 16, 4 and 1
+// units as far as these fit a tile and a page, one map for each piece size (one
+// map in all for page sizes whose R is 32 or 64, and for those of 16 up to 48).
 #pragma once
 
 #include <cuda.h>

@@ -254,9 +254,9 @@ __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, co
             stopped_at = kFrom;
             if (i + 1 < w.last) {
                 // The next tile's place is taken for a while yet: into L2 with
-                // it (256 requests, 128 heads, bf16: 472 -> 453 us when it was
-                // added; a tile of codes, half as large, gains nothing; two
-                // tiles ahead is no better than one).
+                // it (256 requests, 128 heads, when it was added: bf16 472 ->
+                // 453 us; a tile of codes by whole panels 470 -> 465, panel by
+                // panel no gain; two tiles ahead is no better than one).
                 plan(i + 1);
                 if ((i & 1u) == hb || a.HB == 1) {
                     if constexpr (WHOLE) {
