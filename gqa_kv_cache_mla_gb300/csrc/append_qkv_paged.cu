@@ -31,7 +31,7 @@
 // 142, 190 us.  One pass ahead instead of two: 134, 140 and 136 us; the next
 // item's first rows loaded before an item ends: 143, 154, 146 us (spills).  One
 // token: 2.3 us on the device.  With few rows a token (4 + 2 x 1 heads of 96)
-// the lookups of a token are most of its work: 47 k tokens 60 us, a quarter of
+// the lookups of a token are most of its work: 46 k tokens 58 us, a quarter of
 // the copy rate.
 #include <cstdint>
 

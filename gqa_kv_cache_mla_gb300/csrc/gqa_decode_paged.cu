@@ -19,10 +19,11 @@
 // per CTA keep up to 190 KB in flight per SM.
 //
 // Measured, 32 query and 8 key-value heads of 128: 8 requests of up to 131072
-// positions, bf16 301 us (6.7 TB/s, 99 % of the card's copy rate); 256 of up to
-// 8192, E4M3 329 us (6.6 TB/s, 97 %), pages of 16 449 us; 32 of up to 4096,
-// bf16 53 us (5.2 TB/s, some 12 us of it before the first and after the last
-// byte); one token over 901 positions 10.4 us.
+// positions, bf16 302 us (6.7 TB/s, 99 % of the card's copy rate); 256 of up to
+// 8192, E4M3 331 us (6.5 TB/s, 96 %), with a cap 365, with a distance bias 372,
+// pages of 16 454, of 100 457, heads of 64 222 (72 %), of 96 328 (73 %); 32 of
+// up to 4096, bf16 53 us (5.2 TB/s, some 12 us of it before the first and after
+// the last byte); one token over 901 positions 9.9 us.
 //
 // CTAs of neighbouring key-value heads walk the same piece side by side
 // (`lanes`): a token's heads lie next to each other, so what one CTA reads
@@ -204,7 +205,7 @@ __device__ __forceinline__ void feed(const GqaArgs& a, const CacheMaps& maps,
             // A tile lies in one page: one copy of each half, and all that it
             // takes is the same in every lane.  (The general way below takes
             // longer to feed than E4M3 tiles take to consume: 256 requests, 363
-            // us against 329, heads of 64 330 against 232.)
+            // us against 329 when it was added, heads of 64 330 against 232.)
             auto plan = [&](uint32_t i) {
                 return plan_page(a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
                                  (w.span.tile0 + i) * kTile, w.span.start, w.span.hi);

@@ -34,9 +34,9 @@
 // a late softmax holds up the other.
 //
 // Measured, contexts of up to 8192 positions: 256 requests, 128 heads, bf16
-// 411 us (716 TF/s, 38 % of the card's matrix rate), E4M3 453 us; 64 heads,
-// bf16 225 us (5.5 TB/s, 82 % of its copy rate); one token, 16 heads, 1501
-// positions 14.6 us.  A tile of 64 positions takes some 3700 cycles, of which
+// 408 us (720 TF/s, 39 % of the card's matrix rate), E4M3 456 us; 64 heads,
+// bf16 225 us (5.6 TB/s, 82 % of its copy rate), E4M3 250; 16 heads 204 and 220;
+// one token, 16 heads, 1501 positions 14.7 us.  A tile of 64 positions takes some 3700 cycles, of which
 // the products fill 1900: with 64 rows a 16-deep step of S reads 2 KB of Q and
 // 2 KB of K from shared memory at 128 bytes a cycle, and a step of O^T 4 KB
 // and 2 KB.  The rest is the round of a tile's place (copy 1600 cycles, S 1400,
@@ -154,7 +154,7 @@ __device__ __forceinline__ float* slot_of(const MlaArgs& a, uint32_t cta, uint32
 // ---------------------------------------------------------------- feeding
 
 // Of pages of whole tiles a group is one copy of three panels; three copies of
-// one panel each took 433 us instead of 411.
+// one panel each took 433 us instead of 411 when it was changed.
 template <bool FP8, bool WHOLE, Hook HOOK, uint32_t WHICH>
 __device__ __forceinline__ void feed(const MlaArgs& a, const CacheMaps& maps, const QMaps& qm,
                                      Smem<FP8, WHOLE>& sm) {
