@@ -36,9 +36,12 @@
 #include <cstdint>
 
 #include "kva_common.cuh"
+#include "kva_int4.cuh"
 
 namespace kvw {
 namespace {
+
+enum class Held { kBf16, kE4m3, kInt4 };
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -57,7 +60,10 @@ struct AppendArgs {
     uint32_t* err_flags;
     unsigned char* k_base;  // K plane of the layer
     unsigned char* v_base;
-    int64_t s_page, s_token, s_head;  // elements
+    int64_t s_page, s_token, s_head;  // elements (of 4 bits: bytes)
+    uint16_t* k_scales;               // of a cache in 4 bits, as are the strides
+    uint16_t* v_scales;
+    int64_t sc_page, sc_head;
     float eps, weight_offset, k_scale, v_scale, inv_d;
     uint32_t B, T, Hq, Hk, D, rope, freqs_rows, num_pages, max_pages;
     uint32_t rows, passes, chunks, items;  // head rows per token; passes per item; items per token
@@ -65,7 +71,15 @@ struct AppendArgs {
     FastDiv ps, chunk_div;
 };
 
-template <int TL, bool INTERLEAVED, bool FP8, bool MROPE>
+// The fp32 pattern of the largest |value| of eight (a NaN's above all).
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+}
+
+template <int TL, bool INTERLEAVED, Held HELD, bool MROPE>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a) {
     extern __shared__ uint32_t s_tables[];
     uint32_t* s_off = s_tables;
@@ -124,6 +138,16 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a)
         const int64_t slot = stores_kv ? slot_row(a.page_table, a.max_pages, a.num_pages, a.ps,
                                                   a.s_page, a.s_token, 0, b, pos)
                                        : -1;
+        [[maybe_unused]] int64_t scale_slot = 0;
+        if constexpr (HELD == Held::kInt4) {
+            // the page and the row once more, from what slot_row has looked up
+            if (slot >= 0) {
+                const uint32_t idx = fast_div((uint32_t)pos, a.ps);
+                scale_slot = (int64_t)__ldg(a.page_table + (uint64_t)b * a.max_pages + idx) *
+                                 a.sc_page +
+                             ((uint32_t)pos - idx * a.ps.d);
+            }
+        }
         float cs[16];
         bool position_ok = true;
         if (a.rope) {
@@ -219,12 +243,45 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a)
                         }
                     }
                 }
+                [[maybe_unused]] uint32_t tops[TL < 8 ? 2 : 4];  // of the row's groups
+                if constexpr (HELD == Held::kInt4) {
+                    // uniform: some row of the pass is a key or a value
+                    if ((chunk * a.passes + pass + 1) * kTeams > a.Hq) {
+                        const uint32_t t0 = top_of(x0), t1 = top_of(x1);
+#pragma unroll
+                        for (uint32_t g = 0; g < sizeof(tops) / 4; ++g) {
+                            if (g * kGroup >= a.D) break;
+                            uint32_t m = max(e0 / kGroup == g ? t0 : 0u, e1 / kGroup == g ? t1 : 0u);
+#pragma unroll
+                            for (int o = TL / 2; o > 0; o >>= 1)
+                                m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            tops[g] = m;
+                        }
+                    }
+                }
                 if (!active || row >= a.rows) continue;
                 if (is_q) {
                     uint16_t* p = a.q_out + (int64_t)t * a.q_out_stride + (int64_t)row * a.D;
                     st_stream(reinterpret_cast<uint4*>(p + e0), pack8_bf16(x0));
                     st_stream(reinterpret_cast<uint4*>(p + e1), pack8_bf16(x1));
+                } else if (slot >= 0 && HELD == Held::kInt4) {
+                    const uint32_t h = row - a.Hq - (is_v ? a.Hk : 0u);
+                    uint16_t sc0 = 0, sc1 = 0;
+#pragma unroll
+                    for (uint32_t g = 0; g < sizeof(tops) / 4; ++g) {
+                        if (g * kGroup >= a.D) break;
+                        const uint16_t sc = group_scale(tops[g]);
+                        if (e0 / kGroup == g) sc0 = sc;
+                        if (e1 / kGroup == g) sc1 = sc;
+                        if (j == g)
+                            (is_v ? a.v_scales : a.k_scales)[scale_slot + (int64_t)h * a.sc_head +
+                                                             (int64_t)g * a.ps.d] = sc;
+                    }
+                    unsigned char* p = (is_v ? a.v_base : a.k_base) + slot + (int64_t)h * a.s_head;
+                    *reinterpret_cast<uint32_t*>(p + e0 / 2) = codes_of(x0, sc0);
+                    *reinterpret_cast<uint32_t*>(p + e1 / 2) = codes_of(x1, sc1);
                 } else if (slot >= 0) {
+                    constexpr bool FP8 = HELD == Held::kE4m3;
                     constexpr int esz = FP8 ? 1 : 2;
                     const uint32_t h = row - a.Hq - (is_v ? a.Hk : 0u);
                     unsigned char* p =
@@ -238,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a)
     }
 }
 
-template <int TL, bool IL, bool FP8, bool MROPE>
+template <int TL, bool IL, Held HELD, bool MROPE>
 cudaError_t launch(AppendArgs& a, cudaStream_t stream) {
     const size_t smem = (2ull * a.B + 1) * 4;
     uint64_t wave = 0;
-    cudaError_t e = wave_ctas<&append_kernel<TL, IL, FP8, MROPE>>(kThreads, smem, wave);
+    cudaError_t e = wave_ctas<&append_kernel<TL, IL, HELD, MROPE>>(kThreads, smem, wave);
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
     // Passes per item: as many as leave every resident warp two items (angles
@@ -257,38 +314,41 @@ cudaError_t launch(AppendArgs& a, cudaStream_t stream) {
     a.chunk_div = make_fast_div(a.chunks);
     uint64_t grid = ((uint64_t)a.items + kWarps - 1) / kWarps;
     if (grid > wave) grid = wave;
-    return launch_early(&append_kernel<TL, IL, FP8, MROPE>, dim3((unsigned)grid), kThreads, smem,
+    return launch_early(&append_kernel<TL, IL, HELD, MROPE>, dim3((unsigned)grid), kThreads, smem,
                         stream, a);
 }
 
-template <int TL, bool IL>
-cudaError_t pick(AppendArgs& a, bool fp8, bool mrope, cudaStream_t s) {
-    return fp8 ? (mrope ? launch<TL, IL, true, true>(a, s) : launch<TL, IL, true, false>(a, s))
-               : (mrope ? launch<TL, IL, false, true>(a, s) : launch<TL, IL, false, false>(a, s));
+template <int TL, bool IL, Held HELD>
+cudaError_t pick(AppendArgs& a, bool mrope, cudaStream_t s) {
+    return mrope ? launch<TL, IL, HELD, true>(a, s) : launch<TL, IL, HELD, false>(a, s);
 }
 
-}  // namespace
-}  // namespace kvw
+template <int TL, bool IL>
+cudaError_t pick(AppendArgs& a, Held held, bool mrope, cudaStream_t s) {
+    switch (held) {
+        case Held::kBf16: return pick<TL, IL, Held::kBf16>(a, mrope, s);
+        case Held::kE4m3: return pick<TL, IL, Held::kE4m3>(a, mrope, s);
+        default:
+            if constexpr (TL < 32) return pick<TL, IL, Held::kInt4>(a, mrope, s);
+            return cudaErrorInvalidValue;  // heads of 4 bits have 256 columns at most
+    }
+}
 
-extern "C" int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const void* qkv,
-                                    int64_t qkv_row_stride, const uint32_t* input_row_offsets,
-                                    uint32_t num_batches, uint32_t tot_seq_len,
-                                    uint32_t num_q_heads, const void* q_gamma,
-                                    const void* k_gamma, float epsilon, float weight_offset,
-                                    const void* freqs_cis, uint32_t freqs_rows, uint32_t rope_dim,
-                                    const uint32_t* position_ids, int interleaved,
-                                    const uint32_t* mrope_section, const kvw_paged_cache_t* cache,
-                                    float v_scale, uint32_t layer_idx, uint32_t* err_flags,
-                                    cudaStream_t stream) {
-    using namespace kvw;
-    const int st = check_cache(cache, layer_idx, 2);
-    if (st != KVW_OK) return st;
+// Checks the arguments that all kinds of cache share and launches; `a` holds
+// where the cache's values (and scales) go.
+int append(AppendArgs& a, Held held, bool values_ok, void* q_out, int64_t q_out_row_stride,
+           const void* qkv, int64_t qkv_row_stride, const uint32_t* input_row_offsets,
+           uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_q_heads, const void* q_gamma,
+           const void* k_gamma, float epsilon, float weight_offset, const void* freqs_cis,
+           uint32_t freqs_rows, uint32_t rope_dim, const uint32_t* position_ids, int interleaved,
+           const uint32_t* mrope_section, const kvw_paged_cache_t* cache, uint32_t* err_flags,
+           cudaStream_t stream) {
     const uint32_t D = cache->head_size, Hk = cache->num_heads;
     if (D % 16 || D > 512 || num_batches > KVW_MAX_BATCHES) return KVW_EUNSUPPORTED;
     if ((uint64_t)num_q_heads + 2ull * Hk > 4096) return KVW_EUNSUPPORTED;
     const uint32_t rows = num_q_heads + 2 * Hk;
     if ((uint64_t)tot_seq_len * rows > (1ull << 31)) return KVW_EUNSUPPORTED;
-    if (!value_scale_ok(cache, v_scale)) return KVW_EINVAL;
+    if (!values_ok) return KVW_EINVAL;
     if (!qkv || !input_row_offsets || num_batches == 0 || (num_q_heads && !q_out))
         return KVW_EINVAL;
     if (!aligned16(qkv) || !aligned16(q_out) || !aligned4(input_row_offsets) ||
@@ -310,7 +370,6 @@ extern "C" int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const
     }
     if (tot_seq_len == 0) return KVW_OK;
 
-    AppendArgs a = {};
     a.q_out = static_cast<uint16_t*>(q_out);
     a.qkv = static_cast<const uint16_t*>(qkv);
     a.q_out_stride = q_out_row_stride;
@@ -323,17 +382,8 @@ extern "C" int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const
     a.freqs = static_cast<const float*>(freqs_cis);
     a.position_ids = position_ids;
     a.err_flags = err_flags;
-    const int64_t esz = cache_esz(cache);
-    a.k_base = static_cast<unsigned char*>(cache->data) +
-               (int64_t)layer_idx * cache->stride_layer * esz;
-    a.v_base = a.k_base + cache->stride_kv * esz;
-    a.s_page = cache->stride_page;
-    a.s_token = cache->stride_token;
-    a.s_head = cache->stride_head;
     a.eps = epsilon;
     a.weight_offset = weight_offset;
-    a.k_scale = cache->scale;
-    a.v_scale = v_scale;
     a.inv_d = 1.0f / (float)D;
     a.B = num_batches;
     a.T = tot_seq_len;
@@ -350,18 +400,80 @@ extern "C" int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const
         a.sec01 = mrope_section[0] + mrope_section[1];
     }
     a.ps = make_fast_div(cache->page_size);
-    const bool fp8 = cache->dtype == KVW_DTYPE_FP8_E4M3, mr = mrope_section != nullptr;
+    const bool mr = mrope_section != nullptr;
     const uint32_t n = D / 16;
     cudaError_t e;
     if (interleaved)
-        e = n <= 4    ? pick<4, true>(a, fp8, mr, stream)
-            : n <= 8  ? pick<8, true>(a, fp8, mr, stream)
-            : n <= 16 ? pick<16, true>(a, fp8, mr, stream)
-                      : pick<32, true>(a, fp8, mr, stream);
+        e = n <= 4    ? pick<4, true>(a, held, mr, stream)
+            : n <= 8  ? pick<8, true>(a, held, mr, stream)
+            : n <= 16 ? pick<16, true>(a, held, mr, stream)
+                      : pick<32, true>(a, held, mr, stream);
     else
-        e = n <= 4    ? pick<4, false>(a, fp8, mr, stream)
-            : n <= 8  ? pick<8, false>(a, fp8, mr, stream)
-            : n <= 16 ? pick<16, false>(a, fp8, mr, stream)
-                      : pick<32, false>(a, fp8, mr, stream);
+        e = n <= 4    ? pick<4, false>(a, held, mr, stream)
+            : n <= 8  ? pick<8, false>(a, held, mr, stream)
+            : n <= 16 ? pick<16, false>(a, held, mr, stream)
+                      : pick<32, false>(a, held, mr, stream);
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
+}
+
+}  // namespace
+}  // namespace kvw
+
+extern "C" int kva_append_qkv_paged(void* q_out, int64_t q_out_row_stride, const void* qkv,
+                                    int64_t qkv_row_stride, const uint32_t* input_row_offsets,
+                                    uint32_t num_batches, uint32_t tot_seq_len,
+                                    uint32_t num_q_heads, const void* q_gamma,
+                                    const void* k_gamma, float epsilon, float weight_offset,
+                                    const void* freqs_cis, uint32_t freqs_rows, uint32_t rope_dim,
+                                    const uint32_t* position_ids, int interleaved,
+                                    const uint32_t* mrope_section, const kvw_paged_cache_t* cache,
+                                    float v_scale, uint32_t layer_idx, uint32_t* err_flags,
+                                    cudaStream_t stream) {
+    using namespace kvw;
+    const int st = check_cache(cache, layer_idx, 2);
+    if (st != KVW_OK) return st;
+    AppendArgs a = {};
+    const bool fp8 = cache->dtype == KVW_DTYPE_FP8_E4M3;
+    const int64_t esz = cache_esz(cache);
+    a.k_base = static_cast<unsigned char*>(cache->data) +
+               (int64_t)layer_idx * cache->stride_layer * esz;
+    a.v_base = a.k_base + cache->stride_kv * esz;
+    a.s_page = cache->stride_page;
+    a.s_token = cache->stride_token;
+    a.s_head = cache->stride_head;
+    a.k_scale = cache->scale;
+    a.v_scale = v_scale;
+    return append(a, fp8 ? Held::kE4m3 : Held::kBf16, value_scale_ok(cache, v_scale), q_out, q_out_row_stride, qkv, qkv_row_stride,
+                  input_row_offsets, num_batches, tot_seq_len, num_q_heads, q_gamma, k_gamma,
+                  epsilon, weight_offset, freqs_cis, freqs_rows, rope_dim, position_ids,
+                  interleaved, mrope_section, cache, err_flags, stream);
+}
+
+extern "C" int kva_append_qkv_int4(void* q_out, int64_t q_out_row_stride, const void* qkv,
+                                   int64_t qkv_row_stride, const uint32_t* input_row_offsets,
+                                   uint32_t num_batches, uint32_t tot_seq_len,
+                                   uint32_t num_q_heads, const void* q_gamma,
+                                   const void* k_gamma, float epsilon, float weight_offset,
+                                   const void* freqs_cis, uint32_t freqs_rows, uint32_t rope_dim,
+                                   const uint32_t* position_ids, int interleaved,
+                                   const uint32_t* mrope_section, const kvw_paged_cache_t* cache,
+                                   const kva_group_scales_t* scales, uint32_t layer_idx,
+                                   uint32_t* err_flags, cudaStream_t stream) {
+    using namespace kvw;
+    const int st = check_int4(cache, scales, layer_idx);
+    if (st != KVW_OK) return st;
+    AppendArgs a = {};
+    a.k_base = int4_codes(cache, layer_idx, 0);
+    a.v_base = int4_codes(cache, layer_idx, 1);
+    a.s_page = cache->stride_page / 2;
+    a.s_token = cache->stride_token / 2;
+    a.s_head = cache->stride_head / 2;
+    a.k_scales = int4_scales(cache, scales, layer_idx, 0);
+    a.v_scales = int4_scales(cache, scales, layer_idx, 1);
+    a.sc_page = scales->stride_page;
+    a.sc_head = scales->stride_head;
+    return append(a, Held::kInt4, true, q_out, q_out_row_stride, qkv, qkv_row_stride,
+                  input_row_offsets, num_batches, tot_seq_len, num_q_heads, q_gamma, k_gamma,
+                  epsilon, weight_offset, freqs_cis, freqs_rows, rope_dim, position_ids,
+                  interleaved, mrope_section, cache, err_flags, stream);
 }

@@ -1,0 +1,862 @@
+// Attention of new tokens over a paged GQA key-value cache held in 4 bits.
+//
+// Mathematics: the pass of gqa_decode_paged.cu over K = s_k (u - 8) and V =
+// s_v (u - 8), with a scale s for each position and group of 64 columns:
+//   S_j  = sum_g s_k[j, g] (sum_{d in g} q_d u_jd - 8 sum_{d in g} q_d)
+//   O_d  = sum_j (P_j s_v[j, g]) u_jd - 8 sum_j (P_j s_v[j, g])
+// Both offsets are sums over what the matrix instructions see, so they come
+// from the same instructions with a constant operand: 8 sum q once for a
+// segment, where it is the products' first accumulator, and 8 sum (P s_v) as
+// one product per group and 16 positions.
+//
+// Codes as operands: the pattern of a code u in bits 4 to 7 of an fp16 number
+// is u 2^-20, exact, below fp16's smallest normal number.  Four codes lie in 16
+// bits, so an AND takes a pair of codes out of 32 bits after a shift: 7
+// instructions for 8 codes, against 11 to bring them to exact bf16 numbers, and
+// with an offset of 8 to cancel (the bf16 patterns 128 + u alone: 136).  The
+// instruction lines its products up as if such an operand were 2^-14, so that
+// each of its sums may be off by 2^-18 of a code more than fp32's own step (in
+// bits 0 to 3, with 5 instructions for 8 codes, by 2^-14: a column whose heavy
+// positions all hold code 8 was off by 2 % of the little that is left).
+//
+// S = Q K^T has the row block's rows as the instruction's 16 rows; O^T = V^T
+// P^T has them as its 8 columns, once or twice: S leaves its registers in the
+// order in which O^T takes P, and with up to 8 rows O^T costs half as many
+// instructions and half the registers.
+//
+// Weights times scales are fp16.  Their reference m follows the row's largest
+// P s_v, not its largest score: raised when a product passes 2^15, to where
+// the largest is 2^9 (weight_lift).  The sum of weights is fp32.
+//
+// Division of the work, workspace and join are those of gqa_decode_paged.cu.
+#include <cstdint>
+#include <type_traits>
+
+#include "kva_gqa.cuh"
+#include "kva_int4.cuh"
+#include "kva_tma.cuh"
+
+namespace kvw {
+namespace {
+
+// One layer's codes and scales.  A copy takes both planes of some rows of one
+// head and page: the codes as lines of 128 bytes in the 128-byte swizzle
+// (chunk c of line l lies at c ^ (l & 7)), the scales as they lie, group by
+// group.
+struct Int4Maps {
+    CacheMaps codes;  // one map: copies of R rows, R = 16, 32 or 64
+    CUtensorMap scales;
+};
+
+inline int encode_int4_maps(Int4Maps* m, const kvw_paged_cache_t* c, const kva_group_scales_t* s,
+                            uint32_t layer_idx) {
+    const auto encode = tensor_map_encoder();
+    if (!encode) return KVW_ECUDA;
+    const uint32_t rows = rows_per_copy(c->page_size), line_rows = c->head_size / 2;
+    m->codes.levels = 1;
+    m->codes.log_rows = rows == 64 ? 6 : rows == 32 ? 5 : 4;
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    // a dimension of one index takes any legal stride
+    auto bytes = [](int64_t s, uint64_t n) { return n > 1 ? (cuuint64_t)s : (cuuint64_t)16; };
+    {
+        const cuuint64_t dims[5] = {128, (cuuint64_t)c->page_size * line_rows / 128, c->num_heads,
+                                    c->num_pages, 2};
+        const cuuint64_t strides[4] = {128, bytes(c->stride_head / 2, c->num_heads),
+                                       bytes(c->stride_page / 2, c->num_pages),
+                                       (cuuint64_t)(c->stride_kv / 2)};
+        const cuuint32_t box[5] = {128, rows * line_rows / 128, 1, 1, 2};
+        if (encode(&m->codes.map[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, int4_codes(c, layer_idx, 0),
+                   dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KVW_EINVAL;
+    }
+    {
+        const uint32_t groups = groups_of(c->head_size);
+        const cuuint64_t dims[5] = {c->page_size, groups, c->num_heads, c->num_pages, 2};
+        const cuuint64_t strides[4] = {(cuuint64_t)c->page_size * 2,
+                                       bytes(s->stride_head * 2, c->num_heads),
+                                       bytes(s->stride_page * 2, c->num_pages),
+                                       (cuuint64_t)(s->stride_kv * 2)};
+        const cuuint32_t box[5] = {rows, groups, 1, 1, 2};
+        if (encode(&m->scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                   int4_scales(c, s, layer_idx, 0), dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KVW_EINVAL;
+    }
+    return KVW_OK;
+}
+
+// D: head size; NB: blocks of 8 rows (1 or 2).
+template <int D, int NB>
+struct Shape4 {
+    static constexpr int kChunks = D / 32;          // 16-byte chunks of a row of codes
+    static constexpr int kPairs = (kChunks + 1) / 2;  // ldmatrix of 16 rows
+    static constexpr int kGroups = (D + 63) / 64;
+    // Teams of four consumer warps, each a slice of 16 positions of a tile, and
+    // a feeding warp.  Teams take tiles in turn.
+    static constexpr int kTeams = 1;
+    static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : 2;
+    static constexpr int kWarps = 4 * kTeams;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kCodes = 2 * kTile * D / 2;             // bytes of a tile, both planes
+    static constexpr int kScales = 256 * (kGroups < 2 ? 2 : kGroups);  // and of its scales
+    static constexpr int kRing = (kCtas == 3 ? 54 : 84) * 1024 / (kCodes + kScales);
+    static constexpr int kSlots = kRing > 12 ? 12 : kRing;
+    static constexpr int kPadded = D <= 64 ? 64 : D <= 128 ? 128 : 256;  // of a workspace row
+    static constexpr int kQPitch = D * 2 + 16;  // eight rows on distinct banks
+    static constexpr int kQRows = 8 * NB;
+    // rows that join at a time, four rows' stores on distinct banks
+    static constexpr int kJoinPitch = D + 8;
+    static constexpr int kJoinRows = D <= 64 || kWarps == 4 ? (D == 256 ? 2 : 8) : 4;
+    static_assert(kSlots >= 3, "shared memory");
+};
+
+template <int D, int NB>
+struct Smem4 {
+    using Sh = Shape4<D, NB>;
+    unsigned char codes[Sh::kSlots][Sh::kCodes];    // units of [K rows][V rows]
+    unsigned char scales[Sh::kSlots][Sh::kScales];  // units of [K][V][group][row]
+    unsigned char q_raw[2][Sh::kQRows * Sh::kQPitch];
+    float join[Sh::kWarps][Sh::kJoinRows][Sh::kJoinPitch];
+    uint64_t full[Sh::kSlots], empty[Sh::kSlots], q_full[2], q_empty[2], meet;
+    uint64_t there[Sh::kSlots];  // positions of the tile that are there
+    float m[Sh::kWarps][kRows], l[Sh::kWarps][kRows];
+    SplitShared<Sh::kThreads> split;
+    uint32_t stop;  // a wait ran out
+};
+
+// Bytes of shared memory that the scales of a unit of R rows take: copies land
+// on multiples of 128.
+__host__ __device__ __forceinline__ uint32_t scale_unit(uint32_t groups, uint32_t log_rows) {
+    const uint32_t n = 4 * groups << log_rows;
+    return n < 128 ? 128 : n;
+}
+
+// Where 16-byte chunk `c` of row r of a tile's plane lies among its codes.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t log_rows, uint32_t plane, uint32_t r,
+                                            uint32_t c) {
+    const uint32_t unit = r >> log_rows, in = r & ((1u << log_rows) - 1u);
+    const uint32_t x = ((2 * unit + plane) << log_rows) * (D / 2) + in * (D / 2) + 16 * c;
+    return x ^ ((x >> 3) & 0x70u);
+}
+
+// The feeding warp: walks the piece's tiles ahead of the arithmetic.
+template <int D, int NB, Hook HOOK>
+__device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Smem4<D, NB>& sm) {
+    using Sh = Shape4<D, NB>;
+    const uint32_t lane = threadIdx.x & 31u, log_rows = maps.codes.log_rows;
+    const uint32_t row_bytes = D + 4 * Sh::kGroups, s_unit = scale_unit(Sh::kGroups, log_rows);
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    RingPos<Sh::kSlots> at;
+    RingPos<2> q_at;
+    uint32_t bad_page = 0, issued = 0;
+    bool ok = true;
+    while (ok && !w.done()) {
+        const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
+        const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
+        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        prefetch_page(maps.codes, a.page_table, a.max_pages, a.ps, w.b,
+                      (int64_t)(w.span.tile0 + w.first) * kTile, lane);
+        // ---- the queries: one copy per row
+        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_limit);
+        if (!ok) break;
+        const uint32_t rows = w.span.tokens * in_block;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * D * 2);
+        __syncwarp();
+        if (lane < rows) {
+            const uint32_t ct = w.span.tokens == 1 ? 0 : lane / in_block;
+            bulk_load(sm.q_raw[q_at.slot] + lane * Sh::kQPitch,
+                      a.q + (int64_t)(w.t + ct) * a.q_stride +
+                          (int64_t)(kvh * a.G + hb * kRows + (lane - ct * in_block)) * D,
+                      D * 2, &sm.q_full[q_at.slot]);
+        }
+        q_at.step();
+        // ---- the tiles
+        auto copy = [&](uint32_t unit, uint32_t row, uint32_t page) {
+            const uint32_t bar = smem_addr(&sm.full[at.slot]);
+            tma_rows(smem_addr(sm.codes[at.slot]) + ((unit * D) << log_rows), &maps.codes.map[0], 0,
+                     row * (D / 2) / 128, kvh, page, 0, bar);
+            tma_rows(smem_addr(sm.scales[at.slot]) + unit * s_unit, &maps.scales, row, 0, kvh, page,
+                     0, bar);
+        };
+        if (log_rows == 6) {
+            // a tile lies in one page: two copies, the same in every lane
+            auto plan = [&](uint32_t i) {
+                return plan_page(a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
+                                 (w.span.tile0 + i) * kTile, w.span.start, w.span.hi);
+            };
+            PagePlan next = plan(w.first);
+            for (uint32_t i = w.first; ok && i < w.last; ++i) {
+                const PagePlan t = next;
+                if (i + 1 < w.last) next = plan(i + 1);
+                if (!t.valid) bad_page = 1;
+                ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
+                if (!ok) break;
+                if (elect_one()) {
+                    sm.there[at.slot] = t.there;
+                    mbar_arrive_expect_tx(&sm.full[at.slot], t.valid ? kTile * row_bytes : 0);
+                    if (t.valid && !(HOOK == Hook::kWithheld && issued == 0)) copy(0, t.row, t.page);
+                }
+                __syncwarp();
+                at.step();
+                ++issued;
+            }
+            if (ok) w.next(a.split);
+            continue;
+        }
+        for (uint32_t i = w.first; ok && i < w.last; ++i) {
+            const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
+            TilePlan t;
+            plan_tile(maps.codes, a.page_table, a.max_pages, a.num_pages, a.ps, w.b, p_tile,
+                      w.span.start, w.span.hi, t, bad_page);
+            ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
+            if (!ok) break;
+            if (lane == 0) {
+                sm.there[at.slot] = ((uint64_t)t.t_hi << 32) | t.t_lo;
+                mbar_arrive_expect_tx(&sm.full[at.slot], (t.n << log_rows) * row_bytes);
+            }
+            __syncwarp();
+            if (!(HOOK == Hook::kWithheld && issued == 0) && t.copy[0].level != 4)
+                copy(lane, t.copy[0].row, t.copy[0].page);
+            __syncwarp();
+            at.step();
+            ++issued;
+        }
+        if (ok) w.next(a.split);
+    }
+    if (bad_page) flag(a.err_flags, KVW_ERR_PAGE);
+    if (!ok && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+    // Whether or not this warp had to wait in vain: it leaves when the last copy
+    // into each place has landed, or after a bounded time.
+    const uint32_t n = issued < (uint32_t)Sh::kSlots ? issued : (uint32_t)Sh::kSlots;
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t x = issued - 1 - i;
+        leave_phase<HOOK>(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1u, a.wait_limit,
+                          a.err_flags);
+    }
+    for (uint32_t i = 0; i < 2; ++i)
+        leave_phase<HOOK>(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_limit,
+                          a.err_flags);
+}
+
+// Two neighbouring scales of a word.
+__device__ __forceinline__ float scale_lo(uint32_t w) { return bf16_lo(w); }
+__device__ __forceinline__ float scale_hi(uint32_t w) { return bf16_hi(w); }
+
+template <int D, int NB, bool MODS, Hook HOOK>
+__global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
+    gqa_int4_kernel(const GqaArgs a, const __grid_constant__ Int4Maps maps) {
+    using Sh = Shape4<D, NB>;
+    constexpr int CH = Sh::kChunks, NP = Sh::kPairs, NG = Sh::kGroups, W = Sh::kWarps;
+    constexpr int kEach = 2 * NB;             // scores of a product that are looked at
+    constexpr uint32_t kMask = 0x00f000f0u;   // a pair of codes
+    constexpr uint32_t kEight = 0x00800080u;  // 8, as codes are
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    Smem4<D, NB>& sm = *reinterpret_cast<Smem4<D, NB>*>(dyn);
+
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    // the join of the pieces may be scheduled; it waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == Sh::kThreads - 32) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], W);
+        }
+        mbar_init(&sm.meet, W);
+        sm.stop = 0;
+        mbar_init_fence();
+        prefetch_map(&maps.codes.map[0]);
+        prefetch_map(&maps.scales);
+    }
+    wait_for_stream();
+    const bool ok = find_piece(a.split, a.pieces, blockIdx.x / a.lanes, sm.split);
+    OpenPiece* open = reinterpret_cast<OpenPiece*>(a.workspace) + blockIdx.x;
+    if (tid == 0) open->n = 0;
+    if (!ok) {
+        if (blockIdx.x == 0 && tid == 0) flag(a.err_flags, KVW_ERR_OFFSETS);
+        return;
+    }
+    if (warp == W) {
+        feed4<D, NB, HOOK>(a, maps, sm);
+        return;
+    }
+
+    const uint32_t quad = lane >> 2, in_quad = lane & 3u, slice = warp & 3u, team = warp >> 2;
+    RingPos<Sh::kSlots> at;
+    RingPos<2> q_at;
+    uint32_t meet_parity = 0, turn = 0;  // tiles before the present one, modulo the teams
+    // the consumers meet (bounded, so that one that gave up strands nobody)
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.meet);
+        const bool met = wait_phase(&sm.meet, meet_parity, &sm.stop, a.wait_limit);
+        meet_parity ^= 1u;
+        return met;
+    };
+    // ---- places of this lane's operands in a slot, the same for every tile
+    const uint32_t log_rows = maps.codes.log_rows;
+    const uint32_t mrow = slice * 16 + ((lane >> 3) & 1u) * 8 + (lane & 7u), mchunk = lane >> 4;
+    uint32_t k_at[NP], v_at[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint32_t c = 2 * i + mchunk < (uint32_t)CH ? 2 * i + mchunk : 2 * i;
+        k_at[i] = code_at<D>(log_rows, 0, mrow, c);
+        v_at[i] = code_at<D>(log_rows, 1, mrow, c);
+    }
+    // scales of positions 2 * in_quad, + 1 of the slice, + 8; groups 2R bytes apart
+    const uint32_t s_group = 2u << log_rows;
+    const uint32_t s_at = ((slice * 16) >> log_rows) * scale_unit(NG, log_rows) +
+                          2 * (((slice * 16) & ((1u << log_rows) - 1u)) + 2 * in_quad);
+
+    Walk w;
+    w.begin(a.split, sm.split.start);
+    bool alive = true;
+    if constexpr (HOOK == Hook::kAbandoned) {
+        *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
+        alive = false;
+    }
+    while (alive && !w.done()) {
+        const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
+        const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
+        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        const uint32_t rows = w.span.tokens * in_block;
+        const uint32_t head0 = kvh * a.G + hb * kRows;
+        const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
+        if (pos0 + w.span.tokens > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
+        const uint32_t shared_by = w.first == 0 && !w.whole()
+                                       ? sharers(a.split, sm.split.start, w, blockIdx.x / a.lanes)
+                                       : 0;
+
+        // ---- queries: A operands, fp16 rows brought into range by 2^x
+        const uint32_t r0 = quad, r1 = quad + 8;
+        const uint32_t t0 = w.span.tokens == 1 ? 0 : r0 / in_block;  // tokens of the chunk
+        const uint32_t t1 = w.span.tokens == 1 ? 0 : r1 / in_block;
+        alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_limit);
+        if (!alive) break;
+        uint32_t qf[CH][2][kEach];  // step, then pairs 2t of rows r0 (r1), pairs 2t + 1
+        float qs[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const uint32_t r = quad + 8 * n;
+            const unsigned char* q = sm.q_raw[q_at.slot] + r * Sh::kQPitch + 16 * in_quad;
+            uint4 raw[CH];
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                raw[c] = r < rows ? *reinterpret_cast<const uint4*>(q + 64 * c)
+                                  : make_uint4(0, 0, 0, 0);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
+                                             __vmaxu2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1)
+                top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float up, down;
+            row_power(max(top & 0xffffu, top >> 16), up, down);
+            // products are of codes 2^-20 as large
+            qs[n] = a.sm_scale * down * 0x1p20f;
+            qs[n] *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
+            // never 0, a masked score is -inf times this, and never infinite
+            qs[n] = fminf(fmaxf(qs[n], 1.17549435e-38f), 3.4028234e38f);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {  // columns i and i + 4 of the lane's eight
+                qf[c][0][n] = pack2<true>(bf16_lo(raw[c].x) * up, bf16_lo(raw[c].z) * up);
+                qf[c][0][NB + n] = pack2<true>(bf16_hi(raw[c].x) * up, bf16_hi(raw[c].z) * up);
+                qf[c][1][n] = pack2<true>(bf16_lo(raw[c].y) * up, bf16_lo(raw[c].w) * up);
+                qf[c][1][NB + n] = pack2<true>(bf16_hi(raw[c].y) * up, bf16_hi(raw[c].w) * up);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[q_at.slot]);
+        q_at.step();
+        auto times_q = [&](float(&s)[4], int c, int t, uint32_t b0, uint32_t b1) {
+            const uint32_t f[4] = {qf[c][t][0], NB == 2 ? qf[c][t][NB - 1] : 0u, qf[c][t][NB],
+                                   NB == 2 ? qf[c][t][2 * NB - 1] : 0u};
+            mma16816<true>(s, f, b0, b1);
+        };
+        // -8 sum of a group's queries, in units of the products
+        float off[NG][NB];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) times_q(s, c, t, kEight, kEight);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) off[g][n] = -s[2 * n];
+        }
+        [[maybe_unused]] float slope[NB];
+        if constexpr (MODS) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const uint32_t r = quad + 8 * n, ct = n ? t1 : t0;
+                slope[n] = a.slopes && r < rows
+                               ? kLog2e * __ldg(a.slopes + head0 + (r - ct * in_block))
+                               : 0.0f;
+            }
+        }
+        // positions every row of the block sees, and each row's own
+        const int64_t all_hi = pos0, all_lo = pos0 + w.span.tokens - a.split.window;
+        const int64_t own[2] = {pos0 + t0, pos0 + t1};
+
+        float acc[NB][CH][2][4], less[NB][NG][4];  // O^T, and 8 sum (P s_v) in its units
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) acc[n][c][0][e] = acc[n][c][1][e] = 0.0f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) less[n][g][e] = 0.0f;
+            }
+        }
+        float m[NB], l[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0.0f;
+        }
+        const int64_t p_first = (int64_t)(w.span.tile0 + w.first) * kTile + slice * 16;
+
+        // The warp's slice of tile k, in the slot at `at`; EDGE: positions may
+        // be missing, or seen by some rows only.
+        auto tile = [&](uint32_t k, auto edge_const) {
+            constexpr bool EDGE = decltype(edge_const)::value;
+            const uint32_t codes = smem_addr(sm.codes[at.slot]);
+            const unsigned char* sc = sm.scales[at.slot] + s_at;
+            // ---- S = Q K^T
+            float s[2][4];
+            {
+                uint32_t kw[NP][4];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) ldsm4(kw[i], codes + k_at[i]);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float x[2][4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        x[n][0] = x[n][1] = off[g][0];
+                        x[n][2] = x[n][3] = NB == 2 ? off[g][NB - 1] : 0.0f;
+                    }
+#pragma unroll
+                    for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint32_t u = kw[c / 2][2 * (c & 1) + n];
+                            times_q(x[n], c, 0, (u << 4) & kMask, u & kMask);
+                            times_q(x[n], c, 1, (u >> 4) & kMask, (u >> 8) & kMask);
+                        }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t f =
+                            *reinterpret_cast<const uint32_t*>(sc + g * s_group + 16 * n);
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            const float by = e & 1 ? scale_hi(f) : scale_lo(f);
+                            s[n][e] = g == 0 ? by * x[n][e] : fmaf(by, x[n][e], s[n][e]);
+                        }
+                    }
+                }
+            }
+            // ---- cap, distance bias, mask
+            [[maybe_unused]] const int64_t p0 = p_first + (int64_t)k * kTile;
+            if constexpr (MODS) {  // into units of log2
+                if (a.softcap > 0.0f) {
+                    // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd
+                    // series where that loses small scores
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            const float u = s[n][e] * qs[e / 2], v = u * u;
+                            const float near = a.cap_half * u *
+                                               fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3),
+                                                    1.0f);
+                            const float far =
+                                a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
+                            s[n][e] = fabsf(u) < kTanhNear ? near : far;
+                        }
+                }
+                if (a.slopes) {
+                    // slope * (offset in the slice - distance of its start)
+                    const int64_t from = p0 + 2 * in_quad;
+#pragma unroll
+                    for (int r = 0; r < NB; ++r) {
+                        const float f = a.softcap > 0.0f ? 1.0f : qs[r];
+                        const float away = slope[r] * (float)(own[r] - from);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                s[n][2 * r + e] =
+                                    fmaf(s[n][2 * r + e], f,
+                                         fmaf(slope[r], (float)(n * 8 + e), -away));
+                    }
+                } else if (!(a.softcap > 0.0f)) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) s[n][e] *= qs[e / 2];
+                }
+            }
+            [[maybe_unused]] uint32_t seen = 0;  // bit n * kEach + e
+            if constexpr (EDGE) {
+                const uint32_t there = (uint32_t)(sm.there[at.slot] >> (slice * 16));
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const uint32_t j = n * 8 + 2 * in_quad + (e & 1);
+                        const int64_t p = p0 + j;
+                        if (((there >> j) & 1u) && p <= own[e / 2] &&
+                            p > own[e / 2] - a.split.window)
+                            seen |= 1u << (n * kEach + e);
+                        else
+                            s[n][e] = -INFINITY;
+                    }
+            }
+            auto kept = [&](int n, int e) { return !EDGE || ((seen >> (n * kEach + e)) & 1u); };
+            // ---- weights, and weights times scales as operands
+            float p[2][4];
+            uint32_t b[NB][NG][2];
+            const unsigned char* sv = sc + NG * s_group;
+            auto weights = [&]() {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        // a row that has seen no position keeps m = -inf: subtract 0
+                        const float ref = m[e / 2] == -INFINITY ? 0.0f : m[e / 2];
+                        p[n][e] = fast_exp2(MODS ? s[n][e] - ref : fmaf(s[n][e], qs[e / 2], -ref));
+                    }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t f =
+                            *reinterpret_cast<const uint32_t*>(sv + g * s_group + 16 * n);
+#pragma unroll
+                        for (int r = 0; r < NB; ++r) {
+                            float x = p[n][2 * r] * scale_lo(f), y = p[n][2 * r + 1] * scale_hi(f);
+                            if (!kept(n, 2 * r)) x = 0.0f;  // whatever its scale holds
+                            if (!kept(n, 2 * r + 1)) y = 0.0f;
+                            b[r][g][n] = pack2<true>(x, y);
+                        }
+                    }
+            };
+            weights();
+            // Does a row's reference have to rise?  (All patterns are of numbers
+            // that are not negative; a NaN's is above 2^15's.)
+            bool rises = false;
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    top = __vmaxu2(top, __vmaxu2(b[r][g][0] & 0x7fff7fffu, b[r][g][1] & 0x7fff7fffu));
+                rises |= (top >> 16) > 0x7800u || (top & 0xffffu) > 0x7800u || m[r] == -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, rises)) {
+                float f[NB];
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    // the row's largest weight times scale, in log2
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float by = 0x1p-40f;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                const uint32_t x =
+                                    *reinterpret_cast<const uint32_t*>(sv + g * s_group + 16 * n);
+                                by = fmaxf(by, fabsf(e ? scale_hi(x) : scale_lo(x)));
+                            }
+                            const float x = MODS ? s[n][2 * r + e] : s[n][2 * r + e] * qs[r];
+                            if (kept(n, 2 * r + e)) top = fmaxf(top, x + __log2f(by));
+                        }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float next = fmaxf(m[r], top - weight_lift<true>());
+                    f[r] = next == m[r] ? 1.0f : fast_exp2(m[r] - next);
+                    m[r] = next;
+                    l[r] *= f[r];
+                }
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    // of rows 2 * in_quad and the next, which the sums' columns are
+                    const float f0 = __shfl_sync(0xffffffffu, f[r], 8 * in_quad);
+                    const float f1 = __shfl_sync(0xffffffffu, f[r], 8 * in_quad + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            acc[r][c][0][e] *= e & 1 ? f1 : f0;
+                            acc[r][c][1][e] *= e & 1 ? f1 : f0;
+                        }
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) less[r][g][e] *= e & 1 ? f1 : f0;
+                    }
+                }
+                weights();
+            }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) l[e / 2] += p[0][e] + p[1][e];
+            // ---- O^T += V^T (P s_v)^T
+            {
+                uint32_t vw[NP][4];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) ldsm4_trans(vw[i], codes + v_at[i]);
+                const uint32_t eights[4] = {kEight, kEight, kEight, kEight};
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int r = 0; r < NB; ++r)
+                        mma16816<true>(less[r][g], eights, b[r][g][0], b[r][g][1]);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint32_t x = vw[c / 2][2 * (c & 1)], y = vw[c / 2][2 * (c & 1) + 1];
+                    const uint32_t f0[4] = {(x << 4) & kMask, x & kMask, (y << 4) & kMask, y & kMask};
+                    const uint32_t f1[4] = {(x >> 4) & kMask, (x >> 8) & kMask, (y >> 4) & kMask,
+                                            (y >> 8) & kMask};
+#pragma unroll
+                    for (int r = 0; r < NB; ++r) {
+                        mma16816<true>(acc[r][c][0], f0, b[r][c / 2][0], b[r][c / 2][1]);
+                        mma16816<true>(acc[r][c][1], f1, b[r][c / 2][0], b[r][c / 2][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[at.slot]);
+        };
+        // tiles [even0, even1) of the segment: this warp's slices are seen by
+        // every row of the block alike
+        const uint32_t count = w.last - w.first;
+        const int64_t lo_gap = all_lo - p_first, hi_gap = all_hi + 1 - 16 - p_first;
+        const uint32_t even0 = lo_gap <= 0 ? 0u : (uint32_t)((lo_gap + kTile - 1) / kTile);
+        const uint32_t even1 = hi_gap < 0 ? 0u : (uint32_t)(hi_gap / kTile) + 1;
+        for (uint32_t k = 0; k < count; ++k) {
+            if (Sh::kTeams == 1 || turn == team) {
+                alive = wait_phase(&sm.full[at.slot], at.parity, &sm.stop, a.wait_limit);
+                if (!alive) break;
+                const bool all = ((uint32_t)(sm.there[at.slot] >> (slice * 16)) & 0xffffu) == 0xffffu;
+                if (k >= even0 && k < even1 && all)
+                    tile(k, std::false_type{});
+                else
+                    tile(k, std::true_type{});
+            }
+            at.step();
+            if (Sh::kTeams > 1 && ++turn == Sh::kTeams) turn = 0;
+        }
+        if (!alive) break;
+
+        // ---- the warps join, a few rows at a time
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
+            if (in_quad == 0) {
+                sm.m[warp][quad + 8 * n] = m[n];
+                sm.l[warp][quad + 8 * n] = l[n];
+            }
+        }
+        const bool whole = w.whole();
+        float* part = slot_of<Sh::kPadded>(a.workspace, blockIdx.x, w.first == 0 ? 1 : 0);
+        constexpr uint32_t JR = Sh::kJoinRows, quads = D / 4;
+#pragma unroll
+        for (uint32_t round = 0; round < 8 * NB / JR; ++round) {
+            if (round * JR >= rows) break;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t r = 8 * n + 2 * in_quad + e;
+                    if (r / JR != round) continue;
+                    float* mine = sm.join[warp][r % JR] + 4 * quad;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const float off8 = less[n][c / 2][e];
+                        *reinterpret_cast<float4*>(mine + 32 * c) = make_float4(
+                            (acc[n][c][0][e] - off8) * 0x1p20f, (acc[n][c][0][2 + e] - off8) * 0x1p20f,
+                            (acc[n][c][1][e] - off8) * 0x1p20f, (acc[n][c][1][2 + e] - off8) * 0x1p20f);
+                    }
+                }
+            alive = meet();
+            if (!alive) break;
+            const uint32_t here = rows - round * JR < JR ? rows - round * JR : JR;
+            for (uint32_t x = tid; x < here * quads; x += 32 * W) {
+                const uint32_t rj = x / quads, d = (x - rj * quads) * 4, r = round * JR + rj;
+                float top = sm.m[0][r];
+#pragma unroll
+                for (int v = 1; v < W; ++v) top = fmaxf(top, sm.m[v][r]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                float sum = 0.0f;
+                float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < W; ++v) {
+                    const float f = fast_exp2(sm.m[v][r] - base);
+                    const float4 y = *reinterpret_cast<const float4*>(sm.join[v][rj] + d);
+                    sum += f * sm.l[v][r];
+                    o.x += f * y.x;
+                    o.y += f * y.y;
+                    o.z += f * y.z;
+                    o.w += f * y.w;
+                }
+                if (whole) {
+                    const uint32_t ct = r / in_block;
+                    const uint64_t row = (uint64_t)(w.t + ct) * a.Hq + head0 + (r - ct * in_block);
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint2 y;
+                    y.x = pack_bf16x2(o.x * inv, o.y * inv);
+                    y.y = pack_bf16x2(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(a.out + row * D + d) = y;
+                    if (d == 0 && a.lse)
+                        a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4*>(part + r * Sh::kPadded + d) = o;
+                    if (d == 0) {
+                        part[kRows * Sh::kPadded + r] = top;
+                        part[kRows * Sh::kPadded + kRows + r] = sum;
+                    }
+                }
+            }
+            alive = meet();
+            if (!alive) break;
+        }
+        if (!alive) break;
+        if (shared_by && tid == 0) {
+            OpenPiece x;
+            x.n = shared_by;
+            x.t = w.t;
+            x.tokens = w.span.tokens;
+            x.block = block;
+            *open = x;
+        }
+        w.next(a.split);
+    }
+    if (!alive && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
+}
+
+template <int D, int NB, bool MODS, Hook HOOK>
+cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
+    using Sh = Shape4<D, NB>;
+    constexpr size_t smem = sizeof(Smem4<D, NB>);
+    static_assert(smem <= (Sh::kCtas == 3 ? 75 : 113) * 1024, "shared memory of an SM");
+    uint64_t wave = 0;
+    cudaError_t e = wave_ctas<&gqa_int4_kernel<D, NB, MODS, HOOK>>(Sh::kThreads, smem, wave);
+    if (e != cudaSuccess) return e;
+    if (wave == 0) return cudaErrorInvalidConfiguration;
+    const uint32_t ctas = side_by_side(a, wave);
+    e = launch_early(&gqa_int4_kernel<D, NB, MODS, HOOK>, dim3(ctas), Sh::kThreads, smem, stream, a,
+                     maps);
+    if (e != cudaSuccess) return e;
+    return launch_join<Sh::kPadded>(a, ctas, stream);
+}
+
+template <int D, Hook HOOK>
+int launch(GqaArgs& a, const kvw_paged_cache_t* cache, const kva_group_scales_t* scales,
+           uint32_t layer_idx, cudaStream_t stream) {
+    Int4Maps maps;
+    const int st = encode_int4_maps(&maps, cache, scales, layer_idx);
+    if (st != KVW_OK) return st;
+    const bool mods = a.softcap > 0.0f || a.slopes, high = (a.per_token << a.split.log_c) > 8;
+    const cudaError_t e = mods ? (high ? launch_as<D, 2, true, HOOK>(a, maps, stream)
+                                       : launch_as<D, 1, true, HOOK>(a, maps, stream))
+                          : high ? launch_as<D, 2, false, HOOK>(a, maps, stream)
+                                 : launch_as<D, 1, false, HOOK>(a, maps, stream);
+    return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
+}
+
+// Strides that a tensor map takes (see tma_strides_ok), of codes and scales.
+bool int4_strides_ok(const kvw_paged_cache_t* c, const kva_group_scales_t* s) {
+    auto ok = [](int64_t codes, int64_t scales, uint64_t n) {
+        return n <= 1 || (codes > 0 && codes / 2 < (1ll << 40) && scales > 0 &&
+                          scales < (1ll << 39));
+    };
+    return ok(c->stride_head, s->stride_head, c->num_heads) &&
+           ok(c->stride_page, s->stride_page, c->num_pages) && ok(c->stride_kv, s->stride_kv, 2);
+}
+
+int int4_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
+               const uint32_t* input_row_offsets, uint32_t num_batches, uint32_t tot_seq_len,
+               uint32_t num_q_heads, const kvw_paged_cache_t* cache,
+               const kva_group_scales_t* scales, uint32_t layer_idx, float sm_scale, float softcap,
+               uint32_t window, const float* alibi_slopes, void* workspace,
+               uint64_t workspace_bytes, uint32_t* err_flags, cudaStream_t stream, Hook hook,
+               uint64_t wait_ns) {
+    const int st = check_int4(cache, scales, layer_idx);
+    if (st != KVW_OK) return st;
+    GqaArgs a = {};
+    const int bad = gqa_arguments(a, out, lse, q, q_row_stride, input_row_offsets, num_batches,
+                                  tot_seq_len, num_q_heads, cache, sm_scale, softcap, window,
+                                  alibi_slopes, workspace, workspace_bytes, err_flags,
+                                  tma_sizes_ok(cache), true, int4_strides_ok(cache, scales));
+    if (bad != KVW_OK || tot_seq_len == 0) return bad;
+    a.k_scale = a.v_scale = 1.0f;
+    a.wait_limit = wait_cycles(wait_ns);
+    auto run = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+#ifdef KVW_TEST_HOOKS
+        if (hook == Hook::kWithheld)
+            return launch<D, Hook::kWithheld>(a, cache, scales, layer_idx, stream);
+        if (hook == Hook::kAbandoned)
+            return launch<D, Hook::kAbandoned>(a, cache, scales, layer_idx, stream);
+#else
+        if (hook != Hook::kNone) return (int)KVW_EUNSUPPORTED;
+#endif
+        return launch<D, Hook::kNone>(a, cache, scales, layer_idx, stream);
+    };
+    switch (a.D) {
+        case 64: return run(std::integral_constant<int, 64>{});
+        case 96: return run(std::integral_constant<int, 96>{});
+        case 128: return run(std::integral_constant<int, 128>{});
+        default: return run(std::integral_constant<int, 256>{});
+    }
+}
+
+}  // namespace
+}  // namespace kvw
+
+extern "C" int kva_gqa_decode_int4(void* out, float* lse, const void* q, int64_t q_row_stride,
+                                   const uint32_t* input_row_offsets, uint32_t num_batches,
+                                   uint32_t tot_seq_len, uint32_t num_q_heads,
+                                   const kvw_paged_cache_t* cache,
+                                   const kva_group_scales_t* scales, uint32_t layer_idx,
+                                   float sm_scale, float softcap, uint32_t window,
+                                   const float* alibi_slopes, void* workspace,
+                                   uint64_t workspace_bytes, uint32_t* err_flags,
+                                   cudaStream_t stream) {
+    return kvw::int4_entry(out, lse, q, q_row_stride, input_row_offsets, num_batches, tot_seq_len,
+                           num_q_heads, cache, scales, layer_idx, sm_scale, softcap, window,
+                           alibi_slopes, workspace, workspace_bytes, err_flags, stream,
+                           kvw::Hook::kNone, kvw::kWaitLimitNs);
+}
+
+#ifdef KVW_TEST_HOOKS
+// Test builds only: as in gqa_decode_paged.cu, the first tile of every CTA is
+// announced but never copied, or the consumers leave at once.
+extern "C" int kva_test_gqa_int4(void* out, const void* q, int64_t q_row_stride,
+                                 const uint32_t* input_row_offsets, uint32_t num_batches,
+                                 uint32_t tot_seq_len, uint32_t num_q_heads,
+                                 const kvw_paged_cache_t* cache, const kva_group_scales_t* scales,
+                                 uint32_t layer_idx, void* workspace, uint64_t workspace_bytes,
+                                 uint32_t* err_flags, cudaStream_t stream, uint64_t wait_ns,
+                                 int abandoned) {
+    return kvw::int4_entry(out, nullptr, q, q_row_stride, input_row_offsets, num_batches,
+                           tot_seq_len, num_q_heads, cache, scales, layer_idx, 0.1f, 0.0f, 0,
+                           nullptr, workspace, workspace_bytes, err_flags, stream,
+                           abandoned ? kvw::Hook::kAbandoned : kvw::Hook::kWithheld, wait_ns);
+}
+#endif

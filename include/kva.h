@@ -10,13 +10,19 @@
  *                            its request's paged keys and values
  *   kva_mla_decode_paged     the same over the paged latent cache (absorbed
  *                            queries, one 576-wide row for all heads)
+ *   kva_append_qkv_int4, kva_gather_kv_int4, kva_gqa_decode_int4
+ *                            appending to a cache held in 4 bits, reading it
+ *                            back as bf16 rows, attention over it
+ *   kva_extend_page_tables   pages for the new tokens from a list of free
+ *                            ones, and the tokens' slots
  * One step of a layer is append (GQA) or kvw_mla_rope_rmsnorm_quant (MLA)
- * followed by the decode call, on one stream.
+ * followed by the decode call, on one stream; the page tables are extended
+ * once before the layers of a step.
  *
  * Conventions: those of kvw.h (asynchronous, caller-owned pointers, host
  * argument errors returned before any launch, device data errors reported as
  * KVW_ERR_* bits in *err_flags, ragged batches through input_row_offsets),
- * and for the two attention calls:
+ * and for the attention calls:
  * - They enqueue two kernels on `stream`: the attention, split over the
  *   contexts of all tokens so that every CTA reads the same amount of cache,
  *   and a join of the pieces.  The split depends only on the lengths, the
@@ -189,6 +195,136 @@ int kva_mla_decode_paged(void* out, float* lse, const void* q_latent,
 
 /* Bytes of workspace for kva_mla_decode_paged, into *bytes (host). */
 int kva_mla_decode_workspace(uint32_t num_heads, uint64_t* bytes);
+
+/*
+ * A cache held in 4 bits: kvw_paged_cache_t with the dtype below, taken by the
+ * *_int4 calls alone.  A value is scale * (code - 8), with a code of 4 bits
+ * for each and a bf16 scale for each group of 64 columns of a row (a last
+ * group of 32 where head_size is 96): 4.25 bits a value for heads of 64, 128
+ * and 256.  The rows of a head lie one after another in a page:
+ *   codes    column c of row r is the low (c even) or high (c odd) half of
+ *            byte c / 2 of the row at
+ *              data + (page*stride_page + kv*stride_kv + layer*stride_layer
+ *                      + head*stride_head + r*head_size) / 2 bytes
+ *            (the descriptor's strides count codes, stride_token = head_size)
+ *   scales   bf16, that of group g of row r at
+ *              data + page*stride_page + kv*stride_kv + layer*stride_layer
+ *                   + head*stride_head + g*page_size + r  elements
+ * head_size 64, 96, 128 or 256 and page_size a multiple of 16 (else
+ * KVW_EUNSUPPORTED); stride_token = head_size, the other strides multiples of
+ * 16 bytes, both data pointers 16-byte aligned (else KVW_EINVAL).  The
+ * descriptor's scale is not used.  Dense layouts: codes [pages, 2, layers,
+ * heads, page_size, head_size / 2] bytes, scales [pages, 2, layers, heads,
+ * groups, page_size].
+ */
+enum kva_dtype { KVA_DTYPE_INT4 = 3 };
+
+typedef struct kva_group_scales {
+    void* data; /* device, bf16 */
+    int64_t stride_page;
+    int64_t stride_kv;
+    int64_t stride_layer;
+    int64_t stride_head;
+} kva_group_scales_t;
+
+/*
+ * kva_append_qkv_paged to a cache held in 4 bits.  With x the values of a
+ * group in fp32 (a key after norm and rotation):
+ *   scale = bf16(max |x| / 7)
+ *   code  = 8 + round_half_even(x / scale), x / scale clamped to -7 .. 7
+ * (code 8 where the scale is 0).  A group that holds an infinity or a NaN
+ * gets the scale NaN, so that all of it reads as NaN.  `scales` is a host
+ * pointer; the other arguments, limits, flags and errors are those of
+ * kva_append_qkv_paged.
+ */
+int kva_append_qkv_int4(void* q_out, int64_t q_out_row_stride, const void* qkv,
+                        int64_t qkv_row_stride, const uint32_t* input_row_offsets,
+                        uint32_t num_batches, uint32_t tot_seq_len, uint32_t num_q_heads,
+                        const void* q_gamma, const void* k_gamma, float epsilon,
+                        float weight_offset, const void* freqs_cis, uint32_t freqs_rows,
+                        uint32_t rope_dim, const uint32_t* position_ids, int interleaved,
+                        const uint32_t* mrope_section, const kvw_paged_cache_t* cache,
+                        const kva_group_scales_t* scales, uint32_t layer_idx,
+                        uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * Rows of a cache held in 4 bits, contiguous and in bf16 (scale * (code - 8),
+ * rounded to nearest even): row first_positions[b] + i of request b goes to
+ * row ctx_offsets[b] + i of k_out and v_out, for i below ctx_offsets[b+1] -
+ * ctx_offsets[b].  With first_positions NULL a request's rows begin at 0 (its
+ * cached prefix); with the lengths before a step and the step's own offsets
+ * the call reads what the step has appended.
+ *
+ *   k_out, v_out     device, bf16, row r at + r*out_row_stride elements
+ *                    (>= num_heads*head_size, multiple of 8), 16-byte aligned;
+ *                    either may be NULL, not both; they do not overlap
+ *   ctx_offsets      device, uint32 [num_batches + 1]: 0, non-decreasing,
+ *                    ending at total_rows (else KVW_ERR_OFFSETS, nothing is
+ *                    written)
+ *   first_positions  device, uint32 [num_batches], or NULL
+ * cache_lengths of the descriptor is not read (but checked as a pointer).  A
+ * row without a valid page is not written (KVW_ERR_PAGE).  total_rows <= 2^31.
+ */
+int kva_gather_kv_int4(void* k_out, void* v_out, int64_t out_row_stride,
+                       const kvw_paged_cache_t* cache, const kva_group_scales_t* scales,
+                       uint32_t layer_idx, const uint32_t* ctx_offsets,
+                       const uint32_t* first_positions, uint32_t num_batches,
+                       uint32_t total_rows, uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * kva_gqa_decode_paged over a cache held in 4 bits: the same formulas with
+ * K and V as their scales and codes have them, the same workspace
+ * (kva_gqa_decode_workspace), limits, flags and errors.  Scores, softmax
+ * statistics and sums are fp32.  The products take fp16 operands: codes are
+ * exact; a query row is brought into fp16's range by a power of two, which
+ * loses only what is below 2^-39 of the row's largest value; a weight times
+ * its value's scale is off by 2^-11 of itself or, for small ones, by 2^-34 of
+ * the row's largest.  Products of 16 columns (of 16 positions) are added up by
+ * one matrix instruction, which may cut each at 2^-17 of a code times the
+ * largest query value (weight times scale) beside fp32's own rounding.
+ * Strides as kva_gqa_decode_paged for codes and scales.
+ */
+int kva_gqa_decode_int4(void* out, float* lse, const void* q, int64_t q_row_stride,
+                        const uint32_t* input_row_offsets, uint32_t num_batches,
+                        uint32_t tot_seq_len, uint32_t num_q_heads,
+                        const kvw_paged_cache_t* cache, const kva_group_scales_t* scales,
+                        uint32_t layer_idx, float sm_scale, float softcap, uint32_t window,
+                        const float* alibi_slopes, void* workspace, uint64_t workspace_bytes,
+                        uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * Pages for a step's new tokens.  Request b holds cache_lengths[b] positions
+ * and gets input_row_offsets[b+1] - input_row_offsets[b] more.  The pages
+ * that hold a cached position stay; each further one up to the last new
+ * position's (or the table's width) gets the next id of the list of free
+ * pages, requests in order:
+ *   have = ceil(len / page_size), need = min(ceil((len + n) / page_size), width)
+ *   page_table[b][have + i] = free_pages[taken + (pages of requests before b) + i]
+ *   taken_out = taken + sum over b of max(need - have, 0), at most num_free
+ *   slot_map[t] = page * page_size + position % page_size, for each new token
+ * Other entries of page_table are left as they are.
+ *
+ *   page_table     device, uint32 [num_batches, max_pages_per_seq], updated
+ *   cache_lengths  device, uint32 [num_batches]
+ *   free_pages     device, uint32 [num_free]: ids, the first `taken` in use
+ *   taken          device, uint32 [1]
+ *   taken_out      device, uint32 [1]; may be `taken` itself
+ *   slot_map       device, int64 [tot_seq_len], or NULL; -1 for no page
+ *   num_pages      ids from here on are not valid
+ * Where the list ends, or holds an id that is not valid, the entries are
+ * KVW_PAGE_UNMAPPED and KVW_ERR_PAGE is set; so it is for a position past the
+ * table's width and for a new token in an open page whose entry is not valid.
+ * Malformed offsets: KVW_ERR_OFFSETS, nothing is written.  With no tokens
+ * nothing is launched: taken_out keeps what it holds.  num_batches <= 8192,
+ * tot_seq_len <= 2^31.  free_pages, lengths and offsets must not overlap what
+ * is written.
+ */
+int kva_extend_page_tables(uint32_t* page_table, uint32_t max_pages_per_seq,
+                           const uint32_t* cache_lengths, const uint32_t* input_row_offsets,
+                           uint32_t num_batches, uint32_t tot_seq_len, uint32_t page_size,
+                           uint32_t num_pages, const uint32_t* free_pages, uint32_t num_free,
+                           const uint32_t* taken, uint32_t* taken_out, int64_t* slot_map,
+                           uint32_t* err_flags, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
