@@ -19,10 +19,12 @@
 // bits 0 to 3, with 5 instructions for 8 codes, by 2^-14: a column whose heavy
 // positions all hold code 8 was off by 2 % of the little that is left).
 //
-// S = Q K^T has the row block's rows as the instruction's 16 rows; O^T = V^T
-// P^T has them as its 8 columns, once or twice: S leaves its registers in the
-// order in which O^T takes P, and with up to 8 rows O^T costs half as many
-// instructions and half the registers.
+// Both products have the row block's rows as the instruction's 8 columns (one
+// or two blocks of them): S^T = K Q^T and O^T = V^T P^T.  Codes are then the
+// operand of 16 rows, so that no half of an instruction is idle with up to 8
+// rows, and P^T passes from the order of one's result to the other's operand
+// by transposing 8 x 8 blocks (movmatrix).  Row i of an operand's upper and
+// lower half are positions 2 i and 2 i + 1, whose scales are one word.
 //
 // Weights times scales are fp16.  Their reference m follows the row's largest
 // P s_v, not its largest score: raised when a product passes 2^15, to where
@@ -244,16 +246,29 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
                           a.err_flags);
 }
 
-// Two neighbouring scales of a word.
-__device__ __forceinline__ float scale_lo(uint32_t w) { return bf16_lo(w); }
-__device__ __forceinline__ float scale_hi(uint32_t w) { return bf16_hi(w); }
+// D = A B + C, with C in registers of its own.
+__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+}
+
+// The transpose of an 8 x 8 block of fp16 values.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 template <int D, int NB, bool MODS, Hook HOOK>
 __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
     gqa_int4_kernel(const GqaArgs a, const __grid_constant__ Int4Maps maps) {
     using Sh = Shape4<D, NB>;
     constexpr int CH = Sh::kChunks, NP = Sh::kPairs, NG = Sh::kGroups, W = Sh::kWarps;
-    constexpr int kEach = 2 * NB;             // scores of a product that are looked at
     constexpr uint32_t kMask = 0x00f000f0u;   // a pair of codes
     constexpr uint32_t kEight = 0x00800080u;  // 8, as codes are
     extern __shared__ __align__(1024) unsigned char dyn[];
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
     };
     // ---- places of this lane's operands in a slot, the same for every tile
     const uint32_t log_rows = maps.codes.log_rows;
-    const uint32_t mrow = slice * 16 + ((lane >> 3) & 1u) * 8 + (lane & 7u), mchunk = lane >> 4;
+    const uint32_t mrow = slice * 16 + 2 * (lane & 7u) + ((lane >> 3) & 1u), mchunk = lane >> 4;
     uint32_t k_at[NP], v_at[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -312,10 +327,10 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
         k_at[i] = code_at<D>(log_rows, 0, mrow, c);
         v_at[i] = code_at<D>(log_rows, 1, mrow, c);
     }
-    // scales of positions 2 * in_quad, + 1 of the slice, + 8; groups 2R bytes apart
+    // scales of positions 2 * quad and the next of the slice; groups 2R bytes apart
     const uint32_t s_group = 2u << log_rows;
     const uint32_t s_at = ((slice * 16) >> log_rows) * scale_unit(NG, log_rows) +
-                          2 * (((slice * 16) & ((1u << log_rows) - 1u)) + 2 * in_quad);
+                          2 * (((slice * 16) & ((1u << log_rows) - 1u)) + 2 * quad);
 
     Walk w;
     w.begin(a.split, sm.split.start);
@@ -336,14 +351,12 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                                        ? sharers(a.split, sm.split.start, w, blockIdx.x / a.lanes)
                                        : 0;
 
-        // ---- queries: A operands, fp16 rows brought into range by 2^x
-        const uint32_t r0 = quad, r1 = quad + 8;
-        const uint32_t t0 = w.span.tokens == 1 ? 0 : r0 / in_block;  // tokens of the chunk
-        const uint32_t t1 = w.span.tokens == 1 ? 0 : r1 / in_block;
+        // ---- queries: B operands, fp16 rows brought into range by 2^x
         alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_limit);
         if (!alive) break;
-        uint32_t qf[CH][2][kEach];  // step, then pairs 2t of rows r0 (r1), pairs 2t + 1
-        float qs[NB];
+        uint32_t qf[NB][CH][2][2];  // of row quad (+ 8): step, pairs 2t and 2t + 1 of its columns
+        float qs[NB][2];            // of rows 2 * in_quad and the next, whose scores the lane has
+        uint32_t token = 0;         // and their tokens in the chunk, 8 bits each
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const uint32_t r = quad + 8 * n;
@@ -362,52 +375,61 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                 top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
             float up, down;
             row_power(max(top & 0xffffu, top >> 16), up, down);
-            // products are of codes 2^-20 as large
-            qs[n] = a.sm_scale * down * 0x1p20f;
-            qs[n] *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
+            // products are of codes 2^-20 as large; scores in units of log2 straight
+            // from the product, or 2 log2(e) / cap of them
+            float by = a.sm_scale * down * 0x1p20f;
+            by *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
             // never 0, a masked score is -inf times this, and never infinite
-            qs[n] = fminf(fmaxf(qs[n], 1.17549435e-38f), 3.4028234e38f);
+            by = fminf(fmaxf(by, 1.17549435e-38f), 3.4028234e38f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qs[n][e] = __shfl_sync(0xffffffffu, by, 8 * in_quad + 4 * e);
+                if (w.span.tokens > 1)
+                    token |= (8 * n + 2 * in_quad + e) / in_block << (16 * n + 8 * e);
+            }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {  // columns i and i + 4 of the lane's eight
-                qf[c][0][n] = pack2<true>(bf16_lo(raw[c].x) * up, bf16_lo(raw[c].z) * up);
-                qf[c][0][NB + n] = pack2<true>(bf16_hi(raw[c].x) * up, bf16_hi(raw[c].z) * up);
-                qf[c][1][n] = pack2<true>(bf16_lo(raw[c].y) * up, bf16_lo(raw[c].w) * up);
-                qf[c][1][NB + n] = pack2<true>(bf16_hi(raw[c].y) * up, bf16_hi(raw[c].w) * up);
+                qf[n][c][0][0] = pack2<true>(bf16_lo(raw[c].x) * up, bf16_lo(raw[c].z) * up);
+                qf[n][c][0][1] = pack2<true>(bf16_hi(raw[c].x) * up, bf16_hi(raw[c].z) * up);
+                qf[n][c][1][0] = pack2<true>(bf16_lo(raw[c].y) * up, bf16_lo(raw[c].w) * up);
+                qf[n][c][1][1] = pack2<true>(bf16_hi(raw[c].y) * up, bf16_hi(raw[c].w) * up);
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty[q_at.slot]);
         q_at.step();
-        auto times_q = [&](float(&s)[4], int c, int t, uint32_t b0, uint32_t b1) {
-            const uint32_t f[4] = {qf[c][t][0], NB == 2 ? qf[c][t][NB - 1] : 0u, qf[c][t][NB],
-                                   NB == 2 ? qf[c][t][2 * NB - 1] : 0u};
-            mma16816<true>(s, f, b0, b1);
-        };
+        const uint32_t eights[4] = {kEight, kEight, kEight, kEight};
         // -8 sum of a group's queries, in units of the products
-        float off[NG][NB];
+        float off[NB][NG][4];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
+            for (int g = 0; g < NG; ++g) {
+                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) times_q(s, c, t, kEight, kEight);
+                for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) off[g][n] = -s[2 * n];
-        }
-        [[maybe_unused]] float slope[NB];
+                    for (int t = 0; t < 2; ++t)
+                        mma16816<true>(x, eights, qf[n][c][t][0], qf[n][c][t][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) off[n][g][e] = -x[e];
+            }
+        [[maybe_unused]] float slope[NB][2];
         if constexpr (MODS) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const uint32_t r = quad + 8 * n, ct = n ? t1 : t0;
-                slope[n] = a.slopes && r < rows
-                               ? kLog2e * __ldg(a.slopes + head0 + (r - ct * in_block))
-                               : 0.0f;
-            }
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t r = 8 * n + 2 * in_quad + e;
+                    const uint32_t ct = (token >> (16 * n + 8 * e)) & 255u;
+                    slope[n][e] = a.slopes && r < rows
+                                      ? kLog2e * __ldg(a.slopes + head0 + (r - ct * in_block))
+                                      : 0.0f;
+                }
         }
         // positions every row of the block sees, and each row's own
         const int64_t all_hi = pos0, all_lo = pos0 + w.span.tokens - a.split.window;
-        const int64_t own[2] = {pos0 + t0, pos0 + t1};
+        auto own = [&](int n, int e) { return pos0 + ((token >> (16 * n + 8 * e)) & 255u); };
 
         float acc[NB][CH][2][4], less[NB][NG][4];  // O^T, and 8 sum (P s_v) in its units
 #pragma unroll
@@ -420,12 +442,13 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                 for (int g = 0; g < NG; ++g) less[n][g][e] = 0.0f;
             }
         }
-        float m[NB], l[NB];
+        float m[NB][2], l[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            m[n] = -INFINITY;
-            l[n] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
         }
+        bool settled = false;  // every row has a reference
         const int64_t p_first = (int64_t)(w.span.tile0 + w.first) * kTile + slice * 16;
 
         // The warp's slice of tile k, in the slot at `at`; EDGE: positions may
@@ -434,51 +457,53 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
             constexpr bool EDGE = decltype(edge_const)::value;
             const uint32_t codes = smem_addr(sm.codes[at.slot]);
             const unsigned char* sc = sm.scales[at.slot] + s_at;
-            // ---- S = Q K^T
-            float s[2][4];
+            // ---- S^T = K Q^T
+            float s[NB][4];  // position 2 * quad: rows 2 * in_quad and the next; then the other's
             {
                 uint32_t kw[NP][4];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) ldsm4(kw[i], codes + k_at[i]);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float x[2][4];
+                    float x[NB][4];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        x[n][0] = x[n][1] = off[g][0];
-                        x[n][2] = x[n][3] = NB == 2 ? off[g][NB - 1] : 0.0f;
-                    }
+                    for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c) {
+                        const uint32_t u = kw[c / 2][2 * (c & 1)], v = kw[c / 2][2 * (c & 1) + 1];
+                        const uint32_t f0[4] = {(u << 4) & kMask, (v << 4) & kMask, u & kMask,
+                                                v & kMask};
+                        const uint32_t f1[4] = {(u >> 4) & kMask, (v >> 4) & kMask, (u >> 8) & kMask,
+                                                (v >> 8) & kMask};
 #pragma unroll
-                    for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const uint32_t u = kw[c / 2][2 * (c & 1) + n];
-                            times_q(x[n], c, 0, (u << 4) & kMask, u & kMask);
-                            times_q(x[n], c, 1, (u >> 4) & kMask, (u >> 8) & kMask);
-                        }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t f =
-                            *reinterpret_cast<const uint32_t*>(sc + g * s_group + 16 * n);
-#pragma unroll
-                        for (int e = 0; e < kEach; ++e) {
-                            const float by = e & 1 ? scale_hi(f) : scale_lo(f);
-                            s[n][e] = g == 0 ? by * x[n][e] : fmaf(by, x[n][e], s[n][e]);
+                        for (int n = 0; n < NB; ++n) {
+                            if (c == 2 * g)
+                                mma_from(x[n], f0, qf[n][c][0][0], qf[n][c][0][1], off[n][g]);
+                            else
+                                mma16816<true>(x[n], f0, qf[n][c][0][0], qf[n][c][0][1]);
+                            mma16816<true>(x[n], f1, qf[n][c][1][0], qf[n][c][1][1]);
                         }
                     }
+                    const uint32_t by = *reinterpret_cast<const uint32_t*>(sc + g * s_group);
+                    const float by0 = bf16_lo(by), by1 = bf16_hi(by);
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float f = e < 2 ? by0 : by1;
+                            s[n][e] = g == 0 ? f * x[n][e] : fmaf(f, x[n][e], s[n][e]);
+                        }
                 }
             }
             // ---- cap, distance bias, mask
-            [[maybe_unused]] const int64_t p0 = p_first + (int64_t)k * kTile;
+            [[maybe_unused]] const int64_t p0 = p_first + (int64_t)k * kTile + 2 * quad;
             if constexpr (MODS) {  // into units of log2
                 if (a.softcap > 0.0f) {
                     // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd
                     // series where that loses small scores
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int e = 0; e < kEach; ++e) {
-                            const float u = s[n][e] * qs[e / 2], v = u * u;
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = s[n][e] * qs[n][e & 1], v = u * u;
                             const float near = a.cap_half * u *
                                                fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3),
                                                     1.0f);
@@ -488,143 +513,137 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                         }
                 }
                 if (a.slopes) {
-                    // slope * (offset in the slice - distance of its start)
-                    const int64_t from = p0 + 2 * in_quad;
 #pragma unroll
-                    for (int r = 0; r < NB; ++r) {
-                        const float f = a.softcap > 0.0f ? 1.0f : qs[r];
-                        const float away = slope[r] * (float)(own[r] - from);
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                s[n][2 * r + e] =
-                                    fmaf(s[n][2 * r + e], f,
-                                         fmaf(slope[r], (float)(n * 8 + e), -away));
-                    }
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = a.softcap > 0.0f ? 1.0f : qs[n][e];
+                            const float bias = -slope[n][e] * (float)(own(n, e) - p0);
+                            s[n][e] = fmaf(s[n][e], f, bias);
+                            s[n][2 + e] = fmaf(s[n][2 + e], f, bias + slope[n][e]);
+                        }
                 } else if (!(a.softcap > 0.0f)) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int e = 0; e < kEach; ++e) s[n][e] *= qs[e / 2];
+                        for (int e = 0; e < 4; ++e) s[n][e] *= qs[n][e & 1];
                 }
             }
-            [[maybe_unused]] uint32_t seen = 0;  // bit n * kEach + e
+            [[maybe_unused]] uint32_t seen = 0;  // bit 4 n + e
             if constexpr (EDGE) {
-                const uint32_t there = (uint32_t)(sm.there[at.slot] >> (slice * 16));
+                const uint32_t there = (uint32_t)(sm.there[at.slot] >> (slice * 16 + 2 * quad));
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) {
-                        const uint32_t j = n * 8 + 2 * in_quad + (e & 1);
-                        const int64_t p = p0 + j;
-                        if (((there >> j) & 1u) && p <= own[e / 2] &&
-                            p > own[e / 2] - a.split.window)
-                            seen |= 1u << (n * kEach + e);
+                    for (int e = 0; e < 4; ++e) {
+                        const int64_t p = p0 + e / 2, last = own(n, e & 1);
+                        if (((there >> (e / 2)) & 1u) && p <= last && p > last - a.split.window)
+                            seen |= 1u << (4 * n + e);
                         else
                             s[n][e] = -INFINITY;
                     }
             }
-            auto kept = [&](int n, int e) { return !EDGE || ((seen >> (n * kEach + e)) & 1u); };
-            // ---- weights, and weights times scales as operands
-            float p[2][4];
-            uint32_t b[NB][NG][2];
+            auto kept = [&](int n, int e) { return !EDGE || ((seen >> (4 * n + e)) & 1u); };
+            // ---- weights, and weights times scales of the values
+            float p[NB][4];
+            uint32_t b[NB][NG][2];  // rows 2 * in_quad and the next, of either position
             const unsigned char* sv = sc + NG * s_group;
             auto weights = [&]() {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         // a row that has seen no position keeps m = -inf: subtract 0
-                        const float ref = m[e / 2] == -INFINITY ? 0.0f : m[e / 2];
-                        p[n][e] = fast_exp2(MODS ? s[n][e] - ref : fmaf(s[n][e], qs[e / 2], -ref));
+                        const float at = m[n][e & 1], ref = at == -INFINITY ? 0.0f : at;
+                        p[n][e] = fast_exp2(MODS ? s[n][e] - ref
+                                                 : fmaf(s[n][e], qs[n][e & 1], -ref));
                     }
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t by = *reinterpret_cast<const uint32_t*>(sv + g * s_group);
+                    const float by0 = bf16_lo(by), by1 = bf16_hi(by);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t f =
-                            *reinterpret_cast<const uint32_t*>(sv + g * s_group + 16 * n);
+                    for (int n = 0; n < NB; ++n) {
+                        float x[4];
 #pragma unroll
-                        for (int r = 0; r < NB; ++r) {
-                            float x = p[n][2 * r] * scale_lo(f), y = p[n][2 * r + 1] * scale_hi(f);
-                            if (!kept(n, 2 * r)) x = 0.0f;  // whatever its scale holds
-                            if (!kept(n, 2 * r + 1)) y = 0.0f;
-                            b[r][g][n] = pack2<true>(x, y);
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = p[n][e] * (e < 2 ? by0 : by1);
+                            if (!kept(n, e)) x[e] = 0.0f;  // whatever its scale holds
                         }
+                        b[n][g][0] = pack2<true>(x[0], x[1]);
+                        b[n][g][1] = pack2<true>(x[2], x[3]);
                     }
+                }
             };
             weights();
-            // Does a row's reference have to rise?  (All patterns are of numbers
-            // that are not negative; a NaN's is above 2^15's.)
-            bool rises = false;
+            // Does a row's reference have to rise?  (The patterns are those of
+            // numbers that are not negative; a NaN's, and those of negative
+            // scales, are above 2^15's.)
+            uint32_t top = 0;
 #pragma unroll
-            for (int r = 0; r < NB; ++r) {
-                uint32_t top = 0;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
-                    top = __vmaxu2(top, __vmaxu2(b[r][g][0] & 0x7fff7fffu, b[r][g][1] & 0x7fff7fffu));
-                rises |= (top >> 16) > 0x7800u || (top & 0xffffu) > 0x7800u || m[r] == -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, rises)) {
-                float f[NB];
+                    top = __vmaxu2(top, __vmaxu2(b[n][g][0], b[n][g][1]));
+            if (__any_sync(0xffffffffu, !settled || __vcmpgtu2(top, 0x78007800u) != 0)) {
+                float least = INFINITY;
 #pragma unroll
-                for (int r = 0; r < NB; ++r) {
-                    // the row's largest weight times scale, in log2
-                    float top = -INFINITY;
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        // the row's largest weight times scale, in log2
+                        float most = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int h = 0; h < 2; ++h) {
                             float by = 0x1p-40f;
 #pragma unroll
                             for (int g = 0; g < NG; ++g) {
                                 const uint32_t x =
-                                    *reinterpret_cast<const uint32_t*>(sv + g * s_group + 16 * n);
-                                by = fmaxf(by, fabsf(e ? scale_hi(x) : scale_lo(x)));
+                                    *reinterpret_cast<const uint32_t*>(sv + g * s_group);
+                                by = fmaxf(by, fabsf(h ? bf16_hi(x) : bf16_lo(x)));
                             }
-                            const float x = MODS ? s[n][2 * r + e] : s[n][2 * r + e] * qs[r];
-                            if (kept(n, 2 * r + e)) top = fmaxf(top, x + __log2f(by));
+                            const float x = s[n][2 * h + e] * (MODS ? 1.0f : qs[n][e]);
+                            if (kept(n, 2 * h + e)) most = fmaxf(most, x + __log2f(by));
                         }
 #pragma unroll
-                    for (int o = 1; o < 4; o <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float next = fmaxf(m[r], top - weight_lift<true>());
-                    f[r] = next == m[r] ? 1.0f : fast_exp2(m[r] - next);
-                    m[r] = next;
-                    l[r] *= f[r];
-                }
+                        for (int o = 4; o < 32; o <<= 1)
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        const float next = fmaxf(m[n][e], most - weight_lift<true>());
+                        const float f = next == m[n][e] ? 1.0f : fast_exp2(m[n][e] - next);
+                        m[n][e] = next;
+                        least = fminf(least, next);
+                        l[n][e] *= f;
 #pragma unroll
-                for (int r = 0; r < NB; ++r) {
-                    // of rows 2 * in_quad and the next, which the sums' columns are
-                    const float f0 = __shfl_sync(0xffffffffu, f[r], 8 * in_quad);
-                    const float f1 = __shfl_sync(0xffffffffu, f[r], 8 * in_quad + 4);
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                            for (int c = 0; c < CH; ++c) {
+                                acc[n][c][0][2 * h + e] *= f;
+                                acc[n][c][1][2 * h + e] *= f;
+                            }
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            acc[r][c][0][e] *= e & 1 ? f1 : f0;
-                            acc[r][c][1][e] *= e & 1 ? f1 : f0;
+                            for (int g = 0; g < NG; ++g) less[n][g][2 * h + e] *= f;
                         }
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) less[r][g][e] *= e & 1 ? f1 : f0;
                     }
-                }
+                settled = __all_sync(0xffffffffu, least > -INFINITY);
                 weights();
             }
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) l[e / 2] += p[0][e] + p[1][e];
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[n][e] += p[n][e] + p[n][2 + e];
             // ---- O^T += V^T (P s_v)^T
             {
                 uint32_t vw[NP][4];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) ldsm4_trans(vw[i], codes + v_at[i]);
-                const uint32_t eights[4] = {kEight, kEight, kEight, kEight};
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int r = 0; r < NB; ++r)
-                        mma16816<true>(less[r][g], eights, b[r][g][0], b[r][g][1]);
+                    for (int g = 0; g < NG; ++g) {
+                        b[n][g][0] = transposed(b[n][g][0]);
+                        b[n][g][1] = transposed(b[n][g][1]);
+                        mma16816<true>(less[n][g], eights, b[n][g][0], b[n][g][1]);
+                    }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     const uint32_t x = vw[c / 2][2 * (c & 1)], y = vw[c / 2][2 * (c & 1) + 1];
@@ -632,9 +651,9 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                     const uint32_t f1[4] = {(x >> 4) & kMask, (x >> 8) & kMask, (y >> 4) & kMask,
                                             (y >> 8) & kMask};
 #pragma unroll
-                    for (int r = 0; r < NB; ++r) {
-                        mma16816<true>(acc[r][c][0], f0, b[r][c / 2][0], b[r][c / 2][1]);
-                        mma16816<true>(acc[r][c][1], f1, b[r][c / 2][0], b[r][c / 2][1]);
+                    for (int n = 0; n < NB; ++n) {
+                        mma16816<true>(acc[n][c][0], f0, b[n][c / 2][0], b[n][c / 2][1]);
+                        mma16816<true>(acc[n][c][1], f1, b[n][c / 2][0], b[n][c / 2][1]);
                     }
                 }
             }
@@ -664,14 +683,17 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
 
         // ---- the warps join, a few rows at a time
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
-            if (in_quad == 0) {
-                sm.m[warp][quad + 8 * n] = m[n];
-                sm.l[warp][quad + 8 * n] = l[n];
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+                if (quad == 0) {
+                    sm.m[warp][8 * n + 2 * in_quad + e] = m[n][e];
+                    sm.l[warp][8 * n + 2 * in_quad + e] = l[n][e];
+                }
             }
-        }
         const bool whole = w.whole();
         float* part = slot_of<Sh::kPadded>(a.workspace, blockIdx.x, w.first == 0 ? 1 : 0);
         constexpr uint32_t JR = Sh::kJoinRows, quads = D / 4;

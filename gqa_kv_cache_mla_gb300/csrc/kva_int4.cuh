@@ -55,7 +55,7 @@ inline uint16_t* int4_scales(const kvw_paged_cache_t* c, const kva_group_scales_
 // Scale of a group whose largest |value| has the fp32 pattern `top`.
 __device__ __forceinline__ uint16_t group_scale(uint32_t top) {
     if (top >= 0x7f800000u) return 0x7fffu;  // an infinity or a NaN: NaN
-    const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
+    const __nv_bfloat16 s = __float2bfloat16_rn(__fmul_rn(__uint_as_float(top), 1.0f / 7.0f));
     return *reinterpret_cast<const uint16_t*>(&s);
 }
 

@@ -230,7 +230,7 @@ typedef struct kva_group_scales {
 /*
  * kva_append_qkv_paged to a cache held in 4 bits.  With x the values of a
  * group in fp32 (a key after norm and rotation):
- *   scale = bf16(max |x| / 7)
+ *   scale = bf16(max |x| * (1 / 7))   (1 / 7 and the product rounded to fp32)
  *   code  = 8 + round_half_even(x / scale), x / scale clamped to -7 .. 7
  * (code 8 where the scale is 0).  A group that holds an infinity or a NaN
  * gets the scale NaN, so that all of it reads as NaN.  `scales` is a host

@@ -40,7 +40,8 @@ def held(x):
     d = x.shape[-1]
     pad = torch.nn.functional.pad(x, (0, -d % GROUP)).unflatten(-1, (-1, GROUP))
     top = pad.abs().amax(-1)
-    scales = torch.where(torch.isfinite(pad).all(-1), top / 7, torch.tensor(float("nan"))).bfloat16()
+    scales = torch.where(torch.isfinite(pad).all(-1), top * torch.tensor(1 / 7),
+                         torch.tensor(float("nan"))).bfloat16()
     s = by_column(scales.float(), d)
     q = torch.where(s > 0, x / s, torch.zeros_like(x)).clamp(-7, 7).round()
     return (q + 8).long(), scales
@@ -199,7 +200,7 @@ def check_held(codes, scales, y, err, what=""):
     fold = lambda x: torch.nn.functional.pad(x, (0, -d % GROUP)).unflatten(-1, (-1, GROUP))
     top, e = fold(y.abs()).amax(-1), fold(err).amax(-1)
     s = scales.double()
-    # the quotient by 7 is rounded to fp32, then to bf16 (2^-134: half its last step)
+    # the seventh is rounded to fp32 twice, then to bf16 (2^-134: half its last step)
     off = (s - top / 7).abs() - (R.HALF_STEP[R.BF16] * top / 7 * (1 + 2.0 ** -8) + e / 7 + 2.0 ** -134)
     assert float(off.max()) <= 0, "%s: scales off by %.3g more" % (what, float(off.max()))
     assert bool(((codes >= 1) & (codes <= 15)).all()), what
