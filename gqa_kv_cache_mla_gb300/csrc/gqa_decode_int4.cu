@@ -97,34 +97,45 @@ struct Shape4 {
     static constexpr int kChunks = D / 32;          // 16-byte chunks of a row of codes
     static constexpr int kPairs = (kChunks + 1) / 2;  // ldmatrix of 16 rows
     static constexpr int kGroups = (D + 63) / 64;
-    // Teams of four consumer warps, each a slice of 16 positions of a tile, and
-    // a feeding warp.  Teams take tiles in turn.
-    static constexpr int kTeams = 1;
-    static constexpr int kCtas = NB == 1 && D <= 128 ? 3 : 2;
-    static constexpr int kWarps = 4 * kTeams;
-    static constexpr int kThreads = 32 * (kWarps + 1);
+    // Four consumer warps, a slice of 16 positions of a tile each, and a feeding
+    // warp.
+    static constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
+    // Tiles of a place of the ring, which arrive and are taken together.
+    static constexpr int kTiles = NB == 1 && D <= 128 ? 2 : 1;
     static constexpr int kCodes = 2 * kTile * D / 2;             // bytes of a tile, both planes
     static constexpr int kScales = 256 * (kGroups < 2 ? 2 : kGroups);  // and of its scales
-    static constexpr int kRing = (kCtas == 3 ? 54 : 84) * 1024 / (kCodes + kScales);
+    static constexpr int kRing = 90 * 1024 / (kTiles * (kCodes + kScales));
     static constexpr int kSlots = kRing > 12 ? 12 : kRing;
     static constexpr int kPadded = D <= 64 ? 64 : D <= 128 ? 128 : 256;  // of a workspace row
     static constexpr int kQPitch = D * 2 + 16;  // eight rows on distinct banks
-    static constexpr int kQRows = 8 * NB;
+    static constexpr int kQRows = 8 * NB, kQBufs = 2;
     // rows that join at a time, four rows' stores on distinct banks
     static constexpr int kJoinPitch = D + 8;
-    static constexpr int kJoinRows = D <= 64 || kWarps == 4 ? (D == 256 ? 2 : 8) : 4;
+    static constexpr int kJoinRows = D == 256 ? 2 : 4;
     static_assert(kSlots >= 3, "shared memory");
+};
+
+// What the consumers need of a segment, from the feeding warp that walks the
+// piece: they would else keep the walk in registers that its tiles need.
+struct Segment {
+    int64_t p_first, pos0;    // position of its first tile, and of the chunk's first token
+    uint32_t count;           // tiles; 0 ends the piece
+    uint32_t t, tokens, rows, in_block, head0, block;
+    uint32_t shared_by;       // pieces that share it, where this one begins it; else 0
+    bool whole, slot1, past;  // a segment of its own; workspace place; past the page table
 };
 
 template <int D, int NB>
 struct Smem4 {
     using Sh = Shape4<D, NB>;
-    unsigned char codes[Sh::kSlots][Sh::kCodes];    // units of [K rows][V rows]
-    unsigned char scales[Sh::kSlots][Sh::kScales];  // units of [K][V][group][row]
-    unsigned char q_raw[2][Sh::kQRows * Sh::kQPitch];
+    unsigned char codes[Sh::kSlots][Sh::kTiles][Sh::kCodes];    // units of [K rows][V rows]
+    unsigned char scales[Sh::kSlots][Sh::kTiles][Sh::kScales];  // units of [K][V][group][row]
+    unsigned char q_raw[Sh::kQBufs][Sh::kQRows * Sh::kQPitch];
     float join[Sh::kWarps][Sh::kJoinRows][Sh::kJoinPitch];
-    uint64_t full[Sh::kSlots], empty[Sh::kSlots], q_full[2], q_empty[2], meet;
-    uint64_t there[Sh::kSlots];  // positions of the tile that are there
+    uint64_t full[Sh::kSlots], empty[Sh::kSlots], q_full[Sh::kQBufs], q_empty[Sh::kQBufs], meet;
+    Segment segment[Sh::kQBufs];
+    uint64_t there[Sh::kSlots][Sh::kTiles];  // positions of the tiles that are there
+    uint32_t even[Sh::kSlots];  // all positions are there, and every row sees them
     float m[Sh::kWarps][kRows], l[Sh::kWarps][kRows];
     SplitShared<Sh::kThreads> split;
     uint32_t stop;  // a wait ran out
@@ -155,20 +166,47 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
     Walk w;
     w.begin(a.split, sm.split.start);
     RingPos<Sh::kSlots> at;
-    RingPos<2> q_at;
+    RingPos<Sh::kQBufs> q_at;
     uint32_t bad_page = 0, issued = 0;
     bool ok = true;
-    while (ok && !w.done()) {
+    while (ok) {
+        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_limit);
+        if (!ok) break;
+        if (w.done()) {
+            if (lane == 0) {
+                sm.segment[q_at.slot].count = 0;
+                mbar_arrive(&sm.q_full[q_at.slot]);
+            }
+            __syncwarp();
+            q_at.step();
+            break;
+        }
         const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
         const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
         prefetch_page(maps.codes, a.page_table, a.max_pages, a.ps, w.b,
                       (int64_t)(w.span.tile0 + w.first) * kTile, lane);
-        // ---- the queries: one copy per row
-        ok = wait_phase(&sm.q_empty[q_at.slot], q_at.parity ^ 1u, &sm.stop, a.wait_limit);
-        if (!ok) break;
+        // ---- the segment, and its queries: one copy per row
         const uint32_t rows = w.span.tokens * in_block;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * D * 2);
+        if (lane == 0) {
+            Segment& x = sm.segment[q_at.slot];
+            x.p_first = (int64_t)(w.span.tile0 + w.first) * kTile;
+            x.pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
+            x.count = w.last - w.first;
+            x.t = w.t;
+            x.tokens = w.span.tokens;
+            x.rows = rows;
+            x.in_block = in_block;
+            x.head0 = kvh * a.G + hb * kRows;
+            x.block = block;
+            x.whole = w.whole();
+            x.slot1 = w.first == 0;
+            x.past = x.pos0 + w.span.tokens > a.split.cap;
+            x.shared_by = w.first == 0 && !x.whole
+                              ? sharers(a.split, sm.split.start, w, blockIdx.x / a.lanes)
+                              : 0;
+            mbar_arrive_expect_tx(&sm.q_full[q_at.slot], rows * D * 2);
+        }
         __syncwarp();
         if (lane < rows) {
             const uint32_t ct = w.span.tokens == 1 ? 0 : lane / in_block;
@@ -179,30 +217,57 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         }
         q_at.step();
         // ---- the tiles
-        auto copy = [&](uint32_t unit, uint32_t row, uint32_t page) {
+        auto copy = [&](uint32_t j, uint32_t unit, uint32_t row, uint32_t page) {
             const uint32_t bar = smem_addr(&sm.full[at.slot]);
-            tma_rows(smem_addr(sm.codes[at.slot]) + ((unit * D) << log_rows), &maps.codes.map[0], 0,
-                     row * (D / 2) / 128, kvh, page, 0, bar);
-            tma_rows(smem_addr(sm.scales[at.slot]) + unit * s_unit, &maps.scales, row, 0, kvh, page,
-                     0, bar);
+            tma_rows(smem_addr(sm.codes[at.slot][j]) + ((unit * D) << log_rows), &maps.codes.map[0],
+                     0, row * (D / 2) / 128, kvh, page, 0, bar);
+            tma_rows(smem_addr(sm.scales[at.slot][j]) + unit * s_unit, &maps.scales, row, 0, kvh,
+                     page, 0, bar);
         };
+        // positions that every row of the block sees
+        const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
+        const int64_t all_lo = pos0 + w.span.tokens - a.split.window, all_hi = pos0;
+        auto seen = [&](int64_t p, int n) { return p >= all_lo && p + n * kTile - 1 <= all_hi; };
+        constexpr int T = Sh::kTiles;
         if (log_rows == 6) {
             // a tile lies in one page: two copies, the same in every lane
             auto plan = [&](uint32_t i) {
                 return plan_page(a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
                                  (w.span.tile0 + i) * kTile, w.span.start, w.span.hi);
             };
-            PagePlan next = plan(w.first);
-            for (uint32_t i = w.first; ok && i < w.last; ++i) {
-                const PagePlan t = next;
-                if (i + 1 < w.last) next = plan(i + 1);
-                if (!t.valid) bad_page = 1;
+            PagePlan next[T];
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                if (w.first + j < w.last) next[j] = plan(w.first + j);
+            for (uint32_t i = w.first; ok && i < w.last; i += T) {
+                PagePlan t[T];
+                uint32_t bytes = 0;
+                bool all = seen((int64_t)(w.span.tile0 + i) * kTile, T);
+#pragma unroll
+                for (int j = 0; j < T; ++j) {
+                    t[j] = next[j];
+                    if (i + j >= w.last) {
+                        t[j].valid = false;
+                        t[j].there = 0;
+                    } else if (!t[j].valid) {
+                        bad_page = 1;
+                    }
+                    bytes += t[j].valid ? kTile * row_bytes : 0;
+                    all = all && t[j].there == ~0ull;
+                    if (i + T + j < w.last) next[j] = plan(i + T + j);
+                }
                 ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 if (elect_one()) {
-                    sm.there[at.slot] = t.there;
-                    mbar_arrive_expect_tx(&sm.full[at.slot], t.valid ? kTile * row_bytes : 0);
-                    if (t.valid && !(HOOK == Hook::kWithheld && issued == 0)) copy(0, t.row, t.page);
+                    sm.even[at.slot] = all;
+#pragma unroll
+                    for (int j = 0; j < T; ++j) sm.there[at.slot][j] = t[j].there;
+                    mbar_arrive_expect_tx(&sm.full[at.slot], bytes);
+                    if (!(HOOK == Hook::kWithheld && issued == 0)) {
+#pragma unroll
+                        for (int j = 0; j < T; ++j)
+                            if (t[j].valid) copy(j, 0, t[j].row, t[j].page);
+                    }
                 }
                 __syncwarp();
                 at.step();
@@ -211,20 +276,37 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             if (ok) w.next(a.split);
             continue;
         }
-        for (uint32_t i = w.first; ok && i < w.last; ++i) {
+        for (uint32_t i = w.first; ok && i < w.last; i += T) {
             const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
-            TilePlan t;
-            plan_tile(maps.codes, a.page_table, a.max_pages, a.num_pages, a.ps, w.b, p_tile,
-                      w.span.start, w.span.hi, t, bad_page);
+            TilePlan t[T];
+            uint32_t units = 0;
+            bool all = seen(p_tile, T);
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                if (i + j < w.last) {
+                    plan_tile(maps.codes, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
+                              p_tile + j * kTile, w.span.start, w.span.hi, t[j], bad_page);
+                } else {
+                    t[j].n = t[j].t_lo = t[j].t_hi = 0;
+                    t[j].copy[0].level = 4;
+                }
+                units += t[j].n;
+                all = all && (t[j].t_lo & t[j].t_hi) == ~0u;
+            }
             ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
             if (lane == 0) {
-                sm.there[at.slot] = ((uint64_t)t.t_hi << 32) | t.t_lo;
-                mbar_arrive_expect_tx(&sm.full[at.slot], (t.n << log_rows) * row_bytes);
+                sm.even[at.slot] = all;
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+                    sm.there[at.slot][j] = ((uint64_t)t[j].t_hi << 32) | t[j].t_lo;
+                mbar_arrive_expect_tx(&sm.full[at.slot], (units << log_rows) * row_bytes);
             }
             __syncwarp();
-            if (!(HOOK == Hook::kWithheld && issued == 0) && t.copy[0].level != 4)
-                copy(lane, t.copy[0].row, t.copy[0].page);
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                if (!(HOOK == Hook::kWithheld && issued == 0) && t[j].copy[0].level != 4)
+                    copy(j, lane, t[j].copy[0].row, t[j].copy[0].page);
             __syncwarp();
             at.step();
             ++issued;
@@ -241,7 +323,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         leave_phase<HOOK>(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1u, a.wait_limit,
                           a.err_flags);
     }
-    for (uint32_t i = 0; i < 2; ++i)
+    for (uint32_t i = 0; i < (uint32_t)Sh::kQBufs; ++i)
         leave_phase<HOOK>(&sm.q_full[i], q_at.parity ^ (i < q_at.slot ? 0u : 1u), a.wait_limit,
                           a.err_flags);
 }
@@ -265,7 +347,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 template <int D, int NB, bool MODS, Hook HOOK>
-__global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
+__global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
     gqa_int4_kernel(const GqaArgs a, const __grid_constant__ Int4Maps maps) {
     using Sh = Shape4<D, NB>;
     constexpr int CH = Sh::kChunks, NP = Sh::kPairs, NG = Sh::kGroups, W = Sh::kWarps;
@@ -282,7 +364,7 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < Sh::kQBufs; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], W);
         }
@@ -305,10 +387,10 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
         return;
     }
 
-    const uint32_t quad = lane >> 2, in_quad = lane & 3u, slice = warp & 3u, team = warp >> 2;
+    const uint32_t quad = lane >> 2, in_quad = lane & 3u, slice = warp;
     RingPos<Sh::kSlots> at;
-    RingPos<2> q_at;
-    uint32_t meet_parity = 0, turn = 0;  // tiles before the present one, modulo the teams
+    RingPos<Sh::kQBufs> q_at;
+    uint32_t meet_parity = 0;
     // the consumers meet (bounded, so that one that gave up strands nobody)
     auto meet = [&]() {
         __syncwarp();
@@ -317,6 +399,9 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
         meet_parity ^= 1u;
         return met;
     };
+    // On the pipe of multiplications, as the one of shifts and ANDs is the
+    // fullest (256 requests 291 -> 280 us); the factor is not known to be 16.
+    auto times16 = [&](uint32_t x) { return x * a.sixteen; };
     // ---- places of this lane's operands in a slot, the same for every tile
     const uint32_t log_rows = maps.codes.log_rows;
     const uint32_t mrow = slice * 16 + 2 * (lane & 7u) + ((lane >> 3) & 1u), mchunk = lane >> 4;
@@ -332,28 +417,19 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
     const uint32_t s_at = ((slice * 16) >> log_rows) * scale_unit(NG, log_rows) +
                           2 * (((slice * 16) & ((1u << log_rows) - 1u)) + 2 * quad);
 
-    Walk w;
-    w.begin(a.split, sm.split.start);
     bool alive = true;
     if constexpr (HOOK == Hook::kAbandoned) {
         *reinterpret_cast<volatile uint32_t*>(&sm.stop) = 1;
         alive = false;
     }
-    while (alive && !w.done()) {
-        const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
-        const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
-        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
-        const uint32_t rows = w.span.tokens * in_block;
-        const uint32_t head0 = kvh * a.G + hb * kRows;
-        const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
-        if (pos0 + w.span.tokens > a.split.cap && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
-        const uint32_t shared_by = w.first == 0 && !w.whole()
-                                       ? sharers(a.split, sm.split.start, w, blockIdx.x / a.lanes)
-                                       : 0;
-
+    while (alive) {
         // ---- queries: B operands, fp16 rows brought into range by 2^x
         alive = wait_phase(&sm.q_full[q_at.slot], q_at.parity, &sm.stop, a.wait_limit);
         if (!alive) break;
+        const Segment& seg = sm.segment[q_at.slot];
+        const uint32_t count = seg.count, rows = seg.rows;
+        if (count == 0) break;
+        if (seg.past && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
         uint32_t qf[NB][CH][2][2];  // of row quad (+ 8): step, pairs 2t and 2t + 1 of its columns
         float qs[NB][2];            // of rows 2 * in_quad and the next, whose scores the lane has
         uint32_t token = 0;         // and their tokens in the chunk, 8 bits each
@@ -384,8 +460,8 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qs[n][e] = __shfl_sync(0xffffffffu, by, 8 * in_quad + 4 * e);
-                if (w.span.tokens > 1)
-                    token |= (8 * n + 2 * in_quad + e) / in_block << (16 * n + 8 * e);
+                if (seg.tokens > 1)
+                    token |= (8 * n + 2 * in_quad + e) / seg.in_block << (16 * n + 8 * e);
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {  // columns i and i + 4 of the lane's eight
@@ -395,9 +471,6 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                 qf[n][c][1][1] = pack2<true>(bf16_hi(raw[c].y) * up, bf16_hi(raw[c].w) * up);
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_empty[q_at.slot]);
-        q_at.step();
         const uint32_t eights[4] = {kEight, kEight, kEight, kEight};
         // -8 sum of a group's queries, in units of the products
         float off[NB][NG][4];
@@ -423,13 +496,12 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                     const uint32_t r = 8 * n + 2 * in_quad + e;
                     const uint32_t ct = (token >> (16 * n + 8 * e)) & 255u;
                     slope[n][e] = a.slopes && r < rows
-                                      ? kLog2e * __ldg(a.slopes + head0 + (r - ct * in_block))
+                                      ? kLog2e * __ldg(a.slopes + seg.head0 + (r - ct * seg.in_block))
                                       : 0.0f;
                 }
         }
-        // positions every row of the block sees, and each row's own
-        const int64_t all_hi = pos0, all_lo = pos0 + w.span.tokens - a.split.window;
-        auto own = [&](int n, int e) { return pos0 + ((token >> (16 * n + 8 * e)) & 255u); };
+        // each row's own position
+        auto own = [&](int n, int e) { return seg.pos0 + ((token >> (16 * n + 8 * e)) & 255u); };
 
         float acc[NB][CH][2][4], less[NB][NG][4];  // O^T, and 8 sum (P s_v) in its units
 #pragma unroll
@@ -442,37 +514,44 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                 for (int g = 0; g < NG; ++g) less[n][g][e] = 0.0f;
             }
         }
-        float m[NB][2], l[NB][2];
+        // the rows' references and sums; a row that has seen no position has m =
+        // -inf and subtracts 0
+        float m[NB][2], ref[NB][2], l[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.0f;
+            ref[n][0] = ref[n][1] = l[n][0] = l[n][1] = 0.0f;
         }
         bool settled = false;  // every row has a reference
-        const int64_t p_first = (int64_t)(w.span.tile0 + w.first) * kTile + slice * 16;
 
-        // The warp's slice of tile k, in the slot at `at`; EDGE: positions may
-        // be missing, or seen by some rows only.
-        auto tile = [&](uint32_t k, auto edge_const) {
+        // The warp's slices of N tiles of the place at `at`, from its tile j on,
+        // tile k of the segment; EDGE: positions may be missing, or seen by some
+        // rows only.
+        auto tiles = [&](uint32_t j, uint32_t k, bool release, auto n_const, auto edge_const) {
+            constexpr int N = decltype(n_const)::value;
             constexpr bool EDGE = decltype(edge_const)::value;
-            const uint32_t codes = smem_addr(sm.codes[at.slot]);
-            const unsigned char* sc = sm.scales[at.slot] + s_at;
+            const uint32_t codes0 = smem_addr(sm.codes[at.slot][j]);
+            const unsigned char* sc0 = sm.scales[at.slot][j] + s_at;
             // ---- S^T = K Q^T
-            float s[NB][4];  // position 2 * quad: rows 2 * in_quad and the next; then the other's
-            {
+            float s[N][NB][4];  // position 2 * quad: rows 2 * in_quad and the next; then the other's
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t codes = codes0 + i * Sh::kCodes;
+                const unsigned char* sc = sc0 + i * Sh::kScales;
                 uint32_t kw[NP][4];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) ldsm4(kw[i], codes + k_at[i]);
+                for (int x = 0; x < NP; ++x) ldsm4(kw[x], codes + k_at[x]);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float x[NB][4];
 #pragma unroll
                     for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c) {
                         const uint32_t u = kw[c / 2][2 * (c & 1)], v = kw[c / 2][2 * (c & 1) + 1];
-                        const uint32_t f0[4] = {(u << 4) & kMask, (v << 4) & kMask, u & kMask,
+                        const uint32_t u8 = u >> 8, v8 = v >> 8;
+                        const uint32_t f0[4] = {times16(u) & kMask, times16(v) & kMask, u & kMask,
                                                 v & kMask};
-                        const uint32_t f1[4] = {(u >> 4) & kMask, (v >> 4) & kMask, (u >> 8) & kMask,
-                                                (v >> 8) & kMask};
+                        const uint32_t f1[4] = {times16(u8) & kMask, times16(v8) & kMask, u8 & kMask,
+                                                v8 & kMask};
 #pragma unroll
                         for (int n = 0; n < NB; ++n) {
                             if (c == 2 * g)
@@ -489,27 +568,27 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float f = e < 2 ? by0 : by1;
-                            s[n][e] = g == 0 ? f * x[n][e] : fmaf(f, x[n][e], s[n][e]);
+                            s[i][n][e] = g == 0 ? f * x[n][e] : fmaf(f, x[n][e], s[i][n][e]);
                         }
                 }
             }
             // ---- cap, distance bias, mask
-            [[maybe_unused]] const int64_t p0 = p_first + (int64_t)k * kTile + 2 * quad;
+            [[maybe_unused]] const int64_t p0 =
+                seg.p_first + (int64_t)k * kTile + slice * 16 + 2 * quad;
             if constexpr (MODS) {  // into units of log2
                 if (a.softcap > 0.0f) {
                     // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd
                     // series where that loses small scores
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float u = s[n][e] * qs[n][e & 1], v = u * u;
+                    for (int x = 0; x < N * NB * 4; ++x) {
+                            const int i = x / (4 * NB), n = x / 4 % NB, e = x % 4;
+                            const float u = s[i][n][e] * qs[n][e & 1], v = u * u;
                             const float near = a.cap_half * u *
                                                fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3),
                                                     1.0f);
                             const float far =
                                 a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
-                            s[n][e] = fabsf(u) < kTanhNear ? near : far;
+                            s[i][n][e] = fabsf(u) < kTanhNear ? near : far;
                         }
                 }
                 if (a.slopes) {
@@ -519,19 +598,23 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                         for (int e = 0; e < 2; ++e) {
                             const float f = a.softcap > 0.0f ? 1.0f : qs[n][e];
                             const float bias = -slope[n][e] * (float)(own(n, e) - p0);
-                            s[n][e] = fmaf(s[n][e], f, bias);
-                            s[n][2 + e] = fmaf(s[n][2 + e], f, bias + slope[n][e]);
+#pragma unroll
+                            for (int i = 0; i < N; ++i) {
+                                const float more = slope[n][e] * (float)(kTile * i);
+                                s[i][n][e] = fmaf(s[i][n][e], f, bias + more);
+                                s[i][n][2 + e] = fmaf(s[i][n][2 + e], f, bias + more + slope[n][e]);
+                            }
                         }
                 } else if (!(a.softcap > 0.0f)) {
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[n][e] *= qs[n][e & 1];
+                    for (int x = 0; x < N * NB * 4; ++x)
+                        s[x / (4 * NB)][x / 4 % NB][x % 4] *= qs[x / 4 % NB][x & 1];
                 }
             }
             [[maybe_unused]] uint32_t seen = 0;  // bit 4 n + e
             if constexpr (EDGE) {
-                const uint32_t there = (uint32_t)(sm.there[at.slot] >> (slice * 16 + 2 * quad));
+                static_assert(N == 1, "edge tiles are taken one by one");
+                const uint32_t there = (uint32_t)(sm.there[at.slot][j] >> (slice * 16 + 2 * quad));
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -540,38 +623,43 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                         if (((there >> (e / 2)) & 1u) && p <= last && p > last - a.split.window)
                             seen |= 1u << (4 * n + e);
                         else
-                            s[n][e] = -INFINITY;
+                            s[0][n][e] = -INFINITY;
                     }
             }
             auto kept = [&](int n, int e) { return !EDGE || ((seen >> (4 * n + e)) & 1u); };
             // ---- weights, and weights times scales of the values
-            float p[NB][4];
-            uint32_t b[NB][NG][2];  // rows 2 * in_quad and the next, of either position
-            const unsigned char* sv = sc + NG * s_group;
+            float p[N][NB][4];
+            uint32_t b[N][NB][NG][2];  // rows 2 * in_quad and the next, of either position
+            auto value_scales = [&](int i, int g) {
+                return *reinterpret_cast<const uint32_t*>(sc0 + i * Sh::kScales +
+                                                          (NG + g) * s_group);
+            };
             auto weights = [&]() {
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int i = 0; i < N; ++i) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a row that has seen no position keeps m = -inf: subtract 0
-                        const float at = m[n][e & 1], ref = at == -INFINITY ? 0.0f : at;
-                        p[n][e] = fast_exp2(MODS ? s[n][e] - ref
-                                                 : fmaf(s[n][e], qs[n][e & 1], -ref));
-                    }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const uint32_t by = *reinterpret_cast<const uint32_t*>(sv + g * s_group);
-                    const float by0 = bf16_lo(by), by1 = bf16_hi(by);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        float x[4];
+                    for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            x[e] = p[n][e] * (e < 2 ? by0 : by1);
-                            if (!kept(n, e)) x[e] = 0.0f;  // whatever its scale holds
+                            p[i][n][e] =
+                                fast_exp2(MODS ? s[i][n][e] - ref[n][e & 1]
+                                               : fmaf(s[i][n][e], qs[n][e & 1], -ref[n][e & 1]));
                         }
-                        b[n][g][0] = pack2<true>(x[0], x[1]);
-                        b[n][g][1] = pack2<true>(x[2], x[3]);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t by = value_scales(i, g);
+                        const float by0 = bf16_lo(by), by1 = bf16_hi(by);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[e] = p[i][n][e] * (e < 2 ? by0 : by1);
+                                if (!kept(n, e)) x[e] = 0.0f;  // whatever its scale holds
+                            }
+                            b[i][n][g][0] = pack2<true>(x[0], x[1]);
+                            b[i][n][g][1] = pack2<true>(x[2], x[3]);
+                        }
                     }
                 }
             };
@@ -581,10 +669,12 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
             // scales, are above 2^15's.)
             uint32_t top = 0;
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    top = __vmaxu2(top, __vmaxu2(b[n][g][0], b[n][g][1]));
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        top = __vmaxu2(top, __vmaxu2(b[i][n][g][0], b[i][n][g][1]));
             if (__any_sync(0xffffffffu, !settled || __vcmpgtu2(top, 0x78007800u) != 0)) {
                 float least = INFINITY;
 #pragma unroll
@@ -594,15 +684,15 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                         // the row's largest weight times scale, in log2
                         float most = -INFINITY;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int y = 0; y < 2 * N; ++y) {
+                            const int i = y / 2, h = y % 2;
                             float by = 0x1p-40f;
 #pragma unroll
                             for (int g = 0; g < NG; ++g) {
-                                const uint32_t x =
-                                    *reinterpret_cast<const uint32_t*>(sv + g * s_group);
+                                const uint32_t x = value_scales(i, g);
                                 by = fmaxf(by, fabsf(h ? bf16_hi(x) : bf16_lo(x)));
                             }
-                            const float x = s[n][2 * h + e] * (MODS ? 1.0f : qs[n][e]);
+                            const float x = s[i][n][2 * h + e] * (MODS ? 1.0f : qs[n][e]);
                             if (kept(n, 2 * h + e)) most = fmaxf(most, x + __log2f(by));
                         }
 #pragma unroll
@@ -611,6 +701,7 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                         const float next = fmaxf(m[n][e], most - weight_lift<true>());
                         const float f = next == m[n][e] ? 1.0f : fast_exp2(m[n][e] - next);
                         m[n][e] = next;
+                        ref[n][e] = next == -INFINITY ? 0.0f : next;
                         least = fminf(least, next);
                         l[n][e] *= f;
 #pragma unroll
@@ -630,54 +721,57 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) l[n][e] += p[n][e] + p[n][2 + e];
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) l[n][e] += p[i][n][e] + p[i][n][2 + e];
             // ---- O^T += V^T (P s_v)^T
-            {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
                 uint32_t vw[NP][4];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) ldsm4_trans(vw[i], codes + v_at[i]);
+                for (int x = 0; x < NP; ++x) ldsm4_trans(vw[x], codes0 + i * Sh::kCodes + v_at[x]);
+                if (i == N - 1 && release) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.empty[at.slot]);
+                }
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        b[n][g][0] = transposed(b[n][g][0]);
-                        b[n][g][1] = transposed(b[n][g][1]);
-                        mma16816<true>(less[n][g], eights, b[n][g][0], b[n][g][1]);
+                        b[i][n][g][0] = transposed(b[i][n][g][0]);
+                        b[i][n][g][1] = transposed(b[i][n][g][1]);
+                        mma16816<true>(less[n][g], eights, b[i][n][g][0], b[i][n][g][1]);
                     }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     const uint32_t x = vw[c / 2][2 * (c & 1)], y = vw[c / 2][2 * (c & 1) + 1];
-                    const uint32_t f0[4] = {(x << 4) & kMask, x & kMask, (y << 4) & kMask, y & kMask};
-                    const uint32_t f1[4] = {(x >> 4) & kMask, (x >> 8) & kMask, (y >> 4) & kMask,
-                                            (y >> 8) & kMask};
+                    const uint32_t x8 = x >> 8, y8 = y >> 8;
+                    const uint32_t f0[4] = {times16(x) & kMask, x & kMask, times16(y) & kMask,
+                                            y & kMask};
+                    const uint32_t f1[4] = {times16(x8) & kMask, x8 & kMask, times16(y8) & kMask,
+                                            y8 & kMask};
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        mma16816<true>(acc[n][c][0], f0, b[n][c / 2][0], b[n][c / 2][1]);
-                        mma16816<true>(acc[n][c][1], f1, b[n][c / 2][0], b[n][c / 2][1]);
+                        mma16816<true>(acc[n][c][0], f0, b[i][n][c / 2][0], b[i][n][c / 2][1]);
+                        mma16816<true>(acc[n][c][1], f1, b[i][n][c / 2][0], b[i][n][c / 2][1]);
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[at.slot]);
         };
-        // tiles [even0, even1) of the segment: this warp's slices are seen by
-        // every row of the block alike
-        const uint32_t count = w.last - w.first;
-        const int64_t lo_gap = all_lo - p_first, hi_gap = all_hi + 1 - 16 - p_first;
-        const uint32_t even0 = lo_gap <= 0 ? 0u : (uint32_t)((lo_gap + kTile - 1) / kTile);
-        const uint32_t even1 = hi_gap < 0 ? 0u : (uint32_t)(hi_gap / kTile) + 1;
-        for (uint32_t k = 0; k < count; ++k) {
-            if (Sh::kTeams == 1 || turn == team) {
-                alive = wait_phase(&sm.full[at.slot], at.parity, &sm.stop, a.wait_limit);
-                if (!alive) break;
-                const bool all = ((uint32_t)(sm.there[at.slot] >> (slice * 16)) & 0xffffu) == 0xffffu;
-                if (k >= even0 && k < even1 && all)
-                    tile(k, std::false_type{});
-                else
-                    tile(k, std::true_type{});
+        using One = std::integral_constant<int, 1>;
+        using All = std::integral_constant<int, Sh::kTiles>;
+        for (uint32_t k = 0; k < count; k += Sh::kTiles) {
+            alive = wait_phase(&sm.full[at.slot], at.parity, &sm.stop, a.wait_limit);
+            if (!alive) break;
+            if (sm.even[at.slot]) {
+                tiles(0, k, true, All{}, std::false_type{});
+            } else {
+                const uint32_t n = count - k < Sh::kTiles ? count - k : Sh::kTiles;
+#pragma unroll 1
+                for (uint32_t j = 0; j < n; ++j)
+                    tiles(j, k + j, j + 1 == n, One{}, std::true_type{});
             }
             at.step();
-            if (Sh::kTeams > 1 && ++turn == Sh::kTeams) turn = 0;
         }
         if (!alive) break;
 
@@ -694,8 +788,7 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                     sm.l[warp][8 * n + 2 * in_quad + e] = l[n][e];
                 }
             }
-        const bool whole = w.whole();
-        float* part = slot_of<Sh::kPadded>(a.workspace, blockIdx.x, w.first == 0 ? 1 : 0);
+        float* part = slot_of<Sh::kPadded>(a.workspace, blockIdx.x, seg.slot1 ? 1 : 0);
         constexpr uint32_t JR = Sh::kJoinRows, quads = D / 4;
 #pragma unroll
         for (uint32_t round = 0; round < 8 * NB / JR; ++round) {
@@ -736,9 +829,10 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
                     o.z += f * y.z;
                     o.w += f * y.w;
                 }
-                if (whole) {
-                    const uint32_t ct = r / in_block;
-                    const uint64_t row = (uint64_t)(w.t + ct) * a.Hq + head0 + (r - ct * in_block);
+                if (seg.whole) {
+                    const uint32_t ct = r / seg.in_block;
+                    const uint64_t row =
+                        (uint64_t)(seg.t + ct) * a.Hq + seg.head0 + (r - ct * seg.in_block);
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     uint2 y;
                     y.x = pack_bf16x2(o.x * inv, o.y * inv);
@@ -758,15 +852,17 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, Shape4<D, NB>::kCtas)
             if (!alive) break;
         }
         if (!alive) break;
-        if (shared_by && tid == 0) {
+        if (seg.shared_by && tid == 0) {
             OpenPiece x;
-            x.n = shared_by;
-            x.t = w.t;
-            x.tokens = w.span.tokens;
-            x.block = block;
+            x.n = seg.shared_by;
+            x.t = seg.t;
+            x.tokens = seg.tokens;
+            x.block = seg.block;
             *open = x;
         }
-        w.next(a.split);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[q_at.slot]);
+        q_at.step();
     }
     if (!alive && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
@@ -775,7 +871,7 @@ template <int D, int NB, bool MODS, Hook HOOK>
 cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
     using Sh = Shape4<D, NB>;
     constexpr size_t smem = sizeof(Smem4<D, NB>);
-    static_assert(smem <= (Sh::kCtas == 3 ? 75 : 113) * 1024, "shared memory of an SM");
+    static_assert(smem <= 113 * 1024, "two CTAs per SM");
     uint64_t wave = 0;
     cudaError_t e = wave_ctas<&gqa_int4_kernel<D, NB, MODS, HOOK>>(Sh::kThreads, smem, wave);
     if (e != cudaSuccess) return e;
@@ -827,6 +923,7 @@ int int4_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
                                   tma_sizes_ok(cache), true, int4_strides_ok(cache, scales));
     if (bad != KVW_OK || tot_seq_len == 0) return bad;
     a.k_scale = a.v_scale = 1.0f;
+    a.sixteen = 16;
     a.wait_limit = wait_cycles(wait_ns);
     auto run = [&](auto d) {
         constexpr int D = decltype(d)::value;

@@ -34,6 +34,7 @@ struct GqaArgs {
     uint32_t lanes;  // row blocks that CTAs of the same piece take side by side
     FastDiv ps;
     int64_t wait_limit;  // cycles
+    uint32_t sixteen;    // 16, for a kernel that wants it unknown
 };
 
 template <int DP>
