@@ -9,15 +9,20 @@
 // segment, where it is the products' first accumulator, and 8 sum (P s_v) as
 // one product per group and 16 positions.
 //
-// Codes as operands: the pattern of a code u in bits 4 to 7 of an fp16 number
-// is u 2^-20, exact, below fp16's smallest normal number.  Four codes lie in 16
-// bits, so an AND takes a pair of codes out of 32 bits after a shift: 7
-// instructions for 8 codes, against 11 to bring them to exact bf16 numbers, and
-// with an offset of 8 to cancel (the bf16 patterns 128 + u alone: 136).  The
-// instruction lines its products up as if such an operand were 2^-14, so that
-// each of its sums may be off by 2^-18 of a code more than fp32's own step (in
-// bits 0 to 3, with 5 instructions for 8 codes, by 2^-14: a column whose heavy
-// positions all hold code 8 was off by 2 % of the little that is left).
+// Codes as operands: the pattern of a code u in the lowest 4 bits of an fp16
+// number is u 2^-24, and in the next 4 it is 16 u 2^-24, both exact.  Four codes
+// lie in 16 bits, so an AND takes a pair of them out of 32 bits and one shift
+// serves two pairs: 5 instructions for 8 codes, against 11 to bring them to
+// exact bf16 numbers (and with the bf16 patterns 128 + u alone the offset to
+// cancel would be 136).  Queries that meet codes 16 times as large are 16 times
+// smaller, and output columns of such codes 16 times as large until the end.
+// The price: these numbers lie below fp16's smallest normal one, 2^-14, and the
+// instruction lines its products up as if each were that large, so it may cut a
+// product at 2^-13 of a code (in units of its other factor).  That is a 2000th
+// of the half code that the cache itself may be off, and less than the fp16
+// rounding of a weight costs a code of +-4.  Codes moved to bits 4 to 7 are cut
+// at 2^-17 and cost two more instructions in eight: 256 requests 217 us against
+// 201.
 //
 // Both products have the row block's rows as the instruction's 8 columns (one
 // or two blocks of them): S^T = K Q^T and O^T = V^T P^T.  Codes are then the
@@ -91,24 +96,24 @@ inline int encode_int4_maps(Int4Maps* m, const kvw_paged_cache_t* c, const kva_g
     return KVW_OK;
 }
 
-// D: head size; NB: blocks of 8 rows (1 or 2).
-template <int D, int NB>
+// D: head size.
+template <int D>
 struct Shape4 {
     static constexpr int kChunks = D / 32;          // 16-byte chunks of a row of codes
-    static constexpr int kPairs = (kChunks + 1) / 2;  // ldmatrix of 16 rows
     static constexpr int kGroups = (D + 63) / 64;
     // Four consumer warps, a slice of 16 positions of a tile each, and a feeding
     // warp.
     static constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);
+    static constexpr int kCtas = D <= 128 ? 3 : 2;  // of an SM
     // Tiles of a place of the ring, which arrive and are taken together.
-    static constexpr int kTiles = NB == 1 && D <= 128 ? 2 : 1;
+    static constexpr int kTiles = D <= 128 ? 2 : 1;
     static constexpr int kCodes = 2 * kTile * D / 2;             // bytes of a tile, both planes
     static constexpr int kScales = 256 * (kGroups < 2 ? 2 : kGroups);  // and of its scales
-    static constexpr int kRing = 90 * 1024 / (kTiles * (kCodes + kScales));
+    static constexpr int kRing = (D == 64 ? 56 : kCtas == 3 ? 54 : 88) * 1024 / (kTiles * (kCodes + kScales));
     static constexpr int kSlots = kRing > 12 ? 12 : kRing;
     static constexpr int kPadded = D <= 64 ? 64 : D <= 128 ? 128 : 256;  // of a workspace row
     static constexpr int kQPitch = D * 2 + 16;  // eight rows on distinct banks
-    static constexpr int kQRows = 8 * NB, kQBufs = 2;
+    static constexpr int kBlock = 8, kQBufs = 2;  // rows of a row block; places for queries
     // rows that join at a time, four rows' stores on distinct banks
     static constexpr int kJoinPitch = D + 8;
     static constexpr int kJoinRows = D == 256 ? 2 : 4;
@@ -125,12 +130,13 @@ struct Segment {
     bool whole, slot1, past;  // a segment of its own; workspace place; past the page table
 };
 
-template <int D, int NB>
+template <int D>
 struct Smem4 {
-    using Sh = Shape4<D, NB>;
+    using Sh = Shape4<D>;
     unsigned char codes[Sh::kSlots][Sh::kTiles][Sh::kCodes];    // units of [K rows][V rows]
     unsigned char scales[Sh::kSlots][Sh::kTiles][Sh::kScales];  // units of [K][V][group][row]
-    unsigned char q_raw[Sh::kQBufs][Sh::kQRows * Sh::kQPitch];
+    unsigned char q_raw[Sh::kQBufs][Sh::kBlock * Sh::kQPitch];
+    uint4 q[Sh::kChunks][32];  // the queries as operands
     float join[Sh::kWarps][Sh::kJoinRows][Sh::kJoinPitch];
     uint64_t full[Sh::kSlots], empty[Sh::kSlots], q_full[Sh::kQBufs], q_empty[Sh::kQBufs], meet;
     Segment segment[Sh::kQBufs];
@@ -158,9 +164,9 @@ __device__ __forceinline__ uint32_t code_at(uint32_t log_rows, uint32_t plane, u
 }
 
 // The feeding warp: walks the piece's tiles ahead of the arithmetic.
-template <int D, int NB, Hook HOOK>
-__device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Smem4<D, NB>& sm) {
-    using Sh = Shape4<D, NB>;
+template <int D, Hook HOOK>
+__device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Smem4<D>& sm) {
+    using Sh = Shape4<D>;
     const uint32_t lane = threadIdx.x & 31u, log_rows = maps.codes.log_rows;
     const uint32_t row_bytes = D + 4 * Sh::kGroups, s_unit = scale_unit(Sh::kGroups, log_rows);
     Walk w;
@@ -183,7 +189,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         }
         const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
         const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
-        const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+        const uint32_t in_block = a.G - hb * a.block_rows < a.per_token ? a.G - hb * a.block_rows : a.per_token;
         prefetch_page(maps.codes, a.page_table, a.max_pages, a.ps, w.b,
                       (int64_t)(w.span.tile0 + w.first) * kTile, lane);
         // ---- the segment, and its queries: one copy per row
@@ -197,7 +203,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             x.tokens = w.span.tokens;
             x.rows = rows;
             x.in_block = in_block;
-            x.head0 = kvh * a.G + hb * kRows;
+            x.head0 = kvh * a.G + hb * a.block_rows;
             x.block = block;
             x.whole = w.whole();
             x.slot1 = w.first == 0;
@@ -212,7 +218,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             const uint32_t ct = w.span.tokens == 1 ? 0 : lane / in_block;
             bulk_load(sm.q_raw[q_at.slot] + lane * Sh::kQPitch,
                       a.q + (int64_t)(w.t + ct) * a.q_stride +
-                          (int64_t)(kvh * a.G + hb * kRows + (lane - ct * in_block)) * D,
+                          (int64_t)(kvh * a.G + hb * a.block_rows + (lane - ct * in_block)) * D,
                       D * 2, &sm.q_full[q_at.slot]);
         }
         q_at.step();
@@ -346,15 +352,15 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return y;
 }
 
-template <int D, int NB, bool MODS, Hook HOOK>
-__global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
+template <int D, bool MODS, Hook HOOK>
+__global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
     gqa_int4_kernel(const GqaArgs a, const __grid_constant__ Int4Maps maps) {
-    using Sh = Shape4<D, NB>;
-    constexpr int CH = Sh::kChunks, NP = Sh::kPairs, NG = Sh::kGroups, W = Sh::kWarps;
-    constexpr uint32_t kMask = 0x00f000f0u;   // a pair of codes
-    constexpr uint32_t kEight = 0x00800080u;  // 8, as codes are
+    using Sh = Shape4<D>;
+    constexpr int CH = Sh::kChunks, NG = Sh::kGroups, W = Sh::kWarps;
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // pairs of codes
+    constexpr uint32_t kEight = 0x00080008u, kEights = 0x00800080u;  // 8, as these are
     extern __shared__ __align__(1024) unsigned char dyn[];
-    Smem4<D, NB>& sm = *reinterpret_cast<Smem4<D, NB>*>(dyn);
+    Smem4<D>& sm = *reinterpret_cast<Smem4<D>*>(dyn);
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     // the join of the pieces may be scheduled; it waits for this grid's end
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
     if (tid == Sh::kThreads - 32) {
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 4);
+            mbar_init(&sm.empty[i], W);
         }
         for (int i = 0; i < Sh::kQBufs; ++i) {
             mbar_init(&sm.q_full[i], 1);
@@ -383,11 +389,12 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
         return;
     }
     if (warp == W) {
-        feed4<D, NB, HOOK>(a, maps, sm);
+        feed4<D, HOOK>(a, maps, sm);
         return;
     }
 
-    const uint32_t quad = lane >> 2, in_quad = lane & 3u, slice = warp;
+    // `warp` is also the slice of 16 positions of every tile that the warp takes
+    const uint32_t quad = lane >> 2, in_quad = lane & 3u;
     RingPos<Sh::kSlots> at;
     RingPos<Sh::kQBufs> q_at;
     uint32_t meet_parity = 0;
@@ -399,23 +406,22 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
         meet_parity ^= 1u;
         return met;
     };
-    // On the pipe of multiplications, as the one of shifts and ANDs is the
-    // fullest (256 requests 291 -> 280 us); the factor is not known to be 16.
-    auto times16 = [&](uint32_t x) { return x * a.sixteen; };
-    // ---- places of this lane's operands in a slot, the same for every tile
+    // ---- places of this lane's operands in a tile, the same for every tile
     const uint32_t log_rows = maps.codes.log_rows;
-    const uint32_t mrow = slice * 16 + 2 * (lane & 7u) + ((lane >> 3) & 1u), mchunk = lane >> 4;
-    uint32_t k_at[NP], v_at[NP];
+    uint32_t k_at[NG], v_at[NG];  // chunks 2 g and 2 g + 1
+    {
+        const uint32_t row = warp * 16 + 2 * (lane & 7u) + ((lane >> 3) & 1u);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const uint32_t c = 2 * i + mchunk < (uint32_t)CH ? 2 * i + mchunk : 2 * i;
-        k_at[i] = code_at<D>(log_rows, 0, mrow, c);
-        v_at[i] = code_at<D>(log_rows, 1, mrow, c);
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t c = 2 * g + (lane >> 4) < (uint32_t)CH ? 2 * g + (lane >> 4) : 2 * g;
+            k_at[g] = code_at<D>(log_rows, 0, row, c);
+            v_at[g] = code_at<D>(log_rows, 1, row, c);
+        }
     }
     // scales of positions 2 * quad and the next of the slice; groups 2R bytes apart
     const uint32_t s_group = 2u << log_rows;
-    const uint32_t s_at = ((slice * 16) >> log_rows) * scale_unit(NG, log_rows) +
-                          2 * (((slice * 16) & ((1u << log_rows) - 1u)) + 2 * quad);
+    const uint32_t s_at = ((warp * 16) >> log_rows) * scale_unit(NG, log_rows) +
+                          2 * (((warp * 16) & ((1u << log_rows) - 1u)) + 2 * quad);
 
     bool alive = true;
     if constexpr (HOOK == Hook::kAbandoned) {
@@ -430,97 +436,96 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
         const uint32_t count = seg.count, rows = seg.rows;
         if (count == 0) break;
         if (seg.past && tid == 0) flag(a.err_flags, KVW_ERR_PAGE);
-        uint32_t qf[NB][CH][2][2];  // of row quad (+ 8): step, pairs 2t and 2t + 1 of its columns
-        float qs[NB][2];            // of rows 2 * in_quad and the next, whose scores the lane has
-        uint32_t token = 0;         // and their tokens in the chunk, 8 bits each
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const uint32_t r = quad + 8 * n;
-            const unsigned char* q = sm.q_raw[q_at.slot] + r * Sh::kQPitch + 16 * in_quad;
-            uint4 raw[CH];
+        // Operands of chunk c come from warp c mod 4, for all warps: in registers
+        // they would leave too few for the tiles.  (The last meeting of the segment
+        // before this one lies behind all reads of the old ones.)
+        float qs[2];         // factors of rows 2 * in_quad and the next, whose scores the lane has
+        uint32_t token = 0;  // and their tokens in the chunk, 16 bits each
+        {
+            const unsigned char* q = sm.q_raw[q_at.slot] + quad * Sh::kQPitch + 16 * in_quad;
+            auto raw = [&](uint32_t c) {  // eight columns of row quad
+                const uint4 v = *reinterpret_cast<const uint4*>(q + 64 * c);
+                return quad < rows ? v : make_uint4(0, 0, 0, 0);
+            };
             uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                raw[c] = r < rows ? *reinterpret_cast<const uint4*>(q + 64 * c)
-                                  : make_uint4(0, 0, 0, 0);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
-                                             __vmaxu2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
+                const uint4 v = raw(c);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
             }
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1)
                 top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
             float up, down;
             row_power(max(top & 0xffffu, top >> 16), up, down);
-            // products are of codes 2^-20 as large; scores in units of log2 straight
+            // products are of codes 2^-24 as large; scores in units of log2 straight
             // from the product, or 2 log2(e) / cap of them
-            float by = a.sm_scale * down * 0x1p20f;
+            float by = a.sm_scale * down * 0x1p24f;
             by *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
             // never 0, a masked score is -inf times this, and never infinite
             by = fminf(fmaxf(by, 1.17549435e-38f), 3.4028234e38f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                qs[n][e] = __shfl_sync(0xffffffffu, by, 8 * in_quad + 4 * e);
-                if (seg.tokens > 1)
-                    token |= (8 * n + 2 * in_quad + e) / seg.in_block << (16 * n + 8 * e);
+                qs[e] = __shfl_sync(0xffffffffu, by, 8 * in_quad + 4 * e);
+                if (seg.tokens > 1) token |= (2 * in_quad + e) / seg.in_block << (16 * e);
             }
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {  // columns i and i + 4 of the lane's eight
-                qf[n][c][0][0] = pack2<true>(bf16_lo(raw[c].x) * up, bf16_lo(raw[c].z) * up);
-                qf[n][c][0][1] = pack2<true>(bf16_hi(raw[c].x) * up, bf16_hi(raw[c].z) * up);
-                qf[n][c][1][0] = pack2<true>(bf16_lo(raw[c].y) * up, bf16_lo(raw[c].w) * up);
-                qf[n][c][1][1] = pack2<true>(bf16_hi(raw[c].y) * up, bf16_hi(raw[c].w) * up);
+            const float up16 = up * 0.0625f;
+#pragma unroll 1
+            for (uint32_t c = warp; c < (uint32_t)CH; c += W) {
+                const uint4 v = raw(c);
+                // columns i and i + 4 of the lane's eight, i = 0 .. 3
+                sm.q[c][lane] =
+                    make_uint4(pack2<true>(bf16_lo(v.x) * up, bf16_lo(v.z) * up),
+                               pack2<true>(bf16_hi(v.x) * up16, bf16_hi(v.z) * up16),
+                               pack2<true>(bf16_lo(v.y) * up, bf16_lo(v.w) * up),
+                               pack2<true>(bf16_hi(v.y) * up16, bf16_hi(v.w) * up16));
             }
         }
-        const uint32_t eights[4] = {kEight, kEight, kEight, kEight};
+        alive = meet();
+        if (!alive) break;
+        const uint32_t eights_k[4] = {kEight, kEight, kEights, kEights};
+        const uint32_t eights_v[4] = {kEight, kEights, kEight, kEights};
         // -8 sum of a group's queries, in units of the products
-        float off[NB][NG][4];
+        float off[NG][4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int g = 0; g < NG; ++g) {
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        mma16816<true>(x, eights, qf[n][c][t][0], qf[n][c][t][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) off[n][g][e] = -x[e];
+            for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c) {
+                const uint4 q = sm.q[c][lane];
+                mma16816<true>(x, eights_k, q.x, q.y);
+                mma16816<true>(x, eights_k, q.z, q.w);
             }
-        [[maybe_unused]] float slope[NB][2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) off[g][e] = -x[e];
+        }
+        auto token_of = [&](int e) { return (token >> (16 * e)) & 0xffffu; };
+        // distance biases of the lane's rows, and the rows' distances from its first
+        // position in tile 0 (those of positions that a row sees fit 32 bits)
+        [[maybe_unused]] float slope[2];
+        [[maybe_unused]] uint32_t far[2];
         if constexpr (MODS) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t r = 8 * n + 2 * in_quad + e;
-                    const uint32_t ct = (token >> (16 * n + 8 * e)) & 255u;
-                    slope[n][e] = a.slopes && r < rows
-                                      ? kLog2e * __ldg(a.slopes + seg.head0 + (r - ct * seg.in_block))
-                                      : 0.0f;
-                }
-        }
-        // each row's own position
-        auto own = [&](int n, int e) { return seg.pos0 + ((token >> (16 * n + 8 * e)) & 255u); };
-
-        float acc[NB][CH][2][4], less[NB][NG][4];  // O^T, and 8 sum (P s_v) in its units
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                for (int c = 0; c < CH; ++c) acc[n][c][0][e] = acc[n][c][1][e] = 0.0f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) less[n][g][e] = 0.0f;
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t r = 2 * in_quad + e;
+                far[e] = (uint32_t)(seg.pos0 + token_of(e) - seg.p_first) - warp * 16 - 2 * quad;
+                slope[e] = a.slopes && r < rows
+                               ? kLog2e * __ldg(a.slopes + seg.head0 + (r - token_of(e) * seg.in_block))
+                               : 0.0f;
             }
         }
+
+        float acc[CH][2][4], less[NG][4];  // O^T, and 8 sum (P s_v) in its units
         // the rows' references and sums; a row that has seen no position has m =
         // -inf and subtracts 0
-        float m[NB][2], ref[NB][2], l[NB][2];
+        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            ref[n][0] = ref[n][1] = l[n][0] = l[n][1] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) acc[c][0][e] = acc[c][1][e] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) less[g][e] = 0.0f;
         }
         bool settled = false;  // every row has a reference
 
@@ -530,136 +535,116 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
         auto tiles = [&](uint32_t j, uint32_t k, bool release, auto n_const, auto edge_const) {
             constexpr int N = decltype(n_const)::value;
             constexpr bool EDGE = decltype(edge_const)::value;
-            const uint32_t codes0 = smem_addr(sm.codes[at.slot][j]);
-            const unsigned char* sc0 = sm.scales[at.slot][j] + s_at;
-            // ---- S^T = K Q^T
-            float s[N][NB][4];  // position 2 * quad: rows 2 * in_quad and the next; then the other's
+            static_assert(N == 1 || !EDGE, "edge tiles are taken one by one");
+            const uint32_t codes = smem_addr(sm.codes[at.slot][j]);
+            const unsigned char* sc = sm.scales[at.slot][j] + s_at;
+            auto scales_of = [&](int i, int g) {  // of both positions; values' after the keys'
+                return *reinterpret_cast<const uint32_t*>(sc + i * Sh::kScales + g * s_group);
+            };
+            // ---- S^T = K Q^T; score e: row 2 * in_quad + e % 2, position 2 * quad + e / 2
+            float s[N][4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t codes = codes0 + i * Sh::kCodes;
-                const unsigned char* sc = sc0 + i * Sh::kScales;
-                uint32_t kw[NP][4];
+            for (int g = 0; g < NG; ++g) {
+                float x[N][4];
+                uint32_t kw[N][4];
 #pragma unroll
-                for (int x = 0; x < NP; ++x) ldsm4(kw[x], codes + k_at[x]);
+                for (int i = 0; i < N; ++i) ldsm4(kw[i], codes + i * Sh::kCodes + k_at[g]);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    float x[NB][4];
+                for (int c = 0; c < 2 && 2 * g + c < CH; ++c) {
+                    const uint4 q = sm.q[2 * g + c][lane];
 #pragma unroll
-                    for (int c = 2 * g; c < 2 * g + 2 && c < CH; ++c) {
-                        const uint32_t u = kw[c / 2][2 * (c & 1)], v = kw[c / 2][2 * (c & 1) + 1];
+                    for (int i = 0; i < N; ++i) {
+                        const uint32_t u = kw[i][2 * c], v = kw[i][2 * c + 1];
                         const uint32_t u8 = u >> 8, v8 = v >> 8;
-                        const uint32_t f0[4] = {times16(u) & kMask, times16(v) & kMask, u & kMask,
-                                                v & kMask};
-                        const uint32_t f1[4] = {times16(u8) & kMask, times16(v8) & kMask, u8 & kMask,
-                                                v8 & kMask};
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            if (c == 2 * g)
-                                mma_from(x[n], f0, qf[n][c][0][0], qf[n][c][0][1], off[n][g]);
-                            else
-                                mma16816<true>(x[n], f0, qf[n][c][0][0], qf[n][c][0][1]);
-                            mma16816<true>(x[n], f1, qf[n][c][1][0], qf[n][c][1][1]);
-                        }
+                        const uint32_t f0[4] = {u & kLow, v & kLow, u & kHigh, v & kHigh};
+                        const uint32_t f1[4] = {u8 & kLow, v8 & kLow, u8 & kHigh, v8 & kHigh};
+                        if (c == 0)
+                            mma_from(x[i], f0, q.x, q.y, off[g]);
+                        else
+                            mma16816<true>(x[i], f0, q.x, q.y);
+                        mma16816<true>(x[i], f1, q.z, q.w);
                     }
-                    const uint32_t by = *reinterpret_cast<const uint32_t*>(sc + g * s_group);
-                    const float by0 = bf16_lo(by), by1 = bf16_hi(by);
+                }
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
+                for (int i = 0; i < N; ++i) {
+                    const uint32_t by = scales_of(i, g);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float f = e < 2 ? by0 : by1;
-                            s[i][n][e] = g == 0 ? f * x[n][e] : fmaf(f, x[n][e], s[i][n][e]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = e < 2 ? bf16_lo(by) : bf16_hi(by);
+                        s[i][e] = g == 0 ? f * x[i][e] : fmaf(f, x[i][e], s[i][e]);
+                    }
                 }
             }
             // ---- cap, distance bias, mask
-            [[maybe_unused]] const int64_t p0 =
-                seg.p_first + (int64_t)k * kTile + slice * 16 + 2 * quad;
             if constexpr (MODS) {  // into units of log2
                 if (a.softcap > 0.0f) {
                     // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd
                     // series where that loses small scores
 #pragma unroll
-                    for (int x = 0; x < N * NB * 4; ++x) {
-                            const int i = x / (4 * NB), n = x / 4 % NB, e = x % 4;
-                            const float u = s[i][n][e] * qs[n][e & 1], v = u * u;
-                            const float near = a.cap_half * u *
-                                               fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3),
-                                                    1.0f);
-                            const float far =
-                                a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
-                            s[i][n][e] = fabsf(u) < kTanhNear ? near : far;
-                        }
+                    for (int x = 0; x < 4 * N; ++x) {
+                        float& y = s[x / 4][x % 4];
+                        const float u = y * qs[x & 1], v = u * u;
+                        const float near =
+                            a.cap_half * u *
+                            fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3), 1.0f);
+                        const float far =
+                            a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
+                        y = fabsf(u) < kTanhNear ? near : far;
+                    }
                 }
                 if (a.slopes) {
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = a.softcap > 0.0f ? 1.0f : qs[e];
+                        const float bias = -slope[e] * (float)(far[e] - k * kTile);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float f = a.softcap > 0.0f ? 1.0f : qs[n][e];
-                            const float bias = -slope[n][e] * (float)(own(n, e) - p0);
-#pragma unroll
-                            for (int i = 0; i < N; ++i) {
-                                const float more = slope[n][e] * (float)(kTile * i);
-                                s[i][n][e] = fmaf(s[i][n][e], f, bias + more);
-                                s[i][n][2 + e] = fmaf(s[i][n][2 + e], f, bias + more + slope[n][e]);
-                            }
+                        for (int i = 0; i < N; ++i) {
+                            const float nearer =
+                                i == 0 ? bias : fmaf(slope[e], (float)(kTile * i), bias);
+                            s[i][e] = fmaf(s[i][e], f, nearer);
+                            s[i][2 + e] = fmaf(s[i][2 + e], f, nearer + slope[e]);
                         }
+                    }
                 } else if (!(a.softcap > 0.0f)) {
 #pragma unroll
-                    for (int x = 0; x < N * NB * 4; ++x)
-                        s[x / (4 * NB)][x / 4 % NB][x % 4] *= qs[x / 4 % NB][x & 1];
+                    for (int x = 0; x < 4 * N; ++x) s[x / 4][x % 4] *= qs[x & 1];
                 }
             }
-            [[maybe_unused]] uint32_t seen = 0;  // bit 4 n + e
+            [[maybe_unused]] uint32_t seen = 0;  // bit e: score e counts
             if constexpr (EDGE) {
-                static_assert(N == 1, "edge tiles are taken one by one");
-                const uint32_t there = (uint32_t)(sm.there[at.slot][j] >> (slice * 16 + 2 * quad));
+                const int64_t p0 = seg.p_first + (int64_t)k * kTile + warp * 16 + 2 * quad;
+                const uint32_t there = (uint32_t)(sm.there[at.slot][j] >> (warp * 16 + 2 * quad));
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int64_t p = p0 + e / 2, last = own(n, e & 1);
-                        if (((there >> (e / 2)) & 1u) && p <= last && p > last - a.split.window)
-                            seen |= 1u << (4 * n + e);
-                        else
-                            s[0][n][e] = -INFINITY;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t p = p0 + e / 2, last = seg.pos0 + token_of(e & 1);
+                    if (((there >> (e / 2)) & 1u) && p <= last && p > last - a.split.window)
+                        seen |= 1u << e;
+                    else
+                        s[0][e] = -INFINITY;
+                }
             }
-            auto kept = [&](int n, int e) { return !EDGE || ((seen >> (4 * n + e)) & 1u); };
+            auto kept = [&](int e) { return !EDGE || ((seen >> e) & 1u); };
             // ---- weights, and weights times scales of the values
-            float p[N][NB][4];
-            uint32_t b[N][NB][NG][2];  // rows 2 * in_quad and the next, of either position
-            auto value_scales = [&](int i, int g) {
-                return *reinterpret_cast<const uint32_t*>(sc0 + i * Sh::kScales +
-                                                          (NG + g) * s_group);
-            };
+            float p[N][4];
+            uint32_t b[N][NG][2];  // rows 2 * in_quad and the next, of either position
             auto weights = [&]() {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[i][n][e] =
-                                fast_exp2(MODS ? s[i][n][e] - ref[n][e & 1]
-                                               : fmaf(s[i][n][e], qs[n][e & 1], -ref[n][e & 1]));
-                        }
+                    for (int e = 0; e < 4; ++e)
+                        p[i][e] = fast_exp2(MODS ? s[i][e] - ref[e & 1]
+                                                 : fmaf(s[i][e], qs[e & 1], -ref[e & 1]));
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const uint32_t by = value_scales(i, g);
-                        const float by0 = bf16_lo(by), by1 = bf16_hi(by);
+                        const uint32_t by = scales_of(i, NG + g);
+                        float x[4];
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            float x[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                x[e] = p[i][n][e] * (e < 2 ? by0 : by1);
-                                if (!kept(n, e)) x[e] = 0.0f;  // whatever its scale holds
-                            }
-                            b[i][n][g][0] = pack2<true>(x[0], x[1]);
-                            b[i][n][g][1] = pack2<true>(x[2], x[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = p[i][e] * (e < 2 ? bf16_lo(by) : bf16_hi(by));
+                            if (!kept(e)) x[e] = 0.0f;  // whatever its scale holds
                         }
+                        b[i][g][0] = pack2<true>(x[0], x[1]);
+                        b[i][g][1] = pack2<true>(x[2], x[3]);
                     }
                 }
             };
@@ -671,89 +656,74 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int g = 0; g < NG; ++g)
-                        top = __vmaxu2(top, __vmaxu2(b[i][n][g][0], b[i][n][g][1]));
+                for (int g = 0; g < NG; ++g)
+                    top = __vmaxu2(top, __vmaxu2(b[i][g][0], b[i][g][1]));
             if (__any_sync(0xffffffffu, !settled || __vcmpgtu2(top, 0x78007800u) != 0)) {
-                float least = INFINITY;
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int e = 0; e < 2; ++e) {
+                    // the row's largest weight times scale, in log2
+                    float most = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // the row's largest weight times scale, in log2
-                        float most = -INFINITY;
+                    for (int y = 0; y < 2 * N; ++y) {
+                        const int i = y / 2, h = y % 2;
+                        float by = 0x1p-40f;
 #pragma unroll
-                        for (int y = 0; y < 2 * N; ++y) {
-                            const int i = y / 2, h = y % 2;
-                            float by = 0x1p-40f;
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                const uint32_t x = value_scales(i, g);
-                                by = fmaxf(by, fabsf(h ? bf16_hi(x) : bf16_lo(x)));
-                            }
-                            const float x = s[i][n][2 * h + e] * (MODS ? 1.0f : qs[n][e]);
-                            if (kept(n, 2 * h + e)) most = fmaxf(most, x + __log2f(by));
+                        for (int g = 0; g < NG; ++g) {
+                            const uint32_t x = scales_of(i, NG + g);
+                            by = fmaxf(by, fabsf(h ? bf16_hi(x) : bf16_lo(x)));
                         }
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                        const float next = fmaxf(m[n][e], most - weight_lift<true>());
-                        const float f = next == m[n][e] ? 1.0f : fast_exp2(m[n][e] - next);
-                        m[n][e] = next;
-                        ref[n][e] = next == -INFINITY ? 0.0f : next;
-                        least = fminf(least, next);
-                        l[n][e] *= f;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int c = 0; c < CH; ++c) {
-                                acc[n][c][0][2 * h + e] *= f;
-                                acc[n][c][1][2 * h + e] *= f;
-                            }
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) less[n][g][2 * h + e] *= f;
-                        }
+                        const float x = s[i][2 * h + e] * (MODS ? 1.0f : qs[e]);
+                        if (kept(2 * h + e)) most = fmaxf(most, x + __log2f(by));
                     }
-                settled = __all_sync(0xffffffffu, least > -INFINITY);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    const float next = fmaxf(m[e], most - weight_lift<true>());
+                    const float f = next == m[e] ? 1.0f : fast_exp2(m[e] - next);
+                    m[e] = next;
+                    ref[e] = next == -INFINITY ? 0.0f : next;
+                    l[e] *= f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            acc[c][0][2 * h + e] *= f;
+                            acc[c][1][2 * h + e] *= f;
+                        }
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) less[g][2 * h + e] *= f;
+                    }
+                }
+                settled = __all_sync(0xffffffffu, fminf(m[0], m[1]) > -INFINITY);
                 weights();
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) l[n][e] += p[i][n][e] + p[i][n][2 + e];
+            for (int i = 0; i < N; ++i) {
+                l[0] += p[i][0] + p[i][2];
+                l[1] += p[i][1] + p[i][3];
+            }
             // ---- O^T += V^T (P s_v)^T
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                uint32_t vw[NP][4];
+            for (int g = 0; g < NG; ++g) {
+                uint32_t vw[N][4];
 #pragma unroll
-                for (int x = 0; x < NP; ++x) ldsm4_trans(vw[x], codes0 + i * Sh::kCodes + v_at[x]);
-                if (i == N - 1 && release) {
+                for (int i = 0; i < N; ++i) ldsm4_trans(vw[i], codes + i * Sh::kCodes + v_at[g]);
+                if (g == NG - 1 && release) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.empty[at.slot]);
                 }
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int i = 0; i < N; ++i) {
+                    const uint32_t b0 = transposed(b[i][g][0]), b1 = transposed(b[i][g][1]);
+                    mma16816<true>(less[g], eights_v, b0, b1);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        b[i][n][g][0] = transposed(b[i][n][g][0]);
-                        b[i][n][g][1] = transposed(b[i][n][g][1]);
-                        mma16816<true>(less[n][g], eights, b[i][n][g][0], b[i][n][g][1]);
-                    }
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const uint32_t x = vw[c / 2][2 * (c & 1)], y = vw[c / 2][2 * (c & 1) + 1];
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-                    const uint32_t f0[4] = {times16(x) & kMask, x & kMask, times16(y) & kMask,
-                                            y & kMask};
-                    const uint32_t f1[4] = {times16(x8) & kMask, x8 & kMask, times16(y8) & kMask,
-                                            y8 & kMask};
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        mma16816<true>(acc[n][c][0], f0, b[i][n][c / 2][0], b[i][n][c / 2][1]);
-                        mma16816<true>(acc[n][c][1], f1, b[i][n][c / 2][0], b[i][n][c / 2][1]);
+                    for (int c = 0; c < 2 && 2 * g + c < CH; ++c) {
+                        const uint32_t x = vw[i][2 * c], y = vw[i][2 * c + 1];
+                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t f0[4] = {x & kLow, x & kHigh, y & kLow, y & kHigh};
+                        const uint32_t f1[4] = {x8 & kLow, x8 & kHigh, y8 & kLow, y8 & kHigh};
+                        mma16816<true>(acc[2 * g + c][0], f0, b0, b1);
+                        mma16816<true>(acc[2 * g + c][1], f1, b0, b1);
                     }
                 }
             }
@@ -777,37 +747,32 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
 
         // ---- the warps join, a few rows at a time
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-                if (quad == 0) {
-                    sm.m[warp][8 * n + 2 * in_quad + e] = m[n][e];
-                    sm.l[warp][8 * n + 2 * in_quad + e] = l[n][e];
-                }
+            for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
+            if (quad == 0) {
+                sm.m[warp][2 * in_quad + e] = m[e];
+                sm.l[warp][2 * in_quad + e] = l[e];
             }
+        }
         float* part = slot_of<Sh::kPadded>(a.workspace, blockIdx.x, seg.slot1 ? 1 : 0);
         constexpr uint32_t JR = Sh::kJoinRows, quads = D / 4;
 #pragma unroll
-        for (uint32_t round = 0; round < 8 * NB / JR; ++round) {
+        for (uint32_t round = 0; round < Sh::kBlock / JR; ++round) {
             if (round * JR >= rows) break;
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t r = 2 * in_quad + e;
+                if (r / JR != round) continue;
+                float* mine = sm.join[warp][r % JR] + 4 * quad;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t r = 8 * n + 2 * in_quad + e;
-                    if (r / JR != round) continue;
-                    float* mine = sm.join[warp][r % JR] + 4 * quad;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const float off8 = less[n][c / 2][e];
-                        *reinterpret_cast<float4*>(mine + 32 * c) = make_float4(
-                            (acc[n][c][0][e] - off8) * 0x1p20f, (acc[n][c][0][2 + e] - off8) * 0x1p20f,
-                            (acc[n][c][1][e] - off8) * 0x1p20f, (acc[n][c][1][2 + e] - off8) * 0x1p20f);
-                    }
+                for (int c = 0; c < CH; ++c) {
+                    const float lo = less[c / 2][e], hi = less[c / 2][2 + e];
+                    *reinterpret_cast<float4*>(mine + 32 * c) = make_float4(
+                        (acc[c][0][e] - lo) * 0x1p24f, (acc[c][0][2 + e] - hi) * 0x1p20f,
+                        (acc[c][1][e] - lo) * 0x1p24f, (acc[c][1][2 + e] - hi) * 0x1p20f);
                 }
+            }
             alive = meet();
             if (!alive) break;
             const uint32_t here = rows - round * JR < JR ? rows - round * JR : JR;
@@ -867,17 +832,21 @@ __global__ void __launch_bounds__(Shape4<D, NB>::kThreads, 2)
     if (!alive && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
 
-template <int D, int NB, bool MODS, Hook HOOK>
+template <int D, bool MODS, Hook HOOK>
 cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
-    using Sh = Shape4<D, NB>;
-    constexpr size_t smem = sizeof(Smem4<D, NB>);
-    static_assert(smem <= 113 * 1024, "two CTAs per SM");
+    using Sh = Shape4<D>;
+    constexpr size_t smem = sizeof(Smem4<D>);
+    static_assert(smem <= (Sh::kCtas == 3 ? 75 : 113) * 1024, "shared memory of an SM");
     uint64_t wave = 0;
-    cudaError_t e = wave_ctas<&gqa_int4_kernel<D, NB, MODS, HOOK>>(Sh::kThreads, smem, wave);
+    cudaError_t e = wave_ctas<&gqa_int4_kernel<D, MODS, HOOK>>(Sh::kThreads, smem, wave);
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
+    // A call of few row blocks is short unless its contexts are very long: two
+    // CTAs per SM leave the join's blocks room to wait beside them (one token over
+    // 901 positions 12.0 -> 9.7 us; one over 65536: 25.3 either way).
+    if (Sh::kCtas == 3 && (uint64_t)a.split.T * a.split.blocks <= 16) wave -= wave / 3;
     const uint32_t ctas = side_by_side(a, wave);
-    e = launch_early(&gqa_int4_kernel<D, NB, MODS, HOOK>, dim3(ctas), Sh::kThreads, smem, stream, a,
+    e = launch_early(&gqa_int4_kernel<D, MODS, HOOK>, dim3(ctas), Sh::kThreads, smem, stream, a,
                      maps);
     if (e != cudaSuccess) return e;
     return launch_join<Sh::kPadded>(a, ctas, stream);
@@ -889,11 +858,9 @@ int launch(GqaArgs& a, const kvw_paged_cache_t* cache, const kva_group_scales_t*
     Int4Maps maps;
     const int st = encode_int4_maps(&maps, cache, scales, layer_idx);
     if (st != KVW_OK) return st;
-    const bool mods = a.softcap > 0.0f || a.slopes, high = (a.per_token << a.split.log_c) > 8;
-    const cudaError_t e = mods ? (high ? launch_as<D, 2, true, HOOK>(a, maps, stream)
-                                       : launch_as<D, 1, true, HOOK>(a, maps, stream))
-                          : high ? launch_as<D, 2, false, HOOK>(a, maps, stream)
-                                 : launch_as<D, 1, false, HOOK>(a, maps, stream);
+    const cudaError_t e = a.softcap > 0.0f || a.slopes
+                              ? launch_as<D, true, HOOK>(a, maps, stream)
+                              : launch_as<D, false, HOOK>(a, maps, stream);
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
@@ -920,10 +887,10 @@ int int4_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
     const int bad = gqa_arguments(a, out, lse, q, q_row_stride, input_row_offsets, num_batches,
                                   tot_seq_len, num_q_heads, cache, sm_scale, softcap, window,
                                   alibi_slopes, workspace, workspace_bytes, err_flags,
-                                  tma_sizes_ok(cache), true, int4_strides_ok(cache, scales));
+                                  tma_sizes_ok(cache), true, int4_strides_ok(cache, scales),
+                                  8);
     if (bad != KVW_OK || tot_seq_len == 0) return bad;
     a.k_scale = a.v_scale = 1.0f;
-    a.sixteen = 16;
     a.wait_limit = wait_cycles(wait_ns);
     auto run = [&](auto d) {
         constexpr int D = decltype(d)::value;

@@ -9,7 +9,7 @@
 namespace kvw {
 namespace {
 
-constexpr int kRows = 16;                   // rows of a row block
+constexpr int kRows = 16;                   // rows of a row block, at most
 // tanh y for u = 2 log2(e) y: the series' coefficients in u^2, and u at y = 1/4
 constexpr float kHalfLn2 = 0.5f * kLn2, kTanh3 = kHalfLn2 * kHalfLn2 / 3.0f;
 constexpr float kTanh5 = 2.0f / 15.0f * kHalfLn2 * kHalfLn2 * kHalfLn2 * kHalfLn2;
@@ -29,12 +29,12 @@ struct GqaArgs {
     float sm_scale, k_scale, v_scale;
     float softcap, cap_factor, cap_half;  // in units of log2; 2 log2(e) / the cap; half the cap
     uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
-    uint32_t per_token;     // rows of a token in a row block: G, or 16 with several blocks
+    uint32_t block_rows;    // rows of a row block: kRows, or 8
+    uint32_t per_token;     // rows of a token in a row block: G, or block_rows with several blocks
     uint32_t num_pages, max_pages, pieces;
     uint32_t lanes;  // row blocks that CTAs of the same piece take side by side
     FastDiv ps;
     int64_t wait_limit;  // cycles
-    uint32_t sixteen;    // 16, for a kernel that wants it unknown
 };
 
 template <int DP>
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const uint32_t n = open.n, kvh = a.HB == 1 ? open.block : open.block / a.HB;
     const uint32_t hb = open.block - kvh * a.HB;
-    const uint32_t in_block = a.G - hb * kRows < a.per_token ? a.G - hb * kRows : a.per_token;
+    const uint32_t in_block = a.G - hb * a.block_rows < a.per_token ? a.G - hb * a.block_rows : a.per_token;
     // the rows r0 .. r0 + rows - 1 of this block
     const uint32_t every = open.tokens * in_block, share = (every + gridDim.y - 1) / gridDim.y;
     const uint32_t r0 = blockIdx.y * share;
     if (r0 >= every) return;
     const uint32_t rows = every - r0 < share ? every - r0 : share;
-    const uint32_t head0 = kvh * a.G + hb * kRows;
+    const uint32_t head0 = kvh * a.G + hb * a.block_rows;
     auto part = [&](uint32_t i) { return slot_of<DP>(a.workspace, c0 + i * a.lanes, i == 0 ? 1 : 0); };
 
     for (uint32_t r = warp; r < rows; r += kJoinThreads / 32) {
@@ -228,7 +228,7 @@ inline int gqa_arguments(GqaArgs& a, void* out, float* lse, const void* q, int64
                          const kvw_paged_cache_t* cache, float sm_scale, float softcap,
                          uint32_t window, const float* alibi_slopes, void* workspace,
                          uint64_t workspace_bytes, uint32_t* err_flags, bool sizes_ok,
-                         bool values_ok, bool strides_ok) {
+                         bool values_ok, bool strides_ok, uint32_t block_rows = kRows) {
     const uint32_t D = cache->head_size, Hk = cache->num_heads;
     uint64_t need = 0;
     const int ws = workspace_bytes_for(num_q_heads, Hk, D, &need);
@@ -254,13 +254,14 @@ inline int gqa_arguments(GqaArgs& a, void* out, float* lse, const void* q, int64
     a.split.B = num_batches;
     a.split.T = tot_seq_len;
     a.G = num_q_heads / Hk;
-    a.HB = (a.G + kRows - 1) / kRows;
+    a.block_rows = block_rows;
+    a.HB = (a.G + block_rows - 1) / block_rows;
     a.split.blocks = Hk * a.HB;
-    a.per_token = a.HB == 1 ? a.G : kRows;
-    // tokens of a chunk: as many as fit the 16 rows (a power of two), or 8
+    a.per_token = a.HB == 1 ? a.G : block_rows;
+    // tokens of a chunk: as many as fit the rows (a power of two), or 8 of 16
     // where that holds the average request's (any number of tokens is right)
     const uint64_t per_request = ((uint64_t)tot_seq_len + num_batches - 1) / num_batches;
-    const uint32_t fit = per_request * a.G <= 8 ? 8 : kRows;
+    const uint32_t fit = per_request * a.G <= 8 ? 8 : block_rows;
     while (a.HB == 1 && (2u << a.split.log_c) * a.G <= fit) ++a.split.log_c;
     a.split.min_units = 1;
     a.split.overhead = 3;  // a segment's cost beside its tiles, in tiles (1 to 5: within 2 %)

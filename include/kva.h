@@ -277,10 +277,10 @@ int kva_gather_kv_int4(void* k_out, void* v_out, int64_t out_row_stride,
  * (kva_gqa_decode_workspace), limits, flags and errors.  Scores, softmax
  * statistics and sums are fp32.  The products take fp16 operands: codes are
  * exact; a query row is brought into fp16's range by a power of two, which
- * loses only what is below 2^-39 of the row's largest value; a weight times
+ * loses only what is below 2^-35 of the row's largest value; a weight times
  * its value's scale is off by 2^-11 of itself or, for small ones, by 2^-34 of
  * the row's largest.  Products of 16 columns (of 16 positions) are added up by
- * one matrix instruction, which may cut each at 2^-17 of a code times the
+ * one matrix instruction, which may cut each at 2^-13 of a code times the
  * largest query value (weight times scale) beside fp32's own rounding.
  * Strides as kva_gqa_decode_paged for codes and scales.
  */

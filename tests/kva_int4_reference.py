@@ -142,11 +142,12 @@ def gqa(c, q, sm_scale, softcap=0.0, window=0, slopes=None):
 
     A matrix instruction lines 16 products and the sum before them up at the
     largest exponent and may cut each of the 17 at 2^-23 of that.  A code u is
-    the fp16 number u 2^-20 there, below the smallest normal number 2^-14,
-    whose exponent it is taken with: the cut is at 2^-23 2^-14 2^20 = 2^-17 of
-    a code, times the other operand's power of two (its largest value).  A
-    score is d / 16 instructions, and d / 16 for its offset; an output n / 16
-    full ones and one for each of the eight warps and its offset."""
+    the fp16 number u 2^-24 there (16 u 2^-24 for every other one), below the
+    smallest normal number 2^-14, whose exponent it is taken with: the cut is at
+    2^-23 2^-14 2^24 = 2^-13 of a code, times the other operand's power of two
+    (its largest value).
+    A score is d / 16 instructions, and d / 16 for its offset; an output
+    n / 16 full ones and one for each of the eight warps and its offset."""
     hq, d, hk = q.shape[1], c.head, c.kv_heads
     g = hq // hk
     outs = [torch.zeros(c.T, hq, d, dtype=torch.float64), torch.zeros(c.T, hq, dtype=torch.float64),
@@ -173,7 +174,7 @@ def gqa(c, q, sm_scale, softcap=0.0, window=0, slopes=None):
             if slopes is not None:
                 x = x - float(slopes[h]) * (pos - idx).double()
                 size = size + float(slopes[h]) * (pos + 1)
-            cut = 17 * 2.0 ** -17
+            cut = 17 * 2.0 ** -13
             ds = d * 2.0 ** -24 * float(size.max()) + 2.0 ** -20 + \
                 cut * d / 8 * float(qh.abs().max() * sk.abs().max()) * sm_scale
             top = x.max()

@@ -65,6 +65,11 @@ class Call:
         assert int(self.flags) == flags
         R.check(self.out, out, to, "out")
         R.check(self.lse, lse, tl, "lse")
+        # The cuts of the products bound an element loosely.  Of the whole, the
+        # result's rounding is 2^-8 at most, a weight's 2^-11, and 17 cuts of 2^-13
+        # of a code in one direction, on values of a code and more, 2^-9.
+        if float(out.norm()):
+            R.check_norm(self.out, out, 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -9, "out")
         assert torch.equal(self.keep[0].cpu(), c.code_store)
         assert torch.equal(self.keep[1].cpu().view(torch.int16), c.scale_store.view(torch.int16))
         return out
