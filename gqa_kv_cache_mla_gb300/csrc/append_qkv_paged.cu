@@ -29,7 +29,10 @@
 // per SM (80 registers, a few scalars spilled) against two and four (64
 // registers): bf16 130, 131, 138 us; E4M3 133, 151, 129 us; with norms 133,
 // 142, 190 us.  One pass ahead instead of two: 134, 140 and 136 us; the next
-// item's first rows loaded before an item ends: 143, 154, 146 us (spills).  One
+// item's first rows loaded before an item ends: 143, 154, 146 us (spills).  A
+// cache in 4 bits (683 MB) has more to compute between load and store: four CTAs
+// and one pass ahead 123 us, 83 % of the copy rate (half-split 134, with norms
+// 162); three CTAs 134 (140, 157), three and two passes 153, two and two 138.  One
 // token: 2.3 us on the device.  With few rows a token (4 + 2 x 1 heads of 96)
 // the lookups of a token are most of its work: 46 k tokens 58 us, a quarter of
 // the copy rate.
@@ -80,12 +83,12 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
 }
 
 template <int TL, bool INTERLEAVED, Held HELD, bool MROPE>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, HELD == Held::kInt4 ? 4 : 3) append_kernel(const AppendArgs a) {
     extern __shared__ uint32_t s_tables[];
     uint32_t* s_off = s_tables;
     uint32_t* s_clen = s_tables + a.B + 1;
     constexpr uint32_t kTeams = 32 / TL;
-    constexpr int kAhead = 2;
+    constexpr int kAhead = HELD == Held::kInt4 ? 1 : 2;
     const uint32_t lane = threadIdx.x & 31u, team = lane / TL, j = lane % TL;
     const uint32_t half = a.rope / 16;  // lanes whose pairs turn
     const bool active = j < a.D / 16;

@@ -9,11 +9,13 @@
 //
 // Bound: HBM, and of it the writes: 16 bits a value against 4.25 read.
 //
-// Layout: a warp takes 16 rows of the output (of any requests) and some of the
-// (plane, head) pairs.  Lanes 0 to 15 find a row's request, page and place
-// each, once for all pairs.  Then a lane takes words of 8 codes in row order,
-// so that a load instruction covers whole rows of codes (512 bytes of 8 rows
-// for heads of 128 in four of them) and a store 512 contiguous bytes.
+// Layout: a warp takes 16 rows of the output (8 of 256-wide heads; of any
+// requests) and some of the (plane, head) pairs.  One lane a row finds its
+// request, page and place, once for all pairs; the places wait in shared memory,
+// as registers they would halve the warps of an SM.  Then a lane takes words of
+// 8 codes in row order, so that a load instruction covers whole rows of codes
+// (two for heads of 128) and a store 512 contiguous bytes.  The next pair's
+// words are loaded before a pair's values are stored.
 #include <cstdint>
 
 #include "kva_int4.cuh"
@@ -23,7 +25,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kItemRows = 16;
 
 struct GatherArgs {
     uint16_t* out[2];
@@ -58,11 +59,27 @@ __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t s2) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
+constexpr uint32_t item_rows() {
+    return D == 256 ? 8 : 16;
+}
+
+// Where a row's codes (bytes) and scales (elements) begin in a plane and head;
+// codes below 0: nowhere.
+struct __align__(16) RowPlace {
+    int64_t codes, scales;
+};
+
+// CTAs of an SM: as many as leave the words of two pairs in registers (24 x
+// 16 k rows of 8 heads of 128: three CTAs 441 us, two 337; the same of heads of
+// 64, pages of 16: two 237, three 182, four 171).
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) gather_kernel(const GatherArgs a) {
     extern __shared__ uint32_t s_off[];
-    constexpr uint32_t W = D / 8;              // words of a row
-    constexpr int kEach = kItemRows * W / 32;  // words of a lane
+    constexpr uint32_t R = item_rows<D>(), W = D / 8;  // rows of an item; words of a row
+    constexpr int kEach = R * W / 32;                  // words of a lane
+    __shared__ RowPlace s_place[kWarps][R];
     const uint32_t lane = threadIdx.x & 31u, warps = gridDim.x * kWarps;
+    RowPlace* place = s_place[threadIdx.x >> 5];
     wait_for_stream();
     int ok = 1;
     for (uint32_t i = threadIdx.x; i <= a.B; i += kThreads) {
@@ -78,61 +95,70 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
     }
     for (uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.items; item += warps) {
         const uint32_t block = fast_div(item, a.chunk_div), chunk = item - block * a.chunks;
-        const uint32_t r0 = block * kItemRows;
+        const uint32_t r0 = block * R;
         // ---- lane i: where row r0 + i is
-        int64_t codes = -1, scales = 0;
-        if (lane < kItemRows && r0 + lane < a.rows) {
-            const uint32_t b = find_request(s_off, a.B, r0 + lane);
-            const uint64_t pos = (uint64_t)(a.first ? __ldg(a.first + b) : 0u) +
-                                 (r0 + lane - s_off[b]);
-            if (pos >> 32 == 0) {
-                const uint32_t idx = fast_div((uint32_t)pos, a.ps);
-                const uint32_t row = (uint32_t)pos - idx * a.ps.d;
-                const uint32_t page = idx < a.max_pages
-                                          ? __ldg(a.page_table + (uint64_t)b * a.max_pages + idx)
-                                          : KVW_PAGE_UNMAPPED;
-                if (page < a.num_pages) {
-                    codes = (int64_t)page * a.s_page + (int64_t)row * (D / 2);
-                    scales = (int64_t)page * a.sc_page + row;
+        if (lane < R) {
+            RowPlace x = {-1, 0};
+            if (r0 + lane < a.rows) {
+                const uint32_t b = find_request(s_off, a.B, r0 + lane);
+                const uint64_t pos = (uint64_t)(a.first ? __ldg(a.first + b) : 0u) +
+                                     (r0 + lane - s_off[b]);
+                if (pos >> 32 == 0) {
+                    const uint32_t idx = fast_div((uint32_t)pos, a.ps);
+                    const uint32_t row = (uint32_t)pos - idx * a.ps.d;
+                    const uint32_t page = idx < a.max_pages
+                                              ? __ldg(a.page_table + (uint64_t)b * a.max_pages + idx)
+                                              : KVW_PAGE_UNMAPPED;
+                    if (page < a.num_pages) {
+                        x.codes = (int64_t)page * a.s_page + (int64_t)row * (D / 2);
+                        x.scales = (int64_t)page * a.sc_page + row;
+                    }
                 }
+                if (x.codes < 0 && chunk == 0) flag(a.err_flags, KVW_ERR_PAGE);
             }
-            if (codes < 0 && chunk == 0) flag(a.err_flags, KVW_ERR_PAGE);
+            place[lane] = x;
         }
-        // ---- the lane's words: row r0 + e / W, word e % W of it
-        int64_t at[kEach], sc_at[kEach];
-        bool there[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const uint32_t e = lane + 32u * k, r = e / W, w = e - r * W;
-            const int64_t c = __shfl_sync(0xffffffffu, codes, r);
-            sc_at[k] = __shfl_sync(0xffffffffu, scales, r) + (int64_t)(w / (kGroup / 8)) * a.ps.d;
-            there[k] = c >= 0;
-            at[k] = c + 4 * w;
-        }
-        const uint32_t p1 = min((chunk + 1) * a.pairs, a.planes * a.Hk);
-#pragma unroll 1
-        for (uint32_t p = chunk * a.pairs; p < p1; ++p) {
+        __syncwarp();
+        // word k of the lane: word e % W of row r0 + e / W, e = lane + 32 k
+        auto load = [&](uint32_t p, uint32_t (&word)[kEach], uint32_t (&scale)[kEach]) {
             const uint32_t second = p >= a.Hk, plane = a.plane0 + second, h = p - second * a.Hk;
             const unsigned char* src = a.codes[plane] + (int64_t)h * a.s_head;
             const uint16_t* sc = a.scales[plane] + (int64_t)h * a.sc_head;
-            uint16_t* dst = a.out[plane] + (int64_t)r0 * a.out_stride + (int64_t)h * D;
-            uint32_t word[kEach], s2[kEach];
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                word[k] = s2[k] = 0;
-                if (there[k]) {
-                    word[k] = __ldcs(reinterpret_cast<const uint32_t*>(src + at[k]));
-                    s2[k] = __ldg(sc + sc_at[k]);
-                }
-            }
 #pragma unroll
             for (int k = 0; k < kEach; ++k) {
                 const uint32_t e = lane + 32u * k, r = e / W, w = e - r * W;
-                if (there[k])
+                const RowPlace x = place[r];
+                word[k] = scale[k] = 0;
+                if (x.codes >= 0) {
+                    word[k] = __ldcs(reinterpret_cast<const uint32_t*>(src + x.codes + 4 * w));
+                    scale[k] = __ldg(sc + x.scales + (int64_t)(w / (kGroup / 8)) * a.ps.d);
+                }
+            }
+        };
+        auto store = [&](uint32_t p, const uint32_t (&word)[kEach], const uint32_t (&scale)[kEach]) {
+            const uint32_t second = p >= a.Hk, plane = a.plane0 + second, h = p - second * a.Hk;
+            uint16_t* dst = a.out[plane] + (int64_t)r0 * a.out_stride + (int64_t)h * D;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const uint32_t e = lane + 32u * k, r = e / W, w = e - r * W;
+                if (place[r].codes >= 0)
                     st_stream(reinterpret_cast<uint4*>(dst + (int64_t)r * a.out_stride + 8 * w),
-                              values_of(word[k], s2[k] * 0x10001u));
+                              values_of(word[k], scale[k] * 0x10001u));
+            }
+        };
+        const uint32_t p1 = min((chunk + 1) * a.pairs, a.planes * a.Hk);
+        uint32_t w0[kEach], s0[kEach], w1[kEach], s1[kEach];
+        load(chunk * a.pairs, w0, s0);
+#pragma unroll 1
+        for (uint32_t p = chunk * a.pairs; p < p1; p += 2) {
+            if (p + 1 < p1) load(p + 1, w1, s1);
+            store(p, w0, s0);
+            if (p + 1 < p1) {
+                if (p + 2 < p1) load(p + 2, w0, s0);
+                store(p + 1, w1, s1);
             }
         }
+        __syncwarp();  // the places are read until here
     }
 }
 
@@ -144,7 +170,8 @@ cudaError_t launch(GatherArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
     // Pairs of an item: as many as leave every resident warp four items.
-    const uint32_t blocks = (a.rows + kItemRows - 1) / kItemRows, all = a.planes * a.Hk;
+    constexpr uint32_t R = item_rows<D>();
+    const uint32_t blocks = (a.rows + R - 1) / R, all = a.planes * a.Hk;
     const uint64_t want = 4 * wave * kWarps;
     uint64_t chunks = (want + blocks - 1) / blocks;
     if (chunks > all) chunks = all;
