@@ -263,7 +263,8 @@ int kva_append_qkv_int4(void* q_out, int64_t q_out_row_stride, const void* qkv,
  *                    written)
  *   first_positions  device, uint32 [num_batches], or NULL
  * cache_lengths of the descriptor is not read (but checked as a pointer).  A
- * row without a valid page is not written (KVW_ERR_PAGE).  total_rows <= 2^31.
+ * row without a valid page is not written (KVW_ERR_PAGE).  total_rows <= 2^31
+ * and num_heads <= 2048.
  */
 int kva_gather_kv_int4(void* k_out, void* v_out, int64_t out_row_stride,
                        const kvw_paged_cache_t* cache, const kva_group_scales_t* scales,
