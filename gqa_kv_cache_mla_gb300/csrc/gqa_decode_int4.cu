@@ -189,7 +189,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         }
         const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
         const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
-        const uint32_t in_block = a.G - hb * a.block_rows < a.per_token ? a.G - hb * a.block_rows : a.per_token;
+        const uint32_t in_block = a.G - hb * Sh::kBlock < a.per_token ? a.G - hb * Sh::kBlock : a.per_token;
         prefetch_page(maps.codes, a.page_table, a.max_pages, a.ps, w.b,
                       (int64_t)(w.span.tile0 + w.first) * kTile, lane);
         // ---- the segment, and its queries: one copy per row
@@ -203,7 +203,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             x.tokens = w.span.tokens;
             x.rows = rows;
             x.in_block = in_block;
-            x.head0 = kvh * a.G + hb * a.block_rows;
+            x.head0 = kvh * a.G + hb * Sh::kBlock;
             x.block = block;
             x.whole = w.whole();
             x.slot1 = w.first == 0;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             const uint32_t ct = w.span.tokens == 1 ? 0 : lane / in_block;
             bulk_load(sm.q_raw[q_at.slot] + lane * Sh::kQPitch,
                       a.q + (int64_t)(w.t + ct) * a.q_stride +
-                          (int64_t)(kvh * a.G + hb * a.block_rows + (lane - ct * in_block)) * D,
+                          (int64_t)(kvh * a.G + hb * Sh::kBlock + (lane - ct * in_block)) * D,
                       D * 2, &sm.q_full[q_at.slot]);
         }
         q_at.step();
@@ -849,7 +849,7 @@ cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
     e = launch_early(&gqa_int4_kernel<D, MODS, HOOK>, dim3(ctas), Sh::kThreads, smem, stream, a,
                      maps);
     if (e != cudaSuccess) return e;
-    return launch_join<Sh::kPadded>(a, ctas, stream);
+    return launch_join<Sh::kPadded, Sh::kBlock>(a, ctas, stream);
 }
 
 template <int D, Hook HOOK>
@@ -888,7 +888,7 @@ int int4_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
                                   tot_seq_len, num_q_heads, cache, sm_scale, softcap, window,
                                   alibi_slopes, workspace, workspace_bytes, err_flags,
                                   tma_sizes_ok(cache), true, int4_strides_ok(cache, scales),
-                                  8);
+                                  Shape4<64>::kBlock);
     if (bad != KVW_OK || tot_seq_len == 0) return bad;
     a.k_scale = a.v_scale = 1.0f;
     a.wait_limit = wait_cycles(wait_ns);

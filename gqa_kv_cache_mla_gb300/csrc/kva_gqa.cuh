@@ -29,8 +29,7 @@ struct GqaArgs {
     float sm_scale, k_scale, v_scale;
     float softcap, cap_factor, cap_half;  // in units of log2; 2 log2(e) / the cap; half the cap
     uint32_t Hq, G, HB, D;  // query heads, group size, row blocks per group, head size
-    uint32_t block_rows;    // rows of a row block: kRows, or 8
-    uint32_t per_token;     // rows of a token in a row block: G, or block_rows with several blocks
+    uint32_t per_token;     // rows of a token in a row block: G, or all with several blocks
     uint32_t num_pages, max_pages, pieces;
     uint32_t lanes;  // row blocks that CTAs of the same piece take side by side
     FastDiv ps;
@@ -85,7 +84,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // context of 7118, E4M3, 5 heads of 256: 26 -> 17 us).
 constexpr int kJoinThreads = 512;
 
-template <int DP>
+// BLOCK: rows of a row block.
+template <int DP, uint32_t BLOCK>
 __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a) {
     __shared__ float s_w[kRows][kMaxPieces];
     __shared__ float s_top[kRows], s_sum[kRows];
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const uint32_t n = open.n, kvh = a.HB == 1 ? open.block : open.block / a.HB;
     const uint32_t hb = open.block - kvh * a.HB;
-    const uint32_t in_block = a.G - hb * a.block_rows < a.per_token ? a.G - hb * a.block_rows : a.per_token;
+    const uint32_t in_block = a.G - hb * BLOCK < a.per_token ? a.G - hb * BLOCK : a.per_token;
     // the rows r0 .. r0 + rows - 1 of this block
     const uint32_t every = open.tokens * in_block, share = (every + gridDim.y - 1) / gridDim.y;
     const uint32_t r0 = blockIdx.y * share;
     if (r0 >= every) return;
     const uint32_t rows = every - r0 < share ? every - r0 : share;
-    const uint32_t head0 = kvh * a.G + hb * a.block_rows;
+    const uint32_t head0 = kvh * a.G + hb * BLOCK;
     auto part = [&](uint32_t i) { return slot_of<DP>(a.workspace, c0 + i * a.lanes, i == 0 ? 1 : 0); };
 
     for (uint32_t r = warp; r < rows; r += kJoinThreads / 32) {
@@ -211,12 +211,12 @@ inline uint32_t side_by_side(GqaArgs& a, uint64_t wave) {
     return a.pieces * a.lanes;
 }
 
-template <int DP>
+template <int DP, uint32_t BLOCK = kRows>
 inline cudaError_t launch_join(const GqaArgs& a, uint32_t ctas, cudaStream_t stream) {
     // where a join may be of more than 48 pieces on average, eight blocks take
     // it (one token over 901 positions: 10.4 us with one, 11.4 with eight)
     const uint32_t y = a.pieces > 48ull * a.split.T * a.split.blocks ? 8 : 1;
-    return launch_early(&gqa_join_kernel<DP>, dim3(ctas, y), kJoinThreads, 0, stream, a);
+    return launch_early(&gqa_join_kernel<DP, BLOCK>, dim3(ctas, y), kJoinThreads, 0, stream, a);
 }
 
 // Checks a call's arguments (what the cache's type asks of sizes, values and
@@ -254,7 +254,6 @@ inline int gqa_arguments(GqaArgs& a, void* out, float* lse, const void* q, int64
     a.split.B = num_batches;
     a.split.T = tot_seq_len;
     a.G = num_q_heads / Hk;
-    a.block_rows = block_rows;
     a.HB = (a.G + block_rows - 1) / block_rows;
     a.split.blocks = Hk * a.HB;
     a.per_token = a.HB == 1 ? a.G : block_rows;
