@@ -46,6 +46,9 @@
 namespace kvw {
 namespace {
 
+// What happens to scores: nothing, a distance bias, or a cap and perhaps a bias.
+enum class Mods { kNone, kBias, kCap };
+
 // One layer's codes and scales.  A copy takes both planes of some rows of one
 // head and page: the codes as lines of 128 bytes in the 128-byte swizzle
 // (chunk c of line l lies at c ^ (l & 7)), the scales as they lie, group by
@@ -352,7 +355,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return y;
 }
 
-template <int D, bool MODS, Hook HOOK>
+template <int D, Mods MODS, Hook HOOK>
 __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
     gqa_int4_kernel(const GqaArgs a, const __grid_constant__ Int4Maps maps) {
     using Sh = Shape4<D>;
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
             // products are of codes 2^-24 as large; scores in units of log2 straight
             // from the product, or 2 log2(e) / cap of them
             float by = a.sm_scale * down * 0x1p24f;
-            by *= MODS && a.softcap > 0.0f ? a.cap_factor : kLog2e;
+            by *= MODS == Mods::kCap ? a.cap_factor : kLog2e;
             // never 0, a masked score is -inf times this, and never infinite
             by = fminf(fmaxf(by, 1.17549435e-38f), 3.4028234e38f);
 #pragma unroll
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
         // position in tile 0 (those of positions that a row sees fit 32 bits)
         [[maybe_unused]] float slope[2];
         [[maybe_unused]] uint32_t far[2];
-        if constexpr (MODS) {
+        if constexpr (MODS != Mods::kNone) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t r = 2 * in_quad + e;
@@ -576,38 +579,31 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                 }
             }
             // ---- cap, distance bias, mask
-            if constexpr (MODS) {  // into units of log2
-                if (a.softcap > 0.0f) {
-                    // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd
-                    // series where that loses small scores
+            // (scores of kNone are brought into units of log2 with the weights)
+            if constexpr (MODS == Mods::kCap) {
+                // tanh as in gqa_decode_paged.cu: 1 - 2 / (2^u + 1), its odd series
+                // where that loses small scores
 #pragma unroll
-                    for (int x = 0; x < 4 * N; ++x) {
-                        float& y = s[x / 4][x % 4];
-                        const float u = y * qs[x & 1], v = u * u;
-                        const float near =
-                            a.cap_half * u *
-                            fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3), 1.0f);
-                        const float far =
-                            a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
-                        y = fabsf(u) < kTanhNear ? near : far;
-                    }
+                for (int x = 0; x < 4 * N; ++x) {
+                    float& y = s[x / 4][x % 4];
+                    const float u = y * qs[x & 1], v = u * u;
+                    const float near = a.cap_half * u *
+                                       fmaf(v, fmaf(v, fmaf(v, -kTanh7, kTanh5), -kTanh3), 1.0f);
+                    const float far = a.softcap - __fdividef(2.0f * a.softcap, fast_exp2(u) + 1.0f);
+                    y = fabsf(u) < kTanhNear ? near : far;
                 }
-                if (a.slopes) {
+            }
+            if (MODS == Mods::kBias || (MODS == Mods::kCap && a.slopes)) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = a.softcap > 0.0f ? 1.0f : qs[e];
-                        const float bias = -slope[e] * (float)(far[e] - k * kTile);
+                for (int e = 0; e < 2; ++e) {
+                    const float f = MODS == Mods::kCap ? 1.0f : qs[e];
+                    const float bias = -slope[e] * (float)(far[e] - k * kTile);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const float nearer =
-                                i == 0 ? bias : fmaf(slope[e], (float)(kTile * i), bias);
-                            s[i][e] = fmaf(s[i][e], f, nearer);
-                            s[i][2 + e] = fmaf(s[i][2 + e], f, nearer + slope[e]);
-                        }
+                    for (int i = 0; i < N; ++i) {
+                        const float nearer = i == 0 ? bias : fmaf(slope[e], (float)(kTile * i), bias);
+                        s[i][e] = fmaf(s[i][e], f, nearer);
+                        s[i][2 + e] = fmaf(s[i][2 + e], f, nearer + slope[e]);
                     }
-                } else if (!(a.softcap > 0.0f)) {
-#pragma unroll
-                    for (int x = 0; x < 4 * N; ++x) s[x / 4][x % 4] *= qs[x & 1];
                 }
             }
             [[maybe_unused]] uint32_t seen = 0;  // bit e: score e counts
@@ -632,8 +628,9 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                 for (int i = 0; i < N; ++i) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        p[i][e] = fast_exp2(MODS ? s[i][e] - ref[e & 1]
-                                                 : fmaf(s[i][e], qs[e & 1], -ref[e & 1]));
+                        p[i][e] = fast_exp2(MODS == Mods::kNone
+                                                ? fmaf(s[i][e], qs[e & 1], -ref[e & 1])
+                                                : s[i][e] - ref[e & 1]);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         const uint32_t by = scales_of(i, NG + g);
@@ -672,7 +669,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                             const uint32_t x = scales_of(i, NG + g);
                             by = fmaxf(by, fabsf(h ? bf16_hi(x) : bf16_lo(x)));
                         }
-                        const float x = s[i][2 * h + e] * (MODS ? 1.0f : qs[e]);
+                        const float x = s[i][2 * h + e] * (MODS == Mods::kNone ? qs[e] : 1.0f);
                         if (kept(2 * h + e)) most = fmaxf(most, x + __log2f(by));
                     }
 #pragma unroll
@@ -832,7 +829,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
     if (!alive && lane == 0) flag(a.err_flags, KVW_ERR_TIMEOUT);
 }
 
-template <int D, bool MODS, Hook HOOK>
+template <int D, Mods MODS, Hook HOOK>
 cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
     using Sh = Shape4<D>;
     constexpr size_t smem = sizeof(Smem4<D>);
@@ -858,9 +855,9 @@ int launch(GqaArgs& a, const kvw_paged_cache_t* cache, const kva_group_scales_t*
     Int4Maps maps;
     const int st = encode_int4_maps(&maps, cache, scales, layer_idx);
     if (st != KVW_OK) return st;
-    const cudaError_t e = a.softcap > 0.0f || a.slopes
-                              ? launch_as<D, true, HOOK>(a, maps, stream)
-                              : launch_as<D, false, HOOK>(a, maps, stream);
+    const cudaError_t e = a.softcap > 0.0f ? launch_as<D, Mods::kCap, HOOK>(a, maps, stream)
+                          : a.slopes       ? launch_as<D, Mods::kBias, HOOK>(a, maps, stream)
+                                           : launch_as<D, Mods::kNone, HOOK>(a, maps, stream);
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
@@ -891,6 +888,9 @@ int int4_entry(void* out, float* lse, const void* q, int64_t q_row_stride,
                                   Shape4<64>::kBlock);
     if (bad != KVW_OK || tot_seq_len == 0) return bad;
     a.k_scale = a.v_scale = 1.0f;
+    // a segment's cost beside its tiles, in tiles (64 requests of 4 tokens with 1: 115
+    // us, 3: 109, 5: 107, 8: 111; one token each, up to 512: 38, 36, 35, 36)
+    a.split.overhead = 5;
     a.wait_limit = wait_cycles(wait_ns);
     auto run = [&](auto d) {
         constexpr int D = decltype(d)::value;

@@ -82,15 +82,47 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // their order, the pieces dealt to groups of threads and the groups' sums
 // added up in order.  A long join's rows are dealt to several blocks (one
 // context of 7118, E4M3, 5 heads of 256: 26 -> 17 us).
-constexpr int kJoinThreads = 512;
+//
+// With row blocks of 8 the usual join, of two to four pieces, takes one round
+// trip: all that they hold is loaded beside the word that says how many there
+// are.  Blocks of 256 threads, all resident at once (256 requests of up to 8192
+// over 4 bits 201 -> 197 us, 64 of 4 tokens 113 -> 108).
 
 // BLOCK: rows of a row block.
+template <uint32_t BLOCK>
+constexpr int join_threads() {
+    return BLOCK == kRows ? 512 : 256;
+}
+
 template <int DP, uint32_t BLOCK>
-__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a) {
-    __shared__ float s_w[kRows][kMaxPieces];
-    __shared__ float s_top[kRows], s_sum[kRows];
+__global__ void __launch_bounds__(join_threads<BLOCK>()) gqa_join_kernel(const GqaArgs a) {
+    constexpr int kJoinThreads = join_threads<BLOCK>();
+    __shared__ float s_w[BLOCK][kMaxPieces];
+    __shared__ float s_top[BLOCK], s_sum[BLOCK];
     __shared__ float4 s_acc[kJoinThreads];
+    constexpr int kEach = (BLOCK * DP / 4 + kJoinThreads - 1) / kJoinThreads;  // float4 of a thread
+    constexpr int kFew = DP <= 128 ? 4 : 2;  // pieces loaded at once
+    [[maybe_unused]] float4 x[kEach][kFew];
+    [[maybe_unused]] float x_m[kEach][kFew], x_l[kEach][kFew];
     wait_for_stream();
+    if constexpr (BLOCK < kRows) {
+        if (gridDim.y == 1) {
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                // (a slot past the last piece's is not looked at in the end)
+                const uint32_t c = blockIdx.x + i * a.lanes;
+                const float* from = slot_of<DP>(a.workspace, c < kMaxPieces ? c : 0, i == 0);
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const uint32_t e = threadIdx.x + k * kJoinThreads, r = e / (a.D / 4);
+                    if (r >= BLOCK) continue;
+                    x[k][i] = load_part(from + r * DP + 4 * (e - r * (a.D / 4)));
+                    x_m[k][i] = __ldcg(from + kRows * DP + r);
+                    x_l[k][i] = __ldcg(from + kRows * DP + kRows + r);
+                }
+            }
+        }
+    }
     const OpenPiece open = reinterpret_cast<const OpenPiece*>(a.workspace)[blockIdx.x];
     if (open.n == 0) return;
     const uint32_t c0 = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -104,6 +136,43 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaArgs a)
     const uint32_t rows = every - r0 < share ? every - r0 : share;
     const uint32_t head0 = kvh * a.G + hb * BLOCK;
     auto part = [&](uint32_t i) { return slot_of<DP>(a.workspace, c0 + i * a.lanes, i == 0 ? 1 : 0); };
+    if constexpr (BLOCK < kRows) {
+        if (n <= kFew && gridDim.y == 1) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const uint32_t e = tid + k * kJoinThreads, r = e / (a.D / 4);
+                const uint32_t d = 4 * (e - r * (a.D / 4));
+                if (r >= rows) continue;
+                float top = x_m[k][0];
+#pragma unroll
+                for (int i = 1; i < kFew; ++i)
+                    if ((uint32_t)i < n) top = fmaxf(top, x_m[k][i]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                float l = 0.0f;
+                float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kFew; ++i)
+                    if ((uint32_t)i < n) {
+                        const float f = fast_exp2(x_m[k][i] - base);
+                        l += f * x_l[k][i];
+                        o.x += f * x[k][i].x;
+                        o.y += f * x[k][i].y;
+                        o.z += f * x[k][i].z;
+                        o.w += f * x[k][i].w;
+                    }
+                const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+                const uint32_t ct = r / in_block;
+                const uint64_t row =
+                    (uint64_t)(open.t + ct) * a.Hq + head0 + (r - ct * in_block);
+                uint2 y;
+                y.x = pack_bf16x2(o.x * inv, o.y * inv);
+                y.y = pack_bf16x2(o.z * inv, o.w * inv);
+                *reinterpret_cast<uint2*>(a.out + row * a.D + d) = y;
+                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+            }
+            return;
+        }
+    }
 
     for (uint32_t r = warp; r < rows; r += kJoinThreads / 32) {
         float top = -INFINITY, l_first = 0.0f;  // of the lane's first piece
@@ -216,7 +285,8 @@ inline cudaError_t launch_join(const GqaArgs& a, uint32_t ctas, cudaStream_t str
     // where a join may be of more than 48 pieces on average, eight blocks take
     // it (one token over 901 positions: 10.4 us with one, 11.4 with eight)
     const uint32_t y = a.pieces > 48ull * a.split.T * a.split.blocks ? 8 : 1;
-    return launch_early(&gqa_join_kernel<DP, BLOCK>, dim3(ctas, y), kJoinThreads, 0, stream, a);
+    return launch_early(&gqa_join_kernel<DP, BLOCK>, dim3(ctas, y), join_threads<BLOCK>(), 0, stream,
+                        a);
 }
 
 // Checks a call's arguments (what the cache's type asks of sizes, values and
