@@ -285,37 +285,65 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             if (ok) w.next(a.split);
             continue;
         }
+        // Lane c takes unit c of a place: R rows of one page.  Page ids are looked
+        // up one place ahead (256 requests, pages of 16, 281 -> 230 us; of 32, 200).
+        const uint32_t per_tile = 64u >> log_rows, j = lane / per_tile, unit = lane % per_tile;
+        // (positions that the page table reaches are below 2^32)
+        auto begins = [&](uint32_t i) {
+            return (w.span.tile0 + i) * kTile + (lane << log_rows);
+        };
+        auto page_id = [&](uint32_t i) {
+            const uint32_t idx = fast_div(begins(i), a.ps);
+            return j < (uint32_t)T && i + j < w.last && idx < a.max_pages
+                       ? __ldg(a.page_table + (uint64_t)w.b * a.max_pages + idx)
+                       : (uint32_t)KVW_PAGE_UNMAPPED;
+        };
+        uint32_t next = page_id(w.first);
         for (uint32_t i = w.first; ok && i < w.last; i += T) {
+            const uint32_t page = next, p = begins(i);
+            if (i + T < w.last) next = page_id(i + T);
             const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
-            TilePlan t[T];
-            uint32_t units = 0;
-            bool all = seen(p_tile, T);
+            bool used = j < (uint32_t)T;
+            uint64_t there = ((1ull << (1u << log_rows)) - 1) << (unit << log_rows);
+            if (i + T > w.last || p_tile < w.span.start || p_tile + T * kTile > w.span.hi) {
+                // the unit's positions that count
+                const int64_t lo = p > w.span.start ? (int64_t)p : w.span.start;
+                const int64_t end = p_tile + ((int64_t)(lane + 1) << log_rows);
+                const int64_t hi = end < w.span.hi ? end : w.span.hi;
+                used = used && i + j < w.last && lo < hi;
+                there = used ? ((1ull << (uint32_t)(hi - lo)) - 1)
+                                   << (uint32_t)(lo - p + (unit << log_rows))
+                             : 0;
+            }
+            const bool valid = used && page < a.num_pages;
+            if (used && !valid) bad_page = 1;
+            const bool whole = valid && __popcll(there) == 1 << log_rows;
+            const bool all =
+                __all_sync(0xffffffffu, whole || j >= (uint32_t)T) && seen(p_tile, T);
+            const uint32_t units = __popc(__ballot_sync(0xffffffffu, valid));
+            uint64_t words[T];
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                if (i + j < w.last) {
-                    plan_tile(maps.codes, a.page_table, a.max_pages, a.num_pages, a.ps, w.b,
-                              p_tile + j * kTile, w.span.start, w.span.hi, t[j], bad_page);
-                } else {
-                    t[j].n = t[j].t_lo = t[j].t_hi = 0;
-                    t[j].copy[0].level = 4;
+            for (int t = 0; t < T; ++t) {
+                words[t] = ~0ull;
+                if (!all) {
+                    const uint64_t mine = valid && j == (uint32_t)t ? there : 0;
+                    words[t] = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(mine >> 32)) << 32 |
+                               __reduce_or_sync(0xffffffffu, (uint32_t)mine);
                 }
-                units += t[j].n;
-                all = all && (t[j].t_lo & t[j].t_hi) == ~0u;
             }
             ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
             if (!ok) break;
             if (lane == 0) {
                 sm.even[at.slot] = all;
 #pragma unroll
-                for (int j = 0; j < T; ++j)
-                    sm.there[at.slot][j] = ((uint64_t)t[j].t_hi << 32) | t[j].t_lo;
+                for (int t = 0; t < T; ++t) sm.there[at.slot][t] = words[t];
                 mbar_arrive_expect_tx(&sm.full[at.slot], (units << log_rows) * row_bytes);
             }
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < T; ++j)
-                if (!(HOOK == Hook::kWithheld && issued == 0) && t[j].copy[0].level != 4)
-                    copy(j, lane, t[j].copy[0].row, t[j].copy[0].page);
+            if (valid && !(HOOK == Hook::kWithheld && issued == 0)) {
+                const uint32_t idx = fast_div(p, a.ps);
+                copy(j, unit, p - idx * a.ps.d, page);
+            }
             __syncwarp();
             at.step();
             ++issued;
