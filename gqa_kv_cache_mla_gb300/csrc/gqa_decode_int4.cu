@@ -116,6 +116,9 @@ struct Shape4 {
     static constexpr int kSlots = kRing > 12 ? 12 : kRing;
     static constexpr int kPadded = D <= 64 ? 64 : D <= 128 ? 128 : 256;  // of a workspace row
     static constexpr int kQPitch = D * 2 + 16;  // eight rows on distinct banks
+    // 256-wide heads: what can be worked out again or fetched leaves the registers
+    // to the sums (128 requests of up to 8192: 223 -> 206 us; three CTAs 235, spills)
+    static constexpr bool kLean = D == 256;
     static constexpr int kBlock = 8, kQBufs = 2;  // rows of a row block; places for queries
     // rows that join at a time, four rows' stores on distinct banks
     static constexpr int kJoinPitch = D + 8;
@@ -140,6 +143,8 @@ struct Smem4 {
     unsigned char scales[Sh::kSlots][Sh::kTiles][Sh::kScales];  // units of [K][V][group][row]
     unsigned char q_raw[Sh::kQBufs][Sh::kBlock * Sh::kQPitch];
     uint4 q[Sh::kChunks][32];  // the queries as operands
+    // where kLean: -8 sum of a group's queries for rows 2 i and 2 i + 1
+    float2 off[Sh::kWarps][Sh::kLean ? Sh::kGroups : 1][4];
     float join[Sh::kWarps][Sh::kJoinRows][Sh::kJoinPitch];
     uint64_t full[Sh::kSlots], empty[Sh::kSlots], q_full[Sh::kQBufs], q_empty[Sh::kQBufs], meet;
     Segment segment[Sh::kQBufs];
@@ -439,16 +444,22 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
     };
     // ---- places of this lane's operands in a tile, the same for every tile
     const uint32_t log_rows = maps.codes.log_rows;
-    uint32_t k_at[NG], v_at[NG];  // chunks 2 g and 2 g + 1
+    constexpr int kPlaces = Sh::kLean ? 1 : NG;
+    uint32_t k_at[kPlaces], v_at[kPlaces];  // chunks 2 g and 2 g + 1
     {
         const uint32_t row = warp * 16 + 2 * (lane & 7u) + ((lane >> 3) & 1u);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < kPlaces; ++g) {
             const uint32_t c = 2 * g + (lane >> 4) < (uint32_t)CH ? 2 * g + (lane >> 4) : 2 * g;
             k_at[g] = code_at<D>(log_rows, 0, row, c);
             v_at[g] = code_at<D>(log_rows, 1, row, c);
         }
     }
+    // (a row of 256 codes is a line: its chunks 2 g and 0 lie 32 g apart but for
+    // the swizzle)
+    auto place = [&](const uint32_t(&x)[kPlaces], int g) {
+        return Sh::kLean ? x[0] ^ (32u * g) : x[Sh::kLean ? 0 : g];
+    };
     // scales of positions 2 * quad and the next of the slice; groups 2R bytes apart
     const uint32_t s_group = 2u << log_rows;
     const uint32_t s_at = ((warp * 16) >> log_rows) * scale_unit(NG, log_rows) +
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
         const uint32_t eights_k[4] = {kEight, kEight, kEights, kEights};
         const uint32_t eights_v[4] = {kEight, kEights, kEight, kEights};
         // -8 sum of a group's queries, in units of the products
-        float off[NG][4];
+        [[maybe_unused]] float off[NG][4];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -530,7 +541,9 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) off[g][e] = -x[e];
+            if (Sh::kLean && quad == 0) sm.off[warp][g][in_quad] = make_float2(-x[0], -x[1]);
         }
+        if constexpr (Sh::kLean) __syncwarp();
         auto token_of = [&](int e) { return (token >> (16 * e)) & 0xffffu; };
         // distance biases of the lane's rows, and the rows' distances from its first
         // position in tile 0 (those of positions that a row sees fit 32 bits)
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                 float x[N][4];
                 uint32_t kw[N][4];
 #pragma unroll
-                for (int i = 0; i < N; ++i) ldsm4(kw[i], codes + i * Sh::kCodes + k_at[g]);
+                for (int i = 0; i < N; ++i) ldsm4(kw[i], codes + i * Sh::kCodes + place(k_at, g));
 #pragma unroll
                 for (int c = 0; c < 2 && 2 * g + c < CH; ++c) {
                     const uint4 q = sm.q[2 * g + c][lane];
@@ -589,16 +602,25 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                         const uint32_t u8 = u >> 8, v8 = v >> 8;
                         const uint32_t f0[4] = {u & kLow, v & kLow, u & kHigh, v & kHigh};
                         const uint32_t f1[4] = {u8 & kLow, v8 & kLow, u8 & kHigh, v8 & kHigh};
-                        if (c == 0)
-                            mma_from(x[i], f0, q.x, q.y, off[g]);
-                        else
+                        if (c > 0) {
                             mma16816<true>(x[i], f0, q.x, q.y);
+                        } else if constexpr (Sh::kLean) {
+                            const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_from(x[i], f0, q.x, q.y, none);
+                        } else {
+                            mma_from(x[i], f0, q.x, q.y, off[g]);
+                        }
                         mma16816<true>(x[i], f1, q.z, q.w);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const uint32_t by = scales_of(i, g);
+                    if constexpr (Sh::kLean) {
+                        const float2 o = sm.off[warp][g][in_quad];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[i][e] += e & 1 ? o.y : o.x;
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float f = e < 2 ? bf16_lo(by) : bf16_hi(by);
@@ -673,6 +695,9 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                     }
                 }
             };
+            uint32_t vw[N][4];  // the first group's values are on their way meanwhile
+#pragma unroll
+            for (int i = 0; i < N; ++i) ldsm4_trans(vw[i], codes + i * Sh::kCodes + place(v_at, 0));
             weights();
             // Does a row's reference have to rise?  (The patterns are those of
             // numbers that are not negative; a NaN's, and those of negative
@@ -730,9 +755,11 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
             // ---- O^T += V^T (P s_v)^T
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t vw[N][4];
+                if (g > 0) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) ldsm4_trans(vw[i], codes + i * Sh::kCodes + v_at[g]);
+                    for (int i = 0; i < N; ++i)
+                        ldsm4_trans(vw[i], codes + i * Sh::kCodes + place(v_at, g));
+                }
                 if (g == NG - 1 && release) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.empty[at.slot]);
