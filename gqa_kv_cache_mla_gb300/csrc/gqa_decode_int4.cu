@@ -24,16 +24,35 @@
 // at 2^-17 and cost two more instructions in eight: 256 requests 217 us against
 // 201.
 //
-// Both products have the row block's rows as the instruction's 8 columns (one
-// or two blocks of them): S^T = K Q^T and O^T = V^T P^T.  Codes are then the
-// operand of 16 rows, so that no half of an instruction is idle with up to 8
-// rows, and P^T passes from the order of one's result to the other's operand
-// by transposing 8 x 8 blocks (movmatrix).  Row i of an operand's upper and
-// lower half are positions 2 i and 2 i + 1, whose scales are one word.
+// Both products have the row block's 8 rows as the instruction's columns: S^T =
+// K Q^T and O^T = V^T P^T.  Codes are then the operand of 16 rows, no half of an
+// instruction is idle, and P^T passes from the order of one's result to the
+// other's operand by transposing 8 x 8 blocks (movmatrix).  Row i of an operand's
+// upper and lower half are positions 2 i and 2 i + 1, whose scales are one word.
+// (Queries as the operand of 16 rows, half of them zeros: 364 us instead of 292
+// at that step.  Two row blocks in a pass, for 9 to 16 rows, lack the registers:
+// 64 query over 4 key-value heads 124 us, as two passes side by side 119.  Scores
+// by E4M3 products, whose operand is one AND for 4 codes: 299 us instead of 252;
+// with operands that change they run at half the rate of the fp16 ones.)
 //
 // Weights times scales are fp16.  Their reference m follows the row's largest
 // P s_v, not its largest score: raised when a product passes 2^15, to where
 // the largest is 2^9 (weight_lift).  The sum of weights is fp32.
+//
+// Bound: a tile of 64 positions is 8.7 KB for heads of 128, and what a consumer
+// does for it (S, softmax, O^T for 16 positions each of four warps) some 250
+// instructions a slice, half of an SM's issue slots at the full rate of HBM; the
+// warps wait for each other's results rather than for tiles (feeding alone: 178
+// us of the 197 below).  So: three CTAs of four consumer warps per SM, two tiles
+// at a time, all that can be known once per segment worked out by the feeding
+// warp, queries' operands in shared memory.
+//
+// Measured, 32 query and 8 key-value heads of 128: 256 requests of up to 8192
+// positions 197 us (5.9 TB/s, 88 % of the card's copy rate; one tile at a time
+// 236, two CTAs per SM 217), with a cap 230, with a distance bias 243, pages of 16
+// 233, heads of 64 128, of 96 172, of 256 (128 requests) 205; 64 query heads, 8
+// requests of up to 131072 95 us; 32 of up to 4096 24 us (some 9 of it before the
+// first and after the last byte); one token over 901 positions 9.7 us.
 //
 // Division of the work, workspace and join are those of gqa_decode_paged.cu.
 #include <cstdint>

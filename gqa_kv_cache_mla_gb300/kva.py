@@ -195,15 +195,15 @@ def group_scales(data, strides) -> GroupScalesT:
     return s
 
 
-def int4_cache(codes, scales, page_table, cache_lengths, head_size=None):
+def int4_cache(codes, scales, page_table, cache_lengths):
     """The two descriptors of a cache held in 4 bits, for ``codes`` uint8
     [pages, 2, layers, heads, page_size, head_size / 2] and ``scales`` bf16
     [pages, 2, layers, heads, groups, page_size], views whose last two
-    dimensions are dense (other strides of theirs are not looked at)."""
-    pages, _, layers, heads, page_size, half = codes.shape
-    d = 2 * half if head_size is None else head_size
-    groups = -(-d // GROUP)
-    if tuple(scales.shape) != (pages, 2, layers, heads, groups, page_size) \
+    dimensions are dense."""
+    pages, planes, layers, heads, page_size, half = codes.shape
+    d, groups = 2 * half, -(-2 * half // GROUP)
+    if planes != 2 or tuple(scales.shape) != (pages, 2, layers, heads, groups, page_size) \
+            or codes.element_size() != 1 or scales.element_size() != 2 \
             or tuple(codes.stride()[4:]) != (half, 1) \
             or scales.stride()[5] != 1 or (groups > 1 and scales.stride()[4] != page_size):
         raise ValueError("codes %s and scales %s are not those of a cache in 4 bits"

@@ -542,3 +542,30 @@ def test_gather_malformed_offsets(kva):
                                cache, scales, 1, err_flags=fl)
         torch.cuda.synchronize()
         assert int(fl) == 4 and bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** -20, 2.0 ** -3, 2.0 ** 20, 2.0 ** 65])
+def test_extreme_caps(kva, softcap):
+    """A cap far below the scores, far above them, and one that is none."""
+    c = Q.Int4(152, *lengths(100, 70, 200), kv_heads=1, head=128).fill()
+    x = Call(kva, c, 4, softcap=softcap)
+    x.call()
+    if softcap > 2.0 ** 64:
+        x.softcap = 0.0
+    x.check()
+
+
+def test_slopes_of_either_sign_and_zero(kva):
+    c = Q.Int4(153, [1, 3], [150, 64], kv_heads=1, head=64).fill()
+    x = Call(kva, c, 4, alibi=True)
+    x.slopes = torch.tensor([0.0, -0.125, 0.5, 2.0])
+    x.ds.copy_(x.slopes)
+    x.call()
+    torch.cuda.synchronize()
+    out, lse, to, tl = Q.gqa(c, x.q, x.scale, slopes=x.slopes.abs())
+    for h in (0, 2, 3):
+        R.check(x.out[:, h], out[:, h], to[:, h])
+    # the negative one by hand: its tolerance takes the bias's size
+    want, _, tol, _ = Q.gqa(c, x.q, x.scale, slopes=x.slopes)
+    spread = tol[:, 1] + 2.0 ** -15 * want[:, 1].abs().max()
+    R.check(x.out[:, 1], want[:, 1], spread)

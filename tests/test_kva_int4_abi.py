@@ -246,11 +246,14 @@ def test_descriptors_of_dense_tensors():
     assert (c.stride_page, c.stride_kv, c.stride_layer, c.stride_token, c.stride_head) == \
         (24 * row, 12 * row, 4 * row, 96, row)
     assert (s.stride_page, s.stride_kv, s.stride_layer, s.stride_head) == (1536, 768, 256, 64)
-    for bad in (codes[..., :40], codes.transpose(3, 4), codes[:, :, :2]):
+    for bad in (codes[..., :40], codes.transpose(3, 4), codes[:, :, :2], codes[:, :1],
+                codes.short()):
         with pytest.raises(ValueError):
             kva.int4_cache(bad, scales, table, lens)
     with pytest.raises(ValueError):
         kva.int4_cache(codes, scales[..., :1, :], table, lens)
+    with pytest.raises(ValueError):
+        kva.int4_cache(codes, scales.float(), table, lens)
 
 
 def test_wrapper_checks():
