@@ -87,11 +87,11 @@ def _size(t):
     return t.numel() * t.element_size()
 
 
-def _append(name, place, q_out, qkv, input_row_offsets, cache, freqs_cis, layer_idx, q_gamma,
+def _append(call, place, q_out, qkv, input_row_offsets, cache, freqs_cis, layer_idx, q_gamma,
             k_gamma, epsilon, weight_offset, position_ids, interleaved, mrope_section, err_flags,
             stream, num_batches, tot_seq_len, num_q_heads, q_out_row_stride, qkv_row_stride,
-            freqs_rows, rope_dim, check):
-    """The two appends; ``place`` is what stands between cache and layer."""
+            freqs_rows, rope_dim):
+    """The two appends' status; ``place`` is what stands between cache and layer."""
     B = input_row_offsets.shape[0] - 1 if num_batches is None else num_batches
     T = qkv.shape[0] if tot_seq_len is None else tot_seq_len
     if num_q_heads is None:
@@ -99,20 +99,19 @@ def _append(name, place, q_out, qkv, input_row_offsets, cache, freqs_cis, layer_
     qs = qkv.stride(0) if qkv_row_stride is None else qkv_row_stride
     if q_out_row_stride is None:
         q_out_row_stride = 0 if q_out is None else q_out.stride(0)
-    if freqs_rows is None:
-        freqs_rows = 0 if freqs_cis is None else freqs_cis.shape[0]
-    if rope_dim is None:
-        rope_dim = 0 if freqs_cis is None else freqs_cis.shape[1]
+    if freqs_rows is None or rope_dim is None:
+        size = (0, 0) if freqs_cis is None else freqs_cis.shape
+        freqs_rows = size[0] if freqs_rows is None else freqs_rows
+        rope_dim = size[1] if rope_dim is None else rope_dim
     sec = None
     if mrope_section is not None:
         sec = ctypes.cast((ctypes.c_uint32 * 3)(*[int(v) for v in mrope_section]),
                           ctypes.c_void_p)
-    st = getattr(lib, name)(
+    return call(
         _ptr(q_out), q_out_row_stride, _ptr(qkv), qs, _ptr(input_row_offsets), B, T, num_q_heads,
         _ptr(q_gamma), _ptr(k_gamma), epsilon, weight_offset, _ptr(freqs_cis), freqs_rows,
-        rope_dim, _ptr(position_ids), int(bool(interleaved)), sec, ctypes.byref(cache), place,
+        rope_dim, _ptr(position_ids), 1 if interleaved else 0, sec, ctypes.byref(cache), place,
         layer_idx, _ptr(err_flags), _stream(stream))
-    return _done(st, name, check)
 
 
 def kva_append_qkv_paged(q_out, qkv, input_row_offsets, cache: PagedCacheT, freqs_cis,
@@ -124,10 +123,11 @@ def kva_append_qkv_paged(q_out, qkv, input_row_offsets, cache: PagedCacheT, freq
                          rope_dim=None, check=True) -> int:
     """``q_out`` [tokens, heads, head_size] (or None for no query heads), or any
     [tokens, ...] tensor with ``num_q_heads`` given; ``qkv`` [tokens, columns]."""
-    return _append("kva_append_qkv_paged", v_scale, q_out, qkv, input_row_offsets, cache,
-                   freqs_cis, layer_idx, q_gamma, k_gamma, epsilon, weight_offset, position_ids,
-                   interleaved, mrope_section, err_flags, stream, num_batches, tot_seq_len,
-                   num_q_heads, q_out_row_stride, qkv_row_stride, freqs_rows, rope_dim, check)
+    st = _append(lib.kva_append_qkv_paged, v_scale, q_out, qkv, input_row_offsets, cache,
+                 freqs_cis, layer_idx, q_gamma, k_gamma, epsilon, weight_offset, position_ids,
+                 interleaved, mrope_section, err_flags, stream, num_batches, tot_seq_len,
+                 num_q_heads, q_out_row_stride, qkv_row_stride, freqs_rows, rope_dim)
+    return _done(st, "kva_append_qkv_paged", check)
 
 
 def kva_gqa_decode_workspace(num_q_heads: int, num_kv_heads: int, head_size: int) -> int:
@@ -222,11 +222,11 @@ def kva_append_qkv_int4(q_out, qkv, input_row_offsets, cache: PagedCacheT, scale
                         q_out_row_stride=None, qkv_row_stride=None, freqs_rows=None, rope_dim=None,
                         check=True) -> int:
     """:func:`kva_append_qkv_paged` to a cache held in 4 bits."""
-    return _append("kva_append_qkv_int4", ctypes.byref(scales), q_out, qkv, input_row_offsets,
-                   cache, freqs_cis, layer_idx, q_gamma, k_gamma, epsilon, weight_offset,
-                   position_ids, interleaved, mrope_section, err_flags, stream, num_batches,
-                   tot_seq_len, num_q_heads, q_out_row_stride, qkv_row_stride, freqs_rows,
-                   rope_dim, check)
+    st = _append(lib.kva_append_qkv_int4, ctypes.byref(scales), q_out, qkv, input_row_offsets,
+                 cache, freqs_cis, layer_idx, q_gamma, k_gamma, epsilon, weight_offset,
+                 position_ids, interleaved, mrope_section, err_flags, stream, num_batches,
+                 tot_seq_len, num_q_heads, q_out_row_stride, qkv_row_stride, freqs_rows, rope_dim)
+    return _done(st, "kva_append_qkv_int4", check)
 
 
 def kva_gather_kv_int4(k_out, v_out, ctx_offsets, cache: PagedCacheT, scales: GroupScalesT,

@@ -109,9 +109,10 @@ def _ptr(x):
     """Device address of a tensor (or an int address, or None)."""
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
 
 
 def _stream(stream):

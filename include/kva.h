@@ -275,7 +275,9 @@ int kva_gather_kv_int4(void* k_out, void* v_out, int64_t out_row_stride,
 /*
  * kva_gqa_decode_paged over a cache held in 4 bits: the same formulas with
  * K and V as their scales and codes have them, the same workspace
- * (kva_gqa_decode_workspace), limits, flags and errors.  Scores, softmax
+ * (kva_gqa_decode_workspace), limits, flags and errors.  Rows of neighbouring
+ * tokens share a pass where they fit 8 to a key-value head, and larger groups
+ * of query heads take several passes, side by side.  Scores, softmax
  * statistics and sums are fp32.  The products take fp16 operands: codes are
  * exact; a query row is brought into fp16's range by a power of two, which
  * loses only what is below 2^-35 of the row's largest value; a weight times
