@@ -65,16 +65,22 @@ __device__ __forceinline__ uint16_t group_scale(uint32_t top) {
 // and is below 7.03: the scale is off by 2^-9 of itself at most.
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint16_t scale) {
     const float s = __uint_as_float((uint32_t)scale << 16);
-    constexpr float kMagic = 12582912.0f + 8.0f;  // 1.5 * 2^23: a unit is the last bit
+    // 1.5 * 2^23, whose last bit is a unit: added to it, a code is the pattern's end
+    constexpr float kMagic = 12582912.0f + 8.0f;
+    constexpr uint32_t kPattern = 0x4b400000u;  // of 1.5 * 2^23
     uint32_t word = 0;
     if (refined_ok(s)) {
         const float y = __frcp_rn(s);
+        // one shift and add a code; what the patterns begin with adds up to a constant
+        uint32_t begin = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q0 = __fmul_rn(x[i], y);
             const float q = __fmaf_rn(__fmaf_rn(-q0, s, x[i]), y, q0);
-            word |= (__float_as_uint(__fadd_rn(q, kMagic)) & 15u) << (4 * i);
+            word += __float_as_uint(__fadd_rn(q, kMagic)) << (4 * i);
+            begin += kPattern << (4 * i);
         }
+        word -= begin;
     } else if (s > 0.0f) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
