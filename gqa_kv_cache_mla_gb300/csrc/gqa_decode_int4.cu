@@ -43,14 +43,14 @@
 // does for it (S, softmax, O^T for 16 positions each of four warps) some 250
 // instructions a slice, half of an SM's issue slots at the full rate of HBM; the
 // warps wait for each other's results rather than for tiles (feeding alone: 178
-// us of the 197 below).  So: three CTAs of four consumer warps per SM, two tiles
+// us of the 198 below).  So: three CTAs of four consumer warps per SM, two tiles
 // at a time, all that can be known once per segment worked out by the feeding
 // warp, queries' operands in shared memory.
 //
 // Measured, 32 query and 8 key-value heads of 128: 256 requests of up to 8192
-// positions 197 us (5.9 TB/s, 88 % of the card's copy rate; one tile at a time
-// 236, two CTAs per SM 217), with a cap 230, with a distance bias 243, pages of 16
-// 233, heads of 64 128, of 96 172, of 256 (128 requests) 205; 64 query heads, 8
+// positions 198 us (5.8 TB/s, 87 % of the card's copy rate; one tile at a time
+// 236, two CTAs per SM 217), with a cap 227, with a distance bias 203, pages of 16
+// 233, heads of 64 128, of 96 173, of 256 (128 requests) 206; 64 query heads, 8
 // requests of up to 131072 95 us; 32 of up to 4096 24 us (some 9 of it before the
 // first and after the last byte); one token over 901 positions 9.7 us.
 //
@@ -217,8 +217,13 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         const uint32_t block = w.block * a.lanes + blockIdx.x % a.lanes;
         const uint32_t kvh = a.HB == 1 ? block : block / a.HB, hb = block - kvh * a.HB;
         const uint32_t in_block = a.G - hb * Sh::kBlock < a.per_token ? a.G - hb * Sh::kBlock : a.per_token;
+        // The last tiles come first: with a distance bias their scores are the
+        // largest, and a reference set by them stays (256 requests 243 -> 203 us).
+        constexpr uint32_t T = Sh::kTiles;
+        const uint32_t places = (w.last - w.first + T - 1) / T;
+        const uint32_t final = w.first + (places - 1) * T;  // first tile of the last place
         prefetch_page(maps.codes, a.page_table, a.max_pages, a.ps, w.b,
-                      (int64_t)(w.span.tile0 + w.first) * kTile, lane);
+                      (int64_t)(w.span.tile0 + final) * kTile, lane);
         // ---- the segment, and its queries: one copy per row
         const uint32_t rows = w.span.tokens * in_block;
         if (lane == 0) {
@@ -261,7 +266,6 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         const int64_t pos0 = (int64_t)w.len0 + ((int64_t)w.k << a.split.log_c);
         const int64_t all_lo = pos0 + w.span.tokens - a.split.window, all_hi = pos0;
         auto seen = [&](int64_t p, int n) { return p >= all_lo && p + n * kTile - 1 <= all_hi; };
-        constexpr int T = Sh::kTiles;
         if (log_rows == 6) {
             // a tile lies in one page: two copies, the same in every lane
             auto plan = [&](uint32_t i) {
@@ -270,14 +274,15 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             };
             PagePlan next[T];
 #pragma unroll
-            for (int j = 0; j < T; ++j)
-                if (w.first + j < w.last) next[j] = plan(w.first + j);
-            for (uint32_t i = w.first; ok && i < w.last; i += T) {
+            for (uint32_t j = 0; j < T; ++j)
+                if (final + j < w.last) next[j] = plan(final + j);
+            for (uint32_t place = places; ok && place-- > 0;) {
+                const uint32_t i = w.first + place * T;
                 PagePlan t[T];
                 uint32_t bytes = 0;
                 bool all = seen((int64_t)(w.span.tile0 + i) * kTile, T);
 #pragma unroll
-                for (int j = 0; j < T; ++j) {
+                for (uint32_t j = 0; j < T; ++j) {
                     t[j] = next[j];
                     if (i + j >= w.last) {
                         t[j].valid = false;
@@ -287,18 +292,18 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
                     }
                     bytes += t[j].valid ? kTile * row_bytes : 0;
                     all = all && t[j].there == ~0ull;
-                    if (i + T + j < w.last) next[j] = plan(i + T + j);
+                    if (place > 0) next[j] = plan(i - T + j);
                 }
                 ok = wait_phase(&sm.empty[at.slot], at.parity ^ 1u, &sm.stop, a.wait_limit);
                 if (!ok) break;
                 if (elect_one()) {
                     sm.even[at.slot] = all;
 #pragma unroll
-                    for (int j = 0; j < T; ++j) sm.there[at.slot][j] = t[j].there;
+                    for (uint32_t j = 0; j < T; ++j) sm.there[at.slot][j] = t[j].there;
                     mbar_arrive_expect_tx(&sm.full[at.slot], bytes);
                     if (!(HOOK == Hook::kWithheld && issued == 0)) {
 #pragma unroll
-                        for (int j = 0; j < T; ++j)
+                        for (uint32_t j = 0; j < T; ++j)
                             if (t[j].valid) copy(j, 0, t[j].row, t[j].page);
                     }
                 }
@@ -318,16 +323,17 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         };
         auto page_id = [&](uint32_t i) {
             const uint32_t idx = fast_div(begins(i), a.ps);
-            return j < (uint32_t)T && i + j < w.last && idx < a.max_pages
+            return j < T && i + j < w.last && idx < a.max_pages
                        ? __ldg(a.page_table + (uint64_t)w.b * a.max_pages + idx)
                        : (uint32_t)KVW_PAGE_UNMAPPED;
         };
-        uint32_t next = page_id(w.first);
-        for (uint32_t i = w.first; ok && i < w.last; i += T) {
+        uint32_t next = page_id(final);
+        for (uint32_t place = places; ok && place-- > 0;) {
+            const uint32_t i = w.first + place * T;
             const uint32_t page = next, p = begins(i);
-            if (i + T < w.last) next = page_id(i + T);
+            if (place > 0) next = page_id(i - T);
             const int64_t p_tile = (int64_t)(w.span.tile0 + i) * kTile;
-            bool used = j < (uint32_t)T;
+            bool used = j < T;
             uint64_t there = ((1ull << (1u << log_rows)) - 1) << (unit << log_rows);
             if (i + T > w.last || p_tile < w.span.start || p_tile + T * kTile > w.span.hi) {
                 // the unit's positions that count
@@ -343,14 +349,14 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             if (used && !valid) bad_page = 1;
             const bool whole = valid && __popcll(there) == 1 << log_rows;
             const bool all =
-                __all_sync(0xffffffffu, whole || j >= (uint32_t)T) && seen(p_tile, T);
+                __all_sync(0xffffffffu, whole || j >= T) && seen(p_tile, T);
             const uint32_t units = __popc(__ballot_sync(0xffffffffu, valid));
             uint64_t words[T];
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
+            for (uint32_t t = 0; t < T; ++t) {
                 words[t] = ~0ull;
                 if (!all) {
-                    const uint64_t mine = valid && j == (uint32_t)t ? there : 0;
+                    const uint64_t mine = valid && j == t ? there : 0;
                     words[t] = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(mine >> 32)) << 32 |
                                __reduce_or_sync(0xffffffffu, (uint32_t)mine);
                 }
@@ -360,7 +366,7 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
             if (lane == 0) {
                 sm.even[at.slot] = all;
 #pragma unroll
-                for (int t = 0; t < T; ++t) sm.there[at.slot][t] = words[t];
+                for (uint32_t t = 0; t < T; ++t) sm.there[at.slot][t] = words[t];
                 mbar_arrive_expect_tx(&sm.full[at.slot], (units << log_rows) * row_bytes);
             }
             __syncwarp();
@@ -801,7 +807,8 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
         };
         using One = std::integral_constant<int, 1>;
         using All = std::integral_constant<int, Sh::kTiles>;
-        for (uint32_t k = 0; k < count; k += Sh::kTiles) {
+        for (uint32_t place = (count + Sh::kTiles - 1) / Sh::kTiles; place-- > 0;) {
+            const uint32_t k = place * Sh::kTiles;
             alive = wait_phase(&sm.full[at.slot], at.parity, &sm.stop, a.wait_limit);
             if (!alive) break;
             if (sm.even[at.slot]) {
