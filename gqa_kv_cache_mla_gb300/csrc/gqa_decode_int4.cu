@@ -37,7 +37,12 @@
 //
 // Weights times scales are fp16.  Their reference m follows the row's largest
 // P s_v, not its largest score: raised when a product passes 2^15, to where
-// the largest is 2^9 (weight_lift).  The sum of weights is fp32.
+// the largest is 2^9 (weight_lift).  The sum of weights is fp32.  A position whose
+// values are all zero takes part in it alone, with any weight: so a scale counts as
+// kLeastScale at least in the row's largest, and the reference rises as well when
+// weights or their sum pass kMostSum.  (By the products alone, zero values 80 above
+// the rest made the sum infinite, and with it every other position's share 0; the
+// look at the sums costs 198 -> 201 us of 256 requests, 128 -> 131 of heads of 64.)
 //
 // Bound: a tile of 64 positions is 8.7 KB for heads of 128, and what a consumer
 // does for it (S, softmax, O^T for 16 positions each of four warps) some 250
@@ -64,6 +69,10 @@
 
 namespace kvw {
 namespace {
+
+// A value's scale as the weights' reference sees it, at least; weights that raise
+// the reference, at a time or in all; the sum of a row that has no reference.
+constexpr float kLeastScale = 0x1p-40f, kMostSum = 0x1p100f, kUnset = 0x1p126f;
 
 // What happens to scores: nothing, a distance bias, or a cap and perhaps a bias.
 enum class Mods { kNone, kBias, kCap };
@@ -587,8 +596,8 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
 
         float acc[CH][2][4], less[NG][4];  // O^T, and 8 sum (P s_v) in its units
         // the rows' references and sums; a row that has seen no position has m =
-        // -inf and subtracts 0
-        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
+        // -inf, subtracts 0 and has a sum that asks for a reference
+        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {kUnset, kUnset};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
 #pragma unroll
@@ -596,7 +605,6 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
 #pragma unroll
             for (int g = 0; g < NG; ++g) less[g][e] = 0.0f;
         }
-        bool settled = false;  // every row has a reference
 
         // The warp's slices of N tiles of the place at `at`, from its tile j on,
         // tile k of the segment; EDGE: positions may be missing, or seen by some
@@ -696,23 +704,26 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
             }
             auto kept = [&](int e) { return !EDGE || ((seen >> e) & 1u); };
             // ---- weights, and weights times scales of the values
-            float p[N][4];
+            float sum[N][2];       // of the rows' weights
             uint32_t b[N][NG][2];  // rows 2 * in_quad and the next, of either position
             auto weights = [&]() {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
+                    float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        p[i][e] = fast_exp2(MODS == Mods::kNone
-                                                ? fmaf(s[i][e], qs[e & 1], -ref[e & 1])
-                                                : s[i][e] - ref[e & 1]);
+                        p[e] = fast_exp2(MODS == Mods::kNone
+                                             ? fmaf(s[i][e], qs[e & 1], -ref[e & 1])
+                                             : s[i][e] - ref[e & 1]);
+                    sum[i][0] = p[0] + p[2];
+                    sum[i][1] = p[1] + p[3];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         const uint32_t by = scales_of(i, NG + g);
                         float x[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            x[e] = p[i][e] * (e < 2 ? bf16_lo(by) : bf16_hi(by));
+                            x[e] = p[e] * (e < 2 ? bf16_lo(by) : bf16_hi(by));
                             if (!kept(e)) x[e] = 0.0f;  // whatever its scale holds
                         }
                         b[i][g][0] = pack2<true>(x[0], x[1]);
@@ -728,20 +739,25 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
             // numbers that are not negative; a NaN's, and those of negative
             // scales, are above 2^15's.)
             uint32_t top = 0;
+            float most_sum = fmaxf(l[0], l[1]);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     top = __vmaxu2(top, __vmaxu2(b[i][g][0], b[i][g][1]));
-            if (__any_sync(0xffffffffu, !settled || __vcmpgtu2(top, 0x78007800u) != 0)) {
+                most_sum = fmaxf(most_sum, fmaxf(sum[i][0], sum[i][1]));
+            }
+            if (__any_sync(0xffffffffu,
+                           most_sum > kMostSum || __vcmpgtu2(top, 0x78007800u) != 0)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    // the row's largest weight times scale, in log2
-                    float most = -INFINITY;
+                    // the row's largest weight times scale, in log2, its sum so far as
+                    // a position of zero values
+                    float most = m[e] + __log2f(l[e] * kLeastScale);
 #pragma unroll
                     for (int y = 0; y < 2 * N; ++y) {
                         const int i = y / 2, h = y % 2;
-                        float by = 0x1p-40f;
+                        float by = kLeastScale;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             const uint32_t x = scales_of(i, NG + g);
@@ -769,13 +785,12 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
                         for (int g = 0; g < NG; ++g) less[g][2 * h + e] *= f;
                     }
                 }
-                settled = __all_sync(0xffffffffu, fminf(m[0], m[1]) > -INFINITY);
                 weights();
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                l[0] += p[i][0] + p[i][2];
-                l[1] += p[i][1] + p[i][3];
+                l[0] += sum[i][0];
+                l[1] += sum[i][1];
             }
             // ---- O^T += V^T (P s_v)^T
 #pragma unroll
@@ -826,6 +841,7 @@ __global__ void __launch_bounds__(Shape4<D>::kThreads, Shape4<D>::kCtas)
         // ---- the warps join, a few rows at a time
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            if (m[e] == -INFINITY) l[e] -= kUnset;  // 0, or NaN
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
             if (quad == 0) {
