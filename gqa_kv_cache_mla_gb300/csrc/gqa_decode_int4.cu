@@ -266,8 +266,9 @@ __device__ __forceinline__ void feed4(const GqaArgs& a, const Int4Maps& maps, Sm
         // ---- the tiles
         auto copy = [&](uint32_t j, uint32_t unit, uint32_t row, uint32_t page) {
             const uint32_t bar = smem_addr(&sm.full[at.slot]);
+            // (rows of a copy begin at multiples of 16; a row's bytes would pass 32 bits)
             tma_rows(smem_addr(sm.codes[at.slot][j]) + ((unit * D) << log_rows), &maps.codes.map[0],
-                     0, row * (D / 2) / 128, kvh, page, 0, bar);
+                     0, row / 16 * (D / 16), kvh, page, 0, bar);
             tma_rows(smem_addr(sm.scales[at.slot][j]) + unit * s_unit, &maps.scales, row, 0, kvh,
                      page, 0, bar);
         };
