@@ -106,13 +106,16 @@ def version() -> int:
 
 
 def _ptr(x):
-    """Device address of a tensor (or an int address, or None)."""
+    """Device address of a tensor (or an int address, or None).  Anything else is
+    refused here: ctypes would take bytes, text and arrays as host addresses."""
     if x is None:
         return None
     try:
         return x.data_ptr()
     except AttributeError:
-        return x
+        if isinstance(x, int):
+            return x
+        raise
 
 
 def _stream(stream):

@@ -1,0 +1,35 @@
+"""What the Python bindings take as a device address, and what they refuse before
+the library sees it (no device needed)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from gqa_kv_cache_mla_gb300 import kva, kvw
+
+
+def test_device_addresses():
+    t = torch.zeros(4)
+    assert kvw._ptr(t) == t.data_ptr() and kvw._ptr(None) is None
+    assert kvw._ptr(0x10000) == 0x10000 and kvw._ptr(0) == 0
+
+
+# ctypes would pass the first three on as addresses of host memory
+@pytest.mark.parametrize("other", [b"bytes", "text", (ctypes.c_uint32 * 4)(),
+                                   bytearray(8), [1, 2], (), 1.0, np.zeros(4), np.int64(16)],
+                         ids=lambda x: type(x).__name__)
+def test_nothing_else_is_a_device_address(other):
+    with pytest.raises((AttributeError, TypeError)):
+        kvw._ptr(other)
+    offsets = torch.zeros(2, dtype=torch.int32)
+    cache = kvw.paged_cache(0x10000, kva.DTYPE_INT4, 0x10000, 0x10000, 1, 1, 16, 1, 64,
+                            (2048, 1024, 1024, 64, 1024), max_pages_per_seq=1)
+    scales = kva.group_scales(0x10000, (64, 32, 32, 32))
+    with pytest.raises((AttributeError, TypeError)):
+        kva.kva_gqa_decode_int4(0x10000, 0x10000, offsets, cache, scales, 0, 1.0, other,
+                                num_batches=1, tot_seq_len=0, num_q_heads=1, q_row_stride=64,
+                                workspace_bytes=1 << 30, stream=0)
+    with pytest.raises((AttributeError, TypeError)):
+        kvw.paged_cache(other, kva.DTYPE_INT4, 0x10000, 0x10000, 1, 1, 16, 1, 64,
+                        (2048, 1024, 1024, 64, 1024), max_pages_per_seq=1)
