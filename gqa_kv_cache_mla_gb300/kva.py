@@ -87,6 +87,13 @@ def _size(t):
     return t.numel() * t.element_size()
 
 
+def _check_integers(name, t, size=4):
+    """ValueError unless t holds integers of `size` bytes (or is an address)."""
+    d = getattr(t, "dtype", None)
+    if d is not None and (d.itemsize != size or d.is_floating_point or d.is_complex):
+        raise ValueError("%s: integers of %d bits, not %s" % (name, 8 * size, d))
+
+
 def _append(call, place, q_out, qkv, input_row_offsets, cache, freqs_cis, layer_idx, q_gamma,
             k_gamma, epsilon, weight_offset, position_ids, interleaved, mrope_section, err_flags,
             stream, num_batches, tot_seq_len, num_q_heads, q_out_row_stride, qkv_row_stride,
@@ -199,15 +206,19 @@ def int4_cache(codes, scales, page_table, cache_lengths):
     """The two descriptors of a cache held in 4 bits, for ``codes`` uint8
     [pages, 2, layers, heads, page_size, head_size / 2] and ``scales`` bf16
     [pages, 2, layers, heads, groups, page_size], views whose last two
-    dimensions are dense."""
+    dimensions are dense, an int32 page table and int32 lengths."""
+    import torch
+
+    _check_integers("page_table", page_table)
+    _check_integers("cache_lengths", cache_lengths)
     pages, planes, layers, heads, page_size, half = codes.shape
     d, groups = 2 * half, -(-2 * half // GROUP)
     if planes != 2 or tuple(scales.shape) != (pages, 2, layers, heads, groups, page_size) \
-            or codes.element_size() != 1 or scales.element_size() != 2 \
+            or codes.element_size() != 1 or scales.dtype != torch.bfloat16 \
             or tuple(codes.stride()[4:]) != (half, 1) \
             or scales.stride()[5] != 1 or (groups > 1 and scales.stride()[4] != page_size):
-        raise ValueError("codes %s and scales %s are not those of a cache in 4 bits"
-                         % (tuple(codes.shape), tuple(scales.shape)))
+        raise ValueError("codes %s %s and scales %s %s are not those of a cache in 4 bits"
+                         % (tuple(codes.shape), codes.dtype, tuple(scales.shape), scales.dtype))
     st = codes.stride()
     cache = kvw.paged_cache(codes, DTYPE_INT4, page_table, cache_lengths, pages, layers, page_size,
                             heads, d, (2 * st[0], 2 * st[1], 2 * st[2], d, 2 * st[3]))

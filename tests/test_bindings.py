@@ -33,3 +33,21 @@ def test_nothing_else_is_a_device_address(other):
     with pytest.raises((AttributeError, TypeError)):
         kvw.paged_cache(other, kva.DTYPE_INT4, 0x10000, 0x10000, 1, 1, 16, 1, 64,
                         (2048, 1024, 1024, 64, 1024), max_pages_per_seq=1)
+
+
+# ------------------------------------------------------------------ a cache in 4 bits
+
+def test_types_of_a_cache_in_4_bits():
+    codes = torch.zeros(5, 2, 3, 4, 32, 48, dtype=torch.uint8)
+    scales = torch.zeros(5, 2, 3, 4, 2, 32, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 7, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    kva.int4_cache(codes, scales, table, lens)
+    kva.int4_cache(codes, scales, table.view(torch.uint32), lens.data_ptr())
+    for bad in (scales.half(), scales.view(torch.int16), scales.view(torch.uint16)):
+        with pytest.raises(ValueError):  # their bits are not those of bf16 numbers
+            kva.int4_cache(codes, bad, table, lens)
+    for bad in (table.long(), table.short(), table.float()):
+        with pytest.raises(ValueError):
+            kva.int4_cache(codes, scales, bad, lens)
+        with pytest.raises(ValueError):
+            kva.int4_cache(codes, scales, table, bad[0])
