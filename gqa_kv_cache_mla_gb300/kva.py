@@ -280,13 +280,30 @@ def kva_gqa_decode_int4(out, q, input_row_offsets, cache: PagedCacheT, scales: G
 
 # ------------------------------------------------------------------ page tables
 
+_table_types = set()  # of arguments that a call has found right
+
+
 def kva_extend_page_tables(page_table, cache_lengths, input_row_offsets, free_pages, taken,
                            taken_out, page_size: int, num_pages: int, slot_map=None,
                            err_flags=None, stream=None, *, num_batches=None, tot_seq_len=None,
                            max_pages_per_seq=None, num_free=None, check=True) -> int:
     """``page_table`` int32 [requests, width], ``free_pages`` int32 ids,
     ``taken``, ``taken_out`` int32 [1], ``slot_map`` int64 [tokens] or None
-    (then ``tot_seq_len`` is needed)."""
+    (then ``tot_seq_len`` is needed).  Other types are refused: ids of 64 bits
+    would be read as two each."""
+    try:
+        types = (page_table.dtype, cache_lengths.dtype, input_row_offsets.dtype, free_pages.dtype,
+                 taken.dtype, taken_out.dtype, None if slot_map is None else slot_map.dtype)
+    except AttributeError:  # addresses among them
+        types = None
+    if types not in _table_types:
+        for name, t in (("page_table", page_table), ("cache_lengths", cache_lengths),
+                        ("input_row_offsets", input_row_offsets), ("free_pages", free_pages),
+                        ("taken", taken), ("taken_out", taken_out)):
+            _check_integers(name, t)
+        _check_integers("slot_map", slot_map, 8)
+        if types is not None:
+            _table_types.add(types)
     B = input_row_offsets.shape[0] - 1 if num_batches is None else num_batches
     if tot_seq_len is None:
         if slot_map is None:

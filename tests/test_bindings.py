@@ -51,3 +51,39 @@ def test_types_of_a_cache_in_4_bits():
             kva.int4_cache(codes, scales, bad, lens)
         with pytest.raises(ValueError):
             kva.int4_cache(codes, scales, table, bad[0])
+
+
+# ------------------------------------------------------------------ page tables
+
+NAMES = ["page_table", "cache_lengths", "input_row_offsets", "free_pages", "taken", "taken_out"]
+
+
+def tables(**kw):
+    """A call of no tokens, which launches nothing."""
+    a = {n: torch.zeros(2, dtype=torch.int32) for n in NAMES}
+    a["page_table"] = torch.zeros(1, 7, dtype=torch.int32)
+    a.update(kw)
+    return kva.kva_extend_page_tables(*[a[n] for n in NAMES], 16, 8, stream=0,
+                                      slot_map=a.get("slot_map"), tot_seq_len=0, num_free=2,
+                                      num_batches=1, max_pages_per_seq=7)
+
+
+def test_page_tables_take_tensors_and_addresses():
+    assert tables() == tables(slot_map=torch.zeros(0, dtype=torch.int64)) == kvw.KVW_OK
+    assert tables(**{n: torch.zeros(2, 7, dtype=torch.uint32) for n in NAMES}) == kvw.KVW_OK
+    assert tables(**{n: 0x10000 for n in NAMES}, slot_map=0x10000) == kvw.KVW_OK
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int16, torch.uint8, torch.float32])
+def test_page_tables_are_of_32_bits(name, dtype):
+    """torch.arange gives 64-bit ids, of which every second word would be an id 0."""
+    with pytest.raises(ValueError):
+        tables(**{name: torch.zeros(2, 7, dtype=dtype)})
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.float64])
+def test_slots_are_of_64_bits(dtype):
+    """A narrower buffer would be written past its end."""
+    with pytest.raises(ValueError):
+        tables(slot_map=torch.zeros(4, dtype=dtype))
