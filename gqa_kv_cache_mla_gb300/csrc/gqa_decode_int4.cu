@@ -959,11 +959,11 @@ int launch(GqaArgs& a, const kvw_paged_cache_t* cache, const kva_group_scales_t*
     return e == cudaSuccess ? KVW_OK : KVW_ECUDA;
 }
 
-// Strides that a tensor map takes (see tma_strides_ok), of codes and scales.
+// Strides that a tensor map takes (see tma_strides_ok), of codes and scales that
+// check_int4 has found positive.
 bool int4_strides_ok(const kvw_paged_cache_t* c, const kva_group_scales_t* s) {
     auto ok = [](int64_t codes, int64_t scales, uint64_t n) {
-        return n <= 1 || (codes > 0 && codes / 2 < (1ll << 40) && scales > 0 &&
-                          scales < (1ll << 39));
+        return n <= 1 || (codes / 2 < (1ll << 40) && scales < (1ll << 39));
     };
     return ok(c->stride_head, s->stride_head, c->num_heads) &&
            ok(c->stride_page, s->stride_page, c->num_pages) && ok(c->stride_kv, s->stride_kv, 2);

@@ -27,10 +27,15 @@ inline int check_int4(const kvw_paged_cache_t* c, const kva_group_scales_t* s,
     auto whole = [](int64_t codes, int64_t scales, uint64_t n) {  // multiples of 16 bytes
         return n <= 1 || (codes % 32 == 0 && scales % 8 == 0);
     };
-    if (!whole(c->stride_page, s->stride_page, c->num_pages) ||
-        !whole(c->stride_kv, s->stride_kv, 2) ||
+    // the kernels know a row without a page by a place below 0, and the copy engine
+    // walks forwards only
+    auto rising = [&](int64_t codes, int64_t scales, uint64_t n) {
+        return whole(codes, scales, n) && (n <= 1 || (codes > 0 && scales > 0));
+    };
+    if (!rising(c->stride_page, s->stride_page, c->num_pages) ||
+        !rising(c->stride_kv, s->stride_kv, 2) ||
         !whole(c->stride_layer, s->stride_layer, c->num_layers) ||
-        !whole(c->stride_head, s->stride_head, c->num_heads))
+        !rising(c->stride_head, s->stride_head, c->num_heads))
         return KVW_EINVAL;
     return KVW_OK;
 }

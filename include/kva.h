@@ -212,10 +212,11 @@ int kva_mla_decode_workspace(uint32_t num_heads, uint64_t* bytes);
  *                   + head*stride_head + g*page_size + r  elements
  * head_size 64, 96, 128 or 256 and page_size a multiple of 16 (else
  * KVW_EUNSUPPORTED); stride_token = head_size, the other strides multiples of
- * 16 bytes, both data pointers 16-byte aligned (else KVW_EINVAL).  The
- * descriptor's scale is not used.  Dense layouts: codes [pages, 2, layers,
- * heads, page_size, head_size / 2] bytes, scales [pages, 2, layers, heads,
- * groups, page_size].
+ * 16 bytes, those of pages, planes and heads positive, both data pointers
+ * 16-byte aligned (else KVW_EINVAL; a stride of a dimension of one index is not
+ * looked at).  The descriptor's scale is not used.  Dense layouts: codes [pages,
+ * 2, layers, heads, page_size, head_size / 2] bytes, scales [pages, 2, layers,
+ * heads, groups, page_size].
  */
 enum kva_dtype { KVA_DTYPE_INT4 = 3 };
 
