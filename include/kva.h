@@ -283,9 +283,16 @@ int kva_gather_kv_int4(void* k_out, void* v_out, int64_t out_row_stride,
  * exact; a query row is brought into fp16's range by a power of two, which
  * loses only what is below 2^-35 of the row's largest value; a weight times
  * its value's scale is off by 2^-11 of itself or, for small ones, by 2^-34 of
- * the row's largest.  Products of 16 columns (of 16 positions) are added up by
- * one matrix instruction, which may cut each at 2^-13 of a code times the
- * largest query value (weight times scale) beside fp32's own rounding.
+ * the row's largest (where a scale counts as 2^-40 at least).  Products of 16
+ * columns (of 16 positions) are added up by one matrix instruction, which may
+ * cut each at 2^-13 of a code times the largest query value (weight times
+ * scale) beside fp32's own rounding.
+ * Ranges: scales of values are 0 or from 2^-60 to 2^80 (smaller ones lose bits,
+ * beside larger ones positions of zero values lose their share of the sum).
+ * sm_scale times a query value is below 2^117, with a cap below 2^116 times that
+ * (a row's scores come out too small above).  Scales are finite or NaN, as
+ * kva_append_qkv_int4 writes them: an infinite one may give NaN where the formula
+ * has an infinity, and the reverse.
  * Strides as kva_gqa_decode_paged for codes and scales.
  */
 int kva_gqa_decode_int4(void* out, float* lse, const void* q, int64_t q_row_stride,

@@ -1,7 +1,7 @@
 """Attention over a cache held in 4 bits where weights and value scales are far
-apart: positions of zero values with large scores (GPU).  Calls are large enough
-that a piece takes whole contexts, tile after tile, so that sums are held while
-the reference moves."""
+apart: positions of zero values with large scores, and the ends of the ranges
+that the header gives (GPU).  Calls are large enough that a piece takes whole
+contexts, tile after tile, so that sums are held while the reference moves."""
 import copy
 
 import pytest
@@ -27,7 +27,7 @@ def repeated(c, reps):
 LEAST = 2.0 ** -40  # what a value's scale counts as, at least
 
 
-def run_repeated(kva, c, q, reps, **kw):
+def run_repeated(kva, c, q, reps, least=LEAST, **kw):
     """Every repetition against one evaluation in 64 bits.
 
     A weight times a scale is rounded to fp16, by 2^-34 of the row's largest where
@@ -39,7 +39,7 @@ def run_repeated(kva, c, q, reps, **kw):
     torch.cuda.synchronize()
     assert int(x.flags) == 0
     out, lse, to, tl = Q.gqa(c, q, x.scale, x.softcap, x.window, x.slopes)
-    to += 2.0 ** -34 * LEAST * 7 * (max(c.prior) + 1)
+    to += 2.0 ** -34 * least * 7 * (max(c.prior) + 1)
     for got, want, tol, what in ((x.out, out, to, "out"), (x.lse, lse, tl, "lse")):
         R.check(got.cpu(), want.repeat(reps, *[1] * (want.dim() - 1)),
                 tol.repeat(reps, *[1] * (tol.dim() - 1)), what)
@@ -79,3 +79,38 @@ def test_zero_values_alone(kva, head, q_heads, nats):
     v[:384] = 0
     c.put(0, 1, 0, *Q.held(v))
     run_repeated(kva, c, torch.full((1, q_heads, head), nats / head).bfloat16(), 1200, sm_scale=1.0)
+
+
+@pytest.mark.parametrize("head,q_heads", [(64, 2), (96, 8), (128, 12), (256, 4)])
+@pytest.mark.parametrize("power", [-60, -45, -30, 60, 80])
+def test_values_of_any_size(kva, head, q_heads, power):
+    """A cache whose values are all tiny, or all large, is as exact as any other: at
+    2^-60 the 2^-34 of what counts as 2^-40 is 2^-14 of the largest, within the
+    2^-11 of a weight."""
+    c = Q.Int4(202, *lengths(300, 65, 900), kv_heads=1, head=head, page=64, layers=1,
+               layer=0).fill()
+    c.scales[:, 1] = (c.scales[:, 1].double() * 2.0 ** power).bfloat16()
+    run_repeated(kva, c, c.normal(3, q_heads, head, std=2.0), 300, least=0.0)
+
+
+@pytest.mark.parametrize("head,q_heads", [(64, 2), (128, 12), (256, 4)])
+@pytest.mark.parametrize("zeros", [(0, 512), (512, 896), (64, 128)])
+def test_zero_values_beside_the_largest(kva, head, q_heads, zeros):
+    """Zero values keep their share of the weights beside values of 2^80."""
+    c = Q.Int4(204, *lengths(900, 330), kv_heads=1, head=head, page=64, layers=1, layer=0).fill()
+    c.scales[:, 1] = (c.scales[:, 1].double() * 2.0 ** 80).bfloat16()
+    for b, n in enumerate((900, 330)):
+        ids, row = c.place(b, min(zeros[0], n), min(zeros[1], n))
+        c.scales[ids, 1, c.layer, :, :, row] = 0
+    run_repeated(kva, c, c.normal(2, q_heads, head), 400)
+
+
+@pytest.mark.parametrize("head,q_heads", [(64, 2), (128, 12), (256, 4)])
+@pytest.mark.parametrize("power,softcap", [(100, 0.0), (117, 0.0), (116, 1.0), (118, 4.0)])
+def test_largest_queries(kva, head, q_heads, power, softcap):
+    """Queries whose product with sm_scale is just below 2^117 (2^116 times a cap),
+    over keys as much smaller."""
+    c = Q.Int4(203, *lengths(300, 65), kv_heads=1, head=head, page=64, layers=1, layer=0).fill()
+    c.scales[:, 0] = (c.scales[:, 0].double() * 2.0 ** -power).bfloat16()
+    q = torch.randn(2, q_heads, head, generator=c.gen).clamp(-1.9, 1.9)
+    run_repeated(kva, c, (q * 2.0 ** power).bfloat16(), 4, sm_scale=0.5, softcap=softcap)
