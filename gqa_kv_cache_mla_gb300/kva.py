@@ -248,6 +248,9 @@ def kva_gather_kv_int4(k_out, v_out, ctx_offsets, cache: PagedCacheT, scales: Gr
     one = v_out if k_out is None else k_out
     B = ctx_offsets.shape[0] - 1 if num_batches is None else num_batches
     R = (0 if one is None else one.shape[0]) if total_rows is None else total_rows
+    for out in (k_out, v_out):
+        if hasattr(out, "element_size") and out.element_size() != 2:
+            raise ValueError("rows are written in bf16, not %s" % out.dtype)
     if out_row_stride is None:
         out_row_stride = 0 if one is None else one.stride(0)
         if k_out is not None and v_out is not None and v_out.stride(0) != out_row_stride:

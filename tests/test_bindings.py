@@ -87,3 +87,21 @@ def test_slots_are_of_64_bits(dtype):
     """A narrower buffer would be written past its end."""
     with pytest.raises(ValueError):
         tables(slot_map=torch.zeros(4, dtype=dtype))
+
+
+# ------------------------------------------------------------------ rows of such a cache
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.float8_e4m3fn, torch.float32])
+def test_rows_are_of_16_bits(dtype):
+    """A narrower buffer would be written past its end.  (With no requests the
+    library refuses the call before it launches anything.)"""
+    cache = kvw.paged_cache(0x10000, kva.DTYPE_INT4, 0x10000, 0x10000, 1, 1, 16, 1, 64,
+                            (2048, 1024, 1024, 64, 1024), max_pages_per_seq=1)
+    scales = kva.group_scales(0x10000, (64, 32, 32, 32))
+    off, bad = torch.zeros(1, dtype=torch.int32), torch.zeros(3, 1, 64, dtype=dtype)
+    good = bad.to(torch.bfloat16)
+    for k, v in ((bad, None), (None, bad), (good, bad), (bad, good)):
+        with pytest.raises(ValueError):
+            kva.kva_gather_kv_int4(k, v, off, cache, scales, 0, stream=0)
+    with pytest.raises(kvw.KvwError):
+        kva.kva_gather_kv_int4(good, good, off, cache, scales, 0, stream=0)
