@@ -936,10 +936,14 @@ cudaError_t launch_as(GqaArgs& a, const Int4Maps& maps, cudaStream_t stream) {
     cudaError_t e = wave_ctas<&gqa_int4_kernel<D, MODS, HOOK>>(Sh::kThreads, smem, wave);
     if (e != cudaSuccess) return e;
     if (wave == 0) return cudaErrorInvalidConfiguration;
-    // A call of few row blocks is short unless its contexts are very long: two
-    // CTAs per SM leave the join's blocks room to wait beside them (one token over
-    // 901 positions 12.0 -> 9.7 us; one over 65536: 25.3 either way).
-    if (Sh::kCtas == 3 && (uint64_t)a.split.T * a.split.blocks <= 16) wave -= wave / 3;
+    // Where two CTAs per SM would have a tile each at most, as far as the page table
+    // reaches, two leave the join's blocks room to wait beside them (one token over
+    // 901 positions 10.4 -> 9.7 us).  Longer contexts want all three: one token over
+    // 4096 positions 12.1 us against 12.7, 32768 17.6 against 19.1, 131072 34.4 against
+    // 37.5 (heads of 64, two requests: 28.5, 31.9); two requests of 32768 20.8, 19.6.
+    const uint64_t two = wave - wave / 3;
+    const uint64_t tiles = (uint64_t)(a.split.cap + kTile - 1) / kTile;
+    if (Sh::kCtas == 3 && tiles * a.split.T * a.split.blocks <= two) wave = two;
     const uint32_t ctas = side_by_side(a, wave);
     e = launch_early(&gqa_int4_kernel<D, MODS, HOOK>, dim3(ctas), Sh::kThreads, smem, stream, a,
                      maps);

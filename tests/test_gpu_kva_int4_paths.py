@@ -51,7 +51,7 @@ def test_many_tiles_of_one_segment(kva, head, q_heads, page, softcap):
     """One context, whose table goes through the same 13 pages (of 16: 52) over and
     over: the same mean of the values, and a sum as many times as large.
 
-    A piece adds up at most 55 products of 17 cuts, then four warps and 304 pieces
+    A piece adds up at most 37 products of 17 cuts, then four warps and 456 pieces
     are joined: fewer terms than two periods have, so twice a period's tolerance."""
     period = 13 * (64 if page == 16 else page)
     c = Q.Int4(221, *lengths(period), kv_heads=1, head=head, page=page, layers=1, layer=0,
@@ -115,6 +115,16 @@ def test_bad_pages_among_many_tiles(kva, head, page):
     assert int(x.flags) == 1
     out, _, to, _ = Q.gqa(c, q, x.scale)
     R.check(x.out.cpu(), out.repeat(enough(c, head), 1, 1), to.repeat(enough(c, head), 1, 1))
+
+
+@pytest.mark.parametrize("head", [64, 96, 128])
+@pytest.mark.parametrize("extra", [0, 40, 4000])
+def test_tables_that_reach_further(kva, head, extra):
+    """What the page table could hold, not what it holds, decides on the CTAs."""
+    c = Q.Int4(225, *lengths(901), kv_heads=2, head=head, page=64, table_extra=extra).fill()
+    x = Call(kva, c, 8)
+    x.call()
+    x.check()
 
 
 # ------------------------------------------------------------------ append
