@@ -9,6 +9,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -390,22 +391,23 @@ inline cudaError_t smem_optin(int& out) {
 }
 
 // Allow kernel K `smem` bytes of dynamic shared memory on the current device
-// (the attribute is raised once per device to the largest size asked for).
+// (the attribute is raised once per device to the largest size asked for; one
+// thread at a time, so that a smaller size never comes after a larger one).
 template <auto K>
 inline cudaError_t prepare_smem(size_t smem) {
     static std::atomic<uint64_t> allowed[kMaxDevices];
+    static std::mutex raising;
     if (smem == 0) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool cacheable = dev >= 0 && dev < kMaxDevices;
     if (cacheable && allowed[dev].load(std::memory_order_relaxed) >= smem) return cudaSuccess;
+    const std::lock_guard<std::mutex> lock(raising);
+    if (cacheable && allowed[dev].load(std::memory_order_relaxed) >= smem) return cudaSuccess;
     e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess || !cacheable) return e;
-    uint64_t prev = allowed[dev].load(std::memory_order_relaxed);
-    while (prev < smem && !allowed[dev].compare_exchange_weak(prev, smem)) {
-    }
-    return cudaSuccess;
+    if (e == cudaSuccess && cacheable) allowed[dev].store(smem, std::memory_order_relaxed);
+    return e;
 }
 
 // CTAs of kernel K resident on the whole current device at once with
