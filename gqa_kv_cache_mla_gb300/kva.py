@@ -248,9 +248,13 @@ def kva_gather_kv_int4(k_out, v_out, ctx_offsets, cache: PagedCacheT, scales: Gr
     one = v_out if k_out is None else k_out
     B = ctx_offsets.shape[0] - 1 if num_batches is None else num_batches
     R = (0 if one is None else one.shape[0]) if total_rows is None else total_rows
-    for out in (k_out, v_out):
-        if hasattr(out, "element_size") and out.element_size() != 2:
-            raise ValueError("rows are written in bf16, not %s" % out.dtype)
+    try:
+        wide = (k_out is None or k_out.element_size() == 2) \
+            and (v_out is None or v_out.element_size() == 2)
+    except AttributeError:  # addresses among them
+        wide = True
+    if not wide:
+        raise ValueError("rows are written in bf16")
     if out_row_stride is None:
         out_row_stride = 0 if one is None else one.stride(0)
         if k_out is not None and v_out is not None and v_out.stride(0) != out_row_stride:
@@ -283,7 +287,19 @@ def kva_gqa_decode_int4(out, q, input_row_offsets, cache: PagedCacheT, scales: G
 
 # ------------------------------------------------------------------ page tables
 
-_table_types = set()  # of arguments that a call has found right
+_int32 = _int64 = object()  # torch's types, once a call has looked
+
+
+def _check_tables(*tensors):
+    """The types of a call's tensors, the slot map last."""
+    global _int32, _int64
+    import torch
+
+    _int32, _int64 = torch.int32, torch.int64
+    for name, t in zip(("page_table", "cache_lengths", "input_row_offsets", "free_pages", "taken",
+                        "taken_out"), tensors):
+        _check_integers(name, t)
+    _check_integers("slot_map", tensors[-1], 8)
 
 
 def kva_extend_page_tables(page_table, cache_lengths, input_row_offsets, free_pages, taken,
@@ -294,26 +310,23 @@ def kva_extend_page_tables(page_table, cache_lengths, input_row_offsets, free_pa
     ``taken``, ``taken_out`` int32 [1], ``slot_map`` int64 [tokens] or None
     (then ``tot_seq_len`` is needed).  Other types are refused: ids of 64 bits
     would be read as two each."""
+    # (a small call's time is the host's: comparisons of identity, 0.2 us in all)
     try:
-        types = (page_table.dtype, cache_lengths.dtype, input_row_offsets.dtype, free_pages.dtype,
-                 taken.dtype, taken_out.dtype, None if slot_map is None else slot_map.dtype)
+        right = page_table.dtype is cache_lengths.dtype is input_row_offsets.dtype \
+            is free_pages.dtype is taken.dtype is taken_out.dtype is _int32 \
+            and (slot_map is None or slot_map.dtype is _int64)
     except AttributeError:  # addresses among them
-        types = None
-    if types not in _table_types:
-        for name, t in (("page_table", page_table), ("cache_lengths", cache_lengths),
-                        ("input_row_offsets", input_row_offsets), ("free_pages", free_pages),
-                        ("taken", taken), ("taken_out", taken_out)):
-            _check_integers(name, t)
-        _check_integers("slot_map", slot_map, 8)
-        if types is not None:
-            _table_types.add(types)
-    B = input_row_offsets.shape[0] - 1 if num_batches is None else num_batches
+        right = False
+    if not right:
+        _check_tables(page_table, cache_lengths, input_row_offsets, free_pages, taken, taken_out,
+                      slot_map)
+    B = input_row_offsets.numel() - 1 if num_batches is None else num_batches
     if tot_seq_len is None:
         if slot_map is None:
             raise ValueError("without a slot map the number of tokens has to be given")
-        tot_seq_len = slot_map.shape[0]
+        tot_seq_len = slot_map.numel()
     width = page_table.shape[-1] if max_pages_per_seq is None else max_pages_per_seq
-    nf = free_pages.shape[0] if num_free is None else num_free
+    nf = free_pages.numel() if num_free is None else num_free
     st = lib.kva_extend_page_tables(
         _ptr(page_table), width, _ptr(cache_lengths), _ptr(input_row_offsets), B, tot_seq_len,
         page_size, num_pages, _ptr(free_pages), nf, _ptr(taken), _ptr(taken_out), _ptr(slot_map),
