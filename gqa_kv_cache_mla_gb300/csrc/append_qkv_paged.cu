@@ -32,10 +32,11 @@
 // item's first rows loaded before an item ends: 143, 154, 146 us (spills).  A
 // cache in 4 bits (683 MB) has more to compute between load and store: four CTAs
 // and one pass ahead 121 us, 84 % of the copy rate (half-split 132, with norms
-// 159); five CTAs 138 (146, 196), three 134 (140, 157), three and two passes ahead
-// 153, two and two 138.  One token: 2.3 us on the device.  With few rows a token (4 + 2 x 1 heads of 96)
-// the lookups of a token are most of its work: 46 k tokens 58 us, a quarter of
-// the copy rate.
+// 160; 64 registers, 64 to 68 bytes a thread spilled); five CTAs 138 (146, 196),
+// three 134 (140, 157), three and two passes ahead 153, two and two 138.  One
+// token: 2.3 us on the device.  With few rows a token (4 + 2 x 1 heads of 96) the
+// lookups of a token are most of its work: 46 k tokens 58 us, a quarter of the
+// copy rate.
 #include <cstdint>
 
 #include "kva_common.cuh"

@@ -48,16 +48,19 @@
 // does for it (S, softmax, O^T for 16 positions each of four warps) some 250
 // instructions a slice, half of an SM's issue slots at the full rate of HBM; the
 // warps wait for each other's results rather than for tiles (feeding alone: 178
-// us of the 198 below).  So: three CTAs of four consumer warps per SM, two tiles
+// us of the 201 below).  So: three CTAs of four consumer warps per SM, two tiles
 // at a time, all that can be known once per segment worked out by the feeding
 // warp, queries' operands in shared memory.
 //
 // Measured, 32 query and 8 key-value heads of 128: 256 requests of up to 8192
-// positions 198 us (5.8 TB/s, 87 % of the card's copy rate; one tile at a time
-// 236, two CTAs per SM 217), with a cap 227, with a distance bias 203, pages of 16
-// 233, heads of 64 128, of 96 173, of 256 (128 requests) 206; 64 query heads, 8
-// requests of up to 131072 95 us; 32 of up to 4096 24 us (some 9 of it before the
-// first and after the last byte); one token over 901 positions 9.7 us.
+// positions 201 us (5.7 TB/s, 86 % of the card's copy rate; with 198 at that step,
+// one tile at a time 236, two CTAs per SM 217), with a cap 228 (the instance for
+// heads of 128 spills 16 bytes a thread), with a distance bias 205, pages of 16 235,
+// heads of 64 131, of 96 176, of 256 (128 requests) 207; 64 query heads, 8 requests
+// of up to 131072 97 us; 32 of up to 4096 24 us (some 9 of it before the first and
+// after the last byte); one token over 901 positions 9.7 us, over 65536 24.  A prompt
+// is right and slow, its context converted for every 8 rows: 8 requests of 512 new
+// tokens after up to 4096 940 us, of which the products need 75.
 //
 // Division of the work, workspace and join are those of gqa_decode_paged.cu.
 #include <cstdint>
